@@ -146,10 +146,14 @@ def _norm_inputs(c, seed):
     y = torch.empty(T * k, D, dtype=dt, device="cuda").normal_(generator=g)
     rows = torch.randperm(T * k, generator=g, device="cuda").view(T, k).to(torch.int32)
     if c["holes"]:
-        rows[_rand(g, T, k) < 0.1] = -1  # rows dropped on the way
+        drop = _rand(g, T, k) < 0.1      # rows dropped on the way
+        if T < 64:
+            drop[:, :2] = False
+        rows[drop] = -1
         if T >= 4:
             rows[T // 2] = -1            # a token whose rows were all dropped
-    return dict(x=x, y=y, rows=rows, weights=torch.softmax(_randn(g, T, k), -1),
+    # one row per token needs no weight: the norm would take it out again
+    return dict(x=x, y=y, rows=rows, weights=torch.softmax(_randn(g, T, k), -1) if k > 1 else None,
                 gate=torch.sigmoid(_randn(g, T)), res=1 + 0.1 * _randn(g, D),
                 w_post=1 + 0.1 * _randn(g, D) if c["post"] else None,
                 w_pre=1 + 0.1 * _randn(g, D))
@@ -199,7 +203,8 @@ def prepare(case, seed):
             g = _gen(seed + 1)
             s["dxo"], s["dh"] = (_randn(g, T, D).to(s["x"].dtype) for _ in range(2))
             s["dx"], s["dy"] = torch.empty_like(s["x"]), torch.zeros_like(s["y"])
-            s["dweights"], s["dgate"] = torch.empty(T, k, device=dev), torch.empty(T, device=dev)
+            s["dweights"] = torch.empty(T, k, device=dev) if k > 1 else None
+            s["dgate"] = torch.empty(T, device=dev)
             s["dres"], s["dw_post"], s["dw_pre"] = torch.zeros(3, D, device=dev)
         else:
             s["xo"], s["h"] = torch.empty_like(s["x"]), torch.empty_like(s["x"])
@@ -282,7 +287,7 @@ def _slots(s):
     """Row indices (one past the end for absent ones) and their weights, 0 for absent ones."""
     have = (s["rows"] >= 0) & (s["rows"] < s["y"].shape[0])
     idx = torch.where(have, s["rows"], s["y"].shape[0]).long()
-    return have, idx, torch.where(have, s["weights"], 0.0)
+    return have, idx, torch.where(have, s["weights"] if s["weights"] is not None else 1.0, 0.0)
 
 
 def _rows(s, have, idx):
@@ -323,7 +328,8 @@ def _plain_norm_back(s):
     else:
         out["dgate"] = (dz * y).sum(-1)
         dy = gate * dz
-    out["dweights"] = (dy[:, None] * rows).sum(-1)
+    if s["weights"] is not None:
+        out["dweights"] = (dy[:, None] * rows).sum(-1)
     d = torch.zeros(s["y"].shape[0] + 1, x.shape[1], device=x.device)
     d[idx.reshape(-1)] = (w[..., None] * dy[:, None]).reshape(-1, x.shape[1])
     out["dy"], out["dx"] = d[:-1].to(s["y"].dtype), (s["res"] * dz).to(s["x"].dtype)
@@ -381,8 +387,9 @@ def _run_own(s, c):
                 _ptr(s["w_post"]), _ptr(s["w_pre"]), _ptr(s["rstd"]), dt, T, D, k, _ptr(s["dx"]),
                 _ptr(s["dy"]), _ptr(s["dweights"]), _ptr(s["dgate"]), _ptr(s["dres"]),
                 _ptr(s["dw_post"]) if c["post"] else None, _ptr(s["dw_pre"]), ws)
-            names = ["dw_pre", "dres", "dgate", "dweights", "dy", "dx"]
-            return {n: s[n] for n in names + (["dw_post"] if c["post"] else [])}
+            names = ["dw_pre", "dres", "dgate", "dy", "dx"]
+            names += (["dw_post"] if c["post"] else []) + (["dweights"] if k > 1 else [])
+            return {n: s[n] for n in names}
         abi.moe_block_norm(_ptr(s["x"]), D, _ptr(s["y"]), D, _ptr(s["rows"]), T * k,
                            _ptr(s["weights"]), _ptr(s["gate"]), _ptr(s["res"]), _ptr(s["w_post"]),
                            _ptr(s["w_pre"]), EPS, dt, T, D, k, _ptr(s["xo"]), _ptr(s["h"]),
@@ -459,7 +466,8 @@ def _exact_sum(s):
     y = torch.zeros(T, s["x"].shape[1], dtype=torch.float64, device=s["x"].device)
     for j in range(k):
         r = s["rows"][:, j].long()
-        y += torch.where(r >= 0, s["weights"][:, j].double(), 0.0)[:, None] * s["y"][r].double()
+        w = s["weights"][:, j].double() if k > 1 else 1.0
+        y += torch.where(r >= 0, w, 0.0)[:, None] * s["y"][r].double()
     return y
 
 
@@ -493,10 +501,12 @@ def _exact_norm_back(c, s):
         out["dgate"] = (dz * y).sum(-1)
         dy = dz * gate[:, None]
     out["dy"] = torch.zeros(s["y"].shape, dtype=torch.float64, device=x.device)
-    out["dweights"] = torch.zeros(c["T"], c["k"], dtype=torch.float64, device=x.device)
+    if c["k"] > 1:
+        out["dweights"] = torch.zeros(c["T"], c["k"], dtype=torch.float64, device=x.device)
     for j in range(c["k"]):
         r = s["rows"][:, j].long()
         t = (r >= 0).nonzero().flatten()
-        out["dy"][r[t]] = s["weights"][t, j].double()[:, None] * dy[t]
-        out["dweights"][t, j] = (dy[t] * s["y"][r[t]].double()).sum(-1)
+        out["dy"][r[t]] = (s["weights"][t, j].double()[:, None] if c["k"] > 1 else 1.0) * dy[t]
+        if c["k"] > 1:
+            out["dweights"][t, j] = (dy[t] * s["y"][r[t]].double()).sum(-1)
     return out
