@@ -414,6 +414,127 @@ int all2all_combine_pc_noalloc(symm_heap_t *heap, const void *in, void *out, int
                                int D, int elem_bytes, int tile_s, int block_d, int buffer_num,
                                void *stream);
 
+/* ------------------------------------------- MoE block operators -- */
+/* What a mixture-of-experts block does on one PE's (or all PEs') tokens
+ * around the all-to-all: the router's choice, counts and balance loss; the
+ * norms around the block with its gate and residual scale; and the shared
+ * projection with one low-rank adapter per request.  The tensors are plain
+ * device memory (they may lie in the heap); "NULL allowed" marks the optional
+ * ones.  Outputs must not overlap inputs or each other unless said otherwise.
+ * Calls allocate nothing and may be captured in a CUDA graph.  A workspace
+ * needs no initialisation and is free again when the call's work on the
+ * stream is done; calls that may overlap need one each. */
+
+#define SYMM_DTYPE_F32 2 /* moe_route*, moe_block_norm*: beside SYMM_DTYPE_F16 and _BF16 */
+
+/* Most experts of moe_route, most choices per token, widest rows and most
+ * rows of a token in moe_block_norm, highest adapter rank. */
+#define SYMM_MOE_MAX_EXPERTS 1024
+#define SYMM_MOE_MAX_TOPK 32
+#define SYMM_MOE_MAX_WIDTH 16384
+#define SYMM_MOE_MAX_RANK 128
+
+/* Bytes of device workspace (16-byte aligned) of moe_route.
+ * Errors: SYMM_EINVAL (sizes as for the call). */
+int moe_route_workspace(int G, int T, int E, size_t *bytes);
+
+/* The router of a mixture of experts: for G groups (PEs, or sequences) of T
+ * tokens, the k experts of every token, their weights, each group's
+ * per-expert counts, and its balance and z losses.
+ * logits   device [G*T] rows of E, ld elements apart, of `dtype`.  NaN counts
+ *          as -infinity and +infinity as the largest finite float.
+ * mask     device uint8 [G*T] (NULL allowed = all 1): 0 marks padding.
+ * A token is valid when its mask is not 0 and a logit above -infinity is
+ * left.  With m = max_e l_e, s = sum_e exp(l_e - m), p_e = exp(l_e - m) / s:
+ * experts  int32 [G*T][k]: the k largest logits, largest first, the lower
+ *          index first among equals.  -1 where nothing is left to choose (an
+ *          expert of logit -infinity is never chosen) or the token is invalid.
+ * weights  float [G*T][k]: scale * p_j, over the sum of the chosen p if
+ *          renorm != 0; 0 beside an expert of -1.
+ * counts   int32 [G][E]: choices of expert e by the group's tokens.
+ * tokens   int32 [G]: n, the group's valid tokens.
+ * stats    float [G*T][2]: m and s, for the backward pass; 0 and 0 of an
+ *          invalid token.
+ * loss     float [G][2]: the balance loss E / (k n^2) sum_e counts_e sum_t
+ *          p_te (1 when choices and probabilities are spread evenly), and the
+ *          z loss 1/n sum_t (m + log s)^2; both 0 when n = 0.
+ * Sums are in 32 bits in an order fixed by the sizes: equal inputs give equal
+ * bits.  1 <= E <= SYMM_MOE_MAX_EXPERTS, 1 <= k <= min(E, SYMM_MOE_MAX_TOPK),
+ * ld >= E, G*T < 2^31.  G = 0 is a no-op; T = 0 writes zero counts, tokens
+ * and losses.
+ * Errors: SYMM_EINVAL, SYMM_ECUDA. */
+int moe_route(const void *logits, size_t ld, const uint8_t *mask, int dtype, int G, int T, int E,
+              int k, int renorm, float scale, int32_t *experts, float *weights, int32_t *counts,
+              int32_t *tokens, float *stats, float *loss, void *workspace, void *stream);
+
+/* Gradient of moe_route with respect to the logits.  logits .. scale as
+ * there; experts, counts, tokens, stats as it left them; dweights float
+ * [G*T][k] and dloss float [G][2] (each NULL allowed = 0) are the gradients
+ * of its weights and losses.  The counts are constants of the balance loss,
+ * as is usual: its gradient flows through the probabilities alone.
+ * dlogits  [G*T] rows of E, ldd elements apart, of `dtype`: 0 in invalid
+ *          rows.  May be the logits themselves (same ld).
+ * Errors: SYMM_EINVAL, SYMM_ECUDA. */
+int moe_route_backward(const void *logits, size_t ld, int dtype, int G, int T, int E, int k,
+                       int renorm, float scale, const int32_t *experts, const int32_t *counts,
+                       const int32_t *tokens, const float *stats, const float *dweights,
+                       const float *dloss, void *dlogits, size_t ldd, void *stream);
+
+/* Bytes of device workspace (16-byte aligned) of moe_block_norm_backward.
+ * Errors: SYMM_EINVAL. */
+int moe_block_norm_workspace(int T, int D, size_t *bytes);
+
+/* From a block's output rows to the next block's input, in one pass.  Per
+ * token t, with N(v) = v / sqrt(mean_i v_i^2 + eps):
+ *     y  = sum_{j < k} weights[t][j] * Y[rows[t][j]]      the token's rows
+ *     u  = w_post * N(y)                                  norm after the block
+ *     xo = res * x + gate[t] * u                          residual stream
+ *     h  = w_pre * N(xo)                                  norm before the next
+ * x, xo, h  device [T] rows of D, ld elements apart, of `dtype`.  xo may be x
+ *           itself.  h NULL (with w_pre NULL): no norm after xo.
+ * y         device [yrows] rows of D, ldy elements apart, of `dtype` (for
+ *           instance the combine's output, or what an AllToAll returned).
+ *           NULL: h = w_pre * N(x) alone; rows, weights, gate, res, w_post
+ *           and xo must then be NULL and k 0.
+ * rows      int32 [T][k] (NULL allowed: rows[t][j] = t*k + j).  An index
+ *           outside [0, yrows) is a dropped row: nothing is read and its
+ *           weight does not matter.  A token without rows has y = 0.
+ * weights   float [T][k] (NULL allowed = 1), gate float [T] (NULL allowed =
+ *           1), res float [D] (NULL allowed = 1).
+ * w_post    float [D]; NULL: no norm after the block, u = y.
+ * w_pre     float [D].
+ * rstd      float [T][2] (NULL allowed): 1 / sqrt(mean + eps) of y (1 where
+ *           w_post is NULL) and of xo (1 where h is NULL), for the backward
+ *           pass.
+ * Sums and norms are in 32 bits; xo and h are each rounded once, h from the
+ * unrounded xo.  eps > 0.  0 <= T, 1 <= D <= SYMM_MOE_MAX_WIDTH, 1 <= k <=
+ * SYMM_MOE_MAX_TOPK, T*k < 2^31, ld, ldy >= D.  Pointers are aligned to their
+ * elements; 16-byte aligned rows are faster.  T = 0 is a no-op.
+ * Errors: SYMM_EINVAL, SYMM_ECUDA. */
+int moe_block_norm(const void *x, size_t ld, const void *y, size_t ldy, const int32_t *rows,
+                   size_t yrows, const float *weights, const float *gate, const float *res,
+                   const float *w_post, const float *w_pre, float eps, int dtype, int T, int D,
+                   int k, void *xo, void *h, float *rstd, void *stream);
+
+/* Gradients of moe_block_norm.  dxo and dh (each NULL allowed = 0; dh NULL
+ * exactly when w_pre is) are those of xo and h; x .. w_pre as in the call, xo
+ * its result (y NULL: xo NULL, x stands for it) and rstd what it saved.
+ * dx, dxo, dh: rows ld apart as x.  Outputs:
+ *   dx        [T] rows (may be dxo);
+ *   dy        [yrows] rows, ldy apart: every row that `rows` names (they must
+ *             be distinct) is written, the others are left alone;
+ *   dweights  float [T][k] (NULL allowed; 0 beside dropped rows);
+ *   dgate     float [T], dres, dw_post, dw_pre float [D] (each NULL allowed).
+ * Column sums are taken in 32 bits in an order fixed by the sizes.
+ * Errors: SYMM_EINVAL, SYMM_ECUDA. */
+int moe_block_norm_backward(const void *dxo, const void *dh, const void *x, const void *xo,
+                            size_t ld, const void *y, size_t ldy, const int32_t *rows,
+                            size_t yrows, const float *weights, const float *gate,
+                            const float *res, const float *w_post, const float *w_pre,
+                            const float *rstd, int dtype, int T, int D, int k, void *dx, void *dy,
+                            float *dweights, float *dgate, float *dres, float *dw_post,
+                            float *dw_pre, void *workspace, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -50,6 +50,7 @@ _SZ = ctypes.c_size_t
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _U64 = ctypes.c_uint64
+_F = ctypes.c_float
 
 _SIGS = {
     "symm_heap_init": [_P, _SZ, _I, ctypes.POINTER(_P)],
@@ -79,6 +80,13 @@ _SIGS = {
     "all2all_combine_two_phase": [_P, _P, _P] + [_I] * 8 + [_P, _P, _P],
     "shmem_alltoall": [_P, _P, _P, _P, _I, _SZ, _SZ, _SZ, _P, _P, _P],
     "shmem_allgather": [_P, _P, _P, _I, _SZ, _P, _P, _P],
+    "moe_route_workspace": [_I] * 3 + [ctypes.POINTER(_SZ)],
+    "moe_route": [_P, _SZ, _P] + [_I] * 6 + [_F] + [_P] * 8,
+    "moe_route_backward": [_P, _SZ] + [_I] * 6 + [_F] + [_P] * 7 + [_SZ, _P],
+    "moe_block_norm_workspace": [_I, _I, ctypes.POINTER(_SZ)],
+    "moe_block_norm": [_P, _SZ, _P, _SZ, _P, _SZ] + [_P] * 5 + [_F] + [_I] * 4 + [_P] * 4,
+    "moe_block_norm_backward": [_P] * 4 + [_SZ, _P, _SZ, _P, _SZ] + [_P] * 6 + [_I] * 4 +
+                               [_P] * 9,
 }
 
 _lock = threading.Lock()
@@ -299,3 +307,55 @@ def shmem_alltoall(heap, inp, out, counts, W, row_bytes, in_rows, out_rows, work
 def shmem_allgather(heap, inp, out, W, nbytes, workspace, signals, stream=None):
     _check(lib().shmem_allgather(heap, inp, out, W, nbytes, workspace, signals, _stream(stream)),
            "shmem_allgather")
+
+
+# -------------------------------------------------------- MoE block operators --
+SYMM_DTYPE_F32 = 2
+SYMM_MOE_MAX_EXPERTS = 1024
+SYMM_MOE_MAX_TOPK = 32
+SYMM_MOE_MAX_WIDTH = 16384
+SYMM_MOE_MAX_RANK = 128
+
+
+def moe_route_workspace(G: int, T: int, E: int) -> int:
+    n = _SZ(0)
+    _check(lib().moe_route_workspace(G, T, E, ctypes.byref(n)), "moe_route_workspace")
+    return n.value
+
+
+def moe_route(logits, ld, mask, dtype, G, T, E, k, renorm, scale, experts, weights, counts,
+              tokens, stats, loss, workspace, stream=None):
+    """The router's choice, weights, per-expert counts and losses; see
+    include/symm_a2a.h."""
+    _check(lib().moe_route(logits, ld, mask, dtype, G, T, E, k, renorm, scale, experts, weights,
+                           counts, tokens, stats, loss, workspace, _stream(stream)), "moe_route")
+
+
+def moe_route_backward(logits, ld, dtype, G, T, E, k, renorm, scale, experts, counts, tokens,
+                       stats, dweights, dloss, dlogits, ldd, stream=None):
+    _check(lib().moe_route_backward(logits, ld, dtype, G, T, E, k, renorm, scale, experts, counts,
+                                    tokens, stats, dweights, dloss, dlogits, ldd,
+                                    _stream(stream)), "moe_route_backward")
+
+
+def moe_block_norm_workspace(T: int, D: int) -> int:
+    n = _SZ(0)
+    _check(lib().moe_block_norm_workspace(T, D, ctypes.byref(n)), "moe_block_norm_workspace")
+    return n.value
+
+
+def moe_block_norm(x, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre, eps, dtype, T,
+                   D, k, xo, h, rstd, stream=None):
+    """Weighted rows, norm after the block, gate and residual scale, norm
+    before the next block; see include/symm_a2a.h."""
+    _check(lib().moe_block_norm(x, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre, eps,
+                                dtype, T, D, k, xo, h, rstd, _stream(stream)), "moe_block_norm")
+
+
+def moe_block_norm_backward(dxo, dh, x, xo, ld, y, ldy, rows, yrows, weights, gate, res, w_post,
+                            w_pre, rstd, dtype, T, D, k, dx, dy, dweights, dgate, dres, dw_post,
+                            dw_pre, workspace, stream=None):
+    _check(lib().moe_block_norm_backward(dxo, dh, x, xo, ld, y, ldy, rows, yrows, weights, gate,
+                                         res, w_post, w_pre, rstd, dtype, T, D, k, dx, dy,
+                                         dweights, dgate, dres, dw_post, dw_pre, workspace,
+                                         _stream(stream)), "moe_block_norm_backward")
