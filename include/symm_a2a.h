@@ -535,6 +535,34 @@ int moe_block_norm_backward(const void *dxo, const void *dh, const void *x, cons
                             float *dweights, float *dgate, float *dres, float *dw_post,
                             float *dw_pre, void *workspace, void *stream);
 
+/* Bytes of device workspace (256-byte aligned) of moe_adapter_matmul.
+ * Errors: SYMM_EINVAL (sizes as for the call). */
+int moe_adapter_workspace(int T, int k, int n, int r, size_t *bytes);
+
+/* A projection shared by all requests, with one low-rank adapter per request,
+ * for any mixture of requests in a batch (one token each, whole prompts, both):
+ *     y_t = x_t W + scale_a (x_t A_a) B_a,   a = ids[t].
+ * heap   supplies the spin budget and records a wait that gave up
+ *        (symm_check_error); the tensors need not lie in it.
+ * x      device [T] rows of k, ldx elements apart.
+ * w      device [k] rows of n, ldw elements apart (k x n, row-major).
+ * a, b   device [R][k][r] and [R][r][n], dense; scale float [R].
+ * ids    int32 [T], in any order.  An id outside [0, R) (customarily -1)
+ *        means no adapter: y_t = x_t W.
+ * y      device [T] rows of n, ldy elements apart.
+ * x, w, a, b and y are of `dtype` (SYMM_DTYPE_F16 or _BF16).  Products are
+ * summed in 32 bits, x_t A_a stays in 32 bits, and y is rounded once.  The
+ * order of the sums is fixed by the sizes.
+ * R = 0 (with r = 0): the projection alone; a, b, scale, ids NULL.
+ * 0 <= T <= 2^24; k and n multiples of 8 in [8, 2^20]; r a multiple of 8 up
+ * to SYMM_MOE_MAX_RANK; ldx and ldw multiples of 8; x, w, a 16-byte aligned.
+ * T = 0 is a no-op.
+ * Errors: SYMM_EINVAL, SYMM_ECUDA; SYMM_ETIMEDOUT by symm_check_error(). */
+int moe_adapter_matmul(symm_heap_t *heap, const void *x, size_t ldx, const void *w, size_t ldw,
+                       const void *a, const void *b, const float *scale, const int32_t *ids,
+                       int dtype, int T, int k, int n, int R, int r, void *y, size_t ldy,
+                       void *workspace, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -87,6 +87,8 @@ _SIGS = {
     "moe_block_norm": [_P, _SZ, _P, _SZ, _P, _SZ] + [_P] * 5 + [_F] + [_I] * 4 + [_P] * 4,
     "moe_block_norm_backward": [_P] * 4 + [_SZ, _P, _SZ, _P, _SZ] + [_P] * 6 + [_I] * 4 +
                                [_P] * 9,
+    "moe_adapter_workspace": [_I] * 4 + [ctypes.POINTER(_SZ)],
+    "moe_adapter_matmul": [_P, _P, _SZ, _P, _SZ] + [_P] * 4 + [_I] * 6 + [_P, _SZ, _P, _P],
 }
 
 _lock = threading.Lock()
@@ -359,3 +361,17 @@ def moe_block_norm_backward(dxo, dh, x, xo, ld, y, ldy, rows, yrows, weights, ga
                                          res, w_post, w_pre, rstd, dtype, T, D, k, dx, dy,
                                          dweights, dgate, dres, dw_post, dw_pre, workspace,
                                          _stream(stream)), "moe_block_norm_backward")
+
+
+def moe_adapter_workspace(T: int, k: int, n: int, r: int) -> int:
+    b = _SZ(0)
+    _check(lib().moe_adapter_workspace(T, k, n, r, ctypes.byref(b)), "moe_adapter_workspace")
+    return b.value
+
+
+def moe_adapter_matmul(heap, x, ldx, w, ldw, a, b, scale, ids, dtype, T, k, n, R, r, y, ldy,
+                       workspace, stream=None):
+    """A shared projection with one low-rank adapter per request; see
+    include/symm_a2a.h."""
+    _check(lib().moe_adapter_matmul(heap, x, ldx, w, ldw, a, b, scale, ids, dtype, T, k, n, R, r,
+                                    y, ldy, workspace, _stream(stream)), "moe_adapter_matmul")

@@ -96,3 +96,41 @@ def test_nothing_to_do_launches_nothing():
     abi.moe_route_backward(**dict(BACK, T=0, logits=None))
     abi.moe_block_norm(**dict(NORM, T=0, x=None, xo=None))
     abi.moe_block_norm_backward(**dict(NBACK, T=0, dres=None, dw_post=None, dw_pre=None, dx=None))
+
+
+ADAPTER = dict(x=P, ldx=16, w=2 * P, ldw=24, a=3 * P, b=4 * P, scale=P, ids=P, dtype=BF16, T=4,
+               k=16, n=24, R=2, r=8, y=5 * P, ldy=24, workspace=P - P % 256, stream=0)
+
+
+@pytest.fixture
+def heap():
+    h = abi.symm_heap_init(0x7F0000000000, 4 << 20, 1)
+    yield h
+    abi.symm_heap_destroy(h)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=F32), dict(dtype=7), dict(T=-1), dict(T=(1 << 24) + 1), dict(k=0), dict(k=12),
+    dict(n=0), dict(n=20), dict(k=(1 << 20) + 8), dict(R=-1), dict(r=-8), dict(r=12), dict(r=136),
+    dict(R=0), dict(r=0), dict(ldx=8), dict(ldx=20), dict(ldw=16), dict(ldw=28), dict(ldy=23),
+    dict(ldx=1 << 40), dict(x=None), dict(w=None), dict(a=None), dict(b=None), dict(scale=None),
+    dict(ids=None), dict(y=None), dict(workspace=None), dict(x=P + 8), dict(w=2 * P + 2),
+    dict(a=3 * P + 8), dict(b=4 * P + 1), dict(y=5 * P + 1), dict(ids=P + 2), dict(scale=P + 1),
+    dict(workspace=P - P % 256 + 64), dict(y=P), dict(y=2 * P), dict(y=3 * P), dict(y=4 * P)])
+def test_adapter_refuses(heap, bad):
+    assert code(abi.moe_adapter_matmul, heap, **dict(ADAPTER, **bad)) == E
+
+
+def test_adapter_refuses_no_heap():
+    assert code(abi.moe_adapter_matmul, None, **ADAPTER) == E
+
+
+def test_adapter_workspace():
+    for T, k, n, r in ((1, 8, 8, 8), (0, 8, 8, 0), (300, 4096, 1000, 64), (8192, 4096, 4096, 32)):
+        assert abi.moe_adapter_workspace(T, k, n, r) >= T * r * 4
+    for bad in ((-1, 8, 8, 8), (1, 7, 8, 8), (1, 8, 12, 8), (1, 8, 8, 4), (1, 8, 8, 256)):
+        assert code(abi.moe_adapter_workspace, *bad) == E
+
+
+def test_adapter_without_tokens_launches_nothing(heap):
+    abi.moe_adapter_matmul(heap, **dict(ADAPTER, T=0, x=None, y=None, workspace=None))
