@@ -555,7 +555,7 @@ int moe_adapter_workspace(int T, int k, int n, int r, size_t *bytes);
  * order of the sums is fixed by the sizes.
  * R = 0 (with r = 0): the projection alone; a, b, scale, ids NULL.
  * 0 <= T <= 2^24; k and n multiples of 8 in [8, 2^20]; r a multiple of 8 up
- * to SYMM_MOE_MAX_RANK; ldx and ldw multiples of 8; x, w, a 16-byte aligned.
+ * to SYMM_MOE_MAX_RANK; ldx and ldw multiples of 8; x, w, a, b 16-byte aligned.
  * T = 0 is a no-op.
  * Errors: SYMM_EINVAL, SYMM_ECUDA; SYMM_ETIMEDOUT by symm_check_error(). */
 int moe_adapter_matmul(symm_heap_t *heap, const void *x, size_t ldx, const void *w, size_t ldw,

@@ -1,27 +1,40 @@
 // moe_adapter.cu -- a projection shared by all requests with one low-rank
 // adapter per request: y_t = x_t W + scale_a (x_t A_a) B_a, a = ids_t.
 //
-// Two launches.  The first computes h_t = scale_a x_t A_a in 32 bits (rank r
-// values per token).  The second is the product with W on the tensor cores,
-// with h_t B_a added to the 32-bit accumulators before the one rounding, so
-// any mixture of adapters in any order of tokens costs the large product
-// nothing.
+// Two launches, both on the tensor cores.  The first (rank_kernel) computes
+// h_t = scale_a x_t A_a.  The second (adapter_kernel) is the product with W, in
+// which each adapter of a tile's tokens is a few more K columns: B_a under W,
+// and h (0 in the rows of the other adapters' tokens) beside x.  So any
+// mixture of adapters in any order of tokens is summed in the same 32-bit
+// accumulators before the one rounding.  h enters as the sum of two values of
+// the type, so that its rounding (2^-18 relatively in bf16, 2^-22 in fp16)
+// stays far below the output's.
 //
 // The product is computed as y^T = W^T x^T: the M side of a tile is 128
 // columns of W (W as stored, k x n, is an M-major operand) and the N side BT
-// tokens, 16 to 256.  One token then wastes no more than a narrow N, one
-// kernel serves a decoding step and a prompt, and in the epilogue a warp's 32
-// lanes hold 32 columns of one token: its adapter is the same in all lanes.
+// tokens, 16 to 256.  One token then wastes no more than a narrow N, and one
+// kernel serves a decoding step and a prompt.
 //   warp 0     TMA producer: 64-deep K slices of W (two boxes of 64 columns)
-//              and of x into a ring of shared-memory stages, 128-byte swizzled;
+//              and of x into a ring of shared-memory stages, 128-byte
+//              swizzled; then the adapters' B;
 //   warp 1     MMA issuer: tcgen05.mma kind::f16, M 128, N BT, two
 //              accumulators in TMEM;
-//   warps 2-5  epilogue: tcgen05.ld, the adapters' part, rounding, stores.
+//   warps 2-5  the adapters' h into the ring, then the epilogue: tcgen05.ld,
+//              rounding, stores (a warp's 32 lanes are 32 columns of a token).
 // Tiles that fill the GPU's SMs well are dealt out whole; otherwise the K
 // slices of all tiles form one sequence cut into equal parts, one per CTA,
 // and a tile that several CTAs share is summed, in the CTAs' order, by the
-// last of them to arrive (no CTA waits for another).  Every wait is bounded;
-// a role that gives up records the error in the heap's header.
+// last of them to arrive (no CTA waits for another).  The adapters' columns
+// belong to the part that ends a tile.  The second launch starts while the
+// first runs (programmatic dependent launch) and waits for its results only
+// where it needs them.  Every wait is bounded; a role that gives up records
+// the error in the heap's header.
+//
+// rank_kernel: h^T = A_a^T x^T the same way (A as stored, k x r, is an M-major
+// operand, rows r to 127 of the tile unused).  A CTA sorts the ids of up to 128
+// tokens, gathers the x rows of each adapter's tokens (tile::gather4) as the N
+// side, and takes one part of K; the CTAs of a cluster share the tokens and
+// add their parts in rank order through distributed shared memory.
 #include <algorithm>
 #include <string>
 
@@ -40,24 +53,25 @@ constexpr int kThreads = 192;
 constexpr int kMaxStages = 12;
 constexpr uint32_t kATile = kBM * kBK * 2;
 constexpr uint32_t kRingBytes = 200 * 1024;
-constexpr int kShrinkThreads = 256;
+constexpr int kRankTokens = 128;  // tokens of a rank_kernel CTA, at most
+constexpr int kRankStages = 8;
 
 struct AdapterArgs {
-  const void* x;
-  size_t ldx;
-  const void *a, *b;
   const float* scale;
   const int32_t* ids;
   void* y;
   size_t ldy;
-  uint32_t T, k, n, R, r;
+  uint32_t T, k, n, R, r, r16;  // r16: r in whole K steps of 16
   uint32_t bt, ntok, ncol, ktiles, stages;  // tiles: ncol column blocks x ntok token blocks
   uint32_t split, tmem_cols;
-  float* h;            // [T][r]
-  float* part;         // [CTAs][2][bt][128]
-  uint32_t* arrived;   // [tiles], zeroed by the first launch
+  uint16_t* h;        // [T][2 r16]: high parts, then low parts
+  uint32_t* found;    // [ntok][bt + 1]: number of adapters of a token block, then which
+  float* part;        // [CTAs][2][bt][128]
+  uint32_t* arrived;  // [tiles], zeroed before the product
   uint64_t budget_ns;
   Control* ctl;
+  // rank_kernel: tokens and K slices per CTA, stages, bytes of A and of a stage
+  uint32_t rk_tokens, rk_slices, rk_stages, rk_abytes, rk_stage;
 };
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
@@ -109,99 +123,311 @@ __device__ __forceinline__ uint32_t owner(const AdapterArgs& a, uint64_t u) {
   return (uint32_t)(((u + 1) * gridDim.x - 1) / ((uint64_t)a.ncol * a.ntok * a.ktiles));
 }
 
-// h_t = scale_a x_t A_a: one CTA per token; a thread sums 8 ranks over every
-// KS-th k, the KS sums are joined in order.  Also zeroes the arrival counters.
+// 4 rows of a 2-d tensor map whose box is one row
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int4 rows,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(symm::smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
+      "r"(rows.w), "r"(symm::smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void dependents_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_first_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// The float at `addr` (a shared-memory address of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// Instruction descriptor: fp32 accumulator, both operands of one type, the M
+// side M-major (bit 15), the N side K-major.
+__device__ __forceinline__ uint32_t mma_idesc(uint32_t fmt, uint32_t n) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 15) | ((n >> 3) << 17) |
+         ((uint32_t)(kBM >> 4) << 24);
+}
+constexpr uint64_t kWStep = (16 * 128) >> 4;  // 16 K rows of an M-major tile
+constexpr uint64_t kXStep = 32 >> 4;          // 16 K columns of a K-major tile
+
+// h of up to 128 tokens: see the head of the file.
 template <int FMT>
-__global__ void __launch_bounds__(kShrinkThreads) shrink_kernel(const AdapterArgs a) {
+__global__ void __launch_bounds__(kThreads)
+    rank_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+                const AdapterArgs a) {
   using T = typename Elem<FMT>::T;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
+  // [stages] of A | x rows, 8 KB that the unused M rows may read, then the sums
+  float* sums = reinterpret_cast<float*>(smem + (size_t)a.rk_stages * a.rk_stage + 8192);
+  __shared__ uint64_t full[kRankStages], empty[kRankStages], tfull[2], tempty[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t id_of[256];              // by token
+  __shared__ __align__(16) int order[kRankTokens + 16];  // tokens by adapter; past them T (no row)
+  __shared__ uint32_t sorted[kRankTokens];     // their ids
+  __shared__ uint32_t start[kRankTokens + 1];  // first position of each adapter's tokens
+  __shared__ uint32_t nitems, nvalid;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_rank(), csize = cluster_size();
+  dependents_may_start();
+
+  // for the second launch: its arrival counters, and the adapters of its token blocks
   if (a.split)
-    for (uint32_t i = blockIdx.x * kShrinkThreads + threadIdx.x; i < a.ncol * a.ntok;
-         i += gridDim.x * kShrinkThreads)
+    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < a.ncol * a.ntok;
+         i += gridDim.x * kThreads)
       a.arrived[i] = 0;
-  __shared__ float sums[kShrinkThreads][8];
-  if (a.R == 0) return;
-  const uint32_t V = a.r / 8, KS = kShrinkThreads / V;
-  const uint32_t kk = threadIdx.x / V, v = threadIdx.x % V;
-  for (uint32_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const uint32_t id = (uint32_t)a.ids[t];
-    if (id >= a.R) continue;
-    const T* x = static_cast<const T*>(a.x) + t * a.ldx;
-    const T* A = static_cast<const T*>(a.a) + (size_t)id * a.k * a.r;
-    float s[8] = {};
-    if (kk < KS)
-      for (uint32_t k = kk; k < a.k; k += KS) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(A + (size_t)k * a.r + v * 8);
-        const T* e = reinterpret_cast<const T*>(&raw);
-        const float xv = moe::to_f(x[k]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = fmaf(xv, moe::to_f(e[i]), s[i]);
-      }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sums[threadIdx.x][i] = s[i];
+  for (uint32_t b = blockIdx.x; b < a.ntok; b += gridDim.x) {
+    for (uint32_t i = threadIdx.x; i < a.bt; i += kThreads) {
+      const uint32_t t = b * a.bt + i;
+      id_of[i] = t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
+    }
+    if (threadIdx.x == 0) nitems = 0;
     __syncthreads();
-    if (threadIdx.x < a.r) {
-      float total = 0.f;
-      for (uint32_t q = 0; q < KS; ++q) total += sums[q * V + threadIdx.x / 8][threadIdx.x % 8];
-      a.h[(size_t)t * a.r + threadIdx.x] = a.scale[id] * total;
+    uint32_t* out = a.found + (size_t)b * (a.bt + 1);
+    // the first token of each adapter lists it, in token order
+    if (warp == 0) {
+      uint32_t count = 0;
+      for (uint32_t i0 = 0; i0 < a.bt; i0 += 32) {
+        const uint32_t i = i0 + lane, id = i < a.bt ? id_of[i] : 0xffffffffu;
+        bool mine = id < a.R;
+        for (uint32_t j = 0; j < i && mine; ++j) mine = id_of[j] != id;
+        const uint32_t votes = __ballot_sync(0xffffffffu, mine);
+        if (mine) out[1 + count + __popc(votes & ((1u << lane) - 1))] = id;
+        count += __popc(votes);
+      }
+      if (lane == 0) out[0] = count;
     }
     __syncthreads();
   }
-}
 
-// Adds the adapters' part of 16 tokens from t0 on, column n, and stores them.
-template <int FMT>
-__device__ __forceinline__ void finish16(const AdapterArgs& a, float (&acc)[16], uint32_t t0,
-                                         uint32_t n) {
-  using T = typename Elem<FMT>::T;
-  const bool in = n < a.n;
-  if (a.R)
-    for (uint32_t ic = 0; ic < a.r; ic += 8) {
-      uint32_t have = 0xffffffffu;
-      float b[8];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const uint32_t t = t0 + j;
-        const uint32_t id = t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
-        if (id < a.R) {
-          if (id != have) {
-            const T* B = static_cast<const T*>(a.b) + ((size_t)id * a.r + ic) * a.n + n;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = in ? moe::to_f(B[(size_t)i * a.n]) : 0.f;
-            have = id;
+  // this cluster's tokens, sorted by adapter (tokens without one last)
+  const uint32_t t0 = blockIdx.x / csize * a.rk_tokens;
+  const uint32_t mine = threadIdx.x;
+  if (mine < a.rk_tokens) {
+    const uint32_t t = t0 + mine;
+    const uint32_t id = t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
+    id_of[mine] = id < a.R ? id : 0xffffffffu;
+  }
+  if (threadIdx.x < 16) order[kRankTokens + threadIdx.x] = (int)a.T;
+  __syncthreads();
+  if (mine < a.rk_tokens) {
+    const uint32_t id = id_of[mine];
+    uint32_t pos = 0;
+    for (uint32_t j = 0; j < a.rk_tokens; ++j)
+      pos += id_of[j] < id || (id_of[j] == id && j < mine);
+    order[pos] = (int)(t0 + mine);
+    sorted[pos] = id;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t count = 0, valid = 0;
+    for (uint32_t i0 = 0; i0 < a.rk_tokens; i0 += 32) {
+      const uint32_t i = i0 + lane;
+      const bool ok = i < a.rk_tokens && sorted[i] != 0xffffffffu;
+      const bool first = ok && (i == 0 || sorted[i - 1] != sorted[i]);
+      const uint32_t votes = __ballot_sync(0xffffffffu, first);
+      if (first) start[count + __popc(votes & ((1u << lane) - 1))] = i;
+      count += __popc(votes);
+      valid += __popc(__ballot_sync(0xffffffffu, ok));
+    }
+    if (lane == 0) start[count] = valid, nitems = count, nvalid = valid;
+  }
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < a.rk_stages; ++s) {
+      symm::mbar_init(&full[s], 1);
+      symm::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      symm::mbar_init(&tfull[b], 1);
+      symm::mbar_init(&tempty[b], 128);
+    }
+    symm::mbar_init(&drain, 1);
+    symm::fence_mbar_init();
+  }
+  if (warp == 1) symm::tmem_alloc(&tmem_slot, 256);
+  symm::tc_fence_before();
+  __syncthreads();
+  symm::tc_fence_after();
+  const uint32_t tmem = tmem_slot, items = nitems, valid = nvalid;
+  const uint32_t k0 = min(a.ktiles, crank * a.rk_slices), k1 = min(a.ktiles, k0 + a.rk_slices);
+
+  if (k0 < k1) {
+    if (warp == 0) {
+      if (lane == 0) {  // ----------------------------------- TMA producer
+        uint32_t st = 0, ph = 1, it = 0;
+        bool ok = true;
+        for (uint32_t i = 0; ok && i < items; ++i) {
+          const uint32_t p0 = start[i], rows = start[i + 1] - p0, rows16 = (rows + 15) / 16 * 16;
+          for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
+            if (!symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) {
+              symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+              ok = false;
+              break;
+            }
+            uint8_t* buf = smem + (size_t)st * a.rk_stage;
+            symm::mbar_arrive_expect_tx(&full[st], a.rk_abytes + rows16 * 128);
+            for (uint32_t half = 0; half * 8192 < a.rk_abytes; ++half)
+              symm::tma_load_3d(buf + half * 8192, &map_a, (int)half * 64, (int)(kt * kBK),
+                                (int)sorted[p0], &full[st]);
+            for (uint32_t q = 0; q < rows16; q += 4) {
+              // rows of this adapter; past them T, which is past the end: zeros
+              int4 r;
+              r.x = q + 0 < rows ? order[p0 + q + 0] : (int)a.T;
+              r.y = q + 1 < rows ? order[p0 + q + 1] : (int)a.T;
+              r.z = q + 2 < rows ? order[p0 + q + 2] : (int)a.T;
+              r.w = q + 3 < rows ? order[p0 + q + 3] : (int)a.T;
+              tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
+            }
+            if (++st == a.rk_stages) st = 0, ph ^= 1;
           }
-          const float4* h = reinterpret_cast<const float4*>(a.h + (size_t)t * a.r + ic);
-          const float4 h0 = h[0], h1 = h[1];
-          float s = acc[j];
-          s = fmaf(h0.x, b[0], s), s = fmaf(h0.y, b[1], s);
-          s = fmaf(h0.z, b[2], s), s = fmaf(h0.w, b[3], s);
-          s = fmaf(h1.x, b[4], s), s = fmaf(h1.y, b[5], s);
-          s = fmaf(h1.z, b[6], s), s = fmaf(h1.w, b[7], s);
-          acc[j] = s;
         }
+        for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
+          symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {  // ------------------------------------ MMA issuer
+        uint32_t st = 0, ph = 0;
+        bool ok = true;
+        for (uint32_t i = 0; ok && i < items; ++i) {
+          const uint32_t rows16 = (start[i + 1] - start[i] + 15) / 16 * 16, buf = i & 1;
+          if (!symm::mbar_wait_ab(&tempty[buf], ((i >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
+            symm::record_error(a.ctl, symm::kErrTimedOut, -4);
+            break;
+          }
+          symm::tc_fence_after();
+          const uint32_t idesc = mma_idesc(FMT, rows16);
+          for (uint32_t kt = k0; kt < k1; ++kt) {
+            if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
+              symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+              ok = false;
+              break;
+            }
+            symm::tc_fence_after();
+            const uint8_t* tile = smem + (size_t)st * a.rk_stage;
+            const uint64_t wd = symm::sw128_mnmajor_desc(tile);
+            const uint64_t xd = symm::sw128_kmajor_desc(tile + a.rk_abytes);
+#pragma unroll
+            for (int j = 0; j < kBK / 16; ++j)
+              symm::tc_mma(tmem + buf * 128, wd + kWStep * j, xd + kXStep * j, idesc,
+                           kt != k0 || j != 0);
+            symm::tc_commit(&empty[st]);
+            if (++st == a.rk_stages) st = 0, ph ^= 1;
+          }
+          if (ok) symm::tc_commit(&tfull[buf]);
+        }
+        symm::tc_commit(&drain);
+        symm::mbar_wait(&drain, 0, a.budget_ns);
+      }
+    } else {  // ------------------------------------------- sums of this part
+      const uint32_t q = (uint32_t)(warp & 3), row = 32 * q + lane;
+      for (uint32_t i = 0; i < items; ++i) {
+        const uint32_t p0 = start[i], rows = start[i + 1] - p0, buf = i & 1;
+        if (!symm::mbar_wait_ab(&tfull[buf], (i >> 1) & 1, a.budget_ns, a.ctl)) {
+          symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+          break;
+        }
+        symm::tc_fence_after();
+        if (32 * q < a.r)  // the warp's TMEM lanes hold ranks
+          for (uint32_t c = 0; c < rows; c += 16) {
+            uint32_t v[16];
+            symm::tmem_ld16(tmem + ((32 * q) << 16) + buf * 128 + c, v);
+            if (row < a.r)
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (c + j < rows) sums[(p0 + c + j) * a.r + row] = __uint_as_float(v[j]);
+          }
+        symm::tc_fence_before();
+        symm::mbar_arrive(&tempty[buf]);
       }
     }
-  if (!in) return;
+  } else {
+    for (uint32_t i = threadIdx.x; i < valid * a.r; i += kThreads) sums[i] = 0.f;
+  }
+  __syncwarp();
+  symm::tc_fence_before();
+  cluster_sync();  // every CTA's sums are complete
+  if (warp == 1) {
+    symm::tc_fence_after();
+    symm::tmem_dealloc(tmem, 256);
+  }
+  // each CTA of the cluster joins its share of the tokens, CTAs in order
+  T* H = reinterpret_cast<T*>(a.h);
+  for (uint32_t i = crank * kThreads + threadIdx.x; i < valid * a.r16; i += csize * kThreads) {
+    const uint32_t pos = i / a.r16, c = i % a.r16;
+    float s = 0.f;
+    if (c < a.r) {
+      for (uint32_t b = 0; b < csize; ++b) s += ld_cluster(symm::smem_addr(&sums[pos * a.r + c]), b);
+      s *= a.scale[sorted[pos]];
+    }
+    const T hi = moe::from_f<T>(s);
+    T* out = H + (size_t)order[pos] * 2 * a.r16 + c;
+    out[0] = hi;
+    out[a.r16] = moe::from_f<T>(s - moe::to_f(hi));
+  }
+  cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// The adapters' columns of a tile come in pieces of one ring stage: h's high
+// and low parts side by side while both fit into 64 K columns, else 64 ranks
+// of one part at a time.
+__device__ __forceinline__ uint32_t pieces_of(const AdapterArgs& a) {
+  return a.r16 <= 32 ? 1 : 2 * ((a.r16 + 63) / 64);
+}
+__device__ __forceinline__ uint32_t piece_rows(const AdapterArgs& a, uint32_t p) {  // K rows of B
+  return min(64u, a.r16 - (p >> 1) * 64);
+}
+
+// Stores 16 tokens from t0 on, column n.
+template <int FMT>
+__device__ __forceinline__ void store16(const AdapterArgs& a, const float (&acc)[16], uint32_t t0,
+                                        uint32_t n) {
+  using T = typename Elem<FMT>::T;
+  if (n >= a.n) return;
+  T* y = static_cast<T*>(a.y) + (size_t)t0 * a.ldy + n;
 #pragma unroll
   for (int j = 0; j < 16; ++j)
-    if (t0 + j < a.T)
-      static_cast<T*>(a.y)[(size_t)(t0 + j) * a.ldy + n] = moe::from_f<T>(acc[j]);
+    if (t0 + j < a.T) y[(size_t)j * a.ldy] = moe::from_f<T>(acc[j]);
 }
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     adapter_kernel(const __grid_constant__ CUtensorMap map_w,
-                   const __grid_constant__ CUtensorMap map_x, const AdapterArgs a) {
+                   const __grid_constant__ CUtensorMap map_x,
+                   const __grid_constant__ CUtensorMap map_b, const AdapterArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t stage_bytes = kATile + a.bt * 128;
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], claimed[kMaxStages];
+  __shared__ uint64_t tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot, last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < a.stages; ++s) {
-      symm::mbar_init(&full[s], 1);
+      symm::mbar_init(&full[s], 2);  // the producer, and it again or who wrote h
       symm::mbar_init(&empty[s], 1);
+      symm::mbar_init(&claimed[s], 1);  // the stage is free and h may be written
     }
     for (int b = 0; b < 2; ++b) {
       symm::mbar_init(&tfull[b], 1);
@@ -215,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   symm::tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  const uint32_t npieces = a.R ? pieces_of(a) : 0;
   Walk walk(a);
   Segment s;
 
@@ -222,22 +449,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {  // ------------------------------------- TMA producer
       uint64_t it = 0;
       uint32_t st = 0, ph = 1;
-      bool ok = true;
+      bool ok = true, waited = false;
+      auto claim = [&]() {
+        if (symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) return true;
+        symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+        return ok = false;
+      };
       while (ok && walk.next(a, s)) {
-        const int n0 = (int)(s.tile % a.ncol) * kBM, t0 = (int)(s.tile / a.ncol * a.bt);
+        const int n0 = (int)(s.tile % a.ncol) * kBM;
+        const uint32_t tb = s.tile / a.ncol;
         for (uint32_t kt = s.k0; kt < s.k1; ++kt, ++it) {
-          if (!symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) {
-            symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-            ok = false;
-            break;
-          }
+          if (!claim()) break;
           uint8_t* buf = smem + (size_t)st * stage_bytes;
           symm::mbar_arrive_expect_tx(&full[st], stage_bytes);
           tma_load_2d(buf, &map_w, n0, (int)(kt * kBK), &full[st]);
           tma_load_2d(buf + kATile / 2, &map_w, n0 + 64, (int)(kt * kBK), &full[st]);
-          tma_load_2d(buf + kATile, &map_x, (int)(kt * kBK), t0, &full[st]);
+          tma_load_2d(buf + kATile, &map_x, (int)(kt * kBK), (int)(tb * a.bt), &full[st]);
+          symm::mbar_arrive(&full[st]);
           if (++st == a.stages) st = 0, ph ^= 1;
         }
+        if (!ok || npieces == 0 || s.k1 != a.ktiles) continue;
+        if (!waited) wait_for_first_launch(), waited = true;
+        const uint32_t* found = a.found + (size_t)tb * (a.bt + 1);
+        for (uint32_t p = 0; ok && p < npieces; ++p)
+          for (uint32_t i = 0; i < found[0]; ++i, ++it) {
+            if (!claim()) break;
+            uint8_t* buf = smem + (size_t)st * stage_bytes;
+            const int id = (int)found[1 + i], row = (int)(p >> 1) * 64;
+            symm::mbar_arrive_expect_tx(&full[st], 256 * min(64u, a.r16));
+            symm::tma_load_3d(buf, &map_b, n0, row, id, &full[st]);
+            symm::tma_load_3d(buf + kATile / 2, &map_b, n0 + 64, row, id, &full[st]);
+            symm::mbar_arrive(&claimed[st]);
+            if (++st == a.stages) st = 0, ph ^= 1;
+          }
       }
       // every load issued lands before the CTA may leave (bounded)
       for (uint64_t i = it > a.stages ? it - a.stages : 0; i < it; ++i)
@@ -245,11 +489,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {  // -------------------------------------- MMA issuer
-      // fp32 accumulator, A and B of one type, A (W) M-major, B (x) K-major
-      const uint32_t idesc = (1u << 4) | ((uint32_t)FMT << 7) | ((uint32_t)FMT << 10) |
-                             (1u << 15) | ((a.bt >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+      const uint32_t idesc = mma_idesc(FMT, a.bt);
       uint32_t st = 0, ph = 0, seg = 0;
-      bool ok = true;
+      bool ok = true, waited = false;
+      auto ready = [&]() {
+        if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
+          symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+          return ok = false;
+        }
+        symm::tc_fence_after();
+        return true;
+      };
       for (; ok && walk.next(a, s); ++seg) {
         const uint32_t buf = seg & 1;
         if (!symm::mbar_wait_ab(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
@@ -259,40 +509,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::tc_fence_after();
         const uint32_t acc = tmem + buf * a.bt;
         for (uint32_t kt = s.k0; kt < s.k1; ++kt) {
-          if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
-            symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-            ok = false;
-            break;
-          }
-          symm::tc_fence_after();
+          if (!ready()) break;
           const uint8_t* tile = smem + (size_t)st * stage_bytes;
           const uint64_t wd = symm::sw128_mnmajor_desc(tile);
           const uint64_t xd = symm::sw128_kmajor_desc(tile + kATile);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)  // K = 16: 16 rows of W, 32 bytes of x
-            symm::tc_mma(acc, wd + (uint64_t)((16 * 128) >> 4) * j, xd + 2 * j, idesc,
-                         kt != s.k0 || j != 0);
+          for (int j = 0; j < kBK / 16; ++j)
+            symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, kt != s.k0 || j != 0);
           symm::tc_commit(&empty[st]);
           if (++st == a.stages) st = 0, ph ^= 1;
+        }
+        if (ok && npieces && s.k1 == a.ktiles) {
+          if (!waited) wait_for_first_launch(), waited = true;
+          const uint32_t nfound = a.found[(size_t)(s.tile / a.ncol) * (a.bt + 1)];
+          for (uint32_t p = 0; ok && p < npieces; ++p)
+            for (uint32_t i = 0; i < nfound; ++i) {
+              if (!ready()) break;
+              const uint8_t* tile = smem + (size_t)st * stage_bytes;
+              const uint64_t wd = symm::sw128_mnmajor_desc(tile);
+              const uint64_t xd = symm::sw128_kmajor_desc(tile + kATile);
+              const uint32_t steps = piece_rows(a, p) / 16;
+              for (uint32_t j = 0; j < steps; ++j)
+                symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, 1);
+              if (npieces == 1)  // the low parts, beside the high ones
+                for (uint32_t j = 0; j < steps; ++j)
+                  symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * (steps + j), idesc, 1);
+              symm::tc_commit(&empty[st]);
+              if (++st == a.stages) st = 0, ph ^= 1;
+            }
         }
         if (ok) symm::tc_commit(&tfull[buf]);
       }
       symm::tc_commit(&drain);  // every MMA is complete before TMEM is freed
       symm::mbar_wait(&drain, 0, a.budget_ns);
     }
-  } else {  // -------------------------------------------------- epilogue
+  } else {  // ------------------------------------------ h, and the epilogue
     const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q + 31
     const uint32_t row = 32 * q + lane;       // this thread's column of W in the tile
+    const uint32_t me = threadIdx.x - 64;
     const uint32_t chunks = a.bt / 16;
-    for (uint32_t seg = 0; walk.next(a, s); ++seg) {
+    uint64_t it = 0;
+    uint32_t phases = 0;  // of `claimed`, one bit per stage
+    bool ok = true;
+    wait_for_first_launch();
+    for (uint32_t seg = 0; ok && walk.next(a, s); ++seg) {
       const uint32_t buf = seg & 1;
+      const uint32_t n = (s.tile % a.ncol) * kBM + row, tb = s.tile / a.ncol, t0 = tb * a.bt;
+      it += s.k1 - s.k0;
+      if (npieces && s.k1 == a.ktiles) {
+        const uint32_t* found = a.found + (size_t)tb * (a.bt + 1);
+        const uint32_t nfound = found[0];
+        for (uint32_t p = 0; ok && nfound && p < npieces; ++p) {
+          // this thread's 16-byte chunks of the piece (at most 16: bt 256, 8
+          // chunks a row) and the adapters of their tokens
+          const uint32_t width = (npieces == 1 ? 2 * a.r16 : piece_rows(a, p)) / 8;
+          const uint32_t from = npieces == 1 ? 0 : (p & 1) * a.r16 + (p >> 1) * 64;
+          uint4 v[16];
+          uint32_t id[16], at[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const uint32_t i = me + 128 * c, tr = i / width, ch = i % width, t = t0 + tr;
+            id[c] = 0xffffffffu, v[c] = make_uint4(0, 0, 0, 0);
+            at[c] = tr < a.bt ? tr * 128 + ((ch ^ (tr & 7)) << 4) : 0xffffffffu;
+            if (tr < a.bt && t < a.T) {
+              id[c] = (uint32_t)a.ids[t];
+              if (id[c] < a.R)
+                v[c] = __ldcg(reinterpret_cast<const uint4*>(a.h + (size_t)t * 2 * a.r16 + from) +
+                              ch);
+            }
+          }
+          for (uint32_t i = 0; i < nfound; ++i, ++it) {
+            const uint32_t st = (uint32_t)(it % a.stages);
+            // not `empty`: whose phases this warp does not follow one by one
+            if (!symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl)) {
+              symm::record_error(a.ctl, symm::kErrTimedOut, -7);
+              ok = false;
+              break;
+            }
+            phases ^= 1u << st;
+            uint8_t* tile = smem + (size_t)st * stage_bytes + kATile;
+            const uint32_t want = found[1 + i];
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (at[c] != 0xffffffffu)
+                *reinterpret_cast<uint4*>(tile + at[c]) =
+                    id[c] == want ? v[c] : make_uint4(0, 0, 0, 0);
+            symm::fence_proxy_async_shared();  // h, for the MMAs
+            symm::group_sync(1, 128);
+            if (me == 0) symm::mbar_arrive(&full[st]);
+          }
+        }
+        if (!ok) break;
+      }
       if (!symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
         symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
       }
       symm::tc_fence_after();
       const uint32_t taddr = tmem + ((32 * q) << 16) + buf * a.bt;
-      const uint32_t n = (s.tile % a.ncol) * kBM + row, t0 = s.tile / a.ncol * a.bt;
       const bool whole = s.k0 == 0 && s.k1 == a.ktiles;
       // the first segment of a CTA has slot 0, a later partial one is its last: slot 1
       float* mine = a.part + ((size_t)blockIdx.x * 2 + (seg != 0)) * a.bt * kBM;
@@ -309,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float acc[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) acc[j] = __uint_as_float(v[j]);
-          finish16<FMT>(a, acc, t0 + c * 16, n);
+          store16<FMT>(a, acc, t0 + c * 16, n);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -321,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t first = owner(a, u0), end = owner(a, u0 + a.ktiles - 1) + 1;
       __threadfence();
       symm::group_sync(1, 128);
-      if (threadIdx.x == 64)
+      if (me == 0)
         last = symm::atom_add_acq_rel_u32(&a.arrived[s.tile], 1u) + 1 == end - first;
       symm::group_sync(1, 128);
       if (!last) continue;
@@ -334,11 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) acc[j] += __ldcg(p + (size_t)j * kBM);
         }
-        finish16<FMT>(a, acc, t0 + c * 16, n);
+        store16<FMT>(a, acc, t0 + c * 16, n);
       }
     }
   }
 
+  __syncwarp();
   symm::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -349,9 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // How a call of these sizes is cut up.
 struct Plan {
-  uint32_t bt, ntok, ncol, ktiles, stages, split, ctas, tmem_cols;
-  size_t h_bytes, part_bytes, arrived_bytes;
-  size_t bytes() const { return h_bytes + part_bytes + arrived_bytes; }
+  uint32_t bt, ntok, ncol, ktiles, stages, split, ctas, tmem_cols, r16;
+  uint32_t rk_tokens, rk_cluster, rk_slices, rk_stages, rk_abytes, rk_stage;
+  size_t h_bytes, found_bytes, part_bytes, arrived_bytes;
+  size_t bytes() const { return h_bytes + found_bytes + part_bytes + arrived_bytes; }
 };
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -374,7 +690,21 @@ Plan plan_of(int T, int k, int n, int r) {
   if (p.split && p.ctas < 2) p.split = 0, p.ctas = (uint32_t)std::min<uint64_t>(sms, tiles);
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bt) p.tmem_cols *= 2;
-  p.h_bytes = up((size_t)T * r * 4, 256);
+  p.r16 = (uint32_t)up((size_t)r, 16);
+  // The first launch: clusters of up to 8 CTAs share the K slices of a group of
+  // tokens; groups of up to 128 tokens, smaller ones while that leaves SMs idle.
+  p.rk_cluster = 8;
+  while (p.rk_cluster > 1 && p.rk_cluster > p.ktiles) p.rk_cluster /= 2;
+  const uint32_t groups = std::max(1u, 2 * sms / p.rk_cluster);
+  p.rk_tokens = std::min<uint32_t>(kRankTokens, std::max(1u, ((uint32_t)T + groups - 1) / groups));
+  while (p.rk_cluster > 1 && (T + p.rk_tokens - 1) / p.rk_tokens * p.rk_cluster > 3 * sms)
+    p.rk_cluster /= 2;
+  p.rk_slices = (p.ktiles + p.rk_cluster - 1) / p.rk_cluster;
+  p.rk_abytes = r <= 64 ? 8192 : 16384;
+  p.rk_stage = p.rk_abytes + (uint32_t)up(p.rk_tokens, 16) * 128;
+  p.rk_stages = std::min<uint32_t>(kRankStages, 72 * 1024 / p.rk_stage);
+  p.h_bytes = up((size_t)T * 2 * p.r16 * 2, 256);
+  p.found_bytes = up((size_t)p.ntok * (p.bt + 1) * 4, 256);
   p.part_bytes = p.split ? (size_t)p.ctas * 2 * p.bt * kBM * 4 : 0;
   p.arrived_bytes = p.split ? up((size_t)tiles * 4, 256) : 0;
   return p;
@@ -390,42 +720,87 @@ int check_adapter(const char* what, int T, int k, int n, int r) {
   return SYMM_OK;
 }
 
-// [rows][inner] 2-byte elements, `ld` apart, boxes of 64 x box_rows, 128-byte swizzled.
-int make_map(CUtensorMap* map, const void* base, int fmt, uint64_t inner, uint64_t rows, size_t ld,
-             uint32_t box_rows) {
+// [depth][rows][inner] 2-byte elements, rows `ld` and planes ld * rows apart,
+// boxes of 64 x box_rows, 128-byte swizzled; depth 0: a 2-d map.
+int make_map(CUtensorMap* map, const void* base, int fmt, uint64_t inner, uint64_t rows,
+             uint64_t depth, size_t ld, uint32_t box_rows) {
   auto fn = encode_fn();
   if (!fn) return fail(SYMM_ECUDA, "moe_adapter_matmul: no cuTensorMapEncodeTiled");
-  const cuuint64_t dims[2] = {inner, rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
+  const cuuint64_t dims[3] = {inner, rows, depth};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * rows * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r =
-      fn(map, fmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      fn(map, fmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+         depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(SYMM_ECUDA,
                 "moe_adapter_matmul: tensor map rejected (CUresult " + std::to_string((int)r) + ")");
   return SYMM_OK;
 }
 
+struct Maps {
+  CUtensorMap w, x, a, rows, b;
+};
+
+constexpr size_t kRankSmemMax = 1024 + 72 * 1024 + 8192 + (size_t)kRankTokens * SYMM_MOE_MAX_RANK * 4;
+
+// Once per device: both kernels may use more than 48 KB of shared memory.
 template <int FMT>
-int launch(const Plan& p, const CUtensorMap& map_w, const CUtensorMap& map_x, const AdapterArgs& a,
-           cudaStream_t s) {
-  const size_t smem = 1024 + (size_t)p.stages * (kATile + p.bt * 128);
-  int rc = cuda_check(cudaFuncSetAttribute(adapter_kernel<FMT>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)(1024 + kRingBytes)),
-                      "moe_adapter_matmul: kernel set-up");
+int set_up() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "moe_adapter_matmul: device");
   if (rc) return rc;
-  if (a.R || p.split) {
-    shrink_kernel<FMT><<<a.R ? std::min<uint32_t>(a.T, 1u << 16) : 1u, kShrinkThreads, 0, s>>>(a);
-    rc = cuda_check(cudaGetLastError(), "moe_adapter_matmul: rank products");
-    if (rc) return rc;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && done[dev]) return SYMM_OK;
+  rc = cuda_check(cudaFuncSetAttribute(adapter_kernel<FMT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)(1024 + kRingBytes)),
+                  "moe_adapter_matmul: kernel set-up");
+  if (!rc)
+    rc = cuda_check(cudaFuncSetAttribute(rank_kernel<FMT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kRankSmemMax),
+                    "moe_adapter_matmul: kernel set-up");
+  if (!rc && dev < 64) done[dev] = true;
+  return rc;
+}
+
+template <int FMT>
+int launch(const Plan& p, const Maps& m, const AdapterArgs& a, cudaStream_t s) {
+  int rc = set_up<FMT>();
+  if (rc) return rc;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (a.R) {
+    cfg.gridDim = dim3((a.T + p.rk_tokens - 1) / p.rk_tokens * p.rk_cluster);
+    cfg.dynamicSmemBytes =
+        1024 + (size_t)p.rk_stages * p.rk_stage + 8192 + (size_t)p.rk_tokens * a.r * 4;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.rk_cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    rc = cuda_check(cudaLaunchKernelEx(&cfg, rank_kernel<FMT>, m.a, m.rows, a),
+                    "moe_adapter_matmul: rank products");
+  } else if (p.split) {
+    rc = cuda_check(cudaMemsetAsync(a.arrived, 0, p.arrived_bytes, s),
+                    "moe_adapter_matmul: arrival counters");
   }
-  adapter_kernel<FMT><<<p.ctas, kThreads, smem, s>>>(map_w, map_x, a);
-  return cuda_check(cudaGetLastError(), "moe_adapter_matmul: product");
+  if (rc) return rc;
+  cfg.gridDim = dim3(p.ctas);
+  cfg.dynamicSmemBytes = 1024 + (size_t)p.stages * (kATile + p.bt * 128);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = a.R ? 1 : 0;
+  return cuda_check(cudaLaunchKernelEx(&cfg, adapter_kernel<FMT>, m.w, m.x, m.b, a),
+                    "moe_adapter_matmul: product");
 }
 
 }  // namespace
@@ -460,33 +835,42 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
     if (!x || !w || !y || !workspace || (R && (!a || !b || !scale || !ids)))
       return fail(SYMM_EINVAL, "moe_adapter_matmul: NULL input, output or workspace");
     if (!moe::aligned(x, 16) || !moe::aligned(w, 16) || !moe::aligned(a, 16) ||
-        !moe::aligned(b, 2) || !moe::aligned(y, 2) || !moe::aligned(scale, 4) ||
+        !moe::aligned(b, 16) || !moe::aligned(y, 2) || !moe::aligned(scale, 4) ||
         !moe::aligned(ids, 4) || !moe::aligned(workspace, 256))
-      return fail(SYMM_EINVAL, "moe_adapter_matmul: x, w and a must be 16-byte aligned, workspace "
-                               "256-byte aligned, the rest to their elements");
+      return fail(SYMM_EINVAL, "moe_adapter_matmul: x, w, a and b must be 16-byte aligned, "
+                               "workspace 256-byte aligned, the rest to their elements");
     if (y == x || y == w || y == a || y == b)
       return fail(SYMM_EINVAL, "moe_adapter_matmul: y must not be an input");
     const Plan p = plan_of(T, k, n, r);
     const int fmt = dtype == SYMM_DTYPE_BF16 ? 1 : 0;
-    CUtensorMap map_w, map_x;
-    rc = make_map(&map_w, w, fmt, (uint64_t)n, (uint64_t)k, ldw, kBK);
-    if (rc) return rc;
-    rc = make_map(&map_x, x, fmt, (uint64_t)k, (uint64_t)T, ldx, p.bt);
+    Maps m{};
+    rc = make_map(&m.w, w, fmt, (uint64_t)n, (uint64_t)k, 0, ldw, kBK);
+    if (!rc) rc = make_map(&m.x, x, fmt, (uint64_t)k, (uint64_t)T, 0, ldx, p.bt);
+    if (!rc && R) {
+      rc = make_map(&m.a, a, fmt, (uint64_t)r, (uint64_t)k, (uint64_t)R, (size_t)r, kBK);
+      if (!rc) rc = make_map(&m.rows, x, fmt, (uint64_t)k, (uint64_t)T, 0, ldx, 1);
+      if (!rc)
+        rc = make_map(&m.b, b, fmt, (uint64_t)n, (uint64_t)r, (uint64_t)R, (size_t)n,
+                      std::min(64u, p.r16));
+    }
     if (rc) return rc;
     cudaStream_t s = as_stream(stream);
     rc = ensure_ctrl(heap, s);
     if (rc) return rc;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AdapterArgs g{};
-    g.x = x, g.ldx = ldx, g.a = a, g.b = b, g.scale = scale, g.ids = ids, g.y = y, g.ldy = ldy;
+    g.scale = scale, g.ids = ids, g.y = y, g.ldy = ldy;
     g.T = (uint32_t)T, g.k = (uint32_t)k, g.n = (uint32_t)n, g.R = (uint32_t)R, g.r = (uint32_t)r;
-    g.bt = p.bt, g.ntok = p.ntok, g.ncol = p.ncol, g.ktiles = p.ktiles, g.stages = p.stages;
-    g.split = p.split, g.tmem_cols = p.tmem_cols;
-    g.h = reinterpret_cast<float*>(ws);
-    g.part = reinterpret_cast<float*>(ws + p.h_bytes);
-    g.arrived = reinterpret_cast<uint32_t*>(ws + p.h_bytes + p.part_bytes);
+    g.r16 = p.r16, g.bt = p.bt, g.ntok = p.ntok, g.ncol = p.ncol, g.ktiles = p.ktiles;
+    g.stages = p.stages, g.split = p.split, g.tmem_cols = p.tmem_cols;
+    g.h = reinterpret_cast<uint16_t*>(ws);
+    g.found = reinterpret_cast<uint32_t*>(ws + p.h_bytes);
+    g.part = reinterpret_cast<float*>(ws + p.h_bytes + p.found_bytes);
+    g.arrived = reinterpret_cast<uint32_t*>(ws + p.h_bytes + p.found_bytes + p.part_bytes);
+    g.rk_tokens = p.rk_tokens, g.rk_slices = p.rk_slices, g.rk_stages = p.rk_stages;
+    g.rk_abytes = p.rk_abytes, g.rk_stage = p.rk_stage;
     g.budget_ns = heap->spin_budget;
     g.ctl = reinterpret_cast<Control*>(heap->base);
-    return fmt ? launch<1>(p, map_w, map_x, g, s) : launch<0>(p, map_w, map_x, g, s);
+    return fmt ? launch<1>(p, m, g, s) : launch<0>(p, m, g, s);
   });
 }
