@@ -21,13 +21,11 @@
 //              accumulators in TMEM;
 //   warps 2-5  the adapters' h into the ring, then the epilogue: tcgen05.ld,
 //              rounding, stores (a warp's 32 lanes are 32 columns of a token).
-// Tiles that fill the GPU's SMs well are dealt out whole; otherwise the K
-// slices of all tiles form one sequence cut into equal parts, one per CTA,
-// and a tile that several CTAs share is summed, in the CTAs' order, by the
-// last of them to arrive (no CTA waits for another).  The adapters' columns
-// belong to the part that ends a tile.  The second launch starts while the
-// first runs (programmatic dependent launch) and waits for its results only
-// where it needs them.  Every wait is bounded; a role that gives up records
+// Where whole tiles would leave SMs idle, a cluster of 2 to 8 CTAs shares a
+// tile: each takes a part of K and of the adapters, and the parts are joined in
+// rank order through distributed shared memory, each CTA storing its share of
+// the tokens.  The second launch starts while the first runs (programmatic
+// dependent launch) and waits for its results only where it needs them.  Every wait is bounded; a role that gives up records
 // the error in the heap's header.
 //
 // rank_kernel: h^T = A_a^T x^T the same way (A as stored, k x r, is an M-major
@@ -63,11 +61,9 @@ struct AdapterArgs {
   size_t ldy;
   uint32_t T, k, n, R, r, r16;  // r16: r in whole K steps of 16
   uint32_t bt, ntok, ncol, ktiles, stages;  // tiles: ncol column blocks x ntok token blocks
-  uint32_t split, tmem_cols;
-  uint16_t* h;        // [T][2 r16]: high parts, then low parts
-  uint32_t* found;    // [ntok][bt + 1]: number of adapters of a token block, then which
-  float* part;        // [CTAs][2][bt][128]
-  uint32_t* arrived;  // [tiles], zeroed before the product
+  uint32_t cluster, tmem_cols;  // cluster: CTAs that share a tile
+  uint16_t* h;      // [T][2 r16]: high parts, then low parts
+  uint32_t* found;  // [ntok][bt + 1]: number of adapters of a token block, then which
   uint64_t budget_ns;
   Control* ctl;
   // rank_kernel: tokens and K slices per CTA, stages, bytes of A and of a stage
@@ -91,37 +87,6 @@ template <>
 struct Elem<1> {
   using T = __nv_bfloat16;
 };
-
-// The segments of one CTA: K slices [k0, k1) of a tile.
-struct Segment {
-  uint32_t tile, k0, k1;
-};
-__device__ __forceinline__ uint64_t cut(const AdapterArgs& a, uint32_t cta) {
-  return (uint64_t)a.ncol * a.ntok * a.ktiles * cta / gridDim.x;
-}
-struct Walk {
-  uint64_t at, end;  // slices (split) or tiles (whole)
-  __device__ __forceinline__ explicit Walk(const AdapterArgs& a)
-      : at(a.split ? cut(a, blockIdx.x) : blockIdx.x),
-        end(a.split ? cut(a, blockIdx.x + 1) : (uint64_t)a.ncol * a.ntok) {}
-  __device__ __forceinline__ bool next(const AdapterArgs& a, Segment& s) {
-    if (at >= end) return false;
-    if (!a.split) {
-      s = {(uint32_t)at, 0, a.ktiles};
-      at += gridDim.x;
-      return true;
-    }
-    s.tile = (uint32_t)(at / a.ktiles);
-    s.k0 = (uint32_t)(at - (uint64_t)s.tile * a.ktiles);
-    s.k1 = (uint32_t)min((uint64_t)a.ktiles, s.k0 + (end - at));
-    at += s.k1 - s.k0;
-    return true;
-  }
-};
-// The CTA whose part holds slice u.
-__device__ __forceinline__ uint32_t owner(const AdapterArgs& a, uint64_t u) {
-  return (uint32_t)(((u + 1) * gridDim.x - 1) / ((uint64_t)a.ncol * a.ntok * a.ktiles));
-}
 
 // 4 rows of a 2-d tensor map whose box is one row
 __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int4 rows,
@@ -153,12 +118,23 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                ::: "memory");
 }
-// The float at `addr` (a shared-memory address of this CTA) in CTA `rank` of the cluster.
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+// `addr` (a shared-memory address of this CTA) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_cluster(uint32_t addr, uint32_t rank) {
   uint32_t remote;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
+  return remote;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t remote) {
   float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t remote) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote)
+               : "memory");
   return v;
 }
 
@@ -175,7 +151,7 @@ constexpr uint64_t kXStep = 32 >> 4;          // 16 K columns of a K-major tile
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
     rank_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
-                const AdapterArgs a) {
+                const __grid_constant__ CUtensorMap map_x16, const AdapterArgs a) {
   using T = typename Elem<FMT>::T;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -183,8 +159,9 @@ __global__ void __launch_bounds__(kThreads)
   float* sums = reinterpret_cast<float*>(smem + (size_t)a.rk_stages * a.rk_stage + 8192);
   __shared__ uint64_t full[kRankStages], empty[kRankStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t id_of[256];              // by token
-  __shared__ __align__(16) int order[kRankTokens + 16];  // tokens by adapter; past them T (no row)
+  __shared__ __align__(16) uint32_t id_of[256];  // by token
+  __shared__ uint32_t firsts[8];
+  __shared__ int order[kRankTokens];           // tokens by adapter
   __shared__ uint32_t sorted[kRankTokens];     // their ids
   __shared__ uint32_t start[kRankTokens + 1];  // first position of each adapter's tokens
   __shared__ uint32_t nitems, nvalid;
@@ -192,31 +169,32 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t crank = cluster_rank(), csize = cluster_size();
   dependents_may_start();
 
-  // for the second launch: its arrival counters, and the adapters of its token blocks
-  if (a.split)
-    for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < a.ncol * a.ntok;
-         i += gridDim.x * kThreads)
-      a.arrived[i] = 0;
+  // for the second launch: the adapters of its token blocks
   for (uint32_t b = blockIdx.x; b < a.ntok; b += gridDim.x) {
-    for (uint32_t i = threadIdx.x; i < a.bt; i += kThreads) {
+    for (uint32_t i = threadIdx.x; i < 256; i += kThreads) {
       const uint32_t t = b * a.bt + i;
-      id_of[i] = t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
+      id_of[i] = i < a.bt && t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
     }
-    if (threadIdx.x == 0) nitems = 0;
+    __syncthreads();
+    // the first token of each adapter lists it, in token order
+    for (uint32_t i = threadIdx.x; i < 256; i += kThreads) {
+      const uint32_t id = id_of[i];
+      bool seen = id >= a.R;
+      for (uint32_t j = 0; j < a.bt; j += 4) {  // a multiple of 16
+        const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j]);
+        seen |= (v.x == id && j < i) || (v.y == id && j + 1 < i) || (v.z == id && j + 2 < i) ||
+                (v.w == id && j + 3 < i);
+      }
+      const uint32_t votes = __ballot_sync(0xffffffffu, !seen);
+      if (lane == 0) firsts[i / 32] = votes;
+    }
     __syncthreads();
     uint32_t* out = a.found + (size_t)b * (a.bt + 1);
-    // the first token of each adapter lists it, in token order
-    if (warp == 0) {
-      uint32_t count = 0;
-      for (uint32_t i0 = 0; i0 < a.bt; i0 += 32) {
-        const uint32_t i = i0 + lane, id = i < a.bt ? id_of[i] : 0xffffffffu;
-        bool mine = id < a.R;
-        for (uint32_t j = 0; j < i && mine; ++j) mine = id_of[j] != id;
-        const uint32_t votes = __ballot_sync(0xffffffffu, mine);
-        if (mine) out[1 + count + __popc(votes & ((1u << lane) - 1))] = id;
-        count += __popc(votes);
-      }
-      if (lane == 0) out[0] = count;
+    for (uint32_t i = threadIdx.x; i < 256; i += kThreads) {
+      uint32_t before = __popc(firsts[i / 32] & ((1u << lane) - 1));
+      for (uint32_t w = 0; w < i / 32; ++w) before += __popc(firsts[w]);
+      if ((firsts[i / 32] >> lane) & 1) out[1 + before] = id_of[i];
+      if (i == 255) out[0] = before + (firsts[7] >> 31);
     }
     __syncthreads();
   }
@@ -224,18 +202,22 @@ __global__ void __launch_bounds__(kThreads)
   // this cluster's tokens, sorted by adapter (tokens without one last)
   const uint32_t t0 = blockIdx.x / csize * a.rk_tokens;
   const uint32_t mine = threadIdx.x;
-  if (mine < a.rk_tokens) {
+  if (mine < kRankTokens) {
     const uint32_t t = t0 + mine;
-    const uint32_t id = t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
+    const uint32_t id = mine < a.rk_tokens && t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
     id_of[mine] = id < a.R ? id : 0xffffffffu;
   }
-  if (threadIdx.x < 16) order[kRankTokens + threadIdx.x] = (int)a.T;
   __syncthreads();
   if (mine < a.rk_tokens) {
     const uint32_t id = id_of[mine];
     uint32_t pos = 0;
-    for (uint32_t j = 0; j < a.rk_tokens; ++j)
-      pos += id_of[j] < id || (id_of[j] == id && j < mine);
+    for (uint32_t j = 0; j < a.rk_tokens; j += 4) {  // past rk_tokens: no adapter, sorted last
+      const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j]);
+      pos += v.x < id || (v.x == id && j < mine);
+      pos += v.y < id || (v.y == id && j + 1 < mine);
+      pos += v.z < id || (v.z == id && j + 2 < mine);
+      pos += v.w < id || (v.w == id && j + 3 < mine);
+    }
     order[pos] = (int)(t0 + mine);
     sorted[pos] = id;
   }
@@ -273,38 +255,49 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t k0 = min(a.ktiles, crank * a.rk_slices), k1 = min(a.ktiles, k0 + a.rk_slices);
 
   if (k0 < k1) {
-    if (warp == 0) {
-      if (lane == 0) {  // ----------------------------------- TMA producer
-        uint32_t st = 0, ph = 1, it = 0;
-        bool ok = true;
-        for (uint32_t i = 0; ok && i < items; ++i) {
-          const uint32_t p0 = start[i], rows = start[i + 1] - p0, rows16 = (rows + 15) / 16 * 16;
-          for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
-            if (!symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) {
-              symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-              ok = false;
-              break;
-            }
-            uint8_t* buf = smem + (size_t)st * a.rk_stage;
+    if (warp == 0) {  // --------------------------------------- TMA producer
+      // lane q gathers rows 4q .. 4q + 3 of the adapter; past them T, a row
+      // past the end of x: zeros
+      uint32_t st = 0, ph = 1, it = 0;
+      bool ok = true;
+      for (uint32_t i = 0; ok && i < items; ++i) {
+        const uint32_t p0 = start[i], rows = start[i + 1] - p0, rows16 = (rows + 15) / 16 * 16;
+        const uint32_t q = 4 * lane;
+        int4 r;
+        r.x = q + 0 < rows ? order[p0 + q + 0] : (int)a.T;
+        r.y = q + 1 < rows ? order[p0 + q + 1] : (int)a.T;
+        r.z = q + 2 < rows ? order[p0 + q + 2] : (int)a.T;
+        r.w = q + 3 < rows ? order[p0 + q + 3] : (int)a.T;
+        const int id = (int)sorted[p0];
+        // consecutive tokens (a prompt): boxes of 16 rows, lane q rows 16q ..; the
+        // rows past the adapter's are other tokens', in columns that are not read
+        const bool run = order[p0 + rows - 1] - order[p0] == (int)rows - 1;
+        for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
+          ok = symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) {
+            if (lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+            break;
+          }
+          uint8_t* buf = smem + (size_t)st * a.rk_stage;
+          if (lane == 0) {
             symm::mbar_arrive_expect_tx(&full[st], a.rk_abytes + rows16 * 128);
             for (uint32_t half = 0; half * 8192 < a.rk_abytes; ++half)
-              symm::tma_load_3d(buf + half * 8192, &map_a, (int)half * 64, (int)(kt * kBK),
-                                (int)sorted[p0], &full[st]);
-            for (uint32_t q = 0; q < rows16; q += 4) {
-              // rows of this adapter; past them T, which is past the end: zeros
-              int4 r;
-              r.x = q + 0 < rows ? order[p0 + q + 0] : (int)a.T;
-              r.y = q + 1 < rows ? order[p0 + q + 1] : (int)a.T;
-              r.z = q + 2 < rows ? order[p0 + q + 2] : (int)a.T;
-              r.w = q + 3 < rows ? order[p0 + q + 3] : (int)a.T;
-              tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
-            }
-            if (++st == a.rk_stages) st = 0, ph ^= 1;
+              symm::tma_load_3d(buf + half * 8192, &map_a, (int)half * 64, (int)(kt * kBK), id,
+                                &full[st]);
           }
+          __syncwarp();
+          if (run) {
+            if (16 * lane < rows16)
+              tma_load_2d(buf + a.rk_abytes + lane * 2048, &map_x16, (int)(kt * kBK),
+                          order[p0] + 16 * lane, &full[st]);
+          } else if (q < rows16)
+            tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
+          if (++st == a.rk_stages) st = 0, ph ^= 1;
         }
-        for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
-          symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
       }
+      for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
+        symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
     } else if (warp == 1) {
       if (lane == 0) {  // ------------------------------------ MMA issuer
         uint32_t st = 0, ph = 0;
@@ -377,7 +370,8 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t pos = i / a.r16, c = i % a.r16;
     float s = 0.f;
     if (c < a.r) {
-      for (uint32_t b = 0; b < csize; ++b) s += ld_cluster(symm::smem_addr(&sums[pos * a.r + c]), b);
+      for (uint32_t b = 0; b < csize; ++b)
+        s += ld_cluster(map_cluster(symm::smem_addr(&sums[pos * a.r + c]), b));
       s *= a.scale[sorted[pos]];
     }
     const T hi = moe::from_f<T>(s);
@@ -386,6 +380,14 @@ __global__ void __launch_bounds__(kThreads)
     out[a.r16] = moe::from_f<T>(s - moe::to_f(hi));
   }
   cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+// v[i] of registers
+__device__ __forceinline__ uint32_t pick8(const uint32_t (&v)[8], uint32_t i) {
+  uint32_t x = v[0];
+#pragma unroll
+  for (uint32_t j = 1; j < 8; ++j) x = i == j ? v[j] : x;
+  return x;
 }
 
 // The adapters' columns of a tile come in pieces of one ring stage: h's high
@@ -441,24 +443,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   symm::tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  float* sums = reinterpret_cast<float*>(smem);  // [bt][128], in a cluster of several CTAs
   const uint32_t npieces = a.R ? pieces_of(a) : 0;
-  Walk walk(a);
-  Segment s;
+  // This CTA's tiles, and its part of their K slices and adapters.
+  const uint32_t C = a.cluster, crank = C > 1 ? cluster_rank() : 0;
+  const uint32_t tiles = a.ncol * a.ntok, first = blockIdx.x / C, step = gridDim.x / C;
+  const uint32_t k0 = a.ktiles * crank / C, k1 = a.ktiles * (crank + 1) / C;
 
   if (warp == 0) {
     if (lane == 0) {  // ------------------------------------- TMA producer
       uint64_t it = 0;
       uint32_t st = 0, ph = 1;
+      uint32_t ids[8];
       bool ok = true, waited = false;
       auto claim = [&]() {
         if (symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) return true;
         symm::record_error(a.ctl, symm::kErrTimedOut, -3);
         return ok = false;
       };
-      while (ok && walk.next(a, s)) {
-        const int n0 = (int)(s.tile % a.ncol) * kBM;
-        const uint32_t tb = s.tile / a.ncol;
-        for (uint32_t kt = s.k0; kt < s.k1; ++kt, ++it) {
+      for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+        const int n0 = (int)(tile % a.ncol) * kBM;
+        const uint32_t tb = tile / a.ncol;
+        for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
           if (!claim()) break;
           uint8_t* buf = smem + (size_t)st * stage_bytes;
           symm::mbar_arrive_expect_tx(&full[st], stage_bytes);
@@ -468,14 +474,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           symm::mbar_arrive(&full[st]);
           if (++st == a.stages) st = 0, ph ^= 1;
         }
-        if (!ok || npieces == 0 || s.k1 != a.ktiles) continue;
+        if (!ok || npieces == 0) continue;
         if (!waited) wait_for_first_launch(), waited = true;
         const uint32_t* found = a.found + (size_t)tb * (a.bt + 1);
+        const uint32_t f0 = found[0] * crank / C, nfound = found[0] * (crank + 1) / C - f0;
         for (uint32_t p = 0; ok && p < npieces; ++p)
-          for (uint32_t i = 0; i < found[0]; ++i, ++it) {
+          for (uint32_t i = 0; i < nfound; ++i, ++it) {
+            if (i % 8 == 0)  // 8 at a time: their loads overlap
+#pragma unroll
+              for (uint32_t j = 0; j < 8; ++j) ids[j] = found[1 + f0 + min(i + j, nfound - 1)];
             if (!claim()) break;
             uint8_t* buf = smem + (size_t)st * stage_bytes;
-            const int id = (int)found[1 + i], row = (int)(p >> 1) * 64;
+            const int id = (int)pick8(ids, i % 8), row = (int)(p >> 1) * 64;
             symm::mbar_arrive_expect_tx(&full[st], 256 * min(64u, a.r16));
             symm::tma_load_3d(buf, &map_b, n0, row, id, &full[st]);
             symm::tma_load_3d(buf + kATile / 2, &map_b, n0 + 64, row, id, &full[st]);
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::tc_fence_after();
         return true;
       };
-      for (; ok && walk.next(a, s); ++seg) {
+      for (uint32_t tile = first; ok && tile < tiles; tile += step, ++seg) {
         const uint32_t buf = seg & 1;
         if (!symm::mbar_wait_ab(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
           symm::record_error(a.ctl, symm::kErrTimedOut, -4);
@@ -508,26 +518,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         symm::tc_fence_after();
         const uint32_t acc = tmem + buf * a.bt;
-        for (uint32_t kt = s.k0; kt < s.k1; ++kt) {
+        for (uint32_t kt = k0; kt < k1; ++kt) {
           if (!ready()) break;
-          const uint8_t* tile = smem + (size_t)st * stage_bytes;
-          const uint64_t wd = symm::sw128_mnmajor_desc(tile);
-          const uint64_t xd = symm::sw128_kmajor_desc(tile + kATile);
+          const uint8_t* ring = smem + (size_t)st * stage_bytes;
+          const uint64_t wd = symm::sw128_mnmajor_desc(ring);
+          const uint64_t xd = symm::sw128_kmajor_desc(ring + kATile);
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j)
-            symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, kt != s.k0 || j != 0);
+            symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, kt != k0 || j != 0);
           symm::tc_commit(&empty[st]);
           if (++st == a.stages) st = 0, ph ^= 1;
         }
-        if (ok && npieces && s.k1 == a.ktiles) {
+        if (ok && npieces) {
           if (!waited) wait_for_first_launch(), waited = true;
-          const uint32_t nfound = a.found[(size_t)(s.tile / a.ncol) * (a.bt + 1)];
+          const uint32_t total = a.found[(size_t)(tile / a.ncol) * (a.bt + 1)];
+          const uint32_t nfound = total * (crank + 1) / C - total * crank / C;
           for (uint32_t p = 0; ok && p < npieces; ++p)
             for (uint32_t i = 0; i < nfound; ++i) {
               if (!ready()) break;
-              const uint8_t* tile = smem + (size_t)st * stage_bytes;
-              const uint64_t wd = symm::sw128_mnmajor_desc(tile);
-              const uint64_t xd = symm::sw128_kmajor_desc(tile + kATile);
+              const uint8_t* ring = smem + (size_t)st * stage_bytes;
+              const uint64_t wd = symm::sw128_mnmajor_desc(ring);
+              const uint64_t xd = symm::sw128_kmajor_desc(ring + kATile);
               const uint32_t steps = piece_rows(a, p) / 16;
               for (uint32_t j = 0; j < steps; ++j)
                 symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, 1);
@@ -552,13 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phases = 0;  // of `claimed`, one bit per stage
     bool ok = true;
     wait_for_first_launch();
-    for (uint32_t seg = 0; ok && walk.next(a, s); ++seg) {
+    for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
       const uint32_t buf = seg & 1;
-      const uint32_t n = (s.tile % a.ncol) * kBM + row, tb = s.tile / a.ncol, t0 = tb * a.bt;
-      it += s.k1 - s.k0;
-      if (npieces && s.k1 == a.ktiles) {
+      const uint32_t n = (tile % a.ncol) * kBM + row, tb = tile / a.ncol, t0 = tb * a.bt;
+      it += k1 - k0;
+      if (npieces) {
         const uint32_t* found = a.found + (size_t)tb * (a.bt + 1);
-        const uint32_t nfound = found[0];
+        const uint32_t f0 = found[0] * crank / C, nfound = found[0] * (crank + 1) / C - f0;
         for (uint32_t p = 0; ok && nfound && p < npieces; ++p) {
           // this thread's 16-byte chunks of the piece (at most 16: bt 256, 8
           // chunks a row) and the adapters of their tokens
@@ -578,7 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                               ch);
             }
           }
+          uint32_t ids = 0;  // of 32 adapters, one per lane
           for (uint32_t i = 0; i < nfound; ++i, ++it) {
+            if (i % 32 == 0) ids = found[1 + f0 + min(i + lane, nfound - 1)];
             const uint32_t st = (uint32_t)(it % a.stages);
             // not `empty`: whose phases this warp does not follow one by one
             if (!symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl)) {
@@ -587,12 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             phases ^= 1u << st;
-            uint8_t* tile = smem + (size_t)st * stage_bytes + kATile;
-            const uint32_t want = found[1 + i];
+            uint8_t* ring = smem + (size_t)st * stage_bytes + kATile;
+            const uint32_t want = __shfl_sync(0xffffffffu, ids, (int)(i % 32));
 #pragma unroll
             for (int c = 0; c < 16; ++c)
               if (at[c] != 0xffffffffu)
-                *reinterpret_cast<uint4*>(tile + at[c]) =
+                *reinterpret_cast<uint4*>(ring + at[c]) =
                     id[c] == want ? v[c] : make_uint4(0, 0, 0, 0);
             symm::fence_proxy_async_shared();  // h, for the MMAs
             symm::group_sync(1, 128);
@@ -607,55 +620,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       symm::tc_fence_after();
       const uint32_t taddr = tmem + ((32 * q) << 16) + buf * a.bt;
-      const bool whole = s.k0 == 0 && s.k1 == a.ktiles;
-      // the first segment of a CTA has slot 0, a later partial one is its last: slot 1
-      float* mine = a.part + ((size_t)blockIdx.x * 2 + (seg != 0)) * a.bt * kBM;
 #pragma unroll 1
       for (uint32_t c = 0; c < chunks; ++c) {
         uint32_t v[16];
         symm::tmem_ld16(taddr + c * 16, v);
-        if (c + 1 == chunks) {  // the accumulator is free for the next segment
+        if (c + 1 == chunks) {  // the accumulator is free for the next tile
           symm::tc_fence_before();
           symm::mbar_arrive(&tempty[buf]);
         }
-        if (t0 + c * 16 >= a.T) continue;
-        if (whole) {
-          float acc[16];
+        float acc[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j] = __uint_as_float(v[j]);
-          store16<FMT>(a, acc, t0 + c * 16, n);
-        } else {
+        for (int j = 0; j < 16; ++j) acc[j] = __uint_as_float(v[j]);
+        if (C == 1) {
+          if (t0 + c * 16 < a.T) store16<FMT>(a, acc, t0 + c * 16, n);
+        } else {  // the ring's loads have all been consumed: its memory takes the sums
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            __stcg(mine + (size_t)(c * 16 + j) * kBM + row, __uint_as_float(v[j]));
+          for (int j = 0; j < 16; ++j) sums[(c * 16 + j) * kBM + row] = acc[j];
         }
-      }
-      if (whole) continue;
-      const uint64_t u0 = (uint64_t)s.tile * a.ktiles;
-      const uint32_t first = owner(a, u0), end = owner(a, u0 + a.ktiles - 1) + 1;
-      __threadfence();
-      symm::group_sync(1, 128);
-      if (me == 0)
-        last = symm::atom_add_acq_rel_u32(&a.arrived[s.tile], 1u) + 1 == end - first;
-      symm::group_sync(1, 128);
-      if (!last) continue;
-#pragma unroll 1
-      for (uint32_t c = 0; c < chunks && t0 + c * 16 < a.T; ++c) {
-        float acc[16] = {};
-        for (uint32_t b = first; b < end; ++b) {
-          const float* p =
-              a.part + ((size_t)b * 2 + (cut(a, b) < u0)) * a.bt * kBM + (size_t)c * 16 * kBM + row;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[j] += __ldcg(p + (size_t)j * kBM);
-        }
-        store16<FMT>(a, acc, t0 + c * 16, n);
       }
     }
   }
 
   __syncwarp();
   symm::tc_fence_before();
-  __syncthreads();
+  if (C > 1) {
+    cluster_sync();  // every CTA's sums are complete
+    // this CTA's share of the tokens; a warp takes a token's 128 columns, 4 a lane
+    using T = typename Elem<FMT>::T;
+    const uint32_t tb = first / a.ncol, n = first % a.ncol * kBM + 4 * lane;
+    const uint32_t c1 = min(a.bt * (crank + 1) / C, a.T - tb * a.bt);
+    for (uint32_t c = a.bt * crank / C + warp; c < c1; c += kThreads / 32) {
+      const uint32_t at = symm::smem_addr(sums + c * kBM + 4 * lane);
+      float4 v[8];
+#pragma unroll
+      for (uint32_t b = 0; b < 8; ++b)
+        if (b < C) v[b] = ld_cluster4(map_cluster(at, b));
+      float4 s = v[0];
+#pragma unroll
+      for (uint32_t b = 1; b < 8; ++b)
+        if (b < C) s.x += v[b].x, s.y += v[b].y, s.z += v[b].z, s.w += v[b].w;
+      T* y = static_cast<T*>(a.y) + (size_t)(tb * a.bt + c) * a.ldy + n;
+      if (n + 0 < a.n) y[0] = moe::from_f<T>(s.x);
+      if (n + 1 < a.n) y[1] = moe::from_f<T>(s.y);
+      if (n + 2 < a.n) y[2] = moe::from_f<T>(s.z);
+      if (n + 3 < a.n) y[3] = moe::from_f<T>(s.w);
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     symm::tc_fence_after();
     symm::tmem_dealloc(tmem, a.tmem_cols);
@@ -664,30 +677,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // How a call of these sizes is cut up.
 struct Plan {
-  uint32_t bt, ntok, ncol, ktiles, stages, split, ctas, tmem_cols, r16;
+  uint32_t bt, ntok, ncol, ktiles, stages, cluster, ctas, tmem_cols, r16;
   uint32_t rk_tokens, rk_cluster, rk_slices, rk_stages, rk_abytes, rk_stage;
-  size_t h_bytes, found_bytes, part_bytes, arrived_bytes;
-  size_t bytes() const { return h_bytes + found_bytes + part_bytes + arrived_bytes; }
 };
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Tokens per tile and CTAs per tile: the pair with the least estimated time.
+// A K slice costs its loads, 16 KB of W and 128 bytes a token at about 125
+// bytes a ns per SM, which is more than its MMAs; a round of tiles costs 2 us
+// (filling the ring, the epilogue) and sharing a tile 1.5 us and 10 ns a token.
+void choose_tiles(Plan& p, uint32_t T, uint32_t sms) {
+  double best = 0;
+  for (uint32_t blocks = (T + 255) / 256, i = 0; i < 8; ++i, ++blocks) {
+    const uint32_t bt = (uint32_t)up((T + blocks - 1) / blocks, 16);
+    const uint32_t ntok = (T + bt - 1) / bt;
+    const double slice = 131 + 1.02 * bt;
+    for (uint32_t c = 1; c <= 8 && c <= p.ktiles; c *= 2) {
+      const uint64_t tiles = (uint64_t)p.ncol * ntok;
+      // clusters of 8 do not fill every GPC
+      const uint64_t room = c == 8 ? std::max(1u, sms / 9) : std::max(1u, sms / c);
+      const uint64_t rounds = (tiles + room - 1) / room;
+      const double per = (double)((p.ktiles + c - 1) / c) * slice;
+      const double t = c == 1 ? rounds * per + 2000 + 500 * (rounds - 1)
+                              : rounds * (per + 3500 + 10.0 * bt);
+      if (best == 0 || t < best) best = t, p.bt = bt, p.ntok = ntok, p.cluster = c;
+    }
+    if (bt == 16) break;
+  }
+}
+
 Plan plan_of(int T, int k, int n, int r) {
   Plan p{};
   const uint32_t sms = (uint32_t)std::max(sm_count(), 1);
-  const uint32_t blocks = ((uint32_t)T + 255) / 256;  // token blocks of at most 256
-  p.bt = (uint32_t)up(((uint32_t)T + blocks - 1) / blocks, 16);
-  p.ntok = ((uint32_t)T + p.bt - 1) / p.bt;
   p.ncol = ((uint32_t)n + kBM - 1) / kBM;
   p.ktiles = ((uint32_t)k + kBK - 1) / kBK;
+  choose_tiles(p, (uint32_t)T, sms);
   p.stages = std::min<uint32_t>(kMaxStages, kRingBytes / (kATile + p.bt * 128));
-  const uint64_t tiles = (uint64_t)p.ncol * p.ntok, slices = tiles * p.ktiles;
-  const uint64_t waves = (tiles + sms - 1) / sms;
-  // Whole tiles while the last wave leaves at most a tenth of the SMs' time unused.
-  p.split = tiles * 10 < waves * sms * 9 && p.ktiles > 1;
-  p.ctas = p.split ? (uint32_t)std::min<uint64_t>(sms, std::max<uint64_t>(1, slices / 4))
-                   : (uint32_t)std::min<uint64_t>(sms, tiles);
-  if (p.split && p.ctas < 2) p.split = 0, p.ctas = (uint32_t)std::min<uint64_t>(sms, tiles);
+  const uint32_t tiles = p.ncol * p.ntok;
+  p.ctas = p.cluster > 1 ? tiles * p.cluster : std::min(sms, tiles);
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bt) p.tmem_cols *= 2;
   p.r16 = (uint32_t)up((size_t)r, 16);
@@ -703,12 +731,12 @@ Plan plan_of(int T, int k, int n, int r) {
   p.rk_abytes = r <= 64 ? 8192 : 16384;
   p.rk_stage = p.rk_abytes + (uint32_t)up(p.rk_tokens, 16) * 128;
   p.rk_stages = std::min<uint32_t>(kRankStages, 72 * 1024 / p.rk_stage);
-  p.h_bytes = up((size_t)T * 2 * p.r16 * 2, 256);
-  p.found_bytes = up((size_t)p.ntok * (p.bt + 1) * 4, 256);
-  p.part_bytes = p.split ? (size_t)p.ctas * 2 * p.bt * kBM * 4 : 0;
-  p.arrived_bytes = p.split ? up((size_t)tiles * 4, 256) : 0;
   return p;
 }
+
+// Workspace: h, then the token blocks' adapters (blocks of at least 16 tokens).
+size_t h_bytes(int T, int r) { return up((size_t)T * 2 * up((size_t)r, 16) * 2, 256); }
+size_t found_bytes(int T) { return up(((size_t)T + 256) / 16 * 17 * 4, 256); }
 
 int check_adapter(const char* what, int T, int k, int n, int r) {
   if (T < 0 || T > (1 << 24) || k < 8 || n < 8 || k % 8 || n % 8 || k > (1 << 20) ||
@@ -742,7 +770,7 @@ int make_map(CUtensorMap* map, const void* base, int fmt, uint64_t inner, uint64
 }
 
 struct Maps {
-  CUtensorMap w, x, a, rows, b;
+  CUtensorMap w, x, a, rows, rows16, b;
 };
 
 constexpr size_t kRankSmemMax = 1024 + 72 * 1024 + 8192 + (size_t)kRankTokens * SYMM_MOE_MAX_RANK * 4;
@@ -774,31 +802,29 @@ template <int FMT>
 int launch(const Plan& p, const Maps& m, const AdapterArgs& a, cudaStream_t s) {
   int rc = set_up<FMT>();
   if (rc) return rc;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (a.R) {
     cfg.gridDim = dim3((a.T + p.rk_tokens - 1) / p.rk_tokens * p.rk_cluster);
     cfg.dynamicSmemBytes =
         1024 + (size_t)p.rk_stages * p.rk_stage + 8192 + (size_t)p.rk_tokens * a.r * 4;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.rk_cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    rc = cuda_check(cudaLaunchKernelEx(&cfg, rank_kernel<FMT>, m.a, m.rows, a),
+    cfg.numAttrs = 1;
+    rc = cuda_check(cudaLaunchKernelEx(&cfg, rank_kernel<FMT>, m.a, m.rows, m.rows16, a),
                     "moe_adapter_matmul: rank products");
-  } else if (p.split) {
-    rc = cuda_check(cudaMemsetAsync(a.arrived, 0, p.arrived_bytes, s),
-                    "moe_adapter_matmul: arrival counters");
+    if (rc) return rc;
   }
-  if (rc) return rc;
   cfg.gridDim = dim3(p.ctas);
-  cfg.dynamicSmemBytes = 1024 + (size_t)p.stages * (kATile + p.bt * 128);
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = a.R ? 1 : 0;
+  cfg.dynamicSmemBytes = 1024 + kRingBytes;
+  attr[0].val.clusterDim.x = p.cluster;
+  cfg.numAttrs = a.R ? 2 : 1;
   return cuda_check(cudaLaunchKernelEx(&cfg, adapter_kernel<FMT>, m.w, m.x, m.b, a),
                     "moe_adapter_matmul: product");
 }
@@ -810,7 +836,7 @@ extern "C" int moe_adapter_workspace(int T, int k, int n, int r, size_t* bytes) 
     if (!bytes) return fail(SYMM_EINVAL, "moe_adapter_workspace: NULL bytes");
     int rc = check_adapter("moe_adapter_workspace", T, k, n, r);
     if (rc) return rc;
-    *bytes = T ? plan_of(T, k, n, r).bytes() : 0;
+    *bytes = T ? h_bytes(T, r) + found_bytes(T) : 0;
     return SYMM_OK;
   });
 }
@@ -849,6 +875,7 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
     if (!rc && R) {
       rc = make_map(&m.a, a, fmt, (uint64_t)r, (uint64_t)k, (uint64_t)R, (size_t)r, kBK);
       if (!rc) rc = make_map(&m.rows, x, fmt, (uint64_t)k, (uint64_t)T, 0, ldx, 1);
+      if (!rc) rc = make_map(&m.rows16, x, fmt, (uint64_t)k, (uint64_t)T, 0, ldx, 16);
       if (!rc)
         rc = make_map(&m.b, b, fmt, (uint64_t)n, (uint64_t)r, (uint64_t)R, (size_t)n,
                       std::min(64u, p.r16));
@@ -862,11 +889,9 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
     g.scale = scale, g.ids = ids, g.y = y, g.ldy = ldy;
     g.T = (uint32_t)T, g.k = (uint32_t)k, g.n = (uint32_t)n, g.R = (uint32_t)R, g.r = (uint32_t)r;
     g.r16 = p.r16, g.bt = p.bt, g.ntok = p.ntok, g.ncol = p.ncol, g.ktiles = p.ktiles;
-    g.stages = p.stages, g.split = p.split, g.tmem_cols = p.tmem_cols;
+    g.stages = p.stages, g.cluster = p.cluster, g.tmem_cols = p.tmem_cols;
     g.h = reinterpret_cast<uint16_t*>(ws);
-    g.found = reinterpret_cast<uint32_t*>(ws + p.h_bytes);
-    g.part = reinterpret_cast<float*>(ws + p.h_bytes + p.found_bytes);
-    g.arrived = reinterpret_cast<uint32_t*>(ws + p.h_bytes + p.found_bytes + p.part_bytes);
+    g.found = reinterpret_cast<uint32_t*>(ws + h_bytes(T, r));
     g.rk_tokens = p.rk_tokens, g.rk_slices = p.rk_slices, g.rk_stages = p.rk_stages;
     g.rk_abytes = p.rk_abytes, g.rk_stage = p.rk_stage;
     g.budget_ns = heap->spin_budget;
