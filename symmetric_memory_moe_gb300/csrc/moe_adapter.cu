@@ -29,10 +29,11 @@
 // the error in the heap's header.
 //
 // rank_kernel: h^T = A_a^T x^T the same way (A as stored, k x r, is an M-major
-// operand, rows r to 127 of the tile unused).  A CTA sorts the ids of up to 128
-// tokens, gathers the x rows of each adapter's tokens (tile::gather4) as the N
-// side, and takes one part of K; the CTAs of a cluster share the tokens and
-// add their parts in rank order through distributed shared memory.
+// operand, rows r to 127 of the tile unused).  Per block of 128 tokens, a CTA
+// sorts the ids, and gathers the x rows of each adapter's tokens (tile::gather4)
+// as the N side, for one part of K; the CTAs of a cluster add their parts in
+// rank order through distributed shared memory.  A block's adapters are dealt
+// out to several clusters while there are few blocks.
 #include <algorithm>
 #include <string>
 
@@ -53,6 +54,7 @@ constexpr uint32_t kATile = kBM * kBK * 2;
 constexpr uint32_t kRingBytes = 200 * 1024;
 constexpr int kRankTokens = 128;  // tokens of a rank_kernel CTA, at most
 constexpr int kRankStages = 8;
+constexpr uint32_t kRankBytes = 98 * 1024;  // of its ring and sums, with two CTAs per SM
 
 struct AdapterArgs {
   const float* scale;
@@ -63,11 +65,10 @@ struct AdapterArgs {
   uint32_t bt, ntok, ncol, ktiles, stages;  // tiles: ncol column blocks x ntok token blocks
   uint32_t cluster, tmem_cols;  // cluster: CTAs that share a tile
   uint16_t* h;      // [T][2 r16]: high parts, then low parts
-  uint32_t* found;  // [ntok][bt + 1]: number of adapters of a token block, then which
   uint64_t budget_ns;
   Control* ctl;
-  // rank_kernel: tokens and K slices per CTA, stages, bytes of A and of a stage
-  uint32_t rk_tokens, rk_slices, rk_stages, rk_abytes, rk_stage;
+  // rank_kernel: clusters per token block, stages, bytes of A and of a stage
+  uint32_t rk_share, rk_stages, rk_abytes, rk_stage;
 };
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
@@ -98,6 +99,12 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, i
       "r"(rows.w), "r"(symm::smem_addr(bar))
       : "memory");
 }
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void dependents_may_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
@@ -116,6 +123,13 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// The last one, which no memory access is ordered by: reads of the other CTAs'
+// shared memory have returned their values (they were used), and waiting for
+// this CTA's stores to global memory would only take time.
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;"
                ::: "memory");
 }
 // `addr` (a shared-memory address of this CTA) in CTA `rank` of the cluster.
@@ -151,7 +165,8 @@ constexpr uint64_t kXStep = 32 >> 4;          // 16 K columns of a K-major tile
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
     rank_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
-                const __grid_constant__ CUtensorMap map_x16, const AdapterArgs a) {
+                const __grid_constant__ CUtensorMap map_x16,
+                const __grid_constant__ CUtensorMap map_b, const AdapterArgs a) {
   using T = typename Elem<FMT>::T;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -159,82 +174,16 @@ __global__ void __launch_bounds__(kThreads)
   float* sums = reinterpret_cast<float*>(smem + (size_t)a.rk_stages * a.rk_stage + 8192);
   __shared__ uint64_t full[kRankStages], empty[kRankStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(16) uint32_t id_of[256];  // by token
-  __shared__ uint32_t firsts[8];
+  __shared__ __align__(16) uint32_t id_of[kRankTokens];  // by token
   __shared__ int order[kRankTokens];           // tokens by adapter
   __shared__ uint32_t sorted[kRankTokens];     // their ids
+  __shared__ float scales[kRankTokens];        // their adapters' scales
   __shared__ uint32_t start[kRankTokens + 1];  // first position of each adapter's tokens
-  __shared__ uint32_t nitems, nvalid;
+  __shared__ uint32_t nitems;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), csize = cluster_size();
   dependents_may_start();
 
-  // for the second launch: the adapters of its token blocks
-  for (uint32_t b = blockIdx.x; b < a.ntok; b += gridDim.x) {
-    for (uint32_t i = threadIdx.x; i < 256; i += kThreads) {
-      const uint32_t t = b * a.bt + i;
-      id_of[i] = i < a.bt && t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
-    }
-    __syncthreads();
-    // the first token of each adapter lists it, in token order
-    for (uint32_t i = threadIdx.x; i < 256; i += kThreads) {
-      const uint32_t id = id_of[i];
-      bool seen = id >= a.R;
-      for (uint32_t j = 0; j < a.bt; j += 4) {  // a multiple of 16
-        const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j]);
-        seen |= (v.x == id && j < i) || (v.y == id && j + 1 < i) || (v.z == id && j + 2 < i) ||
-                (v.w == id && j + 3 < i);
-      }
-      const uint32_t votes = __ballot_sync(0xffffffffu, !seen);
-      if (lane == 0) firsts[i / 32] = votes;
-    }
-    __syncthreads();
-    uint32_t* out = a.found + (size_t)b * (a.bt + 1);
-    for (uint32_t i = threadIdx.x; i < 256; i += kThreads) {
-      uint32_t before = __popc(firsts[i / 32] & ((1u << lane) - 1));
-      for (uint32_t w = 0; w < i / 32; ++w) before += __popc(firsts[w]);
-      if ((firsts[i / 32] >> lane) & 1) out[1 + before] = id_of[i];
-      if (i == 255) out[0] = before + (firsts[7] >> 31);
-    }
-    __syncthreads();
-  }
-
-  // this cluster's tokens, sorted by adapter (tokens without one last)
-  const uint32_t t0 = blockIdx.x / csize * a.rk_tokens;
-  const uint32_t mine = threadIdx.x;
-  if (mine < kRankTokens) {
-    const uint32_t t = t0 + mine;
-    const uint32_t id = mine < a.rk_tokens && t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
-    id_of[mine] = id < a.R ? id : 0xffffffffu;
-  }
-  __syncthreads();
-  if (mine < a.rk_tokens) {
-    const uint32_t id = id_of[mine];
-    uint32_t pos = 0;
-    for (uint32_t j = 0; j < a.rk_tokens; j += 4) {  // past rk_tokens: no adapter, sorted last
-      const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j]);
-      pos += v.x < id || (v.x == id && j < mine);
-      pos += v.y < id || (v.y == id && j + 1 < mine);
-      pos += v.z < id || (v.z == id && j + 2 < mine);
-      pos += v.w < id || (v.w == id && j + 3 < mine);
-    }
-    order[pos] = (int)(t0 + mine);
-    sorted[pos] = id;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t count = 0, valid = 0;
-    for (uint32_t i0 = 0; i0 < a.rk_tokens; i0 += 32) {
-      const uint32_t i = i0 + lane;
-      const bool ok = i < a.rk_tokens && sorted[i] != 0xffffffffu;
-      const bool first = ok && (i == 0 || sorted[i - 1] != sorted[i]);
-      const uint32_t votes = __ballot_sync(0xffffffffu, first);
-      if (first) start[count + __popc(votes & ((1u << lane) - 1))] = i;
-      count += __popc(votes);
-      valid += __popc(__ballot_sync(0xffffffffu, ok));
-    }
-    if (lane == 0) start[count] = valid, nitems = count, nvalid = valid;
-  }
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < a.rk_stages; ++s) {
       symm::mbar_init(&full[s], 1);
@@ -247,147 +196,188 @@ __global__ void __launch_bounds__(kThreads)
     symm::mbar_init(&drain, 1);
     symm::fence_mbar_init();
   }
-  if (warp == 1) symm::tmem_alloc(&tmem_slot, 256);
+  if (warp == 5) symm::tmem_alloc(&tmem_slot, 256);
+
+  // this block's tokens, sorted by adapter (tokens without one last)
+  const uint32_t group = blockIdx.x / csize, t0 = group / a.rk_share * kRankTokens;
+  const uint32_t share = group % a.rk_share;  // this cluster's adapters: share, share + rk_share, ..
+  const uint32_t mine = threadIdx.x;
+  if (mine < kRankTokens) {
+    const uint32_t t = t0 + mine;
+    const uint32_t id = t < a.T ? (uint32_t)a.ids[t] : 0xffffffffu;
+    id_of[mine] = id < a.R ? id : 0xffffffffu;
+  }
+  __syncthreads();
+  if (mine < kRankTokens) {
+    const uint32_t id = id_of[mine];
+    uint32_t pos = 0;
+#pragma unroll 8
+    for (uint32_t j = 0; j < kRankTokens; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j]);
+      pos += v.x < id || (v.x == id && j < mine);
+      pos += v.y < id || (v.y == id && j + 1 < mine);
+      pos += v.z < id || (v.z == id && j + 2 < mine);
+      pos += v.w < id || (v.w == id && j + 3 < mine);
+    }
+    order[pos] = (int)(t0 + mine);
+    sorted[pos] = id;
+    scales[pos] = id < a.R ? a.scale[id] : 0.f;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t count = 0, valid = 0;
+    for (uint32_t i0 = 0; i0 < kRankTokens; i0 += 32) {
+      const uint32_t i = i0 + lane;
+      const bool ok = sorted[i] != 0xffffffffu;
+      const bool first = ok && (i == 0 || sorted[i - 1] != sorted[i]);
+      const uint32_t votes = __ballot_sync(0xffffffffu, first);
+      if (first) start[count + __popc(votes & ((1u << lane) - 1))] = i;
+      count += __popc(votes);
+      valid += __popc(__ballot_sync(0xffffffffu, ok));
+    }
+    if (lane == 0) start[count] = valid, nitems = count;
+  }
   symm::tc_fence_before();
   __syncthreads();
   symm::tc_fence_after();
-  const uint32_t tmem = tmem_slot, items = nitems, valid = nvalid;
-  const uint32_t k0 = min(a.ktiles, crank * a.rk_slices), k1 = min(a.ktiles, k0 + a.rk_slices);
+  const uint32_t tmem = tmem_slot, items = nitems;
+  const uint32_t k0 = a.ktiles * crank / csize, k1 = a.ktiles * (crank + 1) / csize;
 
-  if (k0 < k1) {
-    if (warp == 0) {  // --------------------------------------- TMA producer
-      // lane q gathers rows 4q .. 4q + 3 of the adapter; past them T, a row
-      // past the end of x: zeros
-      uint32_t st = 0, ph = 1, it = 0;
+  if (warp == 0) {  // --------------------------------------- TMA producer
+    // lane q gathers rows 4q .. 4q + 3 of the adapter; past them T, a row
+    // past the end of x: zeros
+    uint32_t st = 0, ph = 1, it = 0;
+    bool ok = true;
+    for (uint32_t i = share; ok && i < items; i += a.rk_share) {
+      const uint32_t p0 = start[i], rows = start[i + 1] - p0, rows16 = (rows + 15) / 16 * 16;
+      const uint32_t q = 4 * lane;
+      int4 r;
+      r.x = q + 0 < rows ? order[p0 + q + 0] : (int)a.T;
+      r.y = q + 1 < rows ? order[p0 + q + 1] : (int)a.T;
+      r.z = q + 2 < rows ? order[p0 + q + 2] : (int)a.T;
+      r.w = q + 3 < rows ? order[p0 + q + 3] : (int)a.T;
+      const int id = (int)sorted[p0];
+      // consecutive tokens (a prompt): boxes of 16 rows, lane q rows 16q ..; the
+      // rows past the adapter's are other tokens', in columns that are not read
+      const bool run = order[p0 + rows - 1] - order[p0] == (int)rows - 1;
+      for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
+        ok = symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+          break;
+        }
+        uint8_t* buf = smem + (size_t)st * a.rk_stage;
+        if (lane == 0) {
+          symm::mbar_arrive_expect_tx(&full[st], a.rk_abytes + rows16 * 128);
+          for (uint32_t half = 0; half * 8192 < a.rk_abytes; ++half)
+            symm::tma_load_3d(buf + half * 8192, &map_a, (int)half * 64, (int)(kt * kBK), id,
+                              &full[st]);
+        }
+        __syncwarp();
+        if (run) {
+          if (16 * lane < rows16)
+            tma_load_2d(buf + a.rk_abytes + lane * 2048, &map_x16, (int)(kt * kBK),
+                        order[p0] + 16 * lane, &full[st]);
+        } else if (q < rows16)
+          tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
+        if (++st == a.rk_stages) st = 0, ph ^= 1;
+      }
+    }
+    for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
+      symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
+  } else if (warp == 1) {
+    if (lane == 0) {  // ------------------------------------ MMA issuer
+      uint32_t st = 0, ph = 0;
       bool ok = true;
-      for (uint32_t i = 0; ok && i < items; ++i) {
-        const uint32_t p0 = start[i], rows = start[i + 1] - p0, rows16 = (rows + 15) / 16 * 16;
-        const uint32_t q = 4 * lane;
-        int4 r;
-        r.x = q + 0 < rows ? order[p0 + q + 0] : (int)a.T;
-        r.y = q + 1 < rows ? order[p0 + q + 1] : (int)a.T;
-        r.z = q + 2 < rows ? order[p0 + q + 2] : (int)a.T;
-        r.w = q + 3 < rows ? order[p0 + q + 3] : (int)a.T;
-        const int id = (int)sorted[p0];
-        // consecutive tokens (a prompt): boxes of 16 rows, lane q rows 16q ..; the
-        // rows past the adapter's are other tokens', in columns that are not read
-        const bool run = order[p0 + rows - 1] - order[p0] == (int)rows - 1;
-        for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
-          ok = symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) {
-            if (lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-            break;
-          }
-          uint8_t* buf = smem + (size_t)st * a.rk_stage;
-          if (lane == 0) {
-            symm::mbar_arrive_expect_tx(&full[st], a.rk_abytes + rows16 * 128);
-            for (uint32_t half = 0; half * 8192 < a.rk_abytes; ++half)
-              symm::tma_load_3d(buf + half * 8192, &map_a, (int)half * 64, (int)(kt * kBK), id,
-                                &full[st]);
-          }
-          __syncwarp();
-          if (run) {
-            if (16 * lane < rows16)
-              tma_load_2d(buf + a.rk_abytes + lane * 2048, &map_x16, (int)(kt * kBK),
-                          order[p0] + 16 * lane, &full[st]);
-          } else if (q < rows16)
-            tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
-          if (++st == a.rk_stages) st = 0, ph ^= 1;
-        }
-      }
-      for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
-        symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
-    } else if (warp == 1) {
-      if (lane == 0) {  // ------------------------------------ MMA issuer
-        uint32_t st = 0, ph = 0;
-        bool ok = true;
-        for (uint32_t i = 0; ok && i < items; ++i) {
-          const uint32_t rows16 = (start[i + 1] - start[i] + 15) / 16 * 16, buf = i & 1;
-          if (!symm::mbar_wait_ab(&tempty[buf], ((i >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
-            symm::record_error(a.ctl, symm::kErrTimedOut, -4);
-            break;
-          }
-          symm::tc_fence_after();
-          const uint32_t idesc = mma_idesc(FMT, rows16);
-          for (uint32_t kt = k0; kt < k1; ++kt) {
-            if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
-              symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-              ok = false;
-              break;
-            }
-            symm::tc_fence_after();
-            const uint8_t* tile = smem + (size_t)st * a.rk_stage;
-            const uint64_t wd = symm::sw128_mnmajor_desc(tile);
-            const uint64_t xd = symm::sw128_kmajor_desc(tile + a.rk_abytes);
-#pragma unroll
-            for (int j = 0; j < kBK / 16; ++j)
-              symm::tc_mma(tmem + buf * 128, wd + kWStep * j, xd + kXStep * j, idesc,
-                           kt != k0 || j != 0);
-            symm::tc_commit(&empty[st]);
-            if (++st == a.rk_stages) st = 0, ph ^= 1;
-          }
-          if (ok) symm::tc_commit(&tfull[buf]);
-        }
-        symm::tc_commit(&drain);
-        symm::mbar_wait(&drain, 0, a.budget_ns);
-      }
-    } else {  // ------------------------------------------- sums of this part
-      const uint32_t q = (uint32_t)(warp & 3), row = 32 * q + lane;
-      for (uint32_t i = 0; i < items; ++i) {
-        const uint32_t p0 = start[i], rows = start[i + 1] - p0, buf = i & 1;
-        if (!symm::mbar_wait_ab(&tfull[buf], (i >> 1) & 1, a.budget_ns, a.ctl)) {
-          symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+      for (uint32_t i = share, seg = 0; ok && i < items; i += a.rk_share, ++seg) {
+        const uint32_t rows16 = (start[i + 1] - start[i] + 15) / 16 * 16, buf = seg & 1;
+        if (!symm::mbar_wait_ab(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
+          symm::record_error(a.ctl, symm::kErrTimedOut, -4);
           break;
         }
         symm::tc_fence_after();
-        if (32 * q < a.r)  // the warp's TMEM lanes hold ranks
-          for (uint32_t c = 0; c < rows; c += 16) {
-            uint32_t v[16];
-            symm::tmem_ld16(tmem + ((32 * q) << 16) + buf * 128 + c, v);
-            if (row < a.r)
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (c + j < rows) sums[(p0 + c + j) * a.r + row] = __uint_as_float(v[j]);
+        const uint32_t idesc = mma_idesc(FMT, rows16);
+        for (uint32_t kt = k0; kt < k1; ++kt) {
+          if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
+            symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+            ok = false;
+            break;
           }
-        symm::tc_fence_before();
-        symm::mbar_arrive(&tempty[buf]);
+          symm::tc_fence_after();
+          const uint8_t* tile = smem + (size_t)st * a.rk_stage;
+          const uint64_t wd = symm::sw128_mnmajor_desc(tile);
+          const uint64_t xd = symm::sw128_kmajor_desc(tile + a.rk_abytes);
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j)
+            symm::tc_mma(tmem + buf * 128, wd + kWStep * j, xd + kXStep * j, idesc,
+                         kt != k0 || j != 0);
+          symm::tc_commit(&empty[st]);
+          if (++st == a.rk_stages) st = 0, ph ^= 1;
+        }
+        if (ok) symm::tc_commit(&tfull[buf]);
       }
+      symm::tc_commit(&drain);
+      symm::mbar_wait(&drain, 0, a.budget_ns);
     }
-  } else {
-    for (uint32_t i = threadIdx.x; i < valid * a.r; i += kThreads) sums[i] = 0.f;
+  } else {  // ------------------------------------------- sums of this part
+    const uint32_t q = (uint32_t)(warp & 3), row = 32 * q + lane;
+    // B of these adapters on its way into L2, for the second launch
+    for (uint32_t i = share; i < items; i += a.rk_share)
+      for (uint32_t n0 = ((threadIdx.x - 64) * csize + crank) * 64; n0 < a.n;
+           n0 += 128 * csize * 64)
+        for (uint32_t r0 = 0; r0 < a.r; r0 += 64)
+          prefetch_3d(&map_b, (int)n0, (int)r0, (int)sorted[start[i]]);
+    for (uint32_t i = share, seg = 0; i < items; i += a.rk_share, ++seg) {
+      const uint32_t p0 = start[i], rows = start[i + 1] - p0, buf = seg & 1;
+      if (!symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
+        symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+        break;
+      }
+      symm::tc_fence_after();
+      if (32 * q < a.r)  // the warp's TMEM lanes hold ranks
+        for (uint32_t c = 0; c < rows; c += 16) {
+          uint32_t v[16];
+          symm::tmem_ld16(tmem + ((32 * q) << 16) + buf * 128 + c, v);
+          if (row < a.r)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < rows) sums[(p0 + c + j) * a.r + row] = __uint_as_float(v[j]);
+        }
+      symm::tc_fence_before();
+      symm::mbar_arrive(&tempty[buf]);
+    }
   }
   __syncwarp();
   symm::tc_fence_before();
   cluster_sync();  // every CTA's sums are complete
-  if (warp == 1) {
+  if (warp == 5) {
     symm::tc_fence_after();
     symm::tmem_dealloc(tmem, 256);
   }
-  // each CTA of the cluster joins its share of the tokens, CTAs in order
+  // each CTA of the cluster joins its share of the sums, CTAs in order
   T* H = reinterpret_cast<T*>(a.h);
-  for (uint32_t i = crank * kThreads + threadIdx.x; i < valid * a.r16; i += csize * kThreads) {
-    const uint32_t pos = i / a.r16, c = i % a.r16;
-    float s = 0.f;
-    if (c < a.r) {
-      for (uint32_t b = 0; b < csize; ++b)
-        s += ld_cluster(map_cluster(symm::smem_addr(&sums[pos * a.r + c]), b));
-      s *= a.scale[sorted[pos]];
-    }
-    const T hi = moe::from_f<T>(s);
-    T* out = H + (size_t)order[pos] * 2 * a.r16 + c;
-    out[0] = hi;
-    out[a.r16] = moe::from_f<T>(s - moe::to_f(hi));
-  }
-  cluster_sync();  // no CTA leaves while another reads its sums
-}
-
-// v[i] of registers
-__device__ __forceinline__ uint32_t pick8(const uint32_t (&v)[8], uint32_t i) {
-  uint32_t x = v[0];
+  for (uint32_t item = share; item < items; item += a.rk_share) {
+    const uint32_t p0 = start[item], n = (start[item + 1] - p0) * a.r16;
+    for (uint32_t i = crank * kThreads + threadIdx.x; i < n; i += csize * kThreads) {
+      const uint32_t pos = p0 + i / a.r16, c = i % a.r16;
+      float s = 0.f;
+      if (c < a.r) {
+        const uint32_t at = symm::smem_addr(&sums[pos * a.r + c]);
+        float v[8];
 #pragma unroll
-  for (uint32_t j = 1; j < 8; ++j) x = i == j ? v[j] : x;
-  return x;
+        for (uint32_t b = 0; b < 8; ++b) v[b] = b < csize ? ld_cluster(map_cluster(at, b)) : 0.f;
+#pragma unroll
+        for (uint32_t b = 0; b < 8; ++b) s += v[b];
+        s *= scales[pos];
+      }
+      const T hi = moe::from_f<T>(s);
+      T* out = H + (size_t)order[pos] * 2 * a.r16 + c;
+      out[0] = hi;
+      out[a.r16] = moe::from_f<T>(s - moe::to_f(hi));
+    }
+  }
+  cluster_leave();  // no CTA leaves while another reads its sums
 }
 
 // The adapters' columns of a tile come in pieces of one ring stage: h's high
@@ -421,8 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   const uint32_t stage_bytes = kATile + a.bt * 128;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], claimed[kMaxStages];
-  __shared__ uint64_t tfull[2], tempty[2], drain;
-  __shared__ uint32_t tmem_slot, last;
+  __shared__ uint64_t tfull[2], tempty[2], listed[2], drain;
+  __shared__ uint32_t tmem_slot;
+  // the ids of a tile's tokens, and the adapters among them (how many, which);
+  // two tiles' worth, as the accumulators
+  __shared__ __align__(16) uint32_t id_of[256];
+  __shared__ uint32_t firsts[8], list[2][256], nlist[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -434,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       symm::mbar_init(&tfull[b], 1);
       symm::mbar_init(&tempty[b], 128);
+      symm::mbar_init(&listed[b], 1);
     }
     symm::mbar_init(&drain, 1);
     symm::fence_mbar_init();
@@ -449,49 +444,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t C = a.cluster, crank = C > 1 ? cluster_rank() : 0;
   const uint32_t tiles = a.ncol * a.ntok, first = blockIdx.x / C, step = gridDim.x / C;
   const uint32_t k0 = a.ktiles * crank / C, k1 = a.ktiles * (crank + 1) / C;
+  // The adapters come before the last ring's worth of a long part of K, where
+  // the first launch is done and their loads hide behind W's; else at the end.
+  const uint32_t kp = k1 - k0 > 2 * a.stages ? k1 - a.stages : k1;
 
   if (warp == 0) {
     if (lane == 0) {  // ------------------------------------- TMA producer
       uint64_t it = 0;
       uint32_t st = 0, ph = 1;
-      uint32_t ids[8];
-      bool ok = true, waited = false;
+      bool ok = true;
       auto claim = [&]() {
         if (symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) return true;
         symm::record_error(a.ctl, symm::kErrTimedOut, -3);
         return ok = false;
       };
-      for (uint32_t tile = first; ok && tile < tiles; tile += step) {
+      for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
         const int n0 = (int)(tile % a.ncol) * kBM;
         const uint32_t tb = tile / a.ncol;
-        for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
-          if (!claim()) break;
-          uint8_t* buf = smem + (size_t)st * stage_bytes;
-          symm::mbar_arrive_expect_tx(&full[st], stage_bytes);
-          tma_load_2d(buf, &map_w, n0, (int)(kt * kBK), &full[st]);
-          tma_load_2d(buf + kATile / 2, &map_w, n0 + 64, (int)(kt * kBK), &full[st]);
-          tma_load_2d(buf + kATile, &map_x, (int)(kt * kBK), (int)(tb * a.bt), &full[st]);
-          symm::mbar_arrive(&full[st]);
-          if (++st == a.stages) st = 0, ph ^= 1;
-        }
-        if (!ok || npieces == 0) continue;
-        if (!waited) wait_for_first_launch(), waited = true;
-        const uint32_t* found = a.found + (size_t)tb * (a.bt + 1);
-        const uint32_t f0 = found[0] * crank / C, nfound = found[0] * (crank + 1) / C - f0;
-        for (uint32_t p = 0; ok && p < npieces; ++p)
-          for (uint32_t i = 0; i < nfound; ++i, ++it) {
-            if (i % 8 == 0)  // 8 at a time: their loads overlap
-#pragma unroll
-              for (uint32_t j = 0; j < 8; ++j) ids[j] = found[1 + f0 + min(i + j, nfound - 1)];
+        auto load_slices = [&](uint32_t from, uint32_t to) {
+          for (uint32_t kt = from; ok && kt < to; ++kt, ++it) {
             if (!claim()) break;
             uint8_t* buf = smem + (size_t)st * stage_bytes;
-            const int id = (int)pick8(ids, i % 8), row = (int)(p >> 1) * 64;
-            symm::mbar_arrive_expect_tx(&full[st], 256 * min(64u, a.r16));
-            symm::tma_load_3d(buf, &map_b, n0, row, id, &full[st]);
-            symm::tma_load_3d(buf + kATile / 2, &map_b, n0 + 64, row, id, &full[st]);
-            symm::mbar_arrive(&claimed[st]);
+            symm::mbar_arrive_expect_tx(&full[st], stage_bytes);
+            tma_load_2d(buf, &map_w, n0, (int)(kt * kBK), &full[st]);
+            tma_load_2d(buf + kATile / 2, &map_w, n0 + 64, (int)(kt * kBK), &full[st]);
+            tma_load_2d(buf + kATile, &map_x, (int)(kt * kBK), (int)(tb * a.bt), &full[st]);
+            symm::mbar_arrive(&full[st]);
             if (++st == a.stages) st = 0, ph ^= 1;
           }
+        };
+        load_slices(k0, kp);
+        if (ok && npieces) {
+          const uint32_t buf2 = seg & 1;
+          if (!symm::mbar_wait_ab(&listed[buf2], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
+            symm::record_error(a.ctl, symm::kErrTimedOut, -8);
+            ok = false;
+          }
+          const uint32_t f0 = nlist[buf2] * crank / C, f1 = nlist[buf2] * (crank + 1) / C;
+          for (uint32_t p = 0; ok && p < npieces; ++p)
+            for (uint32_t i = f0; i < f1; ++i, ++it) {
+              if (!claim()) break;
+              uint8_t* buf = smem + (size_t)st * stage_bytes;
+              const int id = (int)list[buf2][i], row = (int)(p >> 1) * 64;
+              symm::mbar_arrive_expect_tx(&full[st], 256 * min(64u, a.r16));
+              symm::tma_load_3d(buf, &map_b, n0, row, id, &full[st]);
+              symm::tma_load_3d(buf + kATile / 2, &map_b, n0 + 64, row, id, &full[st]);
+              symm::mbar_arrive(&claimed[st]);
+              if (++st == a.stages) st = 0, ph ^= 1;
+            }
+        }
+        load_slices(kp, k1);
       }
       // every load issued lands before the CTA may leave (bounded)
       for (uint64_t i = it > a.stages ? it - a.stages : 0; i < it; ++i)
@@ -501,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {  // -------------------------------------- MMA issuer
       const uint32_t idesc = mma_idesc(FMT, a.bt);
       uint32_t st = 0, ph = 0, seg = 0;
-      bool ok = true, waited = false;
+      bool ok = true;
       auto ready = [&]() {
         if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
           symm::record_error(a.ctl, symm::kErrTimedOut, -5);
@@ -518,21 +520,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         symm::tc_fence_after();
         const uint32_t acc = tmem + buf * a.bt;
-        for (uint32_t kt = k0; kt < k1; ++kt) {
-          if (!ready()) break;
-          const uint8_t* ring = smem + (size_t)st * stage_bytes;
-          const uint64_t wd = symm::sw128_mnmajor_desc(ring);
-          const uint64_t xd = symm::sw128_kmajor_desc(ring + kATile);
+        auto multiply = [&](uint32_t from, uint32_t to) {
+          for (uint32_t kt = from; ok && kt < to; ++kt) {
+            if (!ready()) break;
+            const uint8_t* ring = smem + (size_t)st * stage_bytes;
+            const uint64_t wd = symm::sw128_mnmajor_desc(ring);
+            const uint64_t xd = symm::sw128_kmajor_desc(ring + kATile);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)
-            symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, kt != k0 || j != 0);
-          symm::tc_commit(&empty[st]);
-          if (++st == a.stages) st = 0, ph ^= 1;
-        }
+            for (int j = 0; j < kBK / 16; ++j)
+              symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, kt != k0 || j != 0);
+            symm::tc_commit(&empty[st]);
+            if (++st == a.stages) st = 0, ph ^= 1;
+          }
+        };
+        multiply(k0, kp);
         if (ok && npieces) {
-          if (!waited) wait_for_first_launch(), waited = true;
-          const uint32_t total = a.found[(size_t)(tile / a.ncol) * (a.bt + 1)];
-          const uint32_t nfound = total * (crank + 1) / C - total * crank / C;
+          if (!symm::mbar_wait_ab(&listed[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
+            symm::record_error(a.ctl, symm::kErrTimedOut, -9);
+            ok = false;
+          }
+          const uint32_t nfound = nlist[buf] * (crank + 1) / C - nlist[buf] * crank / C;
           for (uint32_t p = 0; ok && p < npieces; ++p)
             for (uint32_t i = 0; i < nfound; ++i) {
               if (!ready()) break;
@@ -549,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (++st == a.stages) st = 0, ph ^= 1;
             }
         }
+        multiply(kp, k1);
         if (ok) symm::tc_commit(&tfull[buf]);
       }
       symm::tc_commit(&drain);  // every MMA is complete before TMEM is freed
@@ -561,16 +569,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t chunks = a.bt / 16;
     uint64_t it = 0;
     uint32_t phases = 0;  // of `claimed`, one bit per stage
-    bool ok = true;
-    wait_for_first_launch();
+    bool ok = true, waited = false;
     for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
       const uint32_t buf = seg & 1;
       const uint32_t n = (tile % a.ncol) * kBM + row, tb = tile / a.ncol, t0 = tb * a.bt;
-      it += k1 - k0;
+      it += kp - k0;
       if (npieces) {
-        const uint32_t* found = a.found + (size_t)tb * (a.bt + 1);
-        const uint32_t f0 = found[0] * crank / C, nfound = found[0] * (crank + 1) / C - f0;
-        for (uint32_t p = 0; ok && nfound && p < npieces; ++p) {
+        // the tokens' adapters, each listed by its first token, in token order
+        for (uint32_t i = me; i < 256; i += 128)
+          id_of[i] = i < a.bt && t0 + i < a.T ? (uint32_t)a.ids[t0 + i] : 0xffffffffu;
+        symm::group_sync(1, 128);
+        for (uint32_t i = me; i < 256; i += 128) {
+          const uint32_t id = id_of[i];
+          bool seen = id >= a.R || (i && id_of[i - 1] == id);
+          for (uint32_t j = 0; j < (i | 31); j += 16) {  // the same for the warp's lanes
+            if (__all_sync(0xffffffffu, seen)) break;
+#pragma unroll
+            for (uint32_t l = 0; l < 16; l += 4) {
+              const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j + l]);
+              seen |= (v.x == id && j + l < i) || (v.y == id && j + l + 1 < i) ||
+                      (v.z == id && j + l + 2 < i) || (v.w == id && j + l + 3 < i);
+            }
+          }
+          const uint32_t votes = __ballot_sync(0xffffffffu, !seen);
+          if (lane == 0) firsts[i / 32] = votes;
+        }
+        symm::group_sync(1, 128);
+        for (uint32_t i = me; i < 256; i += 128) {
+          uint32_t before = __popc(firsts[i / 32] & ((1u << lane) - 1));
+          for (uint32_t w = 0; w < i / 32; ++w) before += __popc(firsts[w]);
+          if ((firsts[i / 32] >> lane) & 1) list[buf][before] = id_of[i];
+          if (i == 255) nlist[buf] = before + (firsts[7] >> 31);
+        }
+        symm::group_sync(1, 128);
+        if (me == 0) symm::mbar_arrive(&listed[buf]);
+        if (!waited) wait_for_first_launch(), waited = true;  // for h
+        const uint32_t f0 = nlist[buf] * crank / C, f1 = nlist[buf] * (crank + 1) / C;
+        for (uint32_t p = 0; ok && f0 < f1 && p < npieces; ++p) {
           // this thread's 16-byte chunks of the piece (at most 16: bt 256, 8
           // chunks a row) and the adapters of their tokens
           const uint32_t width = (npieces == 1 ? 2 * a.r16 : piece_rows(a, p)) / 8;
@@ -583,15 +618,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             id[c] = 0xffffffffu, v[c] = make_uint4(0, 0, 0, 0);
             at[c] = tr < a.bt ? tr * 128 + ((ch ^ (tr & 7)) << 4) : 0xffffffffu;
             if (tr < a.bt && t < a.T) {
-              id[c] = (uint32_t)a.ids[t];
+              id[c] = id_of[tr];
               if (id[c] < a.R)
                 v[c] = __ldcg(reinterpret_cast<const uint4*>(a.h + (size_t)t * 2 * a.r16 + from) +
                               ch);
             }
           }
-          uint32_t ids = 0;  // of 32 adapters, one per lane
-          for (uint32_t i = 0; i < nfound; ++i, ++it) {
-            if (i % 32 == 0) ids = found[1 + f0 + min(i + lane, nfound - 1)];
+          for (uint32_t i = f0; i < f1; ++i, ++it) {
             const uint32_t st = (uint32_t)(it % a.stages);
             // not `empty`: whose phases this warp does not follow one by one
             if (!symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl)) {
@@ -601,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             phases ^= 1u << st;
             uint8_t* ring = smem + (size_t)st * stage_bytes + kATile;
-            const uint32_t want = __shfl_sync(0xffffffffu, ids, (int)(i % 32));
+            const uint32_t want = list[buf][i];
 #pragma unroll
             for (int c = 0; c < 16; ++c)
               if (at[c] != 0xffffffffu)
@@ -614,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
+      it += k1 - kp;
       if (!symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
         symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
@@ -665,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n + 2 < a.n) y[2] = moe::from_f<T>(s.z);
       if (n + 3 < a.n) y[3] = moe::from_f<T>(s.w);
     }
-    cluster_sync();  // no CTA leaves while another reads its sums
+    cluster_leave();  // no CTA leaves while another reads its sums
   } else {
     __syncthreads();
   }
@@ -678,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // How a call of these sizes is cut up.
 struct Plan {
   uint32_t bt, ntok, ncol, ktiles, stages, cluster, ctas, tmem_cols, r16;
-  uint32_t rk_tokens, rk_cluster, rk_slices, rk_stages, rk_abytes, rk_stage;
+  uint32_t rk_share, rk_cluster, rk_blocks, rk_stages, rk_abytes, rk_stage, rk_bytes;
 };
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -719,24 +753,26 @@ Plan plan_of(int T, int k, int n, int r) {
   p.tmem_cols = 32;
   while (p.tmem_cols < 2 * p.bt) p.tmem_cols *= 2;
   p.r16 = (uint32_t)up((size_t)r, 16);
-  // The first launch: clusters of up to 8 CTAs share the K slices of a group of
-  // tokens; groups of up to 128 tokens, smaller ones while that leaves SMs idle.
+  // The first launch: clusters of up to 8 CTAs share the K slices of a block of
+  // 128 tokens; about two CTAs per SM in all.
+  const uint32_t blocks = ((uint32_t)T + kRankTokens - 1) / kRankTokens;
+  p.rk_blocks = blocks;
   p.rk_cluster = 8;
-  while (p.rk_cluster > 1 && p.rk_cluster > p.ktiles) p.rk_cluster /= 2;
-  const uint32_t groups = std::max(1u, 2 * sms / p.rk_cluster);
-  p.rk_tokens = std::min<uint32_t>(kRankTokens, std::max(1u, ((uint32_t)T + groups - 1) / groups));
-  while (p.rk_cluster > 1 && (T + p.rk_tokens - 1) / p.rk_tokens * p.rk_cluster > 3 * sms)
+  while (p.rk_cluster > 1 && (p.rk_cluster > p.ktiles || blocks * p.rk_cluster > 2 * sms))
     p.rk_cluster /= 2;
-  p.rk_slices = (p.ktiles + p.rk_cluster - 1) / p.rk_cluster;
+  p.rk_share = std::max(1u, std::min(std::min((uint32_t)T, (uint32_t)kRankTokens),
+                                     2 * sms / (blocks * p.rk_cluster)));
   p.rk_abytes = r <= 64 ? 8192 : 16384;
-  p.rk_stage = p.rk_abytes + (uint32_t)up(p.rk_tokens, 16) * 128;
-  p.rk_stages = std::min<uint32_t>(kRankStages, 72 * 1024 / p.rk_stage);
+  p.rk_stage = p.rk_abytes + std::min<uint32_t>(kRankTokens, (uint32_t)up((size_t)T, 16)) * 128;
+  // two CTAs per SM while their sums leave room for it
+  const uint32_t sums = std::min<uint32_t>(kRankTokens, (uint32_t)T) * (uint32_t)r * 4;
+  p.rk_stages = std::min<uint32_t>(kRankStages, (kRankBytes - std::min(sums, 32768u)) / p.rk_stage);
+  p.rk_bytes = 1024 + p.rk_stages * p.rk_stage + 8192 + sums;
   return p;
 }
 
-// Workspace: h, then the token blocks' adapters (blocks of at least 16 tokens).
+// Workspace: h.
 size_t h_bytes(int T, int r) { return up((size_t)T * 2 * up((size_t)r, 16) * 2, 256); }
-size_t found_bytes(int T) { return up(((size_t)T + 256) / 16 * 17 * 4, 256); }
 
 int check_adapter(const char* what, int T, int k, int n, int r) {
   if (T < 0 || T > (1 << 24) || k < 8 || n < 8 || k % 8 || n % 8 || k > (1 << 20) ||
@@ -773,7 +809,7 @@ struct Maps {
   CUtensorMap w, x, a, rows, rows16, b;
 };
 
-constexpr size_t kRankSmemMax = 1024 + 72 * 1024 + 8192 + (size_t)kRankTokens * SYMM_MOE_MAX_RANK * 4;
+constexpr size_t kRankSmemMax = 1024 + kRankBytes + 8192 + (size_t)kRankTokens * SYMM_MOE_MAX_RANK * 4;
 
 // Once per device: both kernels may use more than 48 KB of shared memory.
 template <int FMT>
@@ -812,12 +848,11 @@ int launch(const Plan& p, const Maps& m, const AdapterArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   if (a.R) {
-    cfg.gridDim = dim3((a.T + p.rk_tokens - 1) / p.rk_tokens * p.rk_cluster);
-    cfg.dynamicSmemBytes =
-        1024 + (size_t)p.rk_stages * p.rk_stage + 8192 + (size_t)p.rk_tokens * a.r * 4;
+    cfg.gridDim = dim3(p.rk_blocks * p.rk_share * p.rk_cluster);
+    cfg.dynamicSmemBytes = p.rk_bytes;
     attr[0].val.clusterDim.x = p.rk_cluster;
     cfg.numAttrs = 1;
-    rc = cuda_check(cudaLaunchKernelEx(&cfg, rank_kernel<FMT>, m.a, m.rows, m.rows16, a),
+    rc = cuda_check(cudaLaunchKernelEx(&cfg, rank_kernel<FMT>, m.a, m.rows, m.rows16, m.b, a),
                     "moe_adapter_matmul: rank products");
     if (rc) return rc;
   }
@@ -836,7 +871,7 @@ extern "C" int moe_adapter_workspace(int T, int k, int n, int r, size_t* bytes) 
     if (!bytes) return fail(SYMM_EINVAL, "moe_adapter_workspace: NULL bytes");
     int rc = check_adapter("moe_adapter_workspace", T, k, n, r);
     if (rc) return rc;
-    *bytes = T ? h_bytes(T, r) + found_bytes(T) : 0;
+    *bytes = h_bytes(T, r);
     return SYMM_OK;
   });
 }
@@ -858,7 +893,7 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
         ldx > (1ull << 36) || ldw > (1ull << 36) || ldy > (1ull << 36))
       return fail(SYMM_EINVAL, "moe_adapter_matmul: ldx >= k, ldw >= n (multiples of 8), ldy >= n");
     if (T == 0) return SYMM_OK;
-    if (!x || !w || !y || !workspace || (R && (!a || !b || !scale || !ids)))
+    if (!x || !w || !y || (R && !workspace) || (R && (!a || !b || !scale || !ids)))
       return fail(SYMM_EINVAL, "moe_adapter_matmul: NULL input, output or workspace");
     if (!moe::aligned(x, 16) || !moe::aligned(w, 16) || !moe::aligned(a, 16) ||
         !moe::aligned(b, 16) || !moe::aligned(y, 2) || !moe::aligned(scale, 4) ||
@@ -884,16 +919,14 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
     cudaStream_t s = as_stream(stream);
     rc = ensure_ctrl(heap, s);
     if (rc) return rc;
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     AdapterArgs g{};
     g.scale = scale, g.ids = ids, g.y = y, g.ldy = ldy;
     g.T = (uint32_t)T, g.k = (uint32_t)k, g.n = (uint32_t)n, g.R = (uint32_t)R, g.r = (uint32_t)r;
     g.r16 = p.r16, g.bt = p.bt, g.ntok = p.ntok, g.ncol = p.ncol, g.ktiles = p.ktiles;
     g.stages = p.stages, g.cluster = p.cluster, g.tmem_cols = p.tmem_cols;
-    g.h = reinterpret_cast<uint16_t*>(ws);
-    g.found = reinterpret_cast<uint32_t*>(ws + h_bytes(T, r));
-    g.rk_tokens = p.rk_tokens, g.rk_slices = p.rk_slices, g.rk_stages = p.rk_stages;
-    g.rk_abytes = p.rk_abytes, g.rk_stage = p.rk_stage;
+    g.h = static_cast<uint16_t*>(workspace);
+    g.rk_share = p.rk_share, g.rk_stages = p.rk_stages, g.rk_abytes = p.rk_abytes;
+    g.rk_stage = p.rk_stage;
     g.budget_ns = heap->spin_budget;
     g.ctl = reinterpret_cast<Control*>(heap->base);
     return fmt ? launch<1>(p, m, g, s) : launch<0>(p, m, g, s);
