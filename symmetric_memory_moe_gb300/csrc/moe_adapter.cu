@@ -821,15 +821,15 @@ int set_up() {
   if (rc) return rc;
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 64 && done[dev]) return SYMM_OK;
-  rc = cuda_check(cudaFuncSetAttribute(adapter_kernel<FMT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(1024 + kRingBytes)),
-                  "moe_adapter_matmul: kernel set-up");
-  if (!rc)
-    rc = cuda_check(cudaFuncSetAttribute(rank_kernel<FMT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kRankSmemMax),
-                    "moe_adapter_matmul: kernel set-up");
+  auto set = [&](const void* f, cudaFuncAttribute attr, int v) {
+    if (!rc) rc = cuda_check(cudaFuncSetAttribute(f, attr, v), "moe_adapter_matmul: kernel set-up");
+  };
+  const void *product = (const void*)adapter_kernel<FMT>, *ranks = (const void*)rank_kernel<FMT>;
+  set(product, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(1024 + kRingBytes));
+  set(ranks, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRankSmemMax);
+  // the same split of an SM's memory for both: changing it would wait for an idle SM
+  set(product, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  set(ranks, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (!rc && dev < 64) done[dev] = true;
   return rc;
 }
