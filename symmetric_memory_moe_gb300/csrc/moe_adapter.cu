@@ -14,9 +14,10 @@
 // columns of W (W as stored, k x n, is an M-major operand) and the N side BT
 // tokens, 16 to 256.  One token then wastes no more than a narrow N, and one
 // kernel serves a decoding step and a prompt.
-//   warp 0     TMA producer: 64-deep K slices of W (two boxes of 64 columns)
-//              and of x into a ring of shared-memory stages, 128-byte
-//              swizzled; then the adapters' B;
+//   warp 0     TMA producer: K slices of W (two boxes of 64 columns) and of x
+//              into a ring of shared-memory stages, 128-byte swizzled, 64 deep
+//              or, with few tokens, 128 (a slice costs each role some 250
+//              cycles beside its MMAs); and the adapters' B;
 //   warp 1     MMA issuer: tcgen05.mma kind::f16, M 128, N BT, two
 //              accumulators in TMEM;
 //   warps 2-5  the adapters' h into the ring, then the epilogue: tcgen05.ld,
@@ -62,7 +63,9 @@ struct AdapterArgs {
   void* y;
   size_t ldy;
   uint32_t T, k, n, R, r, r16;  // r16: r in whole K steps of 16
-  uint32_t bt, ntok, ncol, ktiles, stages;  // tiles: ncol column blocks x ntok token blocks
+  uint32_t bt, ntok, ncol, stages;  // tiles: ncol column blocks x ntok token blocks
+  uint32_t deep, slices;            // 64-deep K tiles per slice, slices of K
+  uint32_t ktiles;                  // 64-deep K tiles (rank_kernel's slices)
   uint32_t cluster, tmem_cols;  // cluster: CTAs that share a tile
   uint16_t* h;      // [T][2 r16]: high parts, then low parts
   uint64_t budget_ns;
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ float scales[kRankTokens];        // their adapters' scales
   __shared__ uint32_t start[kRankTokens + 1];  // first position of each adapter's tokens
   __shared__ uint32_t nitems;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), csize = cluster_size();
   dependents_may_start();
 
@@ -246,6 +249,7 @@ __global__ void __launch_bounds__(kThreads)
   if (warp == 0) {  // --------------------------------------- TMA producer
     // lane q gathers rows 4q .. 4q + 3 of the adapter; past them T, a row
     // past the end of x: zeros
+    const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 1, it = 0;
     bool ok = true;
     for (uint32_t i = share; ok && i < items; i += a.rk_share) {
@@ -261,14 +265,13 @@ __global__ void __launch_bounds__(kThreads)
       // rows past the adapter's are other tokens', in columns that are not read
       const bool run = order[p0 + rows - 1] - order[p0] == (int)rows - 1;
       for (uint32_t kt = k0; kt < k1; ++kt, ++it) {
-        ok = symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = symm::mbar_wait_warp(&empty[st], ph, a.budget_ns, a.ctl);
         if (!ok) {
-          if (lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+          if (elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
           break;
         }
         uint8_t* buf = smem + (size_t)st * a.rk_stage;
-        if (lane == 0) {
+        if (elected) {
           symm::mbar_arrive_expect_tx(&full[st], a.rk_abytes + rows16 * 128);
           for (uint32_t half = 0; half * 8192 < a.rk_abytes; ++half)
             symm::tma_load_3d(buf + half * 8192, &map_a, (int)half * 64, (int)(kt * kBK), id,
@@ -286,40 +289,34 @@ __global__ void __launch_bounds__(kThreads)
     }
     for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
       symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
-  } else if (warp == 1) {
-    if (lane == 0) {  // ------------------------------------ MMA issuer
-      uint32_t st = 0, ph = 0;
-      bool ok = true;
-      for (uint32_t i = share, seg = 0; ok && i < items; i += a.rk_share, ++seg) {
-        const uint32_t rows16 = (start[i + 1] - start[i] + 15) / 16 * 16, buf = seg & 1;
-        if (!symm::mbar_wait_ab(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
-          symm::record_error(a.ctl, symm::kErrTimedOut, -4);
-          break;
-        }
+  } else if (warp == 1) {  // -------------------------------- MMA issuer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 0;
+    bool ok = true;
+    for (uint32_t i = share, seg = 0; ok && i < items; i += a.rk_share, ++seg) {
+      const uint32_t rows16 = (start[i + 1] - start[i] + 15) / 16 * 16, buf = seg & 1;
+      ok = symm::mbar_wait_warp(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl);
+      const uint32_t idesc = mma_idesc(FMT, rows16);
+      for (uint32_t kt = k0; ok && kt < k1; ++kt) {
+        if (!(ok = symm::mbar_wait_warp(&full[st], ph, a.budget_ns, a.ctl))) break;
         symm::tc_fence_after();
-        const uint32_t idesc = mma_idesc(FMT, rows16);
-        for (uint32_t kt = k0; kt < k1; ++kt) {
-          if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
-            symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-            ok = false;
-            break;
-          }
-          symm::tc_fence_after();
-          const uint8_t* tile = smem + (size_t)st * a.rk_stage;
-          const uint64_t wd = symm::sw128_mnmajor_desc(tile);
-          const uint64_t xd = symm::sw128_kmajor_desc(tile + a.rk_abytes);
+        const uint8_t* tile = smem + (size_t)st * a.rk_stage;
+        const uint64_t wd = symm::sw128_mnmajor_desc(tile);
+        const uint64_t xd = symm::sw128_kmajor_desc(tile + a.rk_abytes);
+        if (elected) {
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j)
             symm::tc_mma(tmem + buf * 128, wd + kWStep * j, xd + kXStep * j, idesc,
                          kt != k0 || j != 0);
           symm::tc_commit(&empty[st]);
-          if (++st == a.rk_stages) st = 0, ph ^= 1;
         }
-        if (ok) symm::tc_commit(&tfull[buf]);
+        if (++st == a.rk_stages) st = 0, ph ^= 1;
       }
-      symm::tc_commit(&drain);
-      symm::mbar_wait(&drain, 0, a.budget_ns);
+      if (ok && elected) symm::tc_commit(&tfull[buf]);
     }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+    if (elected) symm::tc_commit(&drain);
+    symm::mbar_wait(&drain, 0, a.budget_ns);
   } else {  // ------------------------------------------- sums of this part
     const uint32_t q = (uint32_t)(warp & 3), row = 32 * q + lane;
     // B of these adapters on its way into L2, for the second launch
@@ -409,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap map_b, const AdapterArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
-  const uint32_t stage_bytes = kATile + a.bt * 128;
+  const uint32_t abytes = a.deep * kATile, xbytes = a.bt * 128;
+  const uint32_t stage_bytes = abytes + a.deep * xbytes;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], claimed[kMaxStages];
   __shared__ uint64_t tfull[2], tempty[2], listed[2], drain;
   __shared__ uint32_t tmem_slot;
@@ -417,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // two tiles' worth, as the accumulators
   __shared__ __align__(16) uint32_t id_of[256];
   __shared__ uint32_t firsts[8], list[2][256], nlist[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < a.stages; ++s) {
@@ -443,131 +441,134 @@ __global__ void __launch_bounds__(kThreads, 1)
   // This CTA's tiles, and its part of their K slices and adapters.
   const uint32_t C = a.cluster, crank = C > 1 ? cluster_rank() : 0;
   const uint32_t tiles = a.ncol * a.ntok, first = blockIdx.x / C, step = gridDim.x / C;
-  const uint32_t k0 = a.ktiles * crank / C, k1 = a.ktiles * (crank + 1) / C;
+  const uint32_t k0 = a.slices * crank / C, k1 = a.slices * (crank + 1) / C;
   // The adapters come before the last ring's worth of a long part of K, where
   // the first launch is done and their loads hide behind W's; else at the end.
   const uint32_t kp = k1 - k0 > 2 * a.stages ? k1 - a.stages : k1;
 
-  if (warp == 0) {
-    if (lane == 0) {  // ------------------------------------- TMA producer
-      uint64_t it = 0;
-      uint32_t st = 0, ph = 1;
-      bool ok = true;
-      auto claim = [&]() {
-        if (symm::mbar_wait_ab(&empty[st], ph, a.budget_ns, a.ctl)) return true;
-        symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-        return ok = false;
-      };
-      for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
-        const int n0 = (int)(tile % a.ncol) * kBM;
-        const uint32_t tb = tile / a.ncol;
-        auto load_slices = [&](uint32_t from, uint32_t to) {
-          for (uint32_t kt = from; ok && kt < to; ++kt, ++it) {
-            if (!claim()) break;
-            uint8_t* buf = smem + (size_t)st * stage_bytes;
+  if (warp == 0) {  // ----------------------------------------- TMA producer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 1, it = 0;
+    bool ok = true;
+    auto next = [&]() {
+      ++it;
+      if (++st == a.stages) st = 0, ph ^= 1;
+    };
+    for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
+      const int n0 = (int)(tile % a.ncol) * kBM;
+      const uint32_t tb = tile / a.ncol;
+      auto load_slices = [&](uint32_t from, uint32_t to) {
+        for (uint32_t kt = from; ok && kt < to; ++kt) {
+          if (!(ok = symm::mbar_wait_warp(&empty[st], ph, a.budget_ns, a.ctl))) break;
+          uint8_t* buf = smem + (size_t)st * stage_bytes;
+          if (elected) {
             symm::mbar_arrive_expect_tx(&full[st], stage_bytes);
-            tma_load_2d(buf, &map_w, n0, (int)(kt * kBK), &full[st]);
-            tma_load_2d(buf + kATile / 2, &map_w, n0 + 64, (int)(kt * kBK), &full[st]);
-            tma_load_2d(buf + kATile, &map_x, (int)(kt * kBK), (int)(tb * a.bt), &full[st]);
+            const int k = (int)(kt * a.deep * kBK);
+            tma_load_2d(buf, &map_w, n0, k, &full[st]);
+            tma_load_2d(buf + abytes / 2, &map_w, n0 + 64, k, &full[st]);
+            tma_load_2d(buf + abytes, &map_x, k, (int)(tb * a.bt), &full[st]);
+            if (a.deep == 2)
+              tma_load_2d(buf + abytes + xbytes, &map_x, k + kBK, (int)(tb * a.bt), &full[st]);
             symm::mbar_arrive(&full[st]);
-            if (++st == a.stages) st = 0, ph ^= 1;
           }
-        };
-        load_slices(k0, kp);
-        if (ok && npieces) {
-          const uint32_t buf2 = seg & 1;
-          if (!symm::mbar_wait_ab(&listed[buf2], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
-            symm::record_error(a.ctl, symm::kErrTimedOut, -8);
-            ok = false;
-          }
-          const uint32_t f0 = nlist[buf2] * crank / C, f1 = nlist[buf2] * (crank + 1) / C;
-          for (uint32_t p = 0; ok && p < npieces; ++p)
-            for (uint32_t i = f0; i < f1; ++i, ++it) {
-              if (!claim()) break;
-              uint8_t* buf = smem + (size_t)st * stage_bytes;
-              const int id = (int)list[buf2][i], row = (int)(p >> 1) * 64;
+          next();
+        }
+      };
+      load_slices(k0, kp);
+      if (ok && npieces) {
+        const uint32_t lb = seg & 1;
+        ok = symm::mbar_wait_warp(&listed[lb], (seg >> 1) & 1, a.budget_ns, a.ctl);
+        const uint32_t f0 = nlist[lb] * crank / C, f1 = nlist[lb] * (crank + 1) / C;
+        for (uint32_t p = 0; ok && p < npieces; ++p)
+          for (uint32_t i = f0; i < f1; ++i) {
+            if (!(ok = symm::mbar_wait_warp(&empty[st], ph, a.budget_ns, a.ctl))) break;
+            uint8_t* buf = smem + (size_t)st * stage_bytes;
+            const int id = (int)list[lb][i], row = (int)(p >> 1) * 64;
+            if (elected) {
               symm::mbar_arrive_expect_tx(&full[st], 256 * min(64u, a.r16));
               symm::tma_load_3d(buf, &map_b, n0, row, id, &full[st]);
-              symm::tma_load_3d(buf + kATile / 2, &map_b, n0 + 64, row, id, &full[st]);
+              symm::tma_load_3d(buf + abytes / 2, &map_b, n0 + 64, row, id, &full[st]);
               symm::mbar_arrive(&claimed[st]);
-              if (++st == a.stages) st = 0, ph ^= 1;
             }
-        }
-        load_slices(kp, k1);
+            next();
+          }
       }
-      // every load issued lands before the CTA may leave (bounded)
-      for (uint64_t i = it > a.stages ? it - a.stages : 0; i < it; ++i)
-        symm::mbar_wait(&full[i % a.stages], (uint32_t)((i / a.stages) & 1), a.budget_ns);
+      load_slices(kp, k1);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {  // -------------------------------------- MMA issuer
-      const uint32_t idesc = mma_idesc(FMT, a.bt);
-      uint32_t st = 0, ph = 0, seg = 0;
-      bool ok = true;
-      auto ready = [&]() {
-        if (!symm::mbar_wait_ab(&full[st], ph, a.budget_ns, a.ctl)) {
-          symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-          return ok = false;
-        }
-        symm::tc_fence_after();
-        return true;
-      };
-      for (uint32_t tile = first; ok && tile < tiles; tile += step, ++seg) {
-        const uint32_t buf = seg & 1;
-        if (!symm::mbar_wait_ab(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)) {
-          symm::record_error(a.ctl, symm::kErrTimedOut, -4);
-          break;
-        }
-        symm::tc_fence_after();
-        const uint32_t acc = tmem + buf * a.bt;
-        auto multiply = [&](uint32_t from, uint32_t to) {
-          for (uint32_t kt = from; ok && kt < to; ++kt) {
-            if (!ready()) break;
-            const uint8_t* ring = smem + (size_t)st * stage_bytes;
-            const uint64_t wd = symm::sw128_mnmajor_desc(ring);
-            const uint64_t xd = symm::sw128_kmajor_desc(ring + kATile);
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+    // every load issued lands before the CTA may leave (bounded)
+    for (uint32_t i = it > a.stages ? it - a.stages : 0; i < it; ++i)
+      symm::mbar_wait(&full[i % a.stages], (i / a.stages) & 1, a.budget_ns);
+  } else if (warp == 1) {  // ---------------------------------- MMA issuer
+    const bool elected = symm::elect_one();
+    const uint32_t idesc = mma_idesc(FMT, a.bt);
+    uint32_t st = 0, ph = 0, seg = 0;
+    bool ok = true;
+    auto next = [&]() {
+      if (++st == a.stages) st = 0, ph ^= 1;
+    };
+    for (uint32_t tile = first; ok && tile < tiles; tile += step, ++seg) {
+      const uint32_t buf = seg & 1;
+      ok = symm::mbar_wait_warp(&tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl);
+      symm::tc_fence_after();
+      const uint32_t acc = tmem + buf * a.bt;
+      auto multiply = [&](uint32_t from, uint32_t to) {
+        for (uint32_t kt = from; ok && kt < to; ++kt) {
+          if (!(ok = symm::mbar_wait_warp(&full[st], ph, a.budget_ns, a.ctl))) break;
+          symm::tc_fence_after();
+          const uint8_t* ring = smem + (size_t)st * stage_bytes;
+          const uint64_t wd = symm::sw128_mnmajor_desc(ring, abytes / 2);
+          const uint64_t xd = symm::sw128_kmajor_desc(ring + abytes);
+          if (elected) {
 #pragma unroll
             for (int j = 0; j < kBK / 16; ++j)
               symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, kt != k0 || j != 0);
+            if (a.deep == 2)
+#pragma unroll
+              for (int j = 0; j < kBK / 16; ++j)
+                symm::tc_mma(acc, wd + kWStep * (kBK / 16 + j), xd + (xbytes >> 4) + kXStep * j,
+                             idesc, 1);
             symm::tc_commit(&empty[st]);
-            if (++st == a.stages) st = 0, ph ^= 1;
           }
-        };
-        multiply(k0, kp);
-        if (ok && npieces) {
-          if (!symm::mbar_wait_ab(&listed[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
-            symm::record_error(a.ctl, symm::kErrTimedOut, -9);
-            ok = false;
-          }
-          const uint32_t nfound = nlist[buf] * (crank + 1) / C - nlist[buf] * crank / C;
-          for (uint32_t p = 0; ok && p < npieces; ++p)
-            for (uint32_t i = 0; i < nfound; ++i) {
-              if (!ready()) break;
-              const uint8_t* ring = smem + (size_t)st * stage_bytes;
-              const uint64_t wd = symm::sw128_mnmajor_desc(ring);
-              const uint64_t xd = symm::sw128_kmajor_desc(ring + kATile);
-              const uint32_t steps = piece_rows(a, p) / 16;
+          next();
+        }
+      };
+      multiply(k0, kp);
+      if (ok && npieces) {
+        ok = symm::mbar_wait_warp(&listed[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+        const uint32_t mine = nlist[buf] * (crank + 1) / C - nlist[buf] * crank / C;
+        for (uint32_t p = 0; ok && p < npieces; ++p) {
+          const uint32_t steps = piece_rows(a, p) / 16;
+          for (uint32_t i = 0; i < mine; ++i) {
+            if (!(ok = symm::mbar_wait_warp(&full[st], ph, a.budget_ns, a.ctl))) break;
+            symm::tc_fence_after();
+            const uint8_t* ring = smem + (size_t)st * stage_bytes;
+            const uint64_t wd = symm::sw128_mnmajor_desc(ring, abytes / 2);
+            const uint64_t xd = symm::sw128_kmajor_desc(ring + abytes);
+            if (elected) {
               for (uint32_t j = 0; j < steps; ++j)
                 symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, 1);
               if (npieces == 1)  // the low parts, beside the high ones
                 for (uint32_t j = 0; j < steps; ++j)
                   symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * (steps + j), idesc, 1);
               symm::tc_commit(&empty[st]);
-              if (++st == a.stages) st = 0, ph ^= 1;
             }
+            next();
+          }
         }
-        multiply(kp, k1);
-        if (ok) symm::tc_commit(&tfull[buf]);
       }
-      symm::tc_commit(&drain);  // every MMA is complete before TMEM is freed
-      symm::mbar_wait(&drain, 0, a.budget_ns);
+      multiply(kp, k1);
+      if (ok && elected) symm::tc_commit(&tfull[buf]);
     }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+    if (elected) symm::tc_commit(&drain);  // every MMA is complete before TMEM is freed
+    symm::mbar_wait(&drain, 0, a.budget_ns);
   } else {  // ------------------------------------------ h, and the epilogue
     const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q + 31
     const uint32_t row = 32 * q + lane;       // this thread's column of W in the tile
     const uint32_t me = threadIdx.x - 64;
     const uint32_t chunks = a.bt / 16;
-    uint64_t it = 0;
+    uint32_t it = 0;
     uint32_t phases = 0;  // of `claimed`, one bit per stage
     bool ok = true, waited = false;
     for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
@@ -625,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           for (uint32_t i = f0; i < f1; ++i, ++it) {
-            const uint32_t st = (uint32_t)(it % a.stages);
+            const uint32_t st = it % a.stages;
             // not `empty`: whose phases this warp does not follow one by one
             if (!symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl)) {
               symm::record_error(a.ctl, symm::kErrTimedOut, -7);
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             phases ^= 1u << st;
-            uint8_t* ring = smem + (size_t)st * stage_bytes + kATile;
+            uint8_t* ring = smem + (size_t)st * stage_bytes + abytes;
             const uint32_t want = list[buf][i];
 #pragma unroll
             for (int c = 0; c < 16; ++c)
@@ -711,43 +712,49 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // How a call of these sizes is cut up.
 struct Plan {
-  uint32_t bt, ntok, ncol, ktiles, stages, cluster, ctas, tmem_cols, r16;
+  uint32_t bt, ntok, ncol, ktiles, deep, slices, stages, cluster, ctas, tmem_cols, r16;
   uint32_t rk_share, rk_cluster, rk_blocks, rk_stages, rk_abytes, rk_stage, rk_bytes;
 };
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Tokens per tile and CTAs per tile: the pair with the least estimated time.
-// A K slice costs its loads, 16 KB of W and 128 bytes a token at about 125
-// bytes a ns per SM, which is more than its MMAs; a round of tiles costs 2 us
-// (filling the ring, the epilogue) and sharing a tile 1.5 us and 10 ns a token.
-void choose_tiles(Plan& p, uint32_t T, uint32_t sms) {
+// Clusters of c CTAs of the product that are resident at once (their ring
+// leaves one CTA per SM), once asked for each device.
+int resident_clusters(int fmt, uint32_t c);
+
+// Tokens per tile and CTAs per tile: the pair with the least estimated time,
+// fitted to measured times.  A 64-deep K slice costs its loads, 16 KB of W and
+// 128 bytes a token at about 125 bytes a ns per SM, or what the roles need to
+// issue it; a round of tiles costs 2 us (filling the ring, the epilogue), and
+// sharing a tile 1 us and 5 ns a token.
+void choose_tiles(Plan& p, uint32_t T, int fmt) {
   double best = 0;
   for (uint32_t blocks = (T + 255) / 256, i = 0; i < 8; ++i, ++blocks) {
     const uint32_t bt = (uint32_t)up((T + blocks - 1) / blocks, 16);
     const uint32_t ntok = (T + bt - 1) / bt;
+    const uint64_t tiles = (uint64_t)p.ncol * ntok;
     const double slice = 131 + 1.02 * bt;
-    for (uint32_t c = 1; c <= 8 && c <= p.ktiles; c *= 2) {
-      const uint64_t tiles = (uint64_t)p.ncol * ntok;
-      // clusters of 8 do not fill every GPC
-      const uint64_t room = c == 8 ? std::max(1u, sms / 9) : std::max(1u, sms / c);
+    for (uint32_t c = 1; c <= 8 && c <= (p.ktiles + 1) / 2; ++c) {
+      const uint64_t room = (uint64_t)std::max(1, resident_clusters(fmt, c));
       const uint64_t rounds = (tiles + room - 1) / room;
       const double per = (double)((p.ktiles + c - 1) / c) * slice;
       const double t = c == 1 ? rounds * per + 2000 + 500 * (rounds - 1)
-                              : rounds * (per + 3500 + 10.0 * bt);
+                              : rounds * (per + 3000 + 5.0 * bt);
       if (best == 0 || t < best) best = t, p.bt = bt, p.ntok = ntok, p.cluster = c;
     }
     if (bt == 16) break;
   }
 }
 
-Plan plan_of(int T, int k, int n, int r) {
+Plan plan_of(int T, int k, int n, int r, int fmt) {
   Plan p{};
   const uint32_t sms = (uint32_t)std::max(sm_count(), 1);
   p.ncol = ((uint32_t)n + kBM - 1) / kBM;
   p.ktiles = ((uint32_t)k + kBK - 1) / kBK;
-  choose_tiles(p, (uint32_t)T, sms);
-  p.stages = std::min<uint32_t>(kMaxStages, kRingBytes / (kATile + p.bt * 128));
+  choose_tiles(p, (uint32_t)T, fmt);
+  p.deep = p.bt <= 64 ? 2 : 1;
+  p.slices = (p.ktiles + p.deep - 1) / p.deep;
+  p.stages = std::min<uint32_t>(kMaxStages, kRingBytes / (p.deep * (kATile + p.bt * 128)));
   const uint32_t tiles = p.ncol * p.ntok;
   p.ctas = p.cluster > 1 ? tiles * p.cluster : std::min(sms, tiles);
   p.tmem_cols = 32;
@@ -820,7 +827,7 @@ int set_up() {
   int rc = cuda_check(cudaGetDevice(&dev), "moe_adapter_matmul: device");
   if (rc) return rc;
   std::lock_guard<std::mutex> lock(mu);
-  if (dev < 64 && done[dev]) return SYMM_OK;
+  if (dev >= 0 && dev < 64 && done[dev]) return SYMM_OK;
   auto set = [&](const void* f, cudaFuncAttribute attr, int v) {
     if (!rc) rc = cuda_check(cudaFuncSetAttribute(f, attr, v), "moe_adapter_matmul: kernel set-up");
   };
@@ -830,14 +837,41 @@ int set_up() {
   // the same split of an SM's memory for both: changing it would wait for an idle SM
   set(product, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   set(ranks, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-  if (!rc && dev < 64) done[dev] = true;
+  if (!rc && dev >= 0 && dev < 64) done[dev] = true;
   return rc;
+}
+
+int resident_clusters(int fmt, uint32_t c) {
+  static std::mutex mu;
+  static int known[2][64][9] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+  std::lock_guard<std::mutex> lock(mu);
+  int& n = known[fmt][dev][c];
+  if (n) return n;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(c);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 1024 + kRingBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = fmt ? cudaOccupancyMaxActiveClusters(&n, adapter_kernel<1>, &cfg)
+                            : cudaOccupancyMaxActiveClusters(&n, adapter_kernel<0>, &cfg);
+  if (e != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = 0;
+    return std::max(1, sm_count() / (int)c / 2);  // a guess, not kept
+  }
+  return n;
 }
 
 template <int FMT>
 int launch(const Plan& p, const Maps& m, const AdapterArgs& a, cudaStream_t s) {
-  int rc = set_up<FMT>();
-  if (rc) return rc;
+  int rc = SYMM_OK;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
@@ -902,10 +936,12 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
                                "workspace 256-byte aligned, the rest to their elements");
     if (y == x || y == w || y == a || y == b)
       return fail(SYMM_EINVAL, "moe_adapter_matmul: y must not be an input");
-    const Plan p = plan_of(T, k, n, r);
     const int fmt = dtype == SYMM_DTYPE_BF16 ? 1 : 0;
+    rc = fmt ? set_up<1>() : set_up<0>();
+    if (rc) return rc;
+    const Plan p = plan_of(T, k, n, r, fmt);
     Maps m{};
-    rc = make_map(&m.w, w, fmt, (uint64_t)n, (uint64_t)k, 0, ldw, kBK);
+    rc = make_map(&m.w, w, fmt, (uint64_t)n, (uint64_t)k, 0, ldw, p.deep * kBK);
     if (!rc) rc = make_map(&m.x, x, fmt, (uint64_t)k, (uint64_t)T, 0, ldx, p.bt);
     if (!rc && R) {
       rc = make_map(&m.a, a, fmt, (uint64_t)r, (uint64_t)k, (uint64_t)R, (size_t)r, kBK);
@@ -923,6 +959,7 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
     g.scale = scale, g.ids = ids, g.y = y, g.ldy = ldy;
     g.T = (uint32_t)T, g.k = (uint32_t)k, g.n = (uint32_t)n, g.R = (uint32_t)R, g.r = (uint32_t)r;
     g.r16 = p.r16, g.bt = p.bt, g.ntok = p.ntok, g.ncol = p.ncol, g.ktiles = p.ktiles;
+    g.deep = p.deep, g.slices = p.slices;
     g.stages = p.stages, g.cluster = p.cluster, g.tmem_cols = p.tmem_cols;
     g.h = static_cast<uint16_t*>(workspace);
     g.rk_share = p.rk_share, g.rk_stages = p.rk_stages, g.rk_abytes = p.rk_abytes;

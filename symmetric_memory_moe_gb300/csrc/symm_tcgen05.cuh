@@ -25,10 +25,34 @@ __device__ __forceinline__ bool mbar_wait_ab(uint64_t* bar, uint32_t parity, uin
   for (uint64_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 255) == 255 &&
-        (ld_relaxed_u32(&ctl->abort) || globaltimer_ns() - t0 > budget_ns ||
-         it > max_iters))
+        (ld_relaxed_u32(&ctl->abort) || globaltimer_ns() - t0 > budget_ns || it > max_iters))
       return false;
   }
+}
+// The same by a converged warp, with one answer for all its lanes; the loop
+// with the clock stays out of line, off the path of a barrier that is ready.
+static __device__ __noinline__ bool mbar_wait_ab_slow(uint64_t* bar, uint32_t parity,
+                                                      uint64_t budget_ns, const Control* ctl) {
+  return mbar_wait_ab(bar, parity, budget_ns, ctl);
+}
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                               const Control* ctl) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
+         __all_sync(0xffffffffu, mbar_wait_ab_slow(bar, parity, budget_ns, ctl));
+}
+// True in one lane of a converged warp, the same one every time.  A role that
+// one thread would do runs in the whole warp instead, with only the issuing
+// instructions in the elected lane: the compiler then knows that loop
+// counters, barrier addresses and descriptors are the same in all lanes and
+// keeps them in uniform registers, where the instructions want them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z,
                                             uint64_t* bar) {
@@ -120,12 +144,12 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(const void* tile) {
 }
 
 // Shared-memory descriptor of an MN-major operand tile written by TMA in boxes
-// of 64 M- or N-elements (one 128-byte swizzled row) x 64 K-rows: 8-row K
-// groups are 1024 bytes apart, groups of 64 elements one box (64 * 128 bytes)
+// of 64 M- or N-elements (one 128-byte swizzled row) x 64 K-rows (or `box`
+// bytes): 8-row K groups are 1024 bytes apart, groups of 64 elements one box
 // apart.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(const void* tile) {
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(const void* tile, uint32_t box = 64 * 128) {
   const uint64_t addr = smem_addr(tile);
-  return ((addr & 0x3FFFFull) >> 4) | ((uint64_t)((64 * 128) >> 4) << 16) |
+  return ((addr & 0x3FFFFull) >> 4) | ((uint64_t)(box >> 4) << 16) |
          ((1024ull >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
