@@ -50,6 +50,16 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return s;
 }
 
+// The same with one barrier: `red` may be written again only after another
+// barrier of the block.
+__device__ __forceinline__ float block_sum_once(float v, float* red) {
+  v = warp_sum(v);
+  const int lane = threadIdx.x & 31, warps = (int)(blockDim.x >> 5);
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < warps ? red[lane] : 0.f);
+}
+
 inline size_t dtype_bytes(int dtype) { return dtype == SYMM_DTYPE_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) {
   return dtype == SYMM_DTYPE_F16 || dtype == SYMM_DTYPE_BF16 || dtype == SYMM_DTYPE_F32;

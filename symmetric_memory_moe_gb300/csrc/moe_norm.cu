@@ -106,11 +106,85 @@ struct Cols {
         if (at(c, i) < D) row[at(c, i)] = moe::from_f<T>(v[i]);
     }
   }
-  // chunk c of a float vector (any 4-byte alignment); `none` where it is NULL
+  // chunk c of a float vector; `none` where it is NULL
   __device__ __forceinline__ void vec(const float* p, int c, float none,
                                       float (&v)[kChunk]) const {
+    if constexpr (ALIGNED) {
+      const int o = at(c, 0);
+      if (p && o < D) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p + o));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p + o) + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      } else {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = p ? (at(c, i) < D ? p[at(c, i)] : 0.f) : none;
+        for (int i = 0; i < kChunk; ++i) v[i] = p ? 0.f : none;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) v[i] = p ? (at(c, i) < D ? p[at(c, i)] : 0.f) : none;
+    }
+  }
+};
+
+// cp.async of 16 bytes past L1, and its groups.
+__device__ __forceinline__ void copy16(uint32_t smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_group() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most n of this thread's newest groups are pending (n < 16).
+__device__ __forceinline__ void wait_group(int n) {
+#define MOE_WAIT(i) \
+  case i: asm volatile("cp.async.wait_group " #i ";" ::: "memory"); break;
+  switch (n) {
+    MOE_WAIT(1) MOE_WAIT(2) MOE_WAIT(3) MOE_WAIT(4) MOE_WAIT(5) MOE_WAIT(6) MOE_WAIT(7)
+    MOE_WAIT(8) MOE_WAIT(9) MOE_WAIT(10) MOE_WAIT(11) MOE_WAIT(12) MOE_WAIT(13) MOE_WAIT(14)
+    MOE_WAIT(15)
+    default: asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+#undef MOE_WAIT
+}
+
+// A ring of rows in shared memory in which a thread keeps its own columns
+// only: it copies them in (asynchronously, one group per row) and reads them
+// back itself, so nothing but its own groups is waited for, and rows of the
+// next tokens are on their way while a token is summed and normed.
+template <typename T, int CH>
+struct Ring {
+  static constexpr int kVec = (int)sizeof(T) * kChunk / 16;  // 16-byte vectors of a chunk
+  uint32_t base;  // of this thread's first vector
+  int D, rows;
+  __device__ __forceinline__ uint32_t at(int slot, int c, int v) const {
+    return base + (uint32_t)(((slot * CH + c) * kVec + v) * (int)blockDim.x) * 16u;
+  }
+  // starts the copy of `row` (nothing if NULL) as one group
+  __device__ __forceinline__ void fill(int slot, const T* row) const {
+    if (row) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int o = (c * (int)blockDim.x + (int)threadIdx.x) * kChunk;
+        if (o < D)
+#pragma unroll
+          for (int v = 0; v < kVec; ++v)
+            copy16(at(slot, c, v), reinterpret_cast<const uint4*>(row + o) + v);
+      }
+    }
+    commit_group();
+  }
+  __device__ __forceinline__ void read(int slot, int c, float (&f)[kChunk]) const {
+    uint4 raw[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(raw[v].x), "=r"(raw[v].y), "=r"(raw[v].z), "=r"(raw[v].w)
+                   : "r"(at(slot, c, v))
+                   : "memory");
+    const bool in = (c * (int)blockDim.x + (int)threadIdx.x) * kChunk < D;
+    const T* e = reinterpret_cast<const T*>(raw);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) f[i] = in ? moe::to_f(e[i]) : 0.f;
   }
 };
 
@@ -188,6 +262,108 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
     }
     if (a.rstd && threadIdx.x == 0) a.rstd[2 * t] = r1, a.rstd[2 * t + 1] = r2;
   }
+}
+
+// The forward pass on 16-byte aligned rows.  Bound by HBM: (k + 3) rows a
+// token.  The rows of up to `depth` - 1 slots ahead are in flight.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2)
+    norm_stream_kernel(const NormArgs a, const int depth) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[2][kMaxWarps];
+  const Cols<T, true> cols{a.D};
+  const Ring<T, CH> ring{(uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16u, a.D, depth};
+  const float mean = 1.f / (float)a.D;
+  const int items = a.k + 1;  // a token's rows, then its x (k = 0 without y)
+  // what is copied next: item fj of token ft into slot fs
+  size_t ft = blockIdx.x;
+  int fj = 0, fs = 0;
+  uint32_t have = 0;  // slots that hold a row
+  auto fill = [&]() {
+    const T* row = nullptr;
+    if (ft < (size_t)a.T) {
+      if (fj < a.k) {
+        const long long r = row_of(a.rows, a.yrows, ft * a.k + fj);
+        if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
+      } else {
+        row = static_cast<const T*>(a.x) + ft * a.ld;
+      }
+    }
+    ring.fill(fs, row);
+    have = row ? have | (1u << fs) : have & ~(1u << fs);
+    if (++fs == depth) fs = 0;
+    if (++fj == items) fj = 0, ft += gridDim.x;
+  };
+  for (int i = 0; i < depth; ++i) fill();
+  int s = 0;
+  for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
+    float z[CH][kChunk];
+    float r1 = 1.f, r2 = 1.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) z[c][i] = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
+      wait_group(depth - 1);
+      if ((have >> s) & 1) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          float v[kChunk];
+          ring.read(s, c, v);
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) z[c][i] = fmaf(w, v[i], z[c][i]);
+        }
+      }
+      fill();
+      if (++s == depth) s = 0;
+    }
+    if (a.w_post) {
+      float ss = 0.f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) ss = fmaf(z[c][i], z[c][i], ss);
+      r1 = 1.f / sqrtf(moe::block_sum_once(ss, red[0]) * mean + a.eps);
+    }
+    const float sc = (a.gate ? a.gate[t] : 1.f) * r1;
+    wait_group(depth - 1);
+    float ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float v[kChunk];
+      ring.read(s, c, v);
+      if (a.y) {
+        float res[kChunk], w[kChunk];
+        cols.vec(a.res, c, 1.f, res);
+        cols.vec(a.w_post, c, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) z[c][i] = fmaf(sc * w[i], z[c][i], res[i] * v[i]);
+        cols.store(static_cast<T*>(a.xo) + t * a.ld, c, z[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) z[c][i] = v[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) ss = fmaf(z[c][i], z[c][i], ss);
+    }
+    fill();
+    if (++s == depth) s = 0;
+    if (a.h) {
+      r2 = 1.f / sqrtf(moe::block_sum_once(ss, red[1]) * mean + a.eps);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float w[kChunk];
+        cols.vec(a.w_pre, c, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) w[i] *= z[c][i] * r2;
+        cols.store(static_cast<T*>(a.h) + t * a.ld, c, w);
+      }
+    }
+    if (a.rstd && threadIdx.x == 0) a.rstd[2 * t] = r1, a.rstd[2 * t + 1] = r2;
+    if (!a.w_post || !a.h) __syncthreads();  // `red` is free again (see block_sum_once)
+  }
+  wait_group(0);
 }
 
 template <typename T, bool ALIGNED, int CH>
@@ -325,6 +501,202 @@ __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackAr
     }
 }
 
+// The backward pass on 16-byte aligned rows, when the ring holds a whole
+// token: (2k + 5) rows through HBM a token, and Y read twice from shared memory
+// only -- for y, and for the inner products with it.
+template <typename T, int CH>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    norm_back_stream_kernel(const NormBackArgs a, const int depth) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float red[2][kMaxWarps];
+  __shared__ float dots[kMaxWarps][2 * SYMM_MOE_MAX_TOPK];  // <dn, Y_j>, <n, Y_j> per warp
+  const Cols<T, true> cols{a.D};
+  const Ring<T, CH> ring{(uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16u, a.D, depth};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const float mean = 1.f / (float)a.D;
+  float s_res[CH][kChunk], s_post[CH][kChunk], s_pre[CH][kChunk];
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) s_res[c][i] = s_post[c][i] = s_pre[c][i] = 0.f;
+  // a token's rows in the ring: dh, z, dxo, x, Y_0 ..
+  const int items = 4 + a.k;
+  size_t ft = blockIdx.x;
+  int fj = 0, fs = 0;
+  uint32_t have = 0;
+  auto fill = [&]() {
+    const T* row = nullptr;
+    if (ft < (size_t)a.T) {
+      const size_t o = ft * a.ld;
+      if (fj == 0) {
+        if (a.dh) row = static_cast<const T*>(a.dh) + o;
+      } else if (fj == 1) {
+        if (a.dh) row = static_cast<const T*>(a.y ? a.xo : a.x) + o;
+      } else if (fj == 2) {
+        if (a.dxo) row = static_cast<const T*>(a.dxo) + o;
+      } else if (fj == 3) {
+        if (a.dres) row = static_cast<const T*>(a.x) + o;
+      } else {
+        const long long r = row_of(a.rows, a.yrows, ft * a.k + (fj - 4));
+        if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
+      }
+    }
+    ring.fill(fs, row);
+    have = row ? have | (1u << fs) : have & ~(1u << fs);
+    if (++fs == depth) fs = 0;
+    if (++fj == items) fj = 0, ft += gridDim.x;
+  };
+  auto slot = [&](int s, int i) { return s + i < depth ? s + i : s + i - depth; };
+  for (int i = 0; i < depth; ++i) fill();
+  int s = 0;  // the token's first slot
+  for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
+    const float r1 = a.rstd[2 * t], r2 = a.rstd[2 * t + 1];
+    float mqz = 0.f;
+    wait_group(depth - 2);
+    if (a.dh) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float z[kChunk], q[kChunk], w[kChunk];
+        ring.read(s, c, q);
+        ring.read(slot(s, 1), c, z);
+        cols.vec(a.w_pre, c, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) mqz = fmaf(q[i] * w[i], z[i], mqz);
+      }
+      mqz = moe::block_sum_once(mqz, red[0]) * mean;
+    }
+    const float gate = a.gate ? a.gate[t] : 1.f;
+    float dn[CH][kChunk], n[CH][kChunk];  // dn holds dz first
+    wait_group(depth - 4);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (a.dxo) {
+        ring.read(slot(s, 2), c, dn[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) dn[c][i] = 0.f;
+      }
+      float w[kChunk];
+      if (a.dh) {
+        float z[kChunk], q[kChunk];
+        ring.read(s, c, q);
+        ring.read(slot(s, 1), c, z);
+        cols.vec(a.w_pre, c, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          const float zn = z[i] * r2;
+          s_pre[c][i] = fmaf(q[i], zn, s_pre[c][i]);
+          dn[c][i] += r2 * (q[i] * w[i] - zn * (r2 * mqz));
+        }
+      }
+      if (a.dres) {
+        float x[kChunk];
+        ring.read(slot(s, 3), c, x);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) s_res[c][i] = fmaf(dn[c][i], x[i], s_res[c][i]);
+      }
+      cols.vec(a.res, c, 1.f, w);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) w[i] *= dn[c][i];
+      cols.store(static_cast<T*>(a.dx) + t * a.ld, c, w);
+    }
+    for (int i = 0; i < 4; ++i) fill();
+    s = slot(s, 4);
+    if (!a.y) {
+      __syncthreads();  // `red` is free again
+      continue;
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) n[c][i] = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
+      wait_group(depth - 1 - j);
+      const int sj = slot(s, j);
+      if ((have >> sj) & 1)
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          float v[kChunk];
+          ring.read(sj, c, v);
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) n[c][i] = fmaf(w, v[i], n[c][i]);
+        }
+    }
+    float dgate = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[kChunk];
+      cols.vec(a.w_post, c, 1.f, w);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) {
+        n[c][i] *= r1;
+        const float g = gate * dn[c][i];
+        s_post[c][i] = fmaf(g, n[c][i], s_post[c][i]);
+        dgate = fmaf(dn[c][i] * w[i], n[c][i], dgate);
+        dn[c][i] = g * w[i];
+      }
+    }
+    dgate = moe::block_sum_once(dgate, red[1]);
+    const float mdn = a.w_post ? dgate * gate * mean : 0.f;
+    if (a.dgate && threadIdx.x == 0) a.dgate[t] = dgate;
+    for (int j = 0; j < a.k; ++j) {
+      const size_t at = t * a.k + j;
+      const long long r = row_of(a.rows, a.yrows, at);
+      const int sj = slot(s, j);
+      float p = 0.f, q = 0.f;
+      if (r >= 0) {
+        const float wr1 = (a.weights ? __ldg(a.weights + at) : 1.f) * r1;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          if (a.dweights) {
+            float v[kChunk];
+            ring.read(sj, c, v);
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) {
+              p = fmaf(dn[c][i], v[i], p);
+              q = fmaf(n[c][i], v[i], q);
+            }
+          }
+          float o[kChunk];
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i) o[i] = wr1 * (dn[c][i] - n[c][i] * mdn);
+          cols.store(static_cast<T*>(a.dy) + (size_t)r * a.ldy, c, o);
+        }
+      }
+      fill();  // into this row's slot, which is fs
+      if (a.dweights) {
+        p = moe::warp_sum(p);
+        q = moe::warp_sum(q);
+        if (lane == 0) dots[warp][2 * j] = p, dots[warp][2 * j + 1] = q;
+      }
+    }
+    s = slot(s, a.k);
+    __syncthreads();
+    if (a.dweights && (int)threadIdx.x < a.k) {
+      float p = 0.f, q = 0.f;
+      for (int w = 0; w < warps; ++w) {
+        p += dots[w][2 * threadIdx.x];
+        q += dots[w][2 * threadIdx.x + 1];
+      }
+      a.dweights[t * a.k + threadIdx.x] = r1 * (p - mdn * q);
+    }
+  }
+  wait_group(0);
+  float* part = a.part + (size_t)blockIdx.x * 3 * a.D;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      const int o = cols.at(c, i);
+      if (o < a.D) {
+        part[o] = s_res[c][i];
+        part[a.D + o] = s_post[c][i];
+        part[2 * (size_t)a.D + o] = s_pre[c][i];
+      }
+    }
+}
+
 // Adds the CTAs' column sums in their order.
 __global__ void norm_join_kernel(const float* part, int blocks, int D, float* dres, float* dw_post,
                                  float* dw_pre) {
@@ -345,9 +717,32 @@ Shape shape_of(int D) {
   const int ch = chunks <= 256 ? 1 : (chunks <= 1024 ? 2 : 4);
   return {ch, std::min(kMaxThreads, ((chunks + ch - 1) / ch + 31) / 32 * 32)};
 }
+// CTAs, at most: enough threads per SM to fill it.
 int grid_of(int T, int D) {
   const int per_sm = std::max(1, 1024 / shape_of(D).threads);
   return std::max(1, std::min(T, std::max(sm_count(), 1) * std::min(per_sm, 8)));
+}
+
+constexpr size_t kSmemPerSm = 227 * 1024;
+
+// Rows of the forward ring: as many as leave room for two CTAs per SM, 3 to 8;
+// 0: not even 3 fit.  Of the backward ring: a whole token and up to 4 rows of
+// the next; 0: a token does not fit.
+size_t ring_row(int D, size_t es) {
+  const Shape sh = shape_of(D);
+  return (size_t)sh.ch * sh.threads * kChunk * es;
+}
+int forward_depth(int D, size_t es) {
+  const size_t row = ring_row(D, es), most = kSmemPerSm - 2048;
+  const size_t two = (most / 2 - 1024) / row;
+  if (two >= 3) return (int)std::min<size_t>(two, 8);
+  const size_t one = (most - 1024) / row;
+  return one >= 3 ? (int)std::min<size_t>(one, 8) : 0;
+}
+int backward_depth(int D, size_t es, int k) {
+  const size_t fit = (kSmemPerSm - 8192) / ring_row(D, es);
+  const int want = std::min(16, 4 + k + 4);
+  return fit >= (size_t)(4 + k) && 4 + k <= 16 ? (int)std::min<size_t>(fit, want) : 0;
 }
 
 template <typename F>
@@ -386,6 +781,13 @@ bool all_aligned(size_t a, std::initializer_list<const void*> ps) {
   return true;
 }
 
+// Lets kernel f use `bytes` of dynamic shared memory.
+int allow_smem(const void* f, size_t bytes, const char* what) {
+  if (bytes <= 40 * 1024) return SYMM_OK;  // 48 KB with what the kernels hold statically
+  return cuda_check(
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes), what);
+}
+
 }  // namespace
 
 extern "C" int moe_block_norm_workspace(int T, int D, size_t* bytes) {
@@ -422,16 +824,28 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
         !all_aligned(4, {rows, weights, gate, res, w_post, w_pre, rstd}))
       return fail(SYMM_EINVAL, "moe_block_norm: a pointer is not aligned to its elements");
     const bool al = D % kChunk == 0 && all_aligned(16, {x, y, xo, h}) && ld * es % 16 == 0 &&
-                    (!y || ldy * es % 16 == 0);
+                    (!y || ldy * es % 16 == 0) && all_aligned(16, {res, w_post, w_pre});
     const NormArgs a{x, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre, eps,
                      T, D, k, xo, h, rstd};
     const Shape sh = shape_of(D);
     cudaStream_t s = as_stream(stream);
+    const int depth = al ? forward_depth(D, es) : 0;
+    const size_t ring = (size_t)depth * ring_row(D, es);
+    rc = SYMM_OK;
     dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
-      norm_kernel<decltype(t), decltype(b)::value, decltype(c)::value>
-          <<<(unsigned)grid_of(T, D), sh.threads, 0, s>>>(a);
+      using E = decltype(t);
+      constexpr int CH = decltype(c)::value;
+      if (depth) {
+        rc = allow_smem((const void*)norm_stream_kernel<E, CH>, ring, "moe_block_norm: set-up");
+        const int per_sm = (int)std::max<size_t>(
+            1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 1024)));
+        const int grid = std::max(1, std::min(T, std::max(sm_count(), 1) * per_sm));
+        if (!rc) norm_stream_kernel<E, CH><<<(unsigned)grid, sh.threads, ring, s>>>(a, depth);
+      } else {
+        norm_kernel<E, decltype(b)::value, CH><<<(unsigned)grid_of(T, D), sh.threads, 0, s>>>(a);
+      }
     });
-    return cuda_check(cudaGetLastError(), "moe_block_norm: launch");
+    return rc ? rc : cuda_check(cudaGetLastError(), "moe_block_norm: launch");
   });
 }
 
@@ -471,18 +885,32 @@ extern "C" int moe_block_norm_backward(
       return fail(SYMM_EINVAL,
                   "moe_block_norm_backward: a pointer is not aligned to its elements");
     const bool al = D % kChunk == 0 && all_aligned(16, {x, xo, y, dxo, dh, dx, dy}) &&
-                    ld * es % 16 == 0 && (!y || ldy * es % 16 == 0);
+                    ld * es % 16 == 0 && (!y || ldy * es % 16 == 0) &&
+                    all_aligned(16, {res, w_post, w_pre});
     const NormBackArgs a{dxo, dh, x, xo, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre,
                          rstd, T, D, k, dx, dy, dweights, dgate, dres, dw_post, dw_pre,
                          static_cast<float*>(workspace)};
     const Shape sh = shape_of(D);
-    const int grid = grid_of(T, D);
+    int grid = grid_of(T, D);
     cudaStream_t s = as_stream(stream);
+    const int depth = al ? backward_depth(D, es, k) : 0;
+    const size_t ring = (size_t)depth * ring_row(D, es);
+    rc = SYMM_OK;
     dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
-      norm_back_kernel<decltype(t), decltype(b)::value, decltype(c)::value>
-          <<<(unsigned)grid, sh.threads, 0, s>>>(a);
+      using E = decltype(t);
+      constexpr int CH = decltype(c)::value;
+      if (depth) {
+        rc = allow_smem((const void*)norm_back_stream_kernel<E, CH>, ring,
+                        "moe_block_norm_backward: set-up");
+        const int per_sm = (int)std::max<size_t>(
+            1, std::min<size_t>(512 / sh.threads, (kSmemPerSm - 2048) / (ring + 6144)));
+        grid = std::min(grid, std::max(sm_count(), 1) * per_sm);
+        if (!rc) norm_back_stream_kernel<E, CH><<<(unsigned)grid, sh.threads, ring, s>>>(a, depth);
+      } else {
+        norm_back_kernel<E, decltype(b)::value, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
+      }
     });
-    rc = cuda_check(cudaGetLastError(), "moe_block_norm_backward: launch");
+    if (!rc) rc = cuda_check(cudaGetLastError(), "moe_block_norm_backward: launch");
     if (rc || (!dres && !dw_post && !dw_pre)) return rc;
     norm_join_kernel<<<(unsigned)((3 * D + 255) / 256), 256, 0, s>>>(a.part, grid, D, dres, dw_post,
                                                                     dw_pre);
