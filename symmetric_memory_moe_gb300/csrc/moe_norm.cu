@@ -134,6 +134,10 @@ __device__ __forceinline__ void copy16(uint32_t smem, const void* src) {
 __device__ __forceinline__ void commit_group() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
+template <int N>
+__device__ __forceinline__ void wait_groups() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // Waits until at most n of this thread's newest groups are pending (n < 16).
 __device__ __forceinline__ void wait_group(int n) {
 #define MOE_WAIT(i) \
@@ -147,33 +151,112 @@ __device__ __forceinline__ void wait_group(int n) {
 #undef MOE_WAIT
 }
 
-// A ring of rows in shared memory in which a thread keeps its own columns
-// only: it copies them in (asynchronously, one group per row) and reads them
-// back itself, so nothing but its own groups is waited for, and rows of the
-// next tokens are on their way while a token is summed and normed.
+// Two floats in one 64-bit register pair: sm_103a does a multiply-add of both
+// in one instruction, and these kernels are bound by what they can issue
+// before they are bound by HBM.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 mk(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 mk(float both) { return mk(both, both); }
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  return lo + hi;
+}
+
+constexpr int kPairs = kChunk / 2;
+
+// 16 bytes of T as pairs of floats, and back.
+template <typename T>
+__device__ __forceinline__ F2 unpack(uint32_t x);
+template <>
+__device__ __forceinline__ F2 unpack<__nv_bfloat16>(uint32_t x) {
+  return mk(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ F2 unpack<__half>(uint32_t x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return mk(f.x, f.y);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack(F2 a);
+template <>
+__device__ __forceinline__ uint32_t pack<__nv_bfloat16>(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack<__half>(F2 a) {
+  float lo, hi;
+  split(a, lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A thread's columns of aligned rows, and a ring of rows in shared memory in
+// which the thread keeps these columns only: it copies them in
+// (asynchronously, one group per row) and reads them back itself, so nothing
+// but its own groups is waited for, and rows of the next tokens are on their
+// way while a token is summed and normed.  The chunks past D are 0.
 template <typename T, int CH>
 struct Ring {
   static constexpr int kVec = (int)sizeof(T) * kChunk / 16;  // 16-byte vectors of a chunk
-  uint32_t base;  // of this thread's first vector
-  int D, rows;
+  uint32_t base, slot_bytes;  // of this thread's first vector; of a row in shared memory
+  int o[CH];                  // first column of each chunk
+  bool in[CH];                // ... lies in the row
+  __device__ __forceinline__ Ring(const void* smem, int D, int depth) {
+    base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16u;
+    slot_bytes = (uint32_t)(CH * kVec * (int)blockDim.x) * 16u;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      o[c] = (c * (int)blockDim.x + (int)threadIdx.x) * kChunk;
+      in[c] = o[c] < D;
+    }
+    for (int s = 0; s < depth; ++s)
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (!in[c])
+#pragma unroll
+          for (int v = 0; v < kVec; ++v)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(s, c, v)), "r"(0)
+                         : "memory");
+  }
   __device__ __forceinline__ uint32_t at(int slot, int c, int v) const {
-    return base + (uint32_t)(((slot * CH + c) * kVec + v) * (int)blockDim.x) * 16u;
+    return base + (uint32_t)slot * slot_bytes + (uint32_t)((c * kVec + v) * (int)blockDim.x) * 16u;
   }
   // starts the copy of `row` (nothing if NULL) as one group
   __device__ __forceinline__ void fill(int slot, const T* row) const {
     if (row) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int o = (c * (int)blockDim.x + (int)threadIdx.x) * kChunk;
-        if (o < D)
+      for (int c = 0; c < CH; ++c)
+        if (in[c])
 #pragma unroll
           for (int v = 0; v < kVec; ++v)
-            copy16(at(slot, c, v), reinterpret_cast<const uint4*>(row + o) + v);
-      }
+            copy16(at(slot, c, v), reinterpret_cast<const uint4*>(row + o[c]) + v);
     }
     commit_group();
   }
-  __device__ __forceinline__ void read(int slot, int c, float (&f)[kChunk]) const {
+  __device__ __forceinline__ void read(int slot, int c, F2 (&f)[kPairs]) const {
     uint4 raw[kVec];
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
@@ -181,10 +264,40 @@ struct Ring {
                    : "=r"(raw[v].x), "=r"(raw[v].y), "=r"(raw[v].z), "=r"(raw[v].w)
                    : "r"(at(slot, c, v))
                    : "memory");
-    const bool in = (c * (int)blockDim.x + (int)threadIdx.x) * kChunk < D;
-    const T* e = reinterpret_cast<const T*>(raw);
+    if constexpr (kVec == 1) {
+      f[0] = unpack<T>(raw[0].x), f[1] = unpack<T>(raw[0].y);
+      f[2] = unpack<T>(raw[0].z), f[3] = unpack<T>(raw[0].w);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) f[i] = in ? moe::to_f(e[i]) : 0.f;
+      for (int v = 0; v < kVec; ++v) {
+        f[2 * v] = mk(__uint_as_float(raw[v].x), __uint_as_float(raw[v].y));
+        f[2 * v + 1] = mk(__uint_as_float(raw[v].z), __uint_as_float(raw[v].w));
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* row, int c, const F2 (&f)[kPairs]) const {
+    if (!in[c]) return;
+    uint4* p = reinterpret_cast<uint4*>(row + o[c]);
+    if constexpr (kVec == 1) {
+      *p = make_uint4(pack<T>(f[0]), pack<T>(f[1]), pack<T>(f[2]), pack<T>(f[3]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        *reinterpret_cast<ulonglong2*>(p + v) = make_ulonglong2(f[2 * v].v, f[2 * v + 1].v);
+    }
+  }
+  // chunk c of a float vector; `none` where it is NULL
+  __device__ __forceinline__ void vec(const float* p, int c, float none, F2 (&f)[kPairs]) const {
+    if (p && in[c]) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(p + o[c]) + v);
+        f[2 * v].v = x.x, f[2 * v + 1].v = x.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) f[i] = mk(none);
+    }
   }
 };
 
@@ -192,6 +305,17 @@ struct Ring {
 __device__ __forceinline__ long long row_of(const int32_t* rows, size_t yrows, size_t slot) {
   const long long r = rows ? (long long)rows[slot] : (long long)slot;
   return r >= 0 && r < (long long)yrows ? r : -1;
+}
+
+// Token t's slots, one per lane: the row (-1: none) and the weight.
+template <typename A>
+__device__ __forceinline__ int lane_row(const A& a, size_t t, int lane) {
+  if (t >= (size_t)a.T || lane >= a.k) return -1;
+  return (int)row_of(a.rows, a.yrows, t * a.k + lane);
+}
+template <typename A>
+__device__ __forceinline__ float lane_weight(const A& a, size_t t, int lane) {
+  return t < (size_t)a.T && lane < a.k && a.weights ? a.weights[t * a.k + lane] : 1.f;
 }
 
 // y = sum_j w_j Y_j of chunk c, in slot order
@@ -265,105 +389,113 @@ __global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
 }
 
 // The forward pass on 16-byte aligned rows.  Bound by HBM: (k + 3) rows a
-// token.  The rows of up to `depth` - 1 slots ahead are in flight.
-template <typename T, int CH>
-__global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2)
-    norm_stream_kernel(const NormArgs a, const int depth) {
+// token.  The next DEPTH - 1 rows are in flight.
+template <typename T, int CH, int DEPTH>
+__global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2) norm_stream_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
-  const Cols<T, true> cols{a.D};
-  const Ring<T, CH> ring{(uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16u, a.D, depth};
+  const Ring<T, CH> ring(smem, a.D, DEPTH);
+  const int lane = threadIdx.x & 31;
   const float mean = 1.f / (float)a.D;
-  const int items = a.k + 1;  // a token's rows, then its x (k = 0 without y)
-  // what is copied next: item fj of token ft into slot fs
+  const size_t step = gridDim.x;
+  // What is copied next: row fj of token ft (its k rows, then its x) into slot
+  // fs; the token's row numbers, and those of the one after it, in the lanes.
   size_t ft = blockIdx.x;
-  int fj = 0, fs = 0;
+  int fj = 0, fs = 0, frow = lane_row(a, ft, lane), frow2 = lane_row(a, ft + step, lane);
   uint32_t have = 0;  // slots that hold a row
   auto fill = [&]() {
     const T* row = nullptr;
-    if (ft < (size_t)a.T) {
-      if (fj < a.k) {
-        const long long r = row_of(a.rows, a.yrows, ft * a.k + fj);
-        if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
-      } else {
-        row = static_cast<const T*>(a.x) + ft * a.ld;
-      }
+    if (fj < a.k) {
+      const int r = __shfl_sync(0xffffffffu, frow, fj);
+      if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
+      ++fj;
+    } else {
+      if (ft < (size_t)a.T) row = static_cast<const T*>(a.x) + ft * a.ld;
+      fj = 0;
+      ft += step;
+      frow = frow2;
+      frow2 = lane_row(a, ft + step, lane);
     }
     ring.fill(fs, row);
     have = row ? have | (1u << fs) : have & ~(1u << fs);
-    if (++fs == depth) fs = 0;
-    if (++fj == items) fj = 0, ft += gridDim.x;
+    if (++fs == DEPTH) fs = 0;
   };
-  for (int i = 0; i < depth; ++i) fill();
+  for (int i = 0; i < DEPTH; ++i) fill();
   int s = 0;
-  for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
-    float z[CH][kChunk];
+  float weight = lane_weight(a, blockIdx.x, lane);
+  for (size_t t = blockIdx.x; t < (size_t)a.T; t += step) {
+    const float weight2 = lane_weight(a, t + step, lane);
+    const float gate = a.gate ? __ldg(a.gate + t) : 1.f;
+    F2 z[CH][kPairs];
     float r1 = 1.f, r2 = 1.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) z[c][i] = 0.f;
+      for (int i = 0; i < kPairs; ++i) z[c][i] = mk(0.f);
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
-      const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
-      wait_group(depth - 1);
+      const F2 w = mk(__shfl_sync(0xffffffffu, weight, j));
+      wait_groups<DEPTH - 1>();
       if ((have >> s) & 1) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          float v[kChunk];
+          F2 v[kPairs];
           ring.read(s, c, v);
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) z[c][i] = fmaf(w, v[i], z[c][i]);
+          for (int i = 0; i < kPairs; ++i) z[c][i] = fma2(w, v[i], z[c][i]);
         }
       }
       fill();
-      if (++s == depth) s = 0;
+      if (++s == DEPTH) s = 0;
     }
+    weight = weight2;
     if (a.w_post) {
-      float ss = 0.f;
+      F2 ss = mk(0.f);
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) ss = fmaf(z[c][i], z[c][i], ss);
-      r1 = 1.f / sqrtf(moe::block_sum_once(ss, red[0]) * mean + a.eps);
+        for (int i = 0; i < kPairs; ++i) ss = fma2(z[c][i], z[c][i], ss);
+      r1 = 1.f / sqrtf(moe::block_sum_once(sum2(ss), red[0]) * mean + a.eps);
     }
-    const float sc = (a.gate ? a.gate[t] : 1.f) * r1;
-    wait_group(depth - 1);
-    float ss = 0.f;
+    const F2 sc = mk(gate * r1);
+    wait_groups<DEPTH - 1>();
+    F2 ss = mk(0.f);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float v[kChunk];
+      F2 v[kPairs];
       ring.read(s, c, v);
       if (a.y) {
-        float res[kChunk], w[kChunk];
-        cols.vec(a.res, c, 1.f, res);
-        cols.vec(a.w_post, c, 1.f, w);
+        F2 res[kPairs], w[kPairs];
+        ring.vec(a.res, c, 1.f, res);
+        ring.vec(a.w_post, c, 1.f, w);
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) z[c][i] = fmaf(sc * w[i], z[c][i], res[i] * v[i]);
-        cols.store(static_cast<T*>(a.xo) + t * a.ld, c, z[c]);
+        for (int i = 0; i < kPairs; ++i)
+          z[c][i] = fma2(mul2(sc, w[i]), z[c][i], mul2(res[i], v[i]));
+        ring.store(static_cast<T*>(a.xo) + t * a.ld, c, z[c]);
       } else {
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) z[c][i] = v[i];
+        for (int i = 0; i < kPairs; ++i) z[c][i] = v[i];
       }
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) ss = fmaf(z[c][i], z[c][i], ss);
+      for (int i = 0; i < kPairs; ++i) ss = fma2(z[c][i], z[c][i], ss);
     }
     fill();
-    if (++s == depth) s = 0;
+    if (++s == DEPTH) s = 0;
     if (a.h) {
-      r2 = 1.f / sqrtf(moe::block_sum_once(ss, red[1]) * mean + a.eps);
+      r2 = 1.f / sqrtf(moe::block_sum_once(sum2(ss), red[1]) * mean + a.eps);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float w[kChunk];
-        cols.vec(a.w_pre, c, 1.f, w);
+        F2 w[kPairs];
+        ring.vec(a.w_pre, c, 1.f, w);
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) w[i] *= z[c][i] * r2;
-        cols.store(static_cast<T*>(a.h) + t * a.ld, c, w);
+        for (int i = 0; i < kPairs; ++i) w[i] = mul2(w[i], mul2(z[c][i], mk(r2)));
+        ring.store(static_cast<T*>(a.h) + t * a.ld, c, w);
       }
     }
     if (a.rstd && threadIdx.x == 0) a.rstd[2 * t] = r1, a.rstd[2 * t + 1] = r2;
     if (!a.w_post || !a.h) __syncthreads();  // `red` is free again (see block_sum_once)
   }
-  wait_group(0);
+  wait_groups<0>();
 }
 
 template <typename T, bool ALIGNED, int CH>
@@ -509,190 +641,202 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     norm_back_stream_kernel(const NormBackArgs a, const int depth) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
-  __shared__ float dots[kMaxWarps][2 * SYMM_MOE_MAX_TOPK];  // <dn, Y_j>, <n, Y_j> per warp
-  const Cols<T, true> cols{a.D};
-  const Ring<T, CH> ring{(uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16u, a.D, depth};
+  __shared__ float dots[kMaxWarps][SYMM_MOE_MAX_TOPK];  // <dy / r1, Y_j> per warp
+  const Ring<T, CH> ring(smem, a.D, depth);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const float mean = 1.f / (float)a.D;
-  float s_res[CH][kChunk], s_post[CH][kChunk], s_pre[CH][kChunk];
+  const size_t step = gridDim.x;
+  F2 s_res[CH][kPairs], s_post[CH][kPairs], s_pre[CH][kPairs];
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) s_res[c][i] = s_post[c][i] = s_pre[c][i] = 0.f;
+    for (int i = 0; i < kPairs; ++i) s_res[c][i] = s_post[c][i] = s_pre[c][i] = mk(0.f);
   // a token's rows in the ring: dh, z, dxo, x, Y_0 ..
-  const int items = 4 + a.k;
   size_t ft = blockIdx.x;
-  int fj = 0, fs = 0;
+  int fj = 0, fs = 0, frow = lane_row(a, ft, lane), frow2 = lane_row(a, ft + step, lane);
   uint32_t have = 0;
   auto fill = [&]() {
     const T* row = nullptr;
-    if (ft < (size_t)a.T) {
-      const size_t o = ft * a.ld;
-      if (fj == 0) {
-        if (a.dh) row = static_cast<const T*>(a.dh) + o;
-      } else if (fj == 1) {
-        if (a.dh) row = static_cast<const T*>(a.y ? a.xo : a.x) + o;
-      } else if (fj == 2) {
-        if (a.dxo) row = static_cast<const T*>(a.dxo) + o;
-      } else if (fj == 3) {
-        if (a.dres) row = static_cast<const T*>(a.x) + o;
-      } else {
-        const long long r = row_of(a.rows, a.yrows, ft * a.k + (fj - 4));
-        if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
-      }
+    if (fj >= 4) {
+      const int r = __shfl_sync(0xffffffffu, frow, fj - 4);
+      if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
+    } else if (ft < (size_t)a.T) {
+      const void* p = fj == 0   ? a.dh
+                      : fj == 1 ? (a.dh ? (a.y ? a.xo : a.x) : nullptr)
+                      : fj == 2 ? a.dxo
+                                : (a.dres ? a.x : nullptr);
+      if (p) row = static_cast<const T*>(p) + ft * a.ld;
     }
     ring.fill(fs, row);
     have = row ? have | (1u << fs) : have & ~(1u << fs);
     if (++fs == depth) fs = 0;
-    if (++fj == items) fj = 0, ft += gridDim.x;
+    if (++fj == 4 + a.k) {
+      fj = 0;
+      ft += step;
+      frow = frow2;
+      frow2 = lane_row(a, ft + step, lane);
+    }
   };
   auto slot = [&](int s, int i) { return s + i < depth ? s + i : s + i - depth; };
   for (int i = 0; i < depth; ++i) fill();
   int s = 0;  // the token's first slot
-  for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
-    const float r1 = a.rstd[2 * t], r2 = a.rstd[2 * t + 1];
-    float mqz = 0.f;
-    wait_group(depth - 2);
+  float weight = lane_weight(a, blockIdx.x, lane);
+  int row = lane_row(a, blockIdx.x, lane);
+  float r1 = a.rstd[2 * (size_t)blockIdx.x], r2 = a.rstd[2 * (size_t)blockIdx.x + 1];
+  for (size_t t = blockIdx.x; t < (size_t)a.T; t += step) {
+    // the next token's, on their way
+    const float weight2 = lane_weight(a, t + step, lane);
+    const int row2 = lane_row(a, t + step, lane);
+    const size_t tn = t + step < (size_t)a.T ? t + step : t;
+    const float r1n = __ldg(a.rstd + 2 * tn), r2n = __ldg(a.rstd + 2 * tn + 1);
+    const float gate = a.gate ? __ldg(a.gate + t) : 1.f;
+    F2 dn[CH][kPairs];  // dz, then dn, then dy / r1
     if (a.dh) {
+      F2 z[CH][kPairs], q[CH][kPairs];  // z r2, and dh wpre
+      F2 m = mk(0.f);
+      wait_group(depth - 2);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float z[kChunk], q[kChunk], w[kChunk];
-        ring.read(s, c, q);
-        ring.read(slot(s, 1), c, z);
-        cols.vec(a.w_pre, c, 1.f, w);
+        F2 w[kPairs];
+        ring.read(s, c, q[c]);
+        ring.read(slot(s, 1), c, z[c]);
+        ring.vec(a.w_pre, c, 1.f, w);
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) mqz = fmaf(q[i] * w[i], z[i], mqz);
+        for (int i = 0; i < kPairs; ++i) {
+          z[c][i] = mul2(z[c][i], mk(r2));
+          s_pre[c][i] = fma2(q[c][i], z[c][i], s_pre[c][i]);
+          q[c][i] = mul2(q[c][i], w[i]);
+          m = fma2(q[c][i], z[c][i], m);
+        }
       }
-      mqz = moe::block_sum_once(mqz, red[0]) * mean;
+      const float mqz = -moe::block_sum_once(sum2(m), red[0]) * mean;
+      wait_group(depth - 3);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (a.dxo) {
+          ring.read(slot(s, 2), c, dn[c]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) dn[c][i] = mk(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+          dn[c][i] = fma2(mk(r2), fma2(z[c][i], mk(mqz), q[c][i]), dn[c][i]);
+      }
+    } else {
+      wait_group(depth - 3);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) ring.read(slot(s, 2), c, dn[c]);
     }
-    const float gate = a.gate ? a.gate[t] : 1.f;
-    float dn[CH][kChunk], n[CH][kChunk];  // dn holds dz first
     wait_group(depth - 4);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (a.dxo) {
-        ring.read(slot(s, 2), c, dn[c]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) dn[c][i] = 0.f;
-      }
-      float w[kChunk];
-      if (a.dh) {
-        float z[kChunk], q[kChunk];
-        ring.read(s, c, q);
-        ring.read(slot(s, 1), c, z);
-        cols.vec(a.w_pre, c, 1.f, w);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-          const float zn = z[i] * r2;
-          s_pre[c][i] = fmaf(q[i], zn, s_pre[c][i]);
-          dn[c][i] += r2 * (q[i] * w[i] - zn * (r2 * mqz));
-        }
-      }
       if (a.dres) {
-        float x[kChunk];
+        F2 x[kPairs];
         ring.read(slot(s, 3), c, x);
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) s_res[c][i] = fmaf(dn[c][i], x[i], s_res[c][i]);
+        for (int i = 0; i < kPairs; ++i) s_res[c][i] = fma2(dn[c][i], x[i], s_res[c][i]);
       }
-      cols.vec(a.res, c, 1.f, w);
+      F2 w[kPairs];
+      ring.vec(a.res, c, 1.f, w);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) w[i] *= dn[c][i];
-      cols.store(static_cast<T*>(a.dx) + t * a.ld, c, w);
+      for (int i = 0; i < kPairs; ++i) w[i] = mul2(w[i], dn[c][i]);
+      ring.store(static_cast<T*>(a.dx) + t * a.ld, c, w);
     }
+#pragma unroll 1
     for (int i = 0; i < 4; ++i) fill();
     s = slot(s, 4);
-    if (!a.y) {
-      __syncthreads();  // `red` is free again
-      continue;
-    }
+    if (a.y) {
+      F2 n[CH][kPairs];
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) n[c][i] = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      const float w = a.weights ? __ldg(a.weights + t * a.k + j) : 1.f;
-      wait_group(depth - 1 - j);
-      const int sj = slot(s, j);
-      if ((have >> sj) & 1)
+        for (int i = 0; i < kPairs; ++i) n[c][i] = mk(0.f);
+#pragma unroll 1
+      for (int j = 0; j < a.k; ++j) {
+        const F2 w = mk(__shfl_sync(0xffffffffu, weight, j));
+        wait_group(depth - 1 - j);
+        const int sj = slot(s, j);
+        if ((have >> sj) & 1)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          float v[kChunk];
-          ring.read(sj, c, v);
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) n[c][i] = fmaf(w, v[i], n[c][i]);
-        }
-    }
-    float dgate = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float w[kChunk];
-      cols.vec(a.w_post, c, 1.f, w);
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        n[c][i] *= r1;
-        const float g = gate * dn[c][i];
-        s_post[c][i] = fmaf(g, n[c][i], s_post[c][i]);
-        dgate = fmaf(dn[c][i] * w[i], n[c][i], dgate);
-        dn[c][i] = g * w[i];
-      }
-    }
-    dgate = moe::block_sum_once(dgate, red[1]);
-    const float mdn = a.w_post ? dgate * gate * mean : 0.f;
-    if (a.dgate && threadIdx.x == 0) a.dgate[t] = dgate;
-    for (int j = 0; j < a.k; ++j) {
-      const size_t at = t * a.k + j;
-      const long long r = row_of(a.rows, a.yrows, at);
-      const int sj = slot(s, j);
-      float p = 0.f, q = 0.f;
-      if (r >= 0) {
-        const float wr1 = (a.weights ? __ldg(a.weights + at) : 1.f) * r1;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if (a.dweights) {
-            float v[kChunk];
+          for (int c = 0; c < CH; ++c) {
+            F2 v[kPairs];
             ring.read(sj, c, v);
 #pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-              p = fmaf(dn[c][i], v[i], p);
-              q = fmaf(n[c][i], v[i], q);
-            }
+            for (int i = 0; i < kPairs; ++i) n[c][i] = fma2(w, v[i], n[c][i]);
           }
-          float o[kChunk];
+      }
+      F2 dg = mk(0.f);
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) o[i] = wr1 * (dn[c][i] - n[c][i] * mdn);
-          cols.store(static_cast<T*>(a.dy) + (size_t)r * a.ldy, c, o);
+      for (int c = 0; c < CH; ++c) {
+        F2 w[kPairs];
+        ring.vec(a.w_post, c, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          n[c][i] = mul2(n[c][i], mk(r1));
+          const F2 d = mul2(dn[c][i], w[i]);
+          dg = fma2(d, n[c][i], dg);
+          s_post[c][i] = fma2(mul2(mk(gate), dn[c][i]), n[c][i], s_post[c][i]);
+          dn[c][i] = mul2(mk(gate), d);
         }
       }
-      fill();  // into this row's slot, which is fs
-      if (a.dweights) {
-        p = moe::warp_sum(p);
-        q = moe::warp_sum(q);
-        if (lane == 0) dots[warp][2 * j] = p, dots[warp][2 * j + 1] = q;
+      const float dgate = moe::block_sum_once(sum2(dg), red[1]);
+      if (a.dgate && threadIdx.x == 0) a.dgate[t] = dgate;
+      if (a.w_post) {  // the norm's part: dy / r1 = dn - n mean(dn n)
+        const F2 m = mk(-dgate * gate * mean);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) dn[c][i] = fma2(n[c][i], m, dn[c][i]);
       }
+#pragma unroll 1
+      for (int j = 0; j < a.k; ++j) {
+        const int r = __shfl_sync(0xffffffffu, row, j);
+        const F2 wr1 = mk(__shfl_sync(0xffffffffu, weight, j) * r1);
+        const int sj = slot(s, j);
+        F2 p = mk(0.f);
+        if (r >= 0) {
+          T* out = static_cast<T*>(a.dy) + (size_t)r * a.ldy;
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            F2 v[kPairs], d[kPairs];
+            if (a.dweights) {
+              ring.read(sj, c, v);
+#pragma unroll
+              for (int i = 0; i < kPairs; ++i) p = fma2(dn[c][i], v[i], p);
+            }
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) d[i] = mul2(wr1, dn[c][i]);
+            ring.store(out, c, d);
+          }
+        }
+        fill();  // into this row's slot, which is fs
+        if (a.dweights) {
+          const float q = moe::warp_sum(sum2(p));
+          if (lane == 0) dots[warp][j] = q;
+        }
+      }
+      s = slot(s, a.k);
     }
-    s = slot(s, a.k);
-    __syncthreads();
+    __syncthreads();  // dots are complete; `red` is free again
     if (a.dweights && (int)threadIdx.x < a.k) {
-      float p = 0.f, q = 0.f;
-      for (int w = 0; w < warps; ++w) {
-        p += dots[w][2 * threadIdx.x];
-        q += dots[w][2 * threadIdx.x + 1];
-      }
-      a.dweights[t * a.k + threadIdx.x] = r1 * (p - mdn * q);
+      float p = 0.f;
+      for (int w = 0; w < warps; ++w) p += dots[w][threadIdx.x];
+      a.dweights[t * a.k + threadIdx.x] = r1 * p;
     }
+    weight = weight2, row = row2, r1 = r1n, r2 = r2n;
   }
   wait_group(0);
   float* part = a.part + (size_t)blockIdx.x * 3 * a.D;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
+    if (ring.in[c]) {
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      const int o = cols.at(c, i);
-      if (o < a.D) {
-        part[o] = s_res[c][i];
-        part[a.D + o] = s_post[c][i];
-        part[2 * (size_t)a.D + o] = s_pre[c][i];
+      for (int i = 0; i < kPairs; ++i) {
+        float* o = part + ring.o[c] + 2 * i;
+        split(s_res[c][i], o[0], o[1]);
+        split(s_post[c][i], o[a.D], o[a.D + 1]);
+        split(s_pre[c][i], o[2 * (size_t)a.D], o[2 * (size_t)a.D + 1]);
       }
     }
 }
@@ -725,19 +869,17 @@ int grid_of(int T, int D) {
 
 constexpr size_t kSmemPerSm = 227 * 1024;
 
-// Rows of the forward ring: as many as leave room for two CTAs per SM, 3 to 8;
-// 0: not even 3 fit.  Of the backward ring: a whole token and up to 4 rows of
-// the next; 0: a token does not fit.
+// Rows of the forward ring: 7 with two CTAs per SM, else 3; 0: not even 3 fit.
+// Of the backward ring: a whole token and up to 4 rows of the next; 0: a token
+// does not fit.
 size_t ring_row(int D, size_t es) {
   const Shape sh = shape_of(D);
   return (size_t)sh.ch * sh.threads * kChunk * es;
 }
 int forward_depth(int D, size_t es) {
-  const size_t row = ring_row(D, es), most = kSmemPerSm - 2048;
-  const size_t two = (most / 2 - 1024) / row;
-  if (two >= 3) return (int)std::min<size_t>(two, 8);
-  const size_t one = (most - 1024) / row;
-  return one >= 3 ? (int)std::min<size_t>(one, 8) : 0;
+  const size_t row = ring_row(D, es);
+  if (7 * row <= kSmemPerSm / 2 - 2048) return 7;
+  return 3 * row <= kSmemPerSm - 2048 ? 3 : 0;
 }
 int backward_depth(int D, size_t es, int k) {
   const size_t fit = (kSmemPerSm - 8192) / ring_row(D, es);
@@ -836,11 +978,12 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
       using E = decltype(t);
       constexpr int CH = decltype(c)::value;
       if (depth) {
-        rc = allow_smem((const void*)norm_stream_kernel<E, CH>, ring, "moe_block_norm: set-up");
+        const auto kernel = depth == 7 ? norm_stream_kernel<E, CH, 7> : norm_stream_kernel<E, CH, 3>;
+        rc = allow_smem((const void*)kernel, ring, "moe_block_norm: set-up");
         const int per_sm = (int)std::max<size_t>(
             1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 1024)));
         const int grid = std::max(1, std::min(T, std::max(sm_count(), 1) * per_sm));
-        if (!rc) norm_stream_kernel<E, CH><<<(unsigned)grid, sh.threads, ring, s>>>(a, depth);
+        if (!rc) kernel<<<(unsigned)grid, sh.threads, ring, s>>>(a);
       } else {
         norm_kernel<E, decltype(b)::value, CH><<<(unsigned)grid_of(T, D), sh.threads, 0, s>>>(a);
       }
