@@ -183,6 +183,7 @@ __device__ __forceinline__ float sum2(F2 a) {
 }
 
 constexpr int kPairs = kChunk / 2;
+constexpr int kRows = 4;  // rows of Y handled together in the backward pass
 
 // 16 bytes of T as pairs of floats, and back.
 template <typename T>
@@ -651,15 +652,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) s_res[c][i] = s_post[c][i] = s_pre[c][i] = mk(0.f);
-  // a token's rows in the ring: dh, z, dxo, x, Y_0 ..
+  // A token's rows in the ring: dh, z, dxo, x, Y_0 ..  Copied next: item fj of
+  // token ft, into slot fs.
   size_t ft = blockIdx.x;
   int fj = 0, fs = 0, frow = lane_row(a, ft, lane), frow2 = lane_row(a, ft + step, lane);
-  uint32_t have = 0;
+  uint32_t have = 0;  // slots that hold a row of Y
   auto fill = [&]() {
     const T* row = nullptr;
     if (fj >= 4) {
       const int r = __shfl_sync(0xffffffffu, frow, fj - 4);
       if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
+      have = r >= 0 ? have | (1u << fs) : have & ~(1u << fs);
     } else if (ft < (size_t)a.T) {
       const void* p = fj == 0   ? a.dh
                       : fj == 1 ? (a.dh ? (a.y ? a.xo : a.x) : nullptr)
@@ -668,7 +671,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       if (p) row = static_cast<const T*>(p) + ft * a.ld;
     }
     ring.fill(fs, row);
-    have = row ? have | (1u << fs) : have & ~(1u << fs);
     if (++fs == depth) fs = 0;
     if (++fj == 4 + a.k) {
       fj = 0;
@@ -694,7 +696,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     if (a.dh) {
       F2 z[CH][kPairs], q[CH][kPairs];  // z r2, and dh wpre
       F2 m = mk(0.f);
-      wait_group(depth - 2);
+      wait_group(depth - 4);  // all four
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         F2 w[kPairs];
@@ -710,7 +712,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         }
       }
       const float mqz = -moe::block_sum_once(sum2(m), red[0]) * mean;
-      wait_group(depth - 3);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (a.dxo) {
@@ -724,11 +725,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           dn[c][i] = fma2(mk(r2), fma2(z[c][i], mk(mqz), q[c][i]), dn[c][i]);
       }
     } else {
-      wait_group(depth - 3);
+      wait_group(depth - 4);
 #pragma unroll
       for (int c = 0; c < CH; ++c) ring.read(slot(s, 2), c, dn[c]);
     }
-    wait_group(depth - 4);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (a.dres) {
@@ -752,20 +752,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) n[c][i] = mk(0.f);
+      wait_group(depth - a.k);  // all of the token's rows
 #pragma unroll 1
-      for (int j = 0; j < a.k; ++j) {
-        const F2 w = mk(__shfl_sync(0xffffffffu, weight, j));
-        wait_group(depth - 1 - j);
-        const int sj = slot(s, j);
-        if ((have >> sj) & 1)
+      for (int j0 = 0; j0 < a.k; j0 += kRows)
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            F2 v[kPairs];
-            ring.read(sj, c, v);
+        for (int jj = 0; jj < kRows; ++jj) {
+          const int j = j0 + jj, sj = slot(s, j);
+          if (j < a.k && ((have >> sj) & 1)) {
+            const F2 w = mk(__shfl_sync(0xffffffffu, weight, j));
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) n[c][i] = fma2(w, v[i], n[c][i]);
+            for (int c = 0; c < CH; ++c) {
+              F2 v[kPairs];
+              ring.read(sj, c, v);
+#pragma unroll
+              for (int i = 0; i < kPairs; ++i) n[c][i] = fma2(w, v[i], n[c][i]);
+            }
           }
-      }
+        }
       F2 dg = mk(0.f);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -790,30 +793,49 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           for (int i = 0; i < kPairs; ++i) dn[c][i] = fma2(n[c][i], m, dn[c][i]);
       }
 #pragma unroll 1
-      for (int j = 0; j < a.k; ++j) {
-        const int r = __shfl_sync(0xffffffffu, row, j);
-        const F2 wr1 = mk(__shfl_sync(0xffffffffu, weight, j) * r1);
-        const int sj = slot(s, j);
-        F2 p = mk(0.f);
-        if (r >= 0) {
-          T* out = static_cast<T*>(a.dy) + (size_t)r * a.ldy;
+      for (int j0 = 0; j0 < a.k; j0 += kRows) {
+        float q[kRows];
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            F2 v[kPairs], d[kPairs];
-            if (a.dweights) {
-              ring.read(sj, c, v);
+        for (int jj = 0; jj < kRows; ++jj) {
+          const int j = j0 + jj;
+          q[jj] = 0.f;
+          if (j < a.k) {
+            const int r = __shfl_sync(0xffffffffu, row, j);
+            if (r >= 0) {
+              const F2 wr1 = mk(__shfl_sync(0xffffffffu, weight, j) * r1);
+              T* out = static_cast<T*>(a.dy) + (size_t)r * a.ldy;
+              const int sj = slot(s, j);
+              F2 p = mk(0.f);
 #pragma unroll
-              for (int i = 0; i < kPairs; ++i) p = fma2(dn[c][i], v[i], p);
+              for (int c = 0; c < CH; ++c) {
+                F2 v[kPairs], d[kPairs];
+                if (a.dweights) {
+                  ring.read(sj, c, v);
+#pragma unroll
+                  for (int i = 0; i < kPairs; ++i) p = fma2(dn[c][i], v[i], p);
+                }
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) d[i] = mul2(wr1, dn[c][i]);
+                ring.store(out, c, d);
+              }
+              q[jj] = sum2(p);
             }
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i) d[i] = mul2(wr1, dn[c][i]);
-            ring.store(out, c, d);
+            fill();  // into this row's slot, which is fs
           }
         }
-        fill();  // into this row's slot, which is fs
         if (a.dweights) {
-          const float q = moe::warp_sum(sum2(p));
-          if (lane == 0) dots[warp][j] = q;
+          // kRows sums over the lanes at once: the halves of a pair of lanes take
+          // one half of the values each, until a lane has one value left
+          static_assert(kRows == 4, "two halving steps");
+          const bool up = lane & 16, up2 = lane & 8;
+          float u0 = up ? q[2] : q[0], u1 = up ? q[3] : q[1];
+          u0 += __shfl_xor_sync(0xffffffffu, up ? q[0] : q[2], 16);
+          u1 += __shfl_xor_sync(0xffffffffu, up ? q[1] : q[3], 16);
+          float u = (up2 ? u1 : u0) + __shfl_xor_sync(0xffffffffu, up2 ? u0 : u1, 8);
+#pragma unroll
+          for (int o = 4; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+          const int j = j0 + (lane >> 3);
+          if ((lane & 7) == 0 && j < a.k) dots[warp][j] = u;
         }
       }
       s = slot(s, a.k);
