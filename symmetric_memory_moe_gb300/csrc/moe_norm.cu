@@ -138,19 +138,6 @@ template <int N>
 __device__ __forceinline__ void wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Waits until at most n of this thread's newest groups are pending (n < 16).
-__device__ __forceinline__ void wait_group(int n) {
-#define MOE_WAIT(i) \
-  case i: asm volatile("cp.async.wait_group " #i ";" ::: "memory"); break;
-  switch (n) {
-    MOE_WAIT(1) MOE_WAIT(2) MOE_WAIT(3) MOE_WAIT(4) MOE_WAIT(5) MOE_WAIT(6) MOE_WAIT(7)
-    MOE_WAIT(8) MOE_WAIT(9) MOE_WAIT(10) MOE_WAIT(11) MOE_WAIT(12) MOE_WAIT(13) MOE_WAIT(14)
-    MOE_WAIT(15)
-    default: asm volatile("cp.async.wait_group 0;" ::: "memory");
-  }
-#undef MOE_WAIT
-}
-
 // Two floats in one 64-bit register pair: sm_103a does a multiply-add of both
 // in one instruction, and these kernels are bound by what they can issue
 // before they are bound by HBM.
@@ -245,17 +232,14 @@ struct Ring {
   __device__ __forceinline__ uint32_t at(int slot, int c, int v) const {
     return base + (uint32_t)slot * slot_bytes + (uint32_t)((c * kVec + v) * (int)blockDim.x) * 16u;
   }
-  // starts the copy of `row` (nothing if NULL) as one group
-  __device__ __forceinline__ void fill(int slot, const T* row) const {
-    if (row) {
+  // starts the copy of `row`
+  __device__ __forceinline__ void copy(int slot, const T* row) const {
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (in[c])
+    for (int c = 0; c < CH; ++c)
+      if (in[c])
 #pragma unroll
-          for (int v = 0; v < kVec; ++v)
-            copy16(at(slot, c, v), reinterpret_cast<const uint4*>(row + o[c]) + v);
-    }
-    commit_group();
+        for (int v = 0; v < kVec; ++v)
+          copy16(at(slot, c, v), reinterpret_cast<const uint4*>(row + o[c]) + v);
   }
   __device__ __forceinline__ void read(int slot, int c, F2 (&f)[kPairs]) const {
     uint4 raw[kVec];
@@ -417,7 +401,8 @@ __global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2) norm_stream_kern
       frow = frow2;
       frow2 = lane_row(a, ft + step, lane);
     }
-    ring.fill(fs, row);
+    if (row) ring.copy(fs, row);
+    commit_group();
     have = row ? have | (1u << fs) : have & ~(1u << fs);
     if (++fs == DEPTH) fs = 0;
   };
@@ -634,16 +619,19 @@ __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackAr
     }
 }
 
-// The backward pass on 16-byte aligned rows, when the ring holds a whole
+// The backward pass on 16-byte aligned rows, when shared memory holds a whole
 // token: (2k + 5) rows through HBM a token, and Y read twice from shared memory
-// only -- for y, and for the inner products with it.
+// only -- for y, and for the inner products with it.  Every row has its own
+// place there (dh, z, dxo, x, Y_0 ..): the first four are copied in one group
+// for the next token as soon as they are used up, and row j of Y when this
+// token's is.
 template <typename T, int CH>
 __global__ void __launch_bounds__(kMaxThreads, 1)
-    norm_back_stream_kernel(const NormBackArgs a, const int depth) {
+    norm_back_stream_kernel(const NormBackArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
   __shared__ float dots[kMaxWarps][SYMM_MOE_MAX_TOPK];  // <dy / r1, Y_j> per warp
-  const Ring<T, CH> ring(smem, a.D, depth);
+  const Ring<T, CH> ring(smem, a.D, 4 + a.k);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const float mean = 1.f / (float)a.D;
   const size_t step = gridDim.x;
@@ -652,57 +640,55 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) s_res[c][i] = s_post[c][i] = s_pre[c][i] = mk(0.f);
-  // A token's rows in the ring: dh, z, dxo, x, Y_0 ..  Copied next: item fj of
-  // token ft, into slot fs.
-  size_t ft = blockIdx.x;
-  int fj = 0, fs = 0, frow = lane_row(a, ft, lane), frow2 = lane_row(a, ft + step, lane);
-  uint32_t have = 0;  // slots that hold a row of Y
-  auto fill = [&]() {
-    const T* row = nullptr;
-    if (fj >= 4) {
-      const int r = __shfl_sync(0xffffffffu, frow, fj - 4);
-      if (r >= 0) row = static_cast<const T*>(a.y) + (size_t)r * a.ldy;
-      have = r >= 0 ? have | (1u << fs) : have & ~(1u << fs);
-    } else if (ft < (size_t)a.T) {
-      const void* p = fj == 0   ? a.dh
-                      : fj == 1 ? (a.dh ? (a.y ? a.xo : a.x) : nullptr)
-                      : fj == 2 ? a.dxo
-                                : (a.dres ? a.x : nullptr);
-      if (p) row = static_cast<const T*>(p) + ft * a.ld;
+  const T* Y = static_cast<const T*>(a.y);
+  const T* zsrc = static_cast<const T*>(a.y ? a.xo : a.x);
+  auto fill_head = [&](size_t t) {
+    if (t < (size_t)a.T) {
+      const size_t o = t * a.ld;
+      if (a.dh) {
+        ring.copy(0, static_cast<const T*>(a.dh) + o);
+        ring.copy(1, zsrc + o);
+      }
+      if (a.dxo) ring.copy(2, static_cast<const T*>(a.dxo) + o);
+      if (a.dres) ring.copy(3, static_cast<const T*>(a.x) + o);
     }
-    ring.fill(fs, row);
-    if (++fs == depth) fs = 0;
-    if (++fj == 4 + a.k) {
-      fj = 0;
-      ft += step;
-      frow = frow2;
-      frow2 = lane_row(a, ft + step, lane);
-    }
+    commit_group();
   };
-  auto slot = [&](int s, int i) { return s + i < depth ? s + i : s + i - depth; };
-  for (int i = 0; i < depth; ++i) fill();
-  int s = 0;  // the token's first slot
-  float weight = lane_weight(a, blockIdx.x, lane);
-  int row = lane_row(a, blockIdx.x, lane);
-  float r1 = a.rstd[2 * (size_t)blockIdx.x], r2 = a.rstd[2 * (size_t)blockIdx.x + 1];
-  for (size_t t = blockIdx.x; t < (size_t)a.T; t += step) {
+  // A token's slots, one per lane: where the row starts in Y (and in dY), and
+  // the weight; a bit of `rows` for each slot that has a row.
+  size_t t = blockIdx.x;
+  int r = lane_row(a, t, lane), rn = lane_row(a, t + step, lane);
+  size_t off = r < 0 ? 0 : (size_t)r * a.ldy;
+  uint32_t rows = __ballot_sync(0xffffffffu, r >= 0);
+  float weight = lane_weight(a, t, lane);
+  float r1 = a.rstd[2 * t], r2 = a.rstd[2 * t + 1];
+  fill_head(t);
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    const size_t o = __shfl_sync(0xffffffffu, off, j);
+    if ((rows >> j) & 1) ring.copy(4 + j, Y + o);
+  }
+  commit_group();
+  for (; t < (size_t)a.T; t += step) {
     // the next token's, on their way
-    const float weight2 = lane_weight(a, t + step, lane);
-    const int row2 = lane_row(a, t + step, lane);
+    const size_t offn = rn < 0 ? 0 : (size_t)rn * a.ldy;
+    const uint32_t rowsn = __ballot_sync(0xffffffffu, rn >= 0);
+    rn = lane_row(a, t + 2 * step, lane);
+    const float weightn = lane_weight(a, t + step, lane);
     const size_t tn = t + step < (size_t)a.T ? t + step : t;
     const float r1n = __ldg(a.rstd + 2 * tn), r2n = __ldg(a.rstd + 2 * tn + 1);
     const float gate = a.gate ? __ldg(a.gate + t) : 1.f;
     F2 dn[CH][kPairs];  // dz, then dn, then dy / r1
+    wait_groups<1>();   // the first four rows; Y may be pending
     if (a.dh) {
       F2 z[CH][kPairs], q[CH][kPairs];  // z r2, and dh wpre
       F2 m = mk(0.f);
-      wait_group(depth - 4);  // all four
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         F2 w[kPairs];
-        ring.read(s, c, q[c]);
-        ring.read(slot(s, 1), c, z[c]);
         ring.vec(a.w_pre, c, 1.f, w);
+        ring.read(0, c, q[c]);
+        ring.read(1, c, z[c]);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
           z[c][i] = mul2(z[c][i], mk(r2));
@@ -715,7 +701,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (a.dxo) {
-          ring.read(slot(s, 2), c, dn[c]);
+          ring.read(2, c, dn[c]);
         } else {
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) dn[c][i] = mk(0.f);
@@ -725,45 +711,42 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           dn[c][i] = fma2(mk(r2), fma2(z[c][i], mk(mqz), q[c][i]), dn[c][i]);
       }
     } else {
-      wait_group(depth - 4);
 #pragma unroll
-      for (int c = 0; c < CH; ++c) ring.read(slot(s, 2), c, dn[c]);
+      for (int c = 0; c < CH; ++c) ring.read(2, c, dn[c]);
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      F2 w[kPairs];
+      ring.vec(a.res, c, 1.f, w);
       if (a.dres) {
         F2 x[kPairs];
-        ring.read(slot(s, 3), c, x);
+        ring.read(3, c, x);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) s_res[c][i] = fma2(dn[c][i], x[i], s_res[c][i]);
       }
-      F2 w[kPairs];
-      ring.vec(a.res, c, 1.f, w);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) w[i] = mul2(w[i], dn[c][i]);
       ring.store(static_cast<T*>(a.dx) + t * a.ld, c, w);
     }
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) fill();
-    s = slot(s, 4);
+    fill_head(t + step);
     if (a.y) {
       F2 n[CH][kPairs];
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) n[c][i] = mk(0.f);
-      wait_group(depth - a.k);  // all of the token's rows
+      wait_groups<1>();  // Y; the next token's first rows may be pending
 #pragma unroll 1
       for (int j0 = 0; j0 < a.k; j0 += kRows)
 #pragma unroll
         for (int jj = 0; jj < kRows; ++jj) {
-          const int j = j0 + jj, sj = slot(s, j);
-          if (j < a.k && ((have >> sj) & 1)) {
-            const F2 w = mk(__shfl_sync(0xffffffffu, weight, j));
+          const int j = j0 + jj;
+          const F2 w = mk(__shfl_sync(0xffffffffu, weight, j & 31));
+          if ((rows >> (j & 31)) & 1) {  // none past k
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
               F2 v[kPairs];
-              ring.read(sj, c, v);
+              ring.read(4 + j, c, v);
 #pragma unroll
               for (int i = 0; i < kPairs; ++i) n[c][i] = fma2(w, v[i], n[c][i]);
             }
@@ -777,10 +760,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
           n[c][i] = mul2(n[c][i], mk(r1));
-          const F2 d = mul2(dn[c][i], w[i]);
-          dg = fma2(d, n[c][i], dg);
-          s_post[c][i] = fma2(mul2(mk(gate), dn[c][i]), n[c][i], s_post[c][i]);
-          dn[c][i] = mul2(mk(gate), d);
+          const F2 g = mul2(mk(gate), dn[c][i]);
+          s_post[c][i] = fma2(g, n[c][i], s_post[c][i]);
+          dg = fma2(mul2(dn[c][i], w[i]), n[c][i], dg);
+          dn[c][i] = mul2(g, w[i]);
         }
       }
       const float dgate = moe::block_sum_once(sum2(dg), red[1]);
@@ -798,30 +781,27 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
         for (int jj = 0; jj < kRows; ++jj) {
           const int j = j0 + jj;
-          q[jj] = 0.f;
-          if (j < a.k) {
-            const int r = __shfl_sync(0xffffffffu, row, j);
-            if (r >= 0) {
-              const F2 wr1 = mk(__shfl_sync(0xffffffffu, weight, j) * r1);
-              T* out = static_cast<T*>(a.dy) + (size_t)r * a.ldy;
-              const int sj = slot(s, j);
-              F2 p = mk(0.f);
+          const F2 wr1 = mk(__shfl_sync(0xffffffffu, weight, j & 31) * r1);
+          const size_t o = __shfl_sync(0xffffffffu, off, j & 31);
+          const size_t on = __shfl_sync(0xffffffffu, offn, j & 31);
+          F2 p = mk(0.f);
+          if ((rows >> (j & 31)) & 1) {
+            T* out = static_cast<T*>(a.dy) + o;
 #pragma unroll
-              for (int c = 0; c < CH; ++c) {
-                F2 v[kPairs], d[kPairs];
-                if (a.dweights) {
-                  ring.read(sj, c, v);
+            for (int c = 0; c < CH; ++c) {
+              F2 v[kPairs], d[kPairs];
+              if (a.dweights) {
+                ring.read(4 + j, c, v);
 #pragma unroll
-                  for (int i = 0; i < kPairs; ++i) p = fma2(dn[c][i], v[i], p);
-                }
-#pragma unroll
-                for (int i = 0; i < kPairs; ++i) d[i] = mul2(wr1, dn[c][i]);
-                ring.store(out, c, d);
+                for (int i = 0; i < kPairs; ++i) p = fma2(dn[c][i], v[i], p);
               }
-              q[jj] = sum2(p);
+#pragma unroll
+              for (int i = 0; i < kPairs; ++i) d[i] = mul2(wr1, dn[c][i]);
+              ring.store(out, c, d);
             }
-            fill();  // into this row's slot, which is fs
           }
+          q[jj] = sum2(p);
+          if ((rowsn >> (j & 31)) & 1) ring.copy(4 + j, Y + on);
         }
         if (a.dweights) {
           // kRows sums over the lanes at once: the halves of a pair of lanes take
@@ -838,7 +818,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           if ((lane & 7) == 0 && j < a.k) dots[warp][j] = u;
         }
       }
-      s = slot(s, a.k);
+      commit_group();
+    } else {
+      commit_group();  // no rows of Y: an empty group in their place
     }
     __syncthreads();  // dots are complete; `red` is free again
     if (a.dweights && (int)threadIdx.x < a.k) {
@@ -846,9 +828,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       for (int w = 0; w < warps; ++w) p += dots[w][threadIdx.x];
       a.dweights[t * a.k + threadIdx.x] = r1 * p;
     }
-    weight = weight2, row = row2, r1 = r1n, r2 = r2n;
+    off = offn, rows = rowsn, weight = weightn, r1 = r1n, r2 = r2n;
   }
-  wait_group(0);
+  wait_groups<0>();
   float* part = a.part + (size_t)blockIdx.x * 3 * a.D;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -863,16 +845,28 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     }
 }
 
-// Adds the CTAs' column sums in their order.
-__global__ void norm_join_kernel(const float* part, int blocks, int D, float* dres, float* dw_post,
-                                 float* dw_pre) {
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= 3 * D) return;
-  float* out = i < D ? dres : (i < 2 * D ? dw_post : dw_pre);
-  if (!out) return;
+// Adds the CTAs' column sums: a warp's lanes take 32 columns, the CTA's warps
+// an eighth of the partial sums each, in a fixed order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    norm_join_kernel(const float* part, int blocks, int D, float* dres, float* dw_post,
+                     float* dw_pre) {
+  __shared__ float sums[kJoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + lane;
+  float* out = i < D ? dres : (i < 2 * D ? dw_post : (i < 3 * D ? dw_pre : nullptr));
   float s = 0.f;
-  for (int b = 0; b < blocks; ++b) s += part[(size_t)b * 3 * D + i];
-  out[i % D] = s;
+  if (out) {
+    const int b1 = blocks * (warp + 1) / kJoinWarps;
+#pragma unroll 8
+    for (int b = blocks * warp / kJoinWarps; b < b1; ++b) s += part[(size_t)b * 3 * D + i];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && out) {
+    for (int w = 1; w < kJoinWarps; ++w) s += sums[w][lane];
+    out[i % D] = s;
+  }
 }
 
 struct Shape {
@@ -892,8 +886,6 @@ int grid_of(int T, int D) {
 constexpr size_t kSmemPerSm = 227 * 1024;
 
 // Rows of the forward ring: 7 with two CTAs per SM, else 3; 0: not even 3 fit.
-// Of the backward ring: a whole token and up to 4 rows of the next; 0: a token
-// does not fit.
 size_t ring_row(int D, size_t es) {
   const Shape sh = shape_of(D);
   return (size_t)sh.ch * sh.threads * kChunk * es;
@@ -903,10 +895,11 @@ int forward_depth(int D, size_t es) {
   if (7 * row <= kSmemPerSm / 2 - 2048) return 7;
   return 3 * row <= kSmemPerSm - 2048 ? 3 : 0;
 }
-int backward_depth(int D, size_t es, int k) {
-  const size_t fit = (kSmemPerSm - 8192) / ring_row(D, es);
-  const int want = std::min(16, 4 + k + 4);
-  return fit >= (size_t)(4 + k) && 4 + k <= 16 ? (int)std::min<size_t>(fit, want) : 0;
+// Bytes of shared memory of a token's rows in the backward pass; 0: too many.
+size_t back_ring(int D, size_t es, int k) {
+  const Shape sh = shape_of(D);
+  const size_t bytes = (size_t)(4 + k) * sh.ch * sh.threads * kChunk * es;
+  return bytes <= kSmemPerSm - 8192 ? bytes : 0;
 }
 
 template <typename F>
@@ -1055,29 +1048,28 @@ extern "C" int moe_block_norm_backward(
     const NormBackArgs a{dxo, dh, x, xo, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre,
                          rstd, T, D, k, dx, dy, dweights, dgate, dres, dw_post, dw_pre,
                          static_cast<float*>(workspace)};
-    const Shape sh = shape_of(D);
     int grid = grid_of(T, D);
     cudaStream_t s = as_stream(stream);
-    const int depth = al ? backward_depth(D, es, k) : 0;
-    const size_t ring = (size_t)depth * ring_row(D, es);
+    const size_t ring = al ? back_ring(D, es, k) : 0;
+    const Shape sh = shape_of(D);
     rc = SYMM_OK;
     dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
       using E = decltype(t);
       constexpr int CH = decltype(c)::value;
-      if (depth) {
+      if (ring) {
         rc = allow_smem((const void*)norm_back_stream_kernel<E, CH>, ring,
                         "moe_block_norm_backward: set-up");
         const int per_sm = (int)std::max<size_t>(
-            1, std::min<size_t>(512 / sh.threads, (kSmemPerSm - 2048) / (ring + 6144)));
+            1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 6144)));
         grid = std::min(grid, std::max(sm_count(), 1) * per_sm);
-        if (!rc) norm_back_stream_kernel<E, CH><<<(unsigned)grid, sh.threads, ring, s>>>(a, depth);
+        if (!rc) norm_back_stream_kernel<E, CH><<<(unsigned)grid, sh.threads, ring, s>>>(a);
       } else {
         norm_back_kernel<E, decltype(b)::value, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
       }
     });
     if (!rc) rc = cuda_check(cudaGetLastError(), "moe_block_norm_backward: launch");
     if (rc || (!dres && !dw_post && !dw_pre)) return rc;
-    norm_join_kernel<<<(unsigned)((3 * D + 255) / 256), 256, 0, s>>>(a.part, grid, D, dres, dw_post,
+    norm_join_kernel<<<(unsigned)((3 * D + 31) / 32), 32 * kJoinWarps, 0, s>>>(a.part, grid, D, dres, dw_post,
                                                                     dw_pre);
     return cuda_check(cudaGetLastError(), "moe_block_norm_backward: join");
   });
