@@ -10,10 +10,15 @@
 //   dl_e = p_e (a_e - sum_f p_f a_f + 2 (m + log s) / n dz)
 //          (+ u_j (scale dw_j - sum_i u_i scale dw_i), u the chosen softmax, otherwise).
 //
-// One warp per token, its logits in registers.  The sums over tokens stay in
-// a warp's registers over all its tokens, are joined per CTA in shared memory
-// and across CTAs by a second small kernel that adds the partial sums in CTA
-// order, so equal inputs give equal bits.
+// One warp per token, V consecutive logits per lane in registers, the next
+// token's on their way.  The choice costs more than all the rest: k rounds of
+// the warp's largest remaining key.  16-bit logits become unique 32-bit keys,
+// the logit's order above the expert's (complemented) number, which each lane
+// sorts once, so that a round is one warp-wide maximum and the winner moves up
+// its list; 32-bit logits are compared as they are, and the winner looks for its
+// next one.  The sums over tokens stay in a warp's registers over all its
+// tokens, are joined per CTA in shared memory and across CTAs by a second
+// small kernel, in a fixed order, so equal inputs give equal bits.
 #include <algorithm>
 #include <type_traits>
 
@@ -25,6 +30,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kJoinThreads = 1024;
+constexpr unsigned kAll = 0xffffffffu;
 
 struct RouteArgs {
   const void* logits;
@@ -46,48 +53,246 @@ __device__ __forceinline__ float clean(float v) {
   return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
 }
 
-// The losses of one group from its sums: every thread takes experts threadIdx.x, ...
-__device__ __forceinline__ void finish_group(const RouteArgs& a, int g, float dot, float zsum,
-                                             int n) {
-  if (threadIdx.x == 0) {
-    const float n1 = (float)(n > 0 ? n : 1);
-    a.tokens[g] = n;
-    a.loss[2 * g] = dot * ((float)a.E / (float)a.k) / n1 / n1;
-    a.loss[2 * g + 1] = zsum / n1;
+// A lane's logits: experts lane*V .. lane*V + V - 1 of a row, as they lie in
+// memory.  VEC: rows and E are such that a lane's V logits are whole aligned
+// vectors.
+template <typename T, int V, bool VEC>
+struct Raw {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  static constexpr int kUnit = kBytes < 16 ? kBytes : 16;
+  alignas(kUnit) T v[V];
+  __device__ __forceinline__ void load(const T* row, int E, int lane) {
+    const int e0 = lane * V;
+    if constexpr (VEC) {
+      if (e0 >= E) return;
+      if constexpr (kUnit == 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+          reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(row + e0)[i];
+      } else if constexpr (kUnit == 8) {
+        *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(row + e0);
+      } else if constexpr (kUnit == 4) {
+        *reinterpret_cast<uint32_t*>(v) = *reinterpret_cast<const uint32_t*>(row + e0);
+      } else {
+        v[0] = row[e0];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) v[i] = row[e0 + i];
+    }
+  }
+  // the logit as the operator counts it; -infinity past E
+  __device__ __forceinline__ float at(int i, int E, int lane) const {
+    return lane * V + i < E ? clean(moe::to_f(v[i])) : -INFINITY;
+  }
+  __device__ __forceinline__ static void store(T* row, int E, int lane, const float (&d)[V]) {
+    const int e0 = lane * V;
+    alignas(16) T o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = moe::from_f<T>(d[i]);
+    if constexpr (VEC) {
+      if (e0 >= E) return;
+      if constexpr (kUnit == 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i)
+          reinterpret_cast<uint4*>(row + e0)[i] = reinterpret_cast<const uint4*>(o)[i];
+      } else if constexpr (kUnit == 8) {
+        *reinterpret_cast<uint2*>(row + e0) = *reinterpret_cast<const uint2*>(o);
+      } else if constexpr (kUnit == 4) {
+        *reinterpret_cast<uint32_t*>(row + e0) = *reinterpret_cast<const uint32_t*>(o);
+      } else {
+        row[e0] = o[0];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < E) row[e0 + i] = o[i];
+    }
+  }
+};
+
+// Order of a 16-bit float as an unsigned number, and back.
+__device__ __forceinline__ uint32_t order16(uint32_t bits) {
+  return (bits & 0x8000u) ? 0xffffu - bits : bits | 0x8000u;
+}
+__device__ __forceinline__ uint32_t unorder16(uint32_t o) {
+  return (o & 0x8000u) ? o & 0x7fffu : 0xffffu - o;
+}
+
+__device__ __forceinline__ void larger_first(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b), lo = min(a, b);
+  a = hi, b = lo;
+}
+// Batcher's odd-even merge sort of a lane's keys, largest first.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&k)[V]) {
+  static_assert(V <= 8, "a network for up to 8");
+  if constexpr (V >= 2) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) larger_first(k[i], k[i + 1]);
+  }
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      larger_first(k[i], k[i + 2]), larger_first(k[i + 1], k[i + 3]);
+      larger_first(k[i + 1], k[i + 2]);
+    }
+  }
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) larger_first(k[i], k[i + 4]);
+    larger_first(k[2], k[4]), larger_first(k[3], k[5]);
+    larger_first(k[1], k[2]), larger_first(k[3], k[4]), larger_first(k[5], k[6]);
   }
 }
 
-template <typename T, int V>
+// The choices of a token: after choose(), lane j < k has the j-th expert (or
+// -1) and its logit, and every lane the largest logit (-infinity: none left).
+struct Choice {
+  int expert;
+  float logit, top;
+};
+
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ Choice choose16(const Raw<T, V, VEC>& raw, int E, int k, int lane) {
+  // no key for NaN and -infinity; -0 counts as +0
+  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane * V + i;
+    uint32_t bits = *reinterpret_cast<const uint16_t*>(&raw.v[i]);
+    if (bits == 0x8000u) bits = 0;
+    const bool out = e >= E || (bits & 0x7fffu) > kInf || bits == (0x8000u | kInf);
+    key[i] = out ? 0u : (order16(bits) << 16) | (uint32_t)(0xffff - e);
+  }
+  uint32_t head;
+  if constexpr (V <= 8) {
+    sort_keys<V>(key);
+    head = key[0];
+  } else {
+    head = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) head = max(head, key[i]);
+  }
+  uint32_t mine = 0, first = 0;
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = __reduce_max_sync(kAll, head);
+    if (m == 0) break;
+    if (j == 0) first = m;
+    if (lane == j) mine = m;
+    if (head == m) {
+      if constexpr (V <= 8) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+        key[V - 1] = 0;
+        head = key[0];
+      } else {
+        head = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (key[i] == m) key[i] = 0;
+          head = max(head, key[i]);
+        }
+      }
+    }
+  }
+  auto value = [](uint32_t key) {
+    const uint16_t bits = (uint16_t)unorder16(key >> 16);
+    return key ? clean(moe::to_f(*reinterpret_cast<const T*>(&bits))) : -INFINITY;
+  };
+  return {mine ? 0xffff - (int)(mine & 0xffffu) : -1, value(mine), value(first)};
+}
+
+template <int V, bool VEC>
+__device__ __forceinline__ Choice choose32(const Raw<float, V, VEC>& raw, int E, int k, int lane) {
+  float l[V];
+  float head = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    l[i] = raw.at(i, E, lane);
+    head = fmaxf(head, l[i]);
+  }
+  Choice c{-1, -INFINITY, -INFINITY};
+  for (int j = 0; j < k; ++j) {
+    // floats in the order of unsigned numbers (-0 made +0): one instruction
+    // finds the warp's largest
+    const uint32_t bits = __float_as_uint(head + 0.f);
+    const uint32_t key = (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
+    const uint32_t m = __reduce_max_sync(kAll, key);
+    const int src = __ffs(__ballot_sync(kAll, key == m)) - 1;  // the lowest lane: lowest experts
+    int at = 0;
+    const float value = head;
+    if (lane == src) {
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (l[i] == value) at = i;
+      head = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (i == at) l[i] = -INFINITY;
+        head = fmaxf(head, l[i]);
+      }
+    }
+    const float best = __shfl_sync(kAll, value, src);
+    if (best == -INFINITY) break;
+    const int e = __shfl_sync(kAll, lane * V + at, src);
+    if (j == 0) c.top = best;
+    if (lane == j) c.expert = e, c.logit = best;
+  }
+  return c;
+}
+
+// Losses and token count of one group from its sums.
+__device__ __forceinline__ void finish_group(const RouteArgs& a, int g, float dot, float zsum,
+                                             int n) {
+  const float n1 = (float)(n > 0 ? n : 1);
+  a.tokens[g] = n;
+  a.loss[2 * g] = dot * ((float)a.E / (float)a.k) / n1 / n1;
+  a.loss[2 * g + 1] = zsum / n1;
+}
+
+template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
-  extern __shared__ float smem[];  // P [E] per warp in turn, counts [E]
-  float* sp = smem;
-  int* sc = reinterpret_cast<int*>(smem + a.E);
-  __shared__ float red[kWarps];
-  __shared__ float sz[kWarps];
+  extern __shared__ float smem[];  // P [warps][E], counts [E]
+  int* sc = reinterpret_cast<int*>(smem + kWarps * a.E);
+  __shared__ float red[kWarps], sz[kWarps];
   __shared__ int sn[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = blockIdx.x / a.blocks, b = blockIdx.x % a.blocks;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) sp[e] = 0.f, sc[e] = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int e = threadIdx.x; e < a.E; e += kThreads) sc[e] = 0;
   __syncthreads();
   float psum[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) psum[v] = 0.f;
   float zsum = 0.f;
   int n = 0;
-  for (int t = b * kWarps + warp; t < a.T; t += a.blocks * kWarps) {
-    const size_t row = (size_t)g * a.T + t;
-    const T* src = static_cast<const T*>(a.logits) + row * a.ld;
-    float l[V];
-    float m = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = lane + 32 * v;
-      l[v] = e < a.E ? clean(moe::to_f(src[e])) : -INFINITY;
-      m = fmaxf(m, l[v]);
+  const int step = a.blocks * kWarps;
+  const T* logits = static_cast<const T*>(a.logits) + (size_t)g * a.T * a.ld;
+  int t = b * kWarps + warp;
+  Raw<T, V, VEC> raw;
+  uint8_t mask = 1;
+  if (t < a.T) {
+    raw.load(logits + (size_t)t * a.ld, a.E, lane);
+    if (a.mask) mask = a.mask[(size_t)g * a.T + t];
+  }
+  for (; t < a.T; t += step) {
+    const Raw<T, V, VEC> now = raw;
+    const uint8_t on = mask;
+    if (t + step < a.T) {  // the next token's, on their way
+      raw.load(logits + (size_t)(t + step) * a.ld, a.E, lane);
+      if (a.mask) mask = a.mask[(size_t)g * a.T + t + step];
     }
-    m = moe::warp_max(m);
-    const bool valid = (!a.mask || a.mask[row]) && m > -INFINITY;
-    if (!valid) {
+    const size_t row = (size_t)g * a.T + t;
+    Choice c{-1, -INFINITY, -INFINITY};
+    if (on) {
+      if constexpr (std::is_same<T, float>::value) c = choose32(now, a.E, a.k, lane);
+      else c = choose16(now, a.E, a.k, lane);
+    }
+    const float m = c.top;
+    if (m == -INFINITY) {  // padding, or nothing to choose from
       if (lane < a.k) {
         a.experts[row * a.k + lane] = -1;
         a.weights[row * a.k + lane] = 0.f;
@@ -98,99 +303,99 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
     float p[V];
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) s += p[v] = expf(l[v] - m);
+    for (int v = 0; v < V; ++v) s += p[v] = __expf(now.at(v, a.E, lane) - m);
     s = moe::warp_sum(s);
     const float inv = 1.f / s;
 #pragma unroll
-    for (int v = 0; v < V; ++v) psum[v] += p[v] * inv;
+    for (int v = 0; v < V; ++v) psum[v] = fmaf(p[v], inv, psum[v]);
     const float lse = m + logf(s);
-    zsum += lse * lse;
+    zsum = fmaf(lse, lse, zsum);
     ++n;
-    // k rounds of the largest remaining logit; round j's winner stays in lane j
-    float mine = -INFINITY;
-    int chosen = -1;
-    for (int j = 0; j < a.k; ++j) {
-      float best = -INFINITY;
-      int at = 0x7fffffff;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (l[v] > best) best = l[v], at = lane + 32 * v;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        const float ob = __shfl_xor_sync(0xffffffffu, best, o);
-        const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-        if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-      }
-      if (best == -INFINITY) break;
-      if (lane == j) mine = best, chosen = at;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (at == lane + 32 * v) l[v] = -INFINITY;
-    }
-    const float u = expf(mine - m);  // 0 where nothing was chosen
+    const float u = __expf(c.logit - m);  // 0 where nothing was chosen
     const float total = a.renorm ? moe::warp_sum(u) : s;
     if (lane < a.k) {
-      a.experts[row * a.k + lane] = chosen;
+      a.experts[row * a.k + lane] = c.expert;
       a.weights[row * a.k + lane] = a.scale * (u / total);
-      if (chosen >= 0) atomicAdd(&sc[chosen], 1);
+      if (c.expert >= 0) atomicAdd(&sc[c.expert], 1);
     }
-    if (lane == 0) a.stats[2 * row] = m, a.stats[2 * row + 1] = s;
+    if (lane < 2) a.stats[2 * row + lane] = lane ? s : m;
   }
   if (lane == 0) sz[warp] = zsum, sn[warp] = n;
-  for (int w = 0; w < kWarps; ++w) {  // warps in order: a fixed order of the sum
-    if (w == warp) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (lane + 32 * v < a.E) sp[lane + 32 * v] += psum[v];
-    }
-    __syncthreads();
-  }
+  for (int v = 0; v < V; ++v)
+    if (lane * V + v < a.E) smem[warp * a.E + lane * V + v] = psum[v];
+  __syncthreads();
   zsum = 0.f, n = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) zsum += sz[w], n += sn[w];
-  if (a.blocks == 1) {
-    float dot = 0.f;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) {
-      a.counts[(size_t)g * a.E + e] = sc[e];
-      dot += sp[e] * (float)sc[e];
-    }
-    dot = moe::block_sum(dot, red);
-    finish_group(a, g, dot, zsum, n);
-    return;
-  }
   float* part = a.part + (size_t)blockIdx.x * (2 * a.E + 2);
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    part[e] = sp[e];
-    part[a.E + e] = __int_as_float(sc[e]);
-  }
-  if (threadIdx.x == 0) part[2 * a.E] = zsum, part[2 * a.E + 1] = __int_as_float(n);
-}
-
-// One CTA per group adds the CTAs' partial sums in their order.
-__global__ void __launch_bounds__(kThreads) route_join_kernel(const RouteArgs a) {
-  __shared__ float red[kWarps];
-  const int g = blockIdx.x;
-  const size_t step = 2 * a.E + 2;
-  const float* part = a.part + (size_t)g * a.blocks * step;
   float dot = 0.f;
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
     float p = 0.f;
-    int c = 0;
-    for (int b = 0; b < a.blocks; ++b) {
-      p += part[b * step + e];
-      c += __float_as_int(part[b * step + a.E + e]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) p += smem[w * a.E + e];  // warps in order
+    if (a.blocks == 1) {
+      a.counts[(size_t)g * a.E + e] = sc[e];
+      dot = fmaf(p, (float)sc[e], dot);
+    } else {
+      part[e] = p;
+      part[a.E + e] = __int_as_float(sc[e]);
     }
+  }
+  if (a.blocks == 1) {
+    dot = moe::block_sum(dot, red);
+    if (threadIdx.x == 0) finish_group(a, g, dot, zsum, n);
+  } else if (threadIdx.x == 0) {
+    part[2 * a.E] = zsum, part[2 * a.E + 1] = __int_as_float(n);
+  }
+}
+
+// One CTA per group adds the CTAs' partial sums: several threads per expert,
+// each a part of the CTAs in order, and those parts in order.  Started while
+// route_kernel runs; waits for its end.
+__global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const RouteArgs a) {
+  __shared__ float red[kJoinThreads / 32];
+  __shared__ float sp[kJoinThreads];
+  __shared__ int sc[kJoinThreads];
+  __shared__ float sz[32];
+  __shared__ int sn[32];
+  const int g = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t step = 2 * a.E + 2;
+  const float* part = a.part + (size_t)g * a.blocks * step;
+  const int width = (a.E + 31) / 32 * 32, ways = kJoinThreads / width;  // E <= 1024
+  const int e = threadIdx.x % width, way = threadIdx.x / width;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float p = 0.f, z = 0.f;
+  int c = 0, n = 0;
+  if (way < ways && e < a.E) {
+    const int b1 = a.blocks * (way + 1) / ways;
+#pragma unroll 8
+    for (int b = a.blocks * way / ways; b < b1; ++b) {
+      p += __ldcg(part + b * step + e);
+      c += __float_as_int(__ldcg(part + b * step + a.E + e));
+    }
+  }
+  sp[threadIdx.x] = p, sc[threadIdx.x] = c;
+  if (warp == 0) {  // lane b sums CTAs b, b + 32, ..
+    for (int b = lane; b < a.blocks; b += 32) {
+      z += __ldcg(part + b * step + 2 * a.E);
+      n += __float_as_int(__ldcg(part + b * step + 2 * a.E + 1));
+    }
+    sz[lane] = z, sn[lane] = n;
+  }
+  __syncthreads();
+  float dot = 0.f;
+  if (way == 0 && e < a.E) {
+    for (int w = 1; w < ways; ++w) p += sp[w * width + e], c += sc[w * width + e];
     a.counts[(size_t)g * a.E + e] = c;
-    dot += p * (float)c;
+    dot = p * (float)c;
   }
   dot = moe::block_sum(dot, red);
-  float z = 0.f;
-  int n = 0;
-  if (threadIdx.x == 0)
-    for (int b = 0; b < a.blocks; ++b) {
-      z += part[b * step + 2 * a.E];
-      n += __float_as_int(part[b * step + 2 * a.E + 1]);
-    }
-  finish_group(a, g, dot, z, n);
+  if (threadIdx.x == 0) {
+    z = 0.f, n = 0;
+    for (int i = 0; i < 32; ++i) z += sz[i], n += sn[i];
+    finish_group(a, g, dot, z, n);
+  }
 }
 
 struct RouteBackArgs {
@@ -206,63 +411,126 @@ struct RouteBackArgs {
   const float* dloss;
   void* dlogits;
   size_t ldd;
+  int blocks;  // CTAs per group
 };
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArgs a) {
-  const int lane = threadIdx.x & 31;
-  const size_t rows = (size_t)a.G * a.T;
-  const size_t nwarps = (size_t)gridDim.x * kWarps;
-  for (size_t row = (size_t)blockIdx.x * kWarps + (threadIdx.x >> 5); row < rows; row += nwarps) {
-    const int g = (int)(row / a.T);
-    const T* src = static_cast<const T*>(a.logits) + row * a.ld;
-    T* dst = static_cast<T*>(a.dlogits) + row * a.ldd;
-    int at = -1;
-    float dw = 0.f;
-    if (lane < a.k) {
-      at = a.experts[row * a.k + lane];
-      if (at >= a.E) at = -1;
-      if (at >= 0 && a.dweights) dw = a.scale * a.dweights[row * a.k + lane];
+// A lane's V floats in shared memory, 16 bytes at a time.
+template <int V>
+__device__ __forceinline__ void put(float* p, const float (&x)[V]) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = x[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void get(const float* p, float (&x)[V]) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
     }
-    if (__shfl_sync(0xffffffffu, at, 0) < 0) {  // an invalid token
-      for (int e = lane; e < a.E; e += 32) dst[e] = moe::from_f<T>(0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = p[i];
+  }
+}
+
+// CTAs of a group's own, so that a E c / (k n^2) stays in registers.
+template <typename T, int V, bool VEC>
+__global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArgs a) {
+  // [warps][32 V]: the probabilities, then what the chosen experts get (0 elsewhere)
+  extern __shared__ __align__(16) float back_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = blockIdx.x / a.blocks, b = blockIdx.x % a.blocks;
+  float* add = back_smem + warp * 32 * V;
+#pragma unroll
+  for (int v = 0; v < V; ++v) add[lane + 32 * v] = 0.f;
+  __syncwarp();
+  const float n = (float)max(a.tokens[g], 1);
+  const float cb = a.dloss ? a.dloss[2 * g] * ((float)a.E / (float)a.k) / n / n : 0.f;
+  const float cz = a.dloss ? 2.f * a.dloss[2 * g + 1] / n : 0.f;
+  float base[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lane * V + v;
+    base[v] = e < a.E && a.dloss ? cb * (float)a.counts[(size_t)g * a.E + e] : 0.f;
+  }
+  const int step = a.blocks * kWarps;
+  const size_t row0 = (size_t)g * a.T;
+  const T* logits = static_cast<const T*>(a.logits) + row0 * a.ld;
+  T* dlogits = static_cast<T*>(a.dlogits) + row0 * a.ldd;
+  struct Next {
+    Raw<T, V, VEC> raw;
+    int at;
+    float dw, m, s;
+  } next;
+  auto load = [&](int t) {
+    next.raw.load(logits + (size_t)t * a.ld, a.E, lane);
+    next.at = -1, next.dw = 0.f;
+    if (lane < a.k) {
+      next.at = a.experts[(row0 + t) * a.k + lane];
+      if (a.dweights) next.dw = a.dweights[(row0 + t) * a.k + lane];
+    }
+    next.m = a.stats[2 * (row0 + t)], next.s = a.stats[2 * (row0 + t) + 1];
+  };
+  int t = b * kWarps + warp;
+  if (t < a.T) load(t);
+  for (; t < a.T; t += step) {
+    const Next now = next;
+    if (t + step < a.T) load(t + step);  // (in place, a row is written after it is read: below)
+    T* dst = dlogits + (size_t)t * a.ldd;
+    float d[V];
+    if (__shfl_sync(kAll, now.at, 0) < 0) {  // an invalid token
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = 0.f;
+      Raw<T, V, VEC>::store(dst, a.E, lane, d);
       continue;
     }
-    const float m = a.stats[2 * row], s = a.stats[2 * row + 1], inv = 1.f / s;
-    const float n = (float)max(a.tokens[g], 1);
-    const float cb = a.dloss ? a.dloss[2 * g] * ((float)a.E / (float)a.k) / n / n : 0.f;
-    const float cz = a.dloss ? (2.f * a.dloss[2 * g + 1] / n) * (m + logf(s)) : 0.f;
-    float p[V], d[V];
+    const int at = now.at < a.E ? now.at : -1;
+    const float dw = at >= 0 ? a.scale * now.dw : 0.f;
+    const float m = now.m, inv = 1.f / now.s;
+    const float lz = cz * (m + logf(now.s));
+    float p[V];
     float dot = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = lane + 32 * v;
-      p[v] = e < a.E ? expf(clean(moe::to_f(src[e])) - m) * inv : 0.f;
-      d[v] = e < a.E ? cb * (float)a.counts[(size_t)g * a.E + e] : 0.f;
-      dot += p[v] * d[v];
+      p[v] = __expf(now.raw.at(v, a.E, lane) - m) * inv;
+      dot = fmaf(p[v], base[v], dot);
     }
-    // the chosen experts' own probabilities, in the lanes of their slots
-    const float u = at >= 0 ? expf(clean(moe::to_f(src[at])) - m) * inv : 0.f;
-    float add = dw;  // to a (before the softmax's Jacobian), or to dl if renormalised
-    if (a.renorm) {
-      const float q = u / moe::warp_sum(u);
-      add = q * (dw - moe::warp_sum(q * dw));
-    } else {
-      dot += u * dw;
+    if (a.dweights) {
+      // The chosen experts' probabilities, from the lanes that own them to the
+      // lanes of their slots; and what each slot adds, back, by way of shared
+      // memory: to a (before the softmax's Jacobian), or to dl if renormalised.
+      put<V>(add + lane * V, p);
+      __syncwarp();
+      const float u = at >= 0 ? add[at] : 0.f;
+      __syncwarp();
+#pragma unroll
+      for (int v = 0; v < V; ++v) d[v] = 0.f;
+      put<V>(add + lane * V, d);
+      float x = dw;
+      if (a.renorm) {
+        const float q = u / moe::warp_sum(u);
+        x = q * (dw - moe::warp_sum(q * dw));
+      } else {
+        dot = fmaf(u, dw, dot);
+      }
+      __syncwarp();
+      if (at >= 0) add[at] = x;
+      __syncwarp();
     }
     dot = moe::warp_sum(dot);
-#pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = p[v] * (d[v] - dot + cz);
-    for (int j = 0; j < a.k; ++j) {
-      const int e = __shfl_sync(0xffffffffu, at, j);
-      const float x = __shfl_sync(0xffffffffu, add, j);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e == lane + 32 * v) d[v] += a.renorm ? x : p[v] * x;
-    }
+    get<V>(add + lane * V, d);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (lane + 32 * v < a.E) dst[lane + 32 * v] = moe::from_f<T>(d[v]);
+      d[v] = a.renorm ? fmaf(p[v], base[v] - dot + lz, d[v]) : p[v] * (base[v] + d[v] - dot + lz);
+    Raw<T, V, VEC>::store(dst, a.E, lane, d);
+    __syncwarp();
   }
 }
 
@@ -289,6 +557,17 @@ int route_blocks(int G, int T) {
   const int want = (T + kWarps - 1) / kWarps;
   const int most = std::max(1, 4 * sms / std::max(G, 1));
   return std::max(1, std::min(want, most));
+}
+
+// Whether a lane's V logits are whole aligned vectors in every row.
+bool vectors(const void* p, size_t ld, int E, int V, size_t es) {
+  const size_t unit = std::min<size_t>(16, V * es);
+  return E % V == 0 && ld * es % unit == 0 && moe::aligned(p, unit);
+}
+template <typename F>
+void for_vec(bool vec, F&& f) {
+  if (vec) f(std::true_type());
+  else f(std::false_type());
 }
 
 int check_route(const char* what, size_t ld, int dtype, int G, int T, int E, int k) {
@@ -339,14 +618,25 @@ extern "C" int moe_route(const void* logits, size_t ld, const uint8_t* mask, int
     cudaStream_t s = as_stream(stream);
     for_type(dtype, [&](auto t) {
       for_width(E, [&](auto v) {
-        route_kernel<decltype(t), decltype(v)::value>
-            <<<(unsigned)(G * a.blocks), kThreads, 2 * (size_t)E * 4, s>>>(a);
+        constexpr int V = decltype(v)::value;
+        for_vec(vectors(logits, ld, E, V, sizeof(t)), [&](auto vec) {
+          route_kernel<decltype(t), V, decltype(vec)::value>
+              <<<(unsigned)(G * a.blocks), kThreads, (kWarps + 1) * (size_t)E * 4, s>>>(a);
+        });
       });
     });
     rc = cuda_check(cudaGetLastError(), "moe_route: launch");
     if (rc || a.blocks == 1) return rc;
-    route_join_kernel<<<(unsigned)G, kThreads, 0, s>>>(a);
-    return cuda_check(cudaGetLastError(), "moe_route: join");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)G);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_check(cudaLaunchKernelEx(&cfg, route_join_kernel, a), "moe_route: join");
   });
 }
 
@@ -372,15 +662,20 @@ extern "C" int moe_route_backward(const void* logits, size_t ld, int dtype, int 
         !moe::aligned(counts, 4) || !moe::aligned(tokens, 4) || !moe::aligned(stats, 4) ||
         !moe::aligned(dweights, 4) || !moe::aligned(dloss, 4))
       return fail(SYMM_EINVAL, "moe_route_backward: a pointer is not aligned to its elements");
+    const int blocks = std::max(
+        1, std::min((T + kWarps - 1) / kWarps, std::max(sm_count(), 1) * 8 / std::min(G, 1 << 20)));
     RouteBackArgs a{logits, ld, G, T, E, k, renorm ? 1 : 0, scale, experts, counts, tokens, stats,
-                    dweights, dloss, dlogits, ldd};
-    const size_t rows = (size_t)G * T;
-    const unsigned grid = (unsigned)std::min<size_t>((rows + kWarps - 1) / kWarps,
-                                                     (size_t)std::max(sm_count(), 1) * 8);
+                    dweights, dloss, dlogits, ldd, blocks};
     cudaStream_t s = as_stream(stream);
     for_type(dtype, [&](auto t) {
       for_width(E, [&](auto v) {
-        route_back_kernel<decltype(t), decltype(v)::value><<<grid, kThreads, 0, s>>>(a);
+        constexpr int V = decltype(v)::value;
+        const bool vec = vectors(logits, ld, E, V, sizeof(t)) &&
+                         vectors(dlogits, ldd, E, V, sizeof(t));
+        for_vec(vec, [&](auto w) {
+          route_back_kernel<decltype(t), V, decltype(w)::value>
+              <<<(unsigned)G * (unsigned)blocks, kThreads, kWarps * 32 * V * 4, s>>>(a);
+        });
       });
     });
     return cuda_check(cudaGetLastError(), "moe_route_backward: launch");
