@@ -19,6 +19,11 @@
 // next one.  The sums over tokens stay in a warp's registers over all its
 // tokens, are joined per CTA in shared memory and across CTAs by a second
 // small kernel, in a fixed order, so equal inputs give equal bits.
+//
+// Bound by what can be issued (about 300 instructions a token, 5 cycles of a
+// scheduler's time per logit's byte at HBM's rate): so exp, log and quotients are the
+// approximate instructions, 2^-21 relatively, ten times below a gradient step's noise in
+// the weights and losses that they go into.
 #include <algorithm>
 #include <type_traits>
 
@@ -112,6 +117,39 @@ struct Raw {
   }
 };
 
+// A lane's V floats in shared memory, 16 bytes at a time.
+template <int V>
+__device__ __forceinline__ void put(float* p, const float (&x)[V]) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = x[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void get(const float* p, float (&x)[V]) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = p[i];
+  }
+}
+
+// exp of a number that is not above 0, or of -infinity
+__device__ __forceinline__ float exp_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+
 // Order of a 16-bit float as an unsigned number, and back.
 __device__ __forceinline__ uint32_t order16(uint32_t bits) {
   return (bits & 0x8000u) ? 0xffffu - bits : bits | 0x8000u;
@@ -154,50 +192,89 @@ struct Choice {
   float logit, top;
 };
 
-template <typename T, int V, bool VEC>
-__device__ __forceinline__ Choice choose16(const Raw<T, V, VEC>& raw, int E, int k, int lane) {
-  // no key for NaN and -infinity; -0 counts as +0
-  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-  uint32_t key[V];
+// k rounds: `round(j, live)` takes the largest key left and moves the winner up
+// its list, of which no more than `live` keys can still matter; false: none left.
+template <typename F>
+__device__ __forceinline__ void rounds(int k, F&& round) {
+  if (k <= 8) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    uint32_t bits = *reinterpret_cast<const uint16_t*>(&raw.v[i]);
-    if (bits == 0x8000u) bits = 0;
-    const bool out = e >= E || (bits & 0x7fffu) > kInf || bits == (0x8000u | kInf);
-    key[i] = out ? 0u : (order16(bits) << 16) | (uint32_t)(0xffff - e);
-  }
-  uint32_t head;
-  if constexpr (V <= 8) {
-    sort_keys<V>(key);
-    head = key[0];
+    for (int j = 0; j < 8; ++j)
+      if (j >= k || !round(j, 8 - j)) break;
   } else {
-    head = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) head = max(head, key[i]);
-  }
-  uint32_t mine = 0, first = 0;
-  for (int j = 0; j < k; ++j) {
-    const uint32_t m = __reduce_max_sync(kAll, head);
-    if (m == 0) break;
-    if (j == 0) first = m;
-    if (lane == j) mine = m;
-    if (head == m) {
-      if constexpr (V <= 8) {
-#pragma unroll
-        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
-        key[V - 1] = 0;
-        head = key[0];
-      } else {
-        head = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (key[i] == m) key[i] = 0;
-          head = max(head, key[i]);
-        }
-      }
+    for (int j = 0; j < k && round(j, 8); ++j) {
     }
   }
+}
+// The winner of a lane's list moves up.
+template <int V>
+__device__ __forceinline__ void pop(uint32_t (&key)[V], bool win, int live) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i + 1 < live) key[i] = win ? (i + 1 < V ? key[i + 1] : 0u) : key[i];
+}
+
+// 16-bit logits, lists of up to 8.  l: the logits as the operator counts them.
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ Choice choose16(const Raw<T, V, VEC>& raw, int E, int k, int lane,
+                                           float (&l)[V]) {
+  constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  const uint32_t last = 0xffffu - (uint32_t)(lane * V);  // complement of the first expert
+  uint32_t key[V];
+  if constexpr (V >= 2) {
+    // two logits at a time: -0 made +0 (and NaN one pattern) by adding +0, then
+    // the order of unsigned numbers in both halves
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                         __nv_bfloat162>::type;
+    uint32_t x[V / 2], most = 0, least = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      uint32_t w = reinterpret_cast<const uint32_t*>(raw.v)[i];
+      const uint32_t zero = 0;
+      const T2 s = __hadd2(*reinterpret_cast<const T2*>(&w), *reinterpret_cast<const T2*>(&zero));
+      w = *reinterpret_cast<const uint32_t*>(&s);
+      x[i] = w ^ ((((w >> 15) & 0x00010001u) * 0xffffu) | 0x80008000u);
+      most = __vmaxu2(most, x[i]);
+      least = __vminu2(least, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      key[i] = __byte_perm(last - i, x[i / 2], i % 2 ? 0x7610 : 0x5410);
+    const bool active = lane * V < E;
+    // from the lowest finite order to the highest in both halves, all V of them?
+    constexpr uint32_t kLow = 0xffffu - (0x8000u | (kInf - 1)), kHigh = 0x8000u | (kInf - 1);
+    const bool plain = !active || (lane * V + V <= E && (most >> 16) <= kHigh &&
+                                   (most & 0xffffu) <= kHigh && (least >> 16) >= kLow &&
+                                   (least & 0xffffu) >= kLow);
+    if (__all_sync(kAll, plain)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = active ? moe::to_f(raw.v[i]) : -INFINITY;
+      if (!active) key[0] = 0;
+      // (an inactive lane's further keys never come to the head)
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        l[i] = raw.at(i, E, lane);
+        if (l[i] == -INFINITY) key[i] = 0;
+      }
+    }
+    if (active) sort_keys<V>(key);
+  } else {
+    l[0] = raw.at(0, E, lane);
+    uint32_t bits = *reinterpret_cast<const uint16_t*>(&raw.v[0]);
+    if (bits == 0x8000u) bits = 0;
+    key[0] = l[0] == -INFINITY ? 0u : (order16(bits) << 16) | last;
+  }
+  uint32_t mine = 0, first = 0;
+  rounds(k, [&](int j, int live) {
+    const uint32_t m = __reduce_max_sync(kAll, key[0]);
+    if (m == 0) return false;
+    if (j == 0) first = m;
+    if (lane == j) mine = m;
+    const bool win = key[0] == m;
+    if constexpr (V == 1) key[0] = win ? 0u : key[0];
+    else pop<V>(key, win, live);
+    return true;
+  });
   auto value = [](uint32_t key) {
     const uint16_t bits = (uint16_t)unorder16(key >> 16);
     return key ? clean(moe::to_f(*reinterpret_cast<const T*>(&bits))) : -INFINITY;
@@ -205,9 +282,58 @@ __device__ __forceinline__ Choice choose16(const Raw<T, V, VEC>& raw, int E, int
   return {mine ? 0xffff - (int)(mine & 0xffffu) : -1, value(mine), value(first)};
 }
 
+// 32-bit logits, lists of up to 8: the lists are of logits alone, and the
+// slots' lanes look the experts up afterwards, among the V logits of the lane
+// that won (which it leaves in `row`, shared memory of 32 V floats).
 template <int V, bool VEC>
-__device__ __forceinline__ Choice choose32(const Raw<float, V, VEC>& raw, int E, int k, int lane) {
-  float l[V];
+__device__ __forceinline__ Choice choose32(const Raw<float, V, VEC>& raw, int E, int k, int lane,
+                                           float (&l)[V], float* row) {
+  constexpr uint32_t kNone = 0x007fffffu;  // the order of -infinity
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    l[i] = raw.at(i, E, lane);
+    const uint32_t bits = __float_as_uint(l[i] + 0.f);  // -0 made +0
+    key[i] = bits ^ ((uint32_t)((int)bits >> 31) | 0x80000000u);
+  }
+  __syncwarp();  // the last token's look-up is over
+  put<V>(row + lane * V, l);
+  sort_keys<V>(key);
+  uint32_t mine = kNone, first = kNone;
+  int from = 0;
+  rounds(k, [&](int j, int live) {
+    const uint32_t m = __reduce_max_sync(kAll, key[0]);
+    if (m <= kNone) return false;
+    const int src = __ffs(__ballot_sync(kAll, key[0] == m)) - 1;  // lowest lane: lowest experts
+    if (j == 0) first = m;
+    if (lane == j) mine = m, from = src;
+    if constexpr (V == 1) key[0] = lane == src ? 0u : key[0];
+    else pop<V>(key, lane == src, live);
+    return true;
+  });
+  auto value = [&](uint32_t m) {
+    return m > kNone ? __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m) : -INFINITY;
+  };
+  Choice c{-1, value(mine), value(first)};
+  __syncwarp();
+  // the n-th among equals of one lane is the n-th of them there
+  const uint32_t same = __match_any_sync(kAll, mine) & __match_any_sync(kAll, from);
+  int skip = __popc(same & ((1u << lane) - 1));
+  if (mine > kNone) {
+    float v[V];
+    get<V>(row + from * V, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (v[i] == c.logit && skip-- == 0) c.expert = from * V + i;
+  }
+  return c;
+}
+
+// More experts than the lists hold: the winner looks for its next one.
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ Choice choose_wide(const Raw<T, V, VEC>& raw, int E, int k, int lane,
+                                              float (&l)[V]) {
+  uint32_t taken = 0;
   float head = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -216,24 +342,21 @@ __device__ __forceinline__ Choice choose32(const Raw<float, V, VEC>& raw, int E,
   }
   Choice c{-1, -INFINITY, -INFINITY};
   for (int j = 0; j < k; ++j) {
-    // floats in the order of unsigned numbers (-0 made +0): one instruction
-    // finds the warp's largest
     const uint32_t bits = __float_as_uint(head + 0.f);
-    const uint32_t key = (bits & 0x80000000u) ? ~bits : bits | 0x80000000u;
+    const uint32_t key = bits ^ ((uint32_t)((int)bits >> 31) | 0x80000000u);
     const uint32_t m = __reduce_max_sync(kAll, key);
-    const int src = __ffs(__ballot_sync(kAll, key == m)) - 1;  // the lowest lane: lowest experts
+    const int src = __ffs(__ballot_sync(kAll, key == m)) - 1;
     int at = 0;
     const float value = head;
     if (lane == src) {
 #pragma unroll
       for (int i = V - 1; i >= 0; --i)
-        if (l[i] == value) at = i;
+        if (l[i] == value && !((taken >> i) & 1)) at = i;
+      taken |= 1u << at;
       head = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i == at) l[i] = -INFINITY;
-        head = fmaxf(head, l[i]);
-      }
+      for (int i = 0; i < V; ++i)
+        if (!((taken >> i) & 1)) head = fmaxf(head, l[i]);
     }
     const float best = __shfl_sync(kAll, value, src);
     if (best == -INFINITY) break;
@@ -255,8 +378,11 @@ __device__ __forceinline__ void finish_group(const RouteArgs& a, int g, float do
 
 template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
-  extern __shared__ float smem[];  // P [warps][E], counts [E]
+  extern __shared__ __align__(16) float smem[];  // P [warps][E], counts [E]
   int* sc = reinterpret_cast<int*>(smem + kWarps * a.E);
+  // 32-bit logits: a token's, for the look-up of its choices
+  constexpr bool kLook = std::is_same<T, float>::value && V <= 8;
+  __shared__ __align__(16) float row_smem[kLook ? kWarps * 32 * V : 4];
   __shared__ float red[kWarps], sz[kWarps];
   __shared__ int sn[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -287,9 +413,12 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
     }
     const size_t row = (size_t)g * a.T + t;
     Choice c{-1, -INFINITY, -INFINITY};
+    float p[V];  // the logits, then their exponentials
     if (on) {
-      if constexpr (std::is_same<T, float>::value) c = choose32(now, a.E, a.k, lane);
-      else c = choose16(now, a.E, a.k, lane);
+      if constexpr (V > 8) c = choose_wide(now, a.E, a.k, lane, p);
+      else if constexpr (std::is_same<T, float>::value)
+        c = choose32(now, a.E, a.k, lane, p, row_smem + warp * 32 * V);
+      else c = choose16(now, a.E, a.k, lane, p);
     }
     const float m = c.top;
     if (m == -INFINITY) {  // padding, or nothing to choose from
@@ -300,22 +429,21 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
       if (lane < 2) a.stats[2 * row + lane] = 0.f;
       continue;
     }
-    float p[V];
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) s += p[v] = __expf(now.at(v, a.E, lane) - m);
+    for (int v = 0; v < V; ++v) s += p[v] = exp_of(p[v] - m);
     s = moe::warp_sum(s);
-    const float inv = 1.f / s;
+    const float inv = __fdividef(1.f, s);
 #pragma unroll
     for (int v = 0; v < V; ++v) psum[v] = fmaf(p[v], inv, psum[v]);
-    const float lse = m + logf(s);
+    const float lse = m + __logf(s);
     zsum = fmaf(lse, lse, zsum);
     ++n;
-    const float u = __expf(c.logit - m);  // 0 where nothing was chosen
+    const float u = exp_of(c.logit - m);  // 0 where nothing was chosen
     const float total = a.renorm ? moe::warp_sum(u) : s;
     if (lane < a.k) {
       a.experts[row * a.k + lane] = c.expert;
-      a.weights[row * a.k + lane] = a.scale * (u / total);
+      a.weights[row * a.k + lane] = a.scale * __fdividef(u, total);
       if (c.expert >= 0) atomicAdd(&sc[c.expert], 1);
     }
     if (lane < 2) a.stats[2 * row + lane] = lane ? s : m;
@@ -414,32 +542,6 @@ struct RouteBackArgs {
   int blocks;  // CTAs per group
 };
 
-// A lane's V floats in shared memory, 16 bytes at a time.
-template <int V>
-__device__ __forceinline__ void put(float* p, const float (&x)[V]) {
-  if constexpr (V >= 4) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] = x[i];
-  }
-}
-template <int V>
-__device__ __forceinline__ void get(const float* p, float (&x)[V]) {
-  if constexpr (V >= 4) {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p + i);
-      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = p[i];
-  }
-}
-
 // CTAs of a group's own, so that a E c / (k n^2) stays in registers.
 template <typename T, int V, bool VEC>
 __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArgs a) {
@@ -493,13 +595,13 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
     }
     const int at = now.at < a.E ? now.at : -1;
     const float dw = at >= 0 ? a.scale * now.dw : 0.f;
-    const float m = now.m, inv = 1.f / now.s;
-    const float lz = cz * (m + logf(now.s));
+    const float m = now.m, inv = __fdividef(1.f, now.s);
+    const float lz = cz * (m + __logf(now.s));
     float p[V];
     float dot = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      p[v] = __expf(now.raw.at(v, a.E, lane) - m) * inv;
+      p[v] = exp_of(now.raw.at(v, a.E, lane) - m) * inv;
       dot = fmaf(p[v], base[v], dot);
     }
     if (a.dweights) {
@@ -515,7 +617,7 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
       put<V>(add + lane * V, d);
       float x = dw;
       if (a.renorm) {
-        const float q = u / moe::warp_sum(u);
+        const float q = __fdividef(u, moe::warp_sum(u));
         x = q * (dw - moe::warp_sum(q * dw));
       } else {
         dot = fmaf(u, dw, dot);
