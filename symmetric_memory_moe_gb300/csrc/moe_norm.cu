@@ -26,6 +26,9 @@ using namespace symm_host;
 
 namespace {
 
+#ifndef NCAP
+#define NCAP 8
+#endif
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kChunk = 8;
@@ -880,7 +883,7 @@ Shape shape_of(int D) {
 // CTAs, at most: enough threads per SM to fill it.
 int grid_of(int T, int D) {
   const int per_sm = std::max(1, 1024 / shape_of(D).threads);
-  return std::max(1, std::min(T, std::max(sm_count(), 1) * std::min(per_sm, 8)));
+  return std::max(1, std::min(T, std::max(sm_count(), 1) * std::min(per_sm, NCAP)));
 }
 
 constexpr size_t kSmemPerSm = 227 * 1024;
