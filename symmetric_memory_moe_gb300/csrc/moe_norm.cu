@@ -26,9 +26,6 @@ using namespace symm_host;
 
 namespace {
 
-#ifndef NCAP
-#define NCAP 8
-#endif
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kChunk = 8;
@@ -134,6 +131,9 @@ struct Cols {
 __device__ __forceinline__ void copy16(uint32_t smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem), "l"(src) : "memory");
+}
 __device__ __forceinline__ void commit_group() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -204,88 +204,211 @@ __device__ __forceinline__ uint32_t pack<__half>(F2 a) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A thread's columns of aligned rows, and a ring of rows in shared memory in
-// which the thread keeps these columns only: it copies them in
-// (asynchronously, one group per row) and reads them back itself, so nothing
-// but its own groups is waited for, and rows of the next tokens are on their
-// way while a token is summed and normed.  The chunks past D are 0.
-template <typename T, int CH>
+// A thread's columns of every row, and a ring of rows in shared memory in
+// which the thread keeps these columns: it copies them in (asynchronously) and
+// reads them back itself, so nothing but its own copies is waited for, and rows
+// of the next tokens are on their way while a token is summed and normed.
+// Columns past D are 0.
+//
+// WIDE (16-byte aligned rows, D a multiple of 8): chunk c is 8 consecutive
+// columns in 16-byte vectors.  Otherwise chunk c is words of 4 bytes that are
+// blockDim.x apart, a column or (16-bit types) a pair 2i, 2i + 1 of them each.
+// A row of a 16-bit type may start in the middle of a word: its word i then
+// holds columns 2i - 1 and 2i, and a pair is put together from this lane's word
+// and the next lane's (the last lane keeps one word more).
+template <typename T, int CH, bool WIDE>
 struct Ring {
-  static constexpr int kVec = (int)sizeof(T) * kChunk / 16;  // 16-byte vectors of a chunk
-  uint32_t base, slot_bytes;  // of this thread's first vector; of a row in shared memory
-  int o[CH];                  // first column of each chunk
-  bool in[CH];                // ... lies in the row
-  __device__ __forceinline__ Ring(const void* smem, int D, int depth) {
-    base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16u;
-    slot_bytes = (uint32_t)(CH * kVec * (int)blockDim.x) * 16u;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      o[c] = (c * (int)blockDim.x + (int)threadIdx.x) * kChunk;
-      in[c] = o[c] < D;
-    }
-    for (int s = 0; s < depth; ++s)
+  static constexpr int kBytes = (int)sizeof(T) * kChunk;  // of a chunk
+  static constexpr int kVec = WIDE ? kBytes / 16 : kBytes / 4;  // copies of a chunk
+  static constexpr int kUnit = WIDE ? 16 : 4;
+  static constexpr bool kPairs16 = !WIDE && sizeof(T) == 2;
+  uint32_t base, slot_bytes, last_base;  // of this thread's first copy; of a slot
+  uint32_t odd;                          // slots whose row starts in the middle of a word
+  int D;
+  __device__ __forceinline__ Ring(const void* smem, int D_, int depth) : odd(0), D(D_) {
+    const uint32_t s = (uint32_t)__cvta_generic_to_shared(smem);
+    slot_bytes = bytes_of_slot((int)blockDim.x);
+    base = s + threadIdx.x * (uint32_t)kUnit;
+    last_base = s + (uint32_t)(CH * kVec * (int)blockDim.x) * 4u + (threadIdx.x >> 5) * 4u;
+    for (int i = 0; i < depth; ++i)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        if (!in[c])
 #pragma unroll
-          for (int v = 0; v < kVec; ++v)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(s, c, v)), "r"(0)
+        for (int v = 0; v < kVec; ++v) {
+          if (kPairs16 || col(c, v) < D) continue;  // copied, or masked when read
+          if constexpr (WIDE)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(i, c, v)), "r"(0)
                          : "memory");
+          else
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at(i, c, v)), "r"(0) : "memory");
+        }
+  }
+  // of shared memory, per row
+  __host__ __device__ static uint32_t bytes_of_slot(int threads) {
+    const uint32_t words = kPairs16 ? (uint32_t)(CH * kVec * (threads / 32)) * 4u : 0u;
+    return (uint32_t)(CH * kVec * threads) * kUnit + (words + 15u) / 16u * 16u;
   }
   __device__ __forceinline__ uint32_t at(int slot, int c, int v) const {
-    return base + (uint32_t)slot * slot_bytes + (uint32_t)((c * kVec + v) * (int)blockDim.x) * 16u;
+    return base + (uint32_t)slot * slot_bytes +
+           (uint32_t)((c * kVec + v) * (int)blockDim.x) * (uint32_t)kUnit;
+  }
+  // the last lane's further word
+  __device__ __forceinline__ uint32_t at_last(int slot, int c, int v) const {
+    return last_base + (uint32_t)slot * slot_bytes +
+           (uint32_t)((c * kVec + v) * (int)(blockDim.x >> 5)) * 4u;
+  }
+  // first column of copy v of chunk c
+  __device__ __forceinline__ int col(int c, int v) const {
+    if constexpr (WIDE)
+      return (c * (int)blockDim.x + (int)threadIdx.x) * kChunk + v * (16 / (int)sizeof(T));
+    else
+      return ((c * kVec + v) * (int)blockDim.x + (int)threadIdx.x) * (kPairs16 ? 2 : 1);
+  }
+  // columns of pair p of chunk c
+  __device__ __forceinline__ int lo(int c, int p) const {
+    if constexpr (WIDE) return col(c, 0) + 2 * p;
+    else return kPairs16 ? col(c, p) : col(c, 2 * p);
+  }
+  __device__ __forceinline__ int hi(int c, int p) const {
+    if constexpr (WIDE || kPairs16) return lo(c, p) + 1;
+    else return col(c, 2 * p + 1);
   }
   // starts the copy of `row`
-  __device__ __forceinline__ void copy(int slot, const T* row) const {
+  __device__ __forceinline__ void copy(int slot, const T* row) {
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (in[c])
+      for (int c = 0; c < CH; ++c)
+        if (col(c, 0) < D)
 #pragma unroll
-        for (int v = 0; v < kVec; ++v)
-          copy16(at(slot, c, v), reinterpret_cast<const uint4*>(row + o[c]) + v);
-  }
-  __device__ __forceinline__ void read(int slot, int c, F2 (&f)[kPairs]) const {
-    uint4 raw[kVec];
+          for (int v = 0; v < kVec; ++v) copy16(at(slot, c, v), row + col(c, v));
+    } else if constexpr (kPairs16) {
+      const uint32_t mid = (uint32_t)(reinterpret_cast<uintptr_t>(row) >> 1) & 1u;
+      odd = (odd & ~(1u << slot)) | (mid << slot);
 #pragma unroll
-    for (int v = 0; v < kVec; ++v)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(raw[v].x), "=r"(raw[v].y), "=r"(raw[v].z), "=r"(raw[v].w)
-                   : "r"(at(slot, c, v))
-                   : "memory");
-    if constexpr (kVec == 1) {
-      f[0] = unpack<T>(raw[0].x), f[1] = unpack<T>(raw[0].y);
-      f[2] = unpack<T>(raw[0].z), f[3] = unpack<T>(raw[0].w);
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          const int o = col(c, v);
+          if (o < D + (int)mid) copy4(at(slot, c, v), row + o - mid);
+          if (mid && (threadIdx.x & 31) == 31 && o + 1 < D)
+            copy4(at_last(slot, c, v), row + o + 1);
+        }
     } else {
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) {
-        f[2 * v] = mk(__uint_as_float(raw[v].x), __uint_as_float(raw[v].y));
-        f[2 * v + 1] = mk(__uint_as_float(raw[v].z), __uint_as_float(raw[v].w));
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+          if (col(c, v) < D) copy4(at(slot, c, v), row + col(c, v));
+    }
+  }
+  __device__ __forceinline__ void read(int slot, int c, F2 (&f)[kPairs]) const {
+    if constexpr (WIDE) {
+      uint4 raw[kVec];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(raw[v].x), "=r"(raw[v].y), "=r"(raw[v].z), "=r"(raw[v].w)
+                     : "r"(at(slot, c, v))
+                     : "memory");
+      if constexpr (kVec == 1) {
+        f[0] = unpack<T>(raw[0].x), f[1] = unpack<T>(raw[0].y);
+        f[2] = unpack<T>(raw[0].z), f[3] = unpack<T>(raw[0].w);
+      } else {
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          f[2 * v] = mk(__uint_as_float(raw[v].x), __uint_as_float(raw[v].y));
+          f[2 * v + 1] = mk(__uint_as_float(raw[v].z), __uint_as_float(raw[v].w));
+        }
+      }
+    } else {
+      uint32_t w[kVec];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) w[v] = word(at(slot, c, v));
+      if constexpr (kPairs16) {
+        if ((odd >> slot) & 1) {
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            uint32_t next = __shfl_down_sync(0xffffffffu, w[v], 1);
+            if ((threadIdx.x & 31) == 31) next = word(at_last(slot, c, v));
+            w[v] = __funnelshift_r(w[v], next, 16);
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+          // a word may hold a neighbour of the row where the row's columns end
+          if (hi(c, v) >= D) w[v] = lo(c, v) < D ? w[v] & 0xffffu : 0u;
+          f[v] = unpack<T>(w[v]);
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p)
+          f[p] = mk(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1]));
       }
     }
   }
   __device__ __forceinline__ void store(T* row, int c, const F2 (&f)[kPairs]) const {
-    if (!in[c]) return;
-    uint4* p = reinterpret_cast<uint4*>(row + o[c]);
-    if constexpr (kVec == 1) {
-      *p = make_uint4(pack<T>(f[0]), pack<T>(f[1]), pack<T>(f[2]), pack<T>(f[3]));
-    } else {
+    if constexpr (WIDE) {
+      if (col(c, 0) >= D) return;
+      uint4* p = reinterpret_cast<uint4*>(row + col(c, 0));
+      if constexpr (kVec == 1) {
+        *p = make_uint4(pack<T>(f[0]), pack<T>(f[1]), pack<T>(f[2]), pack<T>(f[3]));
+      } else {
 #pragma unroll
-      for (int v = 0; v < kVec; ++v)
-        *reinterpret_cast<ulonglong2*>(p + v) = make_ulonglong2(f[2 * v].v, f[2 * v + 1].v);
+        for (int v = 0; v < kVec; ++v)
+          *reinterpret_cast<ulonglong2*>(p + v) = make_ulonglong2(f[2 * v].v, f[2 * v + 1].v);
+      }
+    } else if constexpr (kPairs16) {
+      const bool mid = (reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        const uint32_t w = pack<T>(f[p]);
+        uint16_t* o = reinterpret_cast<uint16_t*>(row + lo(c, p));
+        if (!mid && hi(c, p) < D) {
+          *reinterpret_cast<uint32_t*>(o) = w;
+        } else {
+          if (lo(c, p) < D) o[0] = (uint16_t)w;
+          if (hi(c, p) < D) o[1] = (uint16_t)(w >> 16);
+        }
+      }
+    } else {
+      put(reinterpret_cast<float*>(row), c, f);
     }
   }
   // chunk c of a float vector; `none` where it is NULL
   __device__ __forceinline__ void vec(const float* p, int c, float none, F2 (&f)[kPairs]) const {
-    if (p && in[c]) {
+    if constexpr (WIDE) {
+      if (p && col(c, 0) < D) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(p + o[c]) + v);
-        f[2 * v].v = x.x, f[2 * v + 1].v = x.y;
+        for (int v = 0; v < 2; ++v) {
+          const ulonglong2 x = __ldg(reinterpret_cast<const ulonglong2*>(p + col(c, 0)) + v);
+          f[2 * v].v = x.x, f[2 * v + 1].v = x.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) f[i] = mk(none);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) f[i] = mk(none);
+      for (int i = 0; i < kPairs; ++i)
+        f[i] = p ? mk(lo(c, i) < D ? __ldg(p + lo(c, i)) : 0.f,
+                      hi(c, i) < D ? __ldg(p + hi(c, i)) : 0.f)
+                 : mk(none);
     }
+  }
+  // ... and stored
+  __device__ __forceinline__ void put(float* p, int c, const F2 (&f)[kPairs]) const {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      float a, b;
+      split(f[i], a, b);
+      if (lo(c, i) < D) p[lo(c, i)] = a;
+      if (hi(c, i) < D) p[hi(c, i)] = b;
+    }
+  }
+  __device__ __forceinline__ static uint32_t word(uint32_t addr) {
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
+    return w;
   }
 };
 
@@ -323,66 +446,13 @@ __device__ __forceinline__ void weighted(const A& a, const C& cols, size_t t, in
   }
 }
 
-template <typename T, bool ALIGNED, int CH>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const NormArgs a) {
-  __shared__ float red[kMaxWarps];
-  const Cols<T, ALIGNED> cols{a.D};
-  const float mean = 1.f / (float)a.D;
-  for (size_t t = blockIdx.x; t < (size_t)a.T; t += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + t * a.ld;
-    float z[CH][kChunk];
-    float r1 = 1.f, r2 = 1.f;
-    if (a.y) {
-      float ss = 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        weighted<T>(a, cols, t, c, z[c]);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) ss = fmaf(z[c][i], z[c][i], ss);
-      }
-      if (a.w_post) r1 = 1.f / sqrtf(moe::block_sum(ss, red) * mean + a.eps);
-      const float s = (a.gate ? a.gate[t] : 1.f) * r1;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float v[kChunk], res[kChunk], w[kChunk];
-        cols.load(x, c, v);
-        cols.vec(a.res, c, 1.f, res);
-        cols.vec(a.w_post, c, 1.f, w);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) z[c][i] = fmaf(s * w[i], z[c][i], res[i] * v[i]);
-        cols.store(static_cast<T*>(a.xo) + t * a.ld, c, z[c]);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) cols.load(x, c, z[c]);
-    }
-    if (a.h) {
-      float ss = 0.f;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) ss = fmaf(z[c][i], z[c][i], ss);
-      r2 = 1.f / sqrtf(moe::block_sum(ss, red) * mean + a.eps);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        float w[kChunk];
-        cols.vec(a.w_pre, c, 1.f, w);
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) w[i] *= z[c][i] * r2;
-        cols.store(static_cast<T*>(a.h) + t * a.ld, c, w);
-      }
-    }
-    if (a.rstd && threadIdx.x == 0) a.rstd[2 * t] = r1, a.rstd[2 * t + 1] = r2;
-  }
-}
-
-// The forward pass on 16-byte aligned rows.  Bound by HBM: (k + 3) rows a
-// token.  The next DEPTH - 1 rows are in flight.
-template <typename T, int CH, int DEPTH>
+// The forward pass.  Bound by HBM: (k + 3) rows a token.  The next DEPTH - 1
+// rows are in flight.
+template <typename T, int CH, bool WIDE, int DEPTH>
 __global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2) norm_stream_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
-  const Ring<T, CH> ring(smem, a.D, DEPTH);
+  Ring<T, CH, WIDE> ring(smem, a.D, DEPTH);
   const int lane = threadIdx.x & 31;
   const float mean = 1.f / (float)a.D;
   const size_t step = gridDim.x;
@@ -622,19 +692,18 @@ __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackAr
     }
 }
 
-// The backward pass on 16-byte aligned rows, when shared memory holds a whole
-// token: (2k + 5) rows through HBM a token, and Y read twice from shared memory
+// The backward pass, when shared memory holds a whole token: (2k + 5) rows through HBM a token, and Y read twice from shared memory
 // only -- for y, and for the inner products with it.  Every row has its own
 // place there (dh, z, dxo, x, Y_0 ..): the first four are copied in one group
 // for the next token as soon as they are used up, and row j of Y when this
 // token's is.
-template <typename T, int CH>
+template <typename T, int CH, bool WIDE>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     norm_back_stream_kernel(const NormBackArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
   __shared__ float dots[kMaxWarps][SYMM_MOE_MAX_TOPK];  // <dy / r1, Y_j> per warp
-  const Ring<T, CH> ring(smem, a.D, 4 + a.k);
+  Ring<T, CH, WIDE> ring(smem, a.D, 4 + a.k);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const float mean = 1.f / (float)a.D;
   const size_t step = gridDim.x;
@@ -836,16 +905,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   wait_groups<0>();
   float* part = a.part + (size_t)blockIdx.x * 3 * a.D;
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-    if (ring.in[c]) {
-#pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        float* o = part + ring.o[c] + 2 * i;
-        split(s_res[c][i], o[0], o[1]);
-        split(s_post[c][i], o[a.D], o[a.D + 1]);
-        split(s_pre[c][i], o[2 * (size_t)a.D], o[2 * (size_t)a.D + 1]);
-      }
-    }
+  for (int c = 0; c < CH; ++c) {
+    ring.put(part, c, s_res[c]);
+    ring.put(part + a.D, c, s_post[c]);
+    ring.put(part + 2 * (size_t)a.D, c, s_pre[c]);
+  }
 }
 
 // Adds the CTAs' column sums: a warp's lanes take 32 columns, the CTA's warps
@@ -880,28 +944,30 @@ Shape shape_of(int D) {
   const int ch = chunks <= 256 ? 1 : (chunks <= 1024 ? 2 : 4);
   return {ch, std::min(kMaxThreads, ((chunks + ch - 1) / ch + 31) / 32 * 32)};
 }
-// CTAs, at most: enough threads per SM to fill it.
-int grid_of(int T, int D) {
-  const int per_sm = std::max(1, 1024 / shape_of(D).threads);
-  return std::max(1, std::min(T, std::max(sm_count(), 1) * std::min(per_sm, NCAP)));
-}
-
 constexpr size_t kSmemPerSm = 227 * 1024;
 
-// Rows of the forward ring: 7 with two CTAs per SM, else 3; 0: not even 3 fit.
-size_t ring_row(int D, size_t es) {
-  const Shape sh = shape_of(D);
-  return (size_t)sh.ch * sh.threads * kChunk * es;
+// CTAs: at most per_sm on every SM, and no more than the rounds of tokens need
+// (the backward pass joins their column sums).
+int grid_of(int T, int per_sm) {
+  const int64_t most = (int64_t)std::max(sm_count(), 1) * per_sm;
+  const int64_t rounds = ((int64_t)T + most - 1) / most;
+  return rounds ? (int)((T + rounds - 1) / rounds) : 1;
 }
-int forward_depth(int D, size_t es) {
-  const size_t row = ring_row(D, es);
-  if (7 * row <= kSmemPerSm / 2 - 2048) return 7;
-  return 3 * row <= kSmemPerSm - 2048 ? 3 : 0;
+int most_per_sm(int D) { return std::max(1, std::min(8, 1024 / shape_of(D).threads)); }
+
+// Bytes of shared memory of a row in a Ring.
+size_t ring_row(int D, size_t es, bool wide) {
+  const Shape sh = shape_of(D);
+  const size_t extra = !wide && es == 2 ? (size_t)sh.ch * 4 * (sh.threads / 32) * 4 : 0;
+  return (size_t)sh.ch * sh.threads * kChunk * es + (extra + 15) / 16 * 16;
+}
+// Rows of the forward ring: 7 with two CTAs per SM, else 3.
+int forward_depth(int D, size_t es, bool wide) {
+  return 7 * ring_row(D, es, wide) <= kSmemPerSm / 2 - 2048 ? 7 : 3;
 }
 // Bytes of shared memory of a token's rows in the backward pass; 0: too many.
-size_t back_ring(int D, size_t es, int k) {
-  const Shape sh = shape_of(D);
-  const size_t bytes = (size_t)(4 + k) * sh.ch * sh.threads * kChunk * es;
+size_t back_ring(int D, size_t es, int k, bool wide) {
+  const size_t bytes = (size_t)(4 + k) * ring_row(D, es, wide);
   return bytes <= kSmemPerSm - 8192 ? bytes : 0;
 }
 
@@ -955,7 +1021,7 @@ extern "C" int moe_block_norm_workspace(int T, int D, size_t* bytes) {
     if (!bytes) return fail(SYMM_EINVAL, "moe_block_norm_workspace: NULL bytes");
     if (T < 0 || D < 1 || D > SYMM_MOE_MAX_WIDTH)
       return fail(SYMM_EINVAL, "moe_block_norm_workspace: T must be >= 0 and D in [1, 16384]");
-    *bytes = ((size_t)grid_of(T, D) * 3 * D * 4 + 255) & ~(size_t)255;
+    *bytes = ((size_t)grid_of(T, most_per_sm(D)) * 3 * D * 4 + 255) & ~(size_t)255;
     return SYMM_OK;
   });
 }
@@ -989,22 +1055,19 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
                      T, D, k, xo, h, rstd};
     const Shape sh = shape_of(D);
     cudaStream_t s = as_stream(stream);
-    const int depth = al ? forward_depth(D, es) : 0;
-    const size_t ring = (size_t)depth * ring_row(D, es);
+    const int depth = forward_depth(D, es, al);
+    const size_t ring = (size_t)depth * ring_row(D, es, al);
+    const int per_sm = (int)std::max<size_t>(
+        1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 1024)));
     rc = SYMM_OK;
     dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
       using E = decltype(t);
       constexpr int CH = decltype(c)::value;
-      if (depth) {
-        const auto kernel = depth == 7 ? norm_stream_kernel<E, CH, 7> : norm_stream_kernel<E, CH, 3>;
-        rc = allow_smem((const void*)kernel, ring, "moe_block_norm: set-up");
-        const int per_sm = (int)std::max<size_t>(
-            1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 1024)));
-        const int grid = std::max(1, std::min(T, std::max(sm_count(), 1) * per_sm));
-        if (!rc) kernel<<<(unsigned)grid, sh.threads, ring, s>>>(a);
-      } else {
-        norm_kernel<E, decltype(b)::value, CH><<<(unsigned)grid_of(T, D), sh.threads, 0, s>>>(a);
-      }
+      constexpr bool WIDE = decltype(b)::value;
+      const auto kernel =
+          depth == 7 ? norm_stream_kernel<E, CH, WIDE, 7> : norm_stream_kernel<E, CH, WIDE, 3>;
+      rc = allow_smem((const void*)kernel, ring, "moe_block_norm: set-up");
+      if (!rc) kernel<<<(unsigned)grid_of(T, per_sm), sh.threads, ring, s>>>(a);
     });
     return rc ? rc : cuda_check(cudaGetLastError(), "moe_block_norm: launch");
   });
@@ -1051,29 +1114,35 @@ extern "C" int moe_block_norm_backward(
     const NormBackArgs a{dxo, dh, x, xo, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre,
                          rstd, T, D, k, dx, dy, dweights, dgate, dres, dw_post, dw_pre,
                          static_cast<float*>(workspace)};
-    int grid = grid_of(T, D);
     cudaStream_t s = as_stream(stream);
-    const size_t ring = al ? back_ring(D, es, k) : 0;
+    if (T == 0) {  // empty sums
+      for (float* p : {dres, dw_post, dw_pre})
+        if (p && !rc)
+          rc = cuda_check(cudaMemsetAsync(p, 0, (size_t)D * 4, s),
+                          "moe_block_norm_backward: empty sums");
+      return rc;
+    }
     const Shape sh = shape_of(D);
+    const size_t ring = back_ring(D, es, k, al);
+    const int fit = ring ? (int)std::max<size_t>(1, (kSmemPerSm - 2048) / (ring + 6144)) : 8;
+    const int grid = grid_of(T, std::min(most_per_sm(D), fit));
     rc = SYMM_OK;
     dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
       using E = decltype(t);
       constexpr int CH = decltype(c)::value;
+      constexpr bool WIDE = decltype(b)::value;
       if (ring) {
-        rc = allow_smem((const void*)norm_back_stream_kernel<E, CH>, ring,
+        rc = allow_smem((const void*)norm_back_stream_kernel<E, CH, WIDE>, ring,
                         "moe_block_norm_backward: set-up");
-        const int per_sm = (int)std::max<size_t>(
-            1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 6144)));
-        grid = std::min(grid, std::max(sm_count(), 1) * per_sm);
-        if (!rc) norm_back_stream_kernel<E, CH><<<(unsigned)grid, sh.threads, ring, s>>>(a);
+        if (!rc) norm_back_stream_kernel<E, CH, WIDE><<<(unsigned)grid, sh.threads, ring, s>>>(a);
       } else {
-        norm_back_kernel<E, decltype(b)::value, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
+        norm_back_kernel<E, WIDE, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
       }
     });
     if (!rc) rc = cuda_check(cudaGetLastError(), "moe_block_norm_backward: launch");
     if (rc || (!dres && !dw_post && !dw_pre)) return rc;
-    norm_join_kernel<<<(unsigned)((3 * D + 31) / 32), 32 * kJoinWarps, 0, s>>>(a.part, grid, D, dres, dw_post,
-                                                                    dw_pre);
+    norm_join_kernel<<<(unsigned)((3 * D + 31) / 32), 32 * kJoinWarps, 0, s>>>(
+        a.part, grid, D, dres, dw_post, dw_pre);
     return cuda_check(cudaGetLastError(), "moe_block_norm_backward: join");
   });
 }

@@ -257,6 +257,36 @@ def test_backward_of_many_tokens_gives_equal_bits():
     check_back(i, "bf16", f, dxo, dh, a)
 
 
+def test_backward_of_no_tokens_gives_empty_sums():
+    g = [torch.full((48,), 9.0, device="cuda") for _ in range(3)]
+    w = torch.ones(48, device="cuda")
+    ws = torch.empty(abi.moe_block_norm_workspace(0, 48), dtype=torch.uint8, device="cuda")
+    abi.moe_block_norm_backward(None, ptr(ws), None, None, 48, ptr(ws), 48, None, 0, None, None,
+                                ptr(w), ptr(w), ptr(w), None, 2, 0, 48, 1, None, None, None, None,
+                                *[ptr(t) for t in g], ptr(ws))
+    for t in g:
+        assert not t.any()
+
+
+ODD = [  # T, D, k, dtype: rows that start in the middle of a word, at the ring's edges
+    (5, 1, 2, "bf16"), (4, 31, 3, "f16"), (6, 63, 2, "bf16"), (3, 255, 8, "f16"),
+    (7, 257, 4, "bf16"), (3, 511, 3, "f16"), (2, 2047, 8, "bf16"), (3, 2049, 2, "f16"),
+    (2, 4097, 8, "bf16"), (2, 7167, 8, "bf16"), (2, 8191, 4, "f16"), (2, 16383, 3, "bf16"),
+    (5, 33, 2, "f32"), (3, 7167, 8, "f32"), (900, 65, 3, "bf16"),
+]
+
+
+@pytest.mark.parametrize("T,D,k,dt", ODD)
+def test_odd_rows(T, D, k, dt):
+    i = make(T, D, k, dt, T + D, drop=True, spare=3)
+    g = torch.Generator().manual_seed(3)
+    dxo, dh = (torch.randn(T, D, generator=g).to(DTYPES[dt]).cuda() for _ in range(2))
+    for ld, ldy in ((D, D), (D + 1, D + 2), (D + 3, D + 1)):
+        f = forward(i, dt, ld, ldy)
+        check_forward(i, dt, *f)
+        check_back(i, dt, f, dxo, dh, back(i, dt, f, dxo, dh, ld, ldy))
+
+
 def test_backward_against_differences():
     """<gradients, directions> against a central difference of the 64-bit scalar."""
     T, D, k = 20, 96, 3
