@@ -137,6 +137,9 @@ __device__ __forceinline__ void copy4(uint32_t smem, const void* src) {
 __device__ __forceinline__ void commit_group() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ void dependents_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -210,26 +213,29 @@ __device__ __forceinline__ uint32_t pack<__half>(F2 a) {
 // of the next tokens are on their way while a token is summed and normed.
 // Columns past D are 0.
 //
-// WIDE (16-byte aligned rows, D a multiple of 8): chunk c is 8 consecutive
-// columns in 16-byte vectors.  Otherwise chunk c is words of 4 bytes that are
-// blockDim.x apart, a column or (16-bit types) a pair 2i, 2i + 1 of them each.
+// NT = 0 (16-byte aligned rows, D a multiple of 8): chunk c is 8 consecutive
+// columns in 16-byte vectors.  Otherwise, with a block of NT threads (known
+// here, so that the many small copies need no address arithmetic), chunk c is
+// words of 4 bytes that are NT words apart, a column or (16-bit types) a pair
+// 2i, 2i + 1 of them each.
 // A row of a 16-bit type may start in the middle of a word: its word i then
 // holds columns 2i - 1 and 2i, and a pair is put together from this lane's word
 // and the next lane's (the last lane keeps one word more).
-template <typename T, int CH, bool WIDE>
+template <typename T, int CH, int NT>
 struct Ring {
+  static constexpr bool WIDE = NT == 0;
   static constexpr int kBytes = (int)sizeof(T) * kChunk;  // of a chunk
   static constexpr int kVec = WIDE ? kBytes / 16 : kBytes / 4;  // copies of a chunk
   static constexpr int kUnit = WIDE ? 16 : 4;
   static constexpr bool kPairs16 = !WIDE && sizeof(T) == 2;
-  uint32_t base, slot_bytes, last_base;  // of this thread's first copy; of a slot
-  uint32_t odd;                          // slots whose row starts in the middle of a word
+  uint32_t base, last_base;  // of this thread's first copy
+  uint32_t odd;              // slots whose row starts in the middle of a word
   int D;
+  __device__ __forceinline__ static int threads() { return WIDE ? (int)blockDim.x : NT; }
   __device__ __forceinline__ Ring(const void* smem, int D_, int depth) : odd(0), D(D_) {
     const uint32_t s = (uint32_t)__cvta_generic_to_shared(smem);
-    slot_bytes = bytes_of_slot((int)blockDim.x);
     base = s + threadIdx.x * (uint32_t)kUnit;
-    last_base = s + (uint32_t)(CH * kVec * (int)blockDim.x) * 4u + (threadIdx.x >> 5) * 4u;
+    last_base = s + (uint32_t)(CH * kVec * threads()) * 4u + (threadIdx.x >> 5) * 4u;
     for (int i = 0; i < depth; ++i)
 #pragma unroll
       for (int c = 0; c < CH; ++c)
@@ -249,20 +255,24 @@ struct Ring {
     return (uint32_t)(CH * kVec * threads) * kUnit + (words + 15u) / 16u * 16u;
   }
   __device__ __forceinline__ uint32_t at(int slot, int c, int v) const {
-    return base + (uint32_t)slot * slot_bytes +
-           (uint32_t)((c * kVec + v) * (int)blockDim.x) * (uint32_t)kUnit;
+    return base + (uint32_t)slot * bytes_of_slot(threads()) +
+           (uint32_t)((c * kVec + v) * threads()) * (uint32_t)kUnit;
   }
   // the last lane's further word
   __device__ __forceinline__ uint32_t at_last(int slot, int c, int v) const {
-    return last_base + (uint32_t)slot * slot_bytes +
-           (uint32_t)((c * kVec + v) * (int)(blockDim.x >> 5)) * 4u;
+    return last_base + (uint32_t)slot * bytes_of_slot(threads()) +
+           (uint32_t)((c * kVec + v) * (threads() / 32)) * 4u;
   }
   // first column of copy v of chunk c
   __device__ __forceinline__ int col(int c, int v) const {
     if constexpr (WIDE)
-      return (c * (int)blockDim.x + (int)threadIdx.x) * kChunk + v * (16 / (int)sizeof(T));
+      return (c * threads() + (int)threadIdx.x) * kChunk + v * (16 / (int)sizeof(T));
     else
-      return ((c * kVec + v) * (int)blockDim.x + (int)threadIdx.x) * (kPairs16 ? 2 : 1);
+      return ((c * kVec + v) * threads() + (int)threadIdx.x) * (kPairs16 ? 2 : 1);
+  }
+  // whether copy v of chunk c lies in the row for every thread (words only)
+  __device__ __forceinline__ bool inside(int c, int v) const {
+    return D >= (c * kVec + v + 1) * threads() * (kPairs16 ? 2 : 1);
   }
   // columns of pair p of chunk c
   __device__ __forceinline__ int lo(int c, int p) const {
@@ -289,7 +299,7 @@ struct Ring {
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
           const int o = col(c, v);
-          if (o < D + (int)mid) copy4(at(slot, c, v), row + o - mid);
+          if (inside(c, v) || o < D + (int)mid) copy4(at(slot, c, v), row + o - mid);
           if (mid && (threadIdx.x & 31) == 31 && o + 1 < D)
             copy4(at_last(slot, c, v), row + o + 1);
         }
@@ -298,7 +308,7 @@ struct Ring {
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
-          if (col(c, v) < D) copy4(at(slot, c, v), row + col(c, v));
+          if (inside(c, v) || col(c, v) < D) copy4(at(slot, c, v), row + col(c, v));
     }
   }
   __device__ __forceinline__ void read(int slot, int c, F2 (&f)[kPairs]) const {
@@ -336,7 +346,7 @@ struct Ring {
 #pragma unroll
         for (int v = 0; v < kVec; ++v) {
           // a word may hold a neighbour of the row where the row's columns end
-          if (hi(c, v) >= D) w[v] = lo(c, v) < D ? w[v] & 0xffffu : 0u;
+          if (!inside(c, v) && hi(c, v) >= D) w[v] = lo(c, v) < D ? w[v] & 0xffffu : 0u;
           f[v] = unpack<T>(w[v]);
         }
       } else {
@@ -363,7 +373,7 @@ struct Ring {
       for (int p = 0; p < kPairs; ++p) {
         const uint32_t w = pack<T>(f[p]);
         uint16_t* o = reinterpret_cast<uint16_t*>(row + lo(c, p));
-        if (!mid && hi(c, p) < D) {
+        if (!mid && (inside(c, p) || hi(c, p) < D)) {
           *reinterpret_cast<uint32_t*>(o) = w;
         } else {
           if (lo(c, p) < D) o[0] = (uint16_t)w;
@@ -446,13 +456,17 @@ __device__ __forceinline__ void weighted(const A& a, const C& cols, size_t t, in
   }
 }
 
+// CTAs of NT (0: up to 512) threads that make up `threads`.
+constexpr int blocks_of(int threads, int NT) { return threads / (NT ? NT : kMaxThreads); }
+
 // The forward pass.  Bound by HBM: (k + 3) rows a token.  The next DEPTH - 1
 // rows are in flight.
-template <typename T, int CH, bool WIDE, int DEPTH>
-__global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2) norm_stream_kernel(const NormArgs a) {
+template <typename T, int CH, int NT, int DEPTH>
+__global__ void __launch_bounds__(NT ? NT : kMaxThreads, CH == 4 ? 1 : blocks_of(1024, NT))
+    norm_stream_kernel(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
-  Ring<T, CH, WIDE> ring(smem, a.D, DEPTH);
+  Ring<T, CH, NT> ring(smem, a.D, DEPTH);
   const int lane = threadIdx.x & 31;
   const float mean = 1.f / (float)a.D;
   const size_t step = gridDim.x;
@@ -559,6 +573,7 @@ __global__ void __launch_bounds__(kMaxThreads, CH == 4 ? 1 : 2) norm_stream_kern
 
 template <typename T, bool ALIGNED, int CH>
 __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackArgs a) {
+  dependents_may_start();
   __shared__ float red[kMaxWarps];
   __shared__ float dots[kMaxWarps][2 * SYMM_MOE_MAX_TOPK];  // <dn, Y_j>, <n, Y_j> per warp
   const Cols<T, ALIGNED> cols{a.D};
@@ -697,13 +712,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackAr
 // place there (dh, z, dxo, x, Y_0 ..): the first four are copied in one group
 // for the next token as soon as they are used up, and row j of Y when this
 // token's is.
-template <typename T, int CH, bool WIDE>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+template <typename T, int CH, int NT>
+__global__ void __launch_bounds__(NT ? NT : kMaxThreads, blocks_of(512, NT))
     norm_back_stream_kernel(const NormBackArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
+  dependents_may_start();
   __shared__ float red[2][kMaxWarps];
   __shared__ float dots[kMaxWarps][SYMM_MOE_MAX_TOPK];  // <dy / r1, Y_j> per warp
-  Ring<T, CH, WIDE> ring(smem, a.D, 4 + a.k);
+  Ring<T, CH, NT> ring(smem, a.D, 4 + a.k);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const float mean = 1.f / (float)a.D;
   const size_t step = gridDim.x;
@@ -913,8 +929,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 }
 
 // Adds the CTAs' column sums: a warp's lanes take 32 columns, the CTA's warps
-// an eighth of the partial sums each, in a fixed order.
-constexpr int kJoinWarps = 8;
+// an equal part of the partial sums each, in a fixed order.  Started while the
+// pass over the tokens runs; waits for its end.
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     norm_join_kernel(const float* part, int blocks, int D, float* dres, float* dw_post,
                      float* dw_pre) {
@@ -923,10 +940,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int i = blockIdx.x * 32 + lane;
   float* out = i < D ? dres : (i < 2 * D ? dw_post : (i < 3 * D ? dw_pre : nullptr));
   float s = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (out) {
     const int b1 = blocks * (warp + 1) / kJoinWarps;
 #pragma unroll 8
-    for (int b = blocks * warp / kJoinWarps; b < b1; ++b) s += part[(size_t)b * 3 * D + i];
+    for (int b = blocks * warp / kJoinWarps; b < b1; ++b) s += __ldcg(part + (size_t)b * 3 * D + i);
   }
   sums[warp][lane] = s;
   __syncthreads();
@@ -936,14 +954,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   }
 }
 
+// Chunks per thread and threads of a block.  Wide rows: two chunks as soon as
+// two warps have one (the work of a token that does not depend on its width
+// is done by every warp: 20 against 16 us at 4000 x 8 rows of 1024).
 struct Shape {
   int ch, threads;
 };
-Shape shape_of(int D) {
+Shape shape_of(int D, bool wide) {
   const int chunks = (D + kChunk - 1) / kChunk;
-  const int ch = chunks <= 256 ? 1 : (chunks <= 1024 ? 2 : 4);
-  return {ch, std::min(kMaxThreads, ((chunks + ch - 1) / ch + 31) / 32 * 32)};
+  if (wide) {
+    const int ch = chunks <= 64 ? 1 : (chunks <= 1024 ? 2 : 4);
+    return {ch, std::min(kMaxThreads, ((chunks + ch - 1) / ch + 31) / 32 * 32)};
+  }
+  if (chunks <= 256) return {1, chunks <= 64 ? 64 : (chunks <= 128 ? 128 : 256)};
+  return {chunks <= 1024 ? 2 : 4, chunks <= 512 ? 256 : 512};
 }
+
 constexpr size_t kSmemPerSm = 227 * 1024;
 
 // CTAs: at most per_sm on every SM, and no more than the rounds of tokens need
@@ -953,11 +979,13 @@ int grid_of(int T, int per_sm) {
   const int64_t rounds = ((int64_t)T + most - 1) / most;
   return rounds ? (int)((T + rounds - 1) / rounds) : 1;
 }
-int most_per_sm(int D) { return std::max(1, std::min(8, 1024 / shape_of(D).threads)); }
+int most_per_sm(int D, bool wide) {
+  return std::max(1, std::min(8, 1024 / shape_of(D, wide).threads));
+}
 
 // Bytes of shared memory of a row in a Ring.
 size_t ring_row(int D, size_t es, bool wide) {
-  const Shape sh = shape_of(D);
+  const Shape sh = shape_of(D, wide);
   const size_t extra = !wide && es == 2 ? (size_t)sh.ch * 4 * (sh.threads / 32) * 4 : 0;
   return (size_t)sh.ch * sh.threads * kChunk * es + (extra + 15) / 16 * 16;
 }
@@ -971,20 +999,34 @@ size_t back_ring(int D, size_t es, int k, bool wide) {
   return bytes <= kSmemPerSm - 8192 ? bytes : 0;
 }
 
+// Calls f with the element type, CH and NT (0: wide rows) as template arguments.
 template <typename F>
-void dispatch(int dtype, bool al, int ch, F&& f) {
-  auto by_ch = [&](auto t, auto b) {
-    if (ch == 1) f(t, b, std::integral_constant<int, 1>());
-    else if (ch == 2) f(t, b, std::integral_constant<int, 2>());
-    else f(t, b, std::integral_constant<int, 4>());
+void dispatch(int dtype, bool wide, Shape sh, F&& f) {
+  auto by_shape = [&](auto t) {
+    using std::integral_constant;
+    auto with = [&](auto ch, auto nt) { f(t, ch, nt); };
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 4> four;
+    if (wide) {
+      const integral_constant<int, 0> any;
+      if (sh.ch == 1) with(one, any);
+      else if (sh.ch == 2) with(two, any);
+      else with(four, any);
+    } else if (sh.ch == 1) {
+      if (sh.threads == 64) with(one, integral_constant<int, 64>());
+      else if (sh.threads == 128) with(one, integral_constant<int, 128>());
+      else with(one, integral_constant<int, 256>());
+    } else if (sh.ch == 2) {
+      if (sh.threads == 256) with(two, integral_constant<int, 256>());
+      else with(two, integral_constant<int, 512>());
+    } else {
+      with(four, integral_constant<int, 512>());
+    }
   };
-  auto by_align = [&](auto t) {
-    if (al) by_ch(t, std::true_type());
-    else by_ch(t, std::false_type());
-  };
-  if (dtype == SYMM_DTYPE_F32) by_align(float());
-  else if (dtype == SYMM_DTYPE_BF16) by_align(__nv_bfloat16());
-  else by_align(__half());
+  if (dtype == SYMM_DTYPE_F32) by_shape(float());
+  else if (dtype == SYMM_DTYPE_BF16) by_shape(__nv_bfloat16());
+  else by_shape(__half());
 }
 
 int check_norm(const char* what, size_t ld, const void* y, size_t ldy, int dtype, int T, int D,
@@ -1021,7 +1063,8 @@ extern "C" int moe_block_norm_workspace(int T, int D, size_t* bytes) {
     if (!bytes) return fail(SYMM_EINVAL, "moe_block_norm_workspace: NULL bytes");
     if (T < 0 || D < 1 || D > SYMM_MOE_MAX_WIDTH)
       return fail(SYMM_EINVAL, "moe_block_norm_workspace: T must be >= 0 and D in [1, 16384]");
-    *bytes = ((size_t)grid_of(T, most_per_sm(D)) * 3 * D * 4 + 255) & ~(size_t)255;
+    const int most = std::max(most_per_sm(D, true), most_per_sm(D, false));
+    *bytes = ((size_t)grid_of(T, most) * 3 * D * 4 + 255) & ~(size_t)255;
     return SYMM_OK;
   });
 }
@@ -1053,19 +1096,18 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
                     (!y || ldy * es % 16 == 0) && all_aligned(16, {res, w_post, w_pre});
     const NormArgs a{x, ld, y, ldy, rows, yrows, weights, gate, res, w_post, w_pre, eps,
                      T, D, k, xo, h, rstd};
-    const Shape sh = shape_of(D);
+    const Shape sh = shape_of(D, al);
     cudaStream_t s = as_stream(stream);
     const int depth = forward_depth(D, es, al);
     const size_t ring = (size_t)depth * ring_row(D, es, al);
     const int per_sm = (int)std::max<size_t>(
         1, std::min<size_t>(1024 / sh.threads, (kSmemPerSm - 2048) / (ring + 1024)));
     rc = SYMM_OK;
-    dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
+    dispatch(dtype, al, sh, [&](auto t, auto c, auto n) {
       using E = decltype(t);
-      constexpr int CH = decltype(c)::value;
-      constexpr bool WIDE = decltype(b)::value;
+      constexpr int CH = decltype(c)::value, NT = decltype(n)::value;
       const auto kernel =
-          depth == 7 ? norm_stream_kernel<E, CH, WIDE, 7> : norm_stream_kernel<E, CH, WIDE, 3>;
+          depth == 7 ? norm_stream_kernel<E, CH, NT, 7> : norm_stream_kernel<E, CH, NT, 3>;
       rc = allow_smem((const void*)kernel, ring, "moe_block_norm: set-up");
       if (!rc) kernel<<<(unsigned)grid_of(T, per_sm), sh.threads, ring, s>>>(a);
     });
@@ -1122,27 +1164,35 @@ extern "C" int moe_block_norm_backward(
                           "moe_block_norm_backward: empty sums");
       return rc;
     }
-    const Shape sh = shape_of(D);
+    const Shape sh = shape_of(D, al);
     const size_t ring = back_ring(D, es, k, al);
     const int fit = ring ? (int)std::max<size_t>(1, (kSmemPerSm - 2048) / (ring + 6144)) : 8;
-    const int grid = grid_of(T, std::min(most_per_sm(D), fit));
+    const int grid = grid_of(T, std::min(most_per_sm(D, al), fit));
     rc = SYMM_OK;
-    dispatch(dtype, al, sh.ch, [&](auto t, auto b, auto c) {
+    dispatch(dtype, al, sh, [&](auto t, auto c, auto n) {
       using E = decltype(t);
-      constexpr int CH = decltype(c)::value;
-      constexpr bool WIDE = decltype(b)::value;
+      constexpr int CH = decltype(c)::value, NT = decltype(n)::value;
       if (ring) {
-        rc = allow_smem((const void*)norm_back_stream_kernel<E, CH, WIDE>, ring,
+        rc = allow_smem((const void*)norm_back_stream_kernel<E, CH, NT>, ring,
                         "moe_block_norm_backward: set-up");
-        if (!rc) norm_back_stream_kernel<E, CH, WIDE><<<(unsigned)grid, sh.threads, ring, s>>>(a);
+        if (!rc) norm_back_stream_kernel<E, CH, NT><<<(unsigned)grid, sh.threads, ring, s>>>(a);
       } else {
-        norm_back_kernel<E, WIDE, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
+        norm_back_kernel<E, NT == 0, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
       }
     });
     if (!rc) rc = cuda_check(cudaGetLastError(), "moe_block_norm_backward: launch");
     if (rc || (!dres && !dw_post && !dw_pre)) return rc;
-    norm_join_kernel<<<(unsigned)((3 * D + 31) / 32), 32 * kJoinWarps, 0, s>>>(
-        a.part, grid, D, dres, dw_post, dw_pre);
-    return cuda_check(cudaGetLastError(), "moe_block_norm_backward: join");
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((3 * D + 31) / 32));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_check(cudaLaunchKernelEx(&cfg, norm_join_kernel, (const float*)a.part, grid, D,
+                                         dres, dw_post, dw_pre),
+                      "moe_block_norm_backward: join");
   });
 }
