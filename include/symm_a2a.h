@@ -551,8 +551,12 @@ int moe_adapter_workspace(int T, int k, int n, int r, size_t *bytes);
  *        means no adapter: y_t = x_t W.
  * y      device [T] rows of n, ldy elements apart.
  * x, w, a, b and y are of `dtype` (SYMM_DTYPE_F16 or _BF16).  Products are
- * summed in 32 bits, x_t A_a stays in 32 bits, and y is rounded once.  The
- * order of the sums is fixed by the sizes.
+ * summed in 32 bits and y is rounded once; scale_a x_t A_a enters the second
+ * product as the sum of two values of `dtype` (16 significant bits of bf16, 21
+ * of fp16, whose range it must not leave).  The order of the sums is fixed by
+ * the sizes.  A value that is not finite stays with its own tokens: in a or x
+ * as in the formula; in b[a] it makes NaN of its block of 128 columns of y_t for
+ * the tokens of adapter a.
  * R = 0 (with r = 0): the projection alone; a, b, scale, ids NULL.
  * 0 <= T <= 2^24; k and n multiples of 8 in [8, 2^20]; r a multiple of 8 up
  * to SYMM_MOE_MAX_RANK; ldx and ldw multiples of 8; x, w, a, b 16-byte aligned.

@@ -387,6 +387,24 @@ __device__ __forceinline__ uint32_t piece_rows(const AdapterArgs& a, uint32_t p)
   return min(64u, a.r16 - (p >> 1) * 64);
 }
 
+// Whether one of two values is an infinity or NaN.
+template <int FMT>
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+  constexpr uint32_t kExp = FMT ? 0x7f80u : 0x7c00u;
+  return (x & kExp) == kExp || (x & (kExp << 16)) == (kExp << 16);
+}
+// Whether p holds in any of the 128 threads of the epilogue (a barrier of theirs).
+__device__ __forceinline__ bool any_of(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
 // Stores 16 tokens from t0 on, column n.
 template <int FMT>
 __device__ __forceinline__ void store16(const AdapterArgs& a, const float (&acc)[16], uint32_t t0,
@@ -415,13 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // two tiles' worth, as the accumulators
   __shared__ __align__(16) uint32_t id_of[256];
   __shared__ uint32_t firsts[8], list[2][256], nlist[2];
+  // a B tile that is not finite: whose tokens (by token), left out (by stage)
+  __shared__ uint8_t spoilt[256], leave_out[kMaxStages];
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < a.stages; ++s) {
       symm::mbar_init(&full[s], 2);  // the producer, and it again or who wrote h
       symm::mbar_init(&empty[s], 1);
-      symm::mbar_init(&claimed[s], 1);  // the stage is free and h may be written
+      symm::mbar_init(&claimed[s], 1);  // B is there, and h may be written
     }
     for (int b = 0; b < 2; ++b) {
       symm::mbar_init(&tfull[b], 1);
@@ -485,10 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* buf = smem + (size_t)st * stage_bytes;
             const int id = (int)list[lb][i], row = (int)(p >> 1) * 64;
             if (elected) {
-              symm::mbar_arrive_expect_tx(&full[st], 256 * min(64u, a.r16));
-              symm::tma_load_3d(buf, &map_b, n0, row, id, &full[st]);
-              symm::tma_load_3d(buf + abytes / 2, &map_b, n0 + 64, row, id, &full[st]);
-              symm::mbar_arrive(&claimed[st]);
+              symm::mbar_arrive_expect_tx(&claimed[st], 256 * min(64u, a.r16));
+              symm::tma_load_3d(buf, &map_b, n0, row, id, &claimed[st]);
+              symm::tma_load_3d(buf + abytes / 2, &map_b, n0 + 64, row, id, &claimed[st]);
+              symm::mbar_arrive(&full[st]);
             }
             next();
           }
@@ -545,11 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* ring = smem + (size_t)st * stage_bytes;
             const uint64_t wd = symm::sw128_mnmajor_desc(ring, abytes / 2);
             const uint64_t xd = symm::sw128_kmajor_desc(ring + abytes);
+            const uint32_t todo = leave_out[st] ? 0 : steps;
             if (elected) {
-              for (uint32_t j = 0; j < steps; ++j)
+              for (uint32_t j = 0; j < todo; ++j)
                 symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, 1);
               if (npieces == 1)  // the low parts, beside the high ones
-                for (uint32_t j = 0; j < steps; ++j)
+                for (uint32_t j = 0; j < todo; ++j)
                   symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * (steps + j), idesc, 1);
               symm::tc_commit(&empty[st]);
             }
@@ -570,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t chunks = a.bt / 16;
     uint32_t it = 0;
     uint32_t phases = 0;  // of `claimed`, one bit per stage
-    bool ok = true, waited = false;
+    bool ok = true, waited = false, any_spoilt = false;
     for (uint32_t tile = first, seg = 0; ok && tile < tiles; tile += step, ++seg) {
       const uint32_t buf = seg & 1;
       const uint32_t n = (tile % a.ncol) * kBM + row, tb = tile / a.ncol, t0 = tb * a.bt;
@@ -605,6 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::group_sync(1, 128);
         if (me == 0) symm::mbar_arrive(&listed[buf]);
         if (!waited) wait_for_first_launch(), waited = true;  // for h
+        any_spoilt = false;
+        for (uint32_t i = me; i < 256; i += 128) spoilt[i] = 0;
         const uint32_t f0 = nlist[buf] * crank / C, f1 = nlist[buf] * (crank + 1) / C;
         for (uint32_t p = 0; ok && f0 < f1 && p < npieces; ++p) {
           // this thread's 16-byte chunks of the piece (at most 16: bt 256, 8
@@ -635,6 +658,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             phases ^= 1u << st;
             uint8_t* ring = smem + (size_t)st * stage_bytes + abytes;
+            // B's tile: two boxes of 64 columns, from the start of the stage
+            bool bad = false;
+            for (uint32_t v = me; v < 16 * min(64u, a.r16); v += 128) {
+              const uint32_t half = v >= 8 * min(64u, a.r16);
+              const uint4 x = *reinterpret_cast<const uint4*>(
+                  ring - abytes + half * (abytes / 2) + (v - half * 8 * min(64u, a.r16)) * 16);
+              bad |= not_finite<FMT>(x.x) | not_finite<FMT>(x.y) | not_finite<FMT>(x.z) |
+                     not_finite<FMT>(x.w);
+            }
             const uint32_t want = list[buf][i];
 #pragma unroll
             for (int c = 0; c < 16; ++c)
@@ -642,8 +674,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(ring + at[c]) =
                     id[c] == want ? v[c] : make_uint4(0, 0, 0, 0);
             symm::fence_proxy_async_shared();  // h, for the MMAs
-            symm::group_sync(1, 128);
-            if (me == 0) symm::mbar_arrive(&full[st]);
+            bad = any_of(bad);
+            if (bad) {
+              any_spoilt = true;
+              for (uint32_t c = me; c < 256; c += 128)
+                if (id_of[c] == want) spoilt[c] = 1;
+              symm::group_sync(1, 128);
+            }
+            if (me == 0) {
+              leave_out[st] = bad;
+              symm::mbar_arrive(&full[st]);
+            }
           }
         }
         if (!ok) break;
@@ -666,6 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float acc[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[j] = __uint_as_float(v[j]);
+        if (any_spoilt)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (spoilt[c * 16 + j]) acc[j] = __uint_as_float(0x7fffffffu);
         if (C == 1) {
           if (t0 + c * 16 < a.T) store16<FMT>(a, acc, t0 + c * 16, n);
         } else {  // the ring's loads have all been consumed: its memory takes the sums

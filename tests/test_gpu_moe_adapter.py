@@ -148,6 +148,27 @@ def test_unused_adapters_may_hold_anything(heap):
     assert torch.equal(y[rest], want[rest])
 
 
+@pytest.mark.parametrize("T,r,dt", [(50, 16, "bf16"), (50, 72, "f16"), (700, 32, "bf16")])
+def test_a_request_with_a_broken_adapter_harms_no_other(heap, T, r, dt):
+    """An infinity or NaN in one adapter stays with the tokens that use it."""
+    i = make(T, 200, 520, 6, r, dt, 5, "mixed")
+    want = run(heap, i, dt)
+    for name, where, value in (("b", (2, r - 1, 519), float("inf")), ("b", (0, 0, 0), float("nan")),
+                               ("b", (5, 3, 77), -float("inf")), ("a", (1, 199, 0), float("nan")),
+                               ("a", (3, 0, r - 1), float("inf"))):
+        j = dict(i, **{name: i[name].clone()})
+        j[name][where] = value
+        y = run(heap, j, dt)
+        own = i["ids"] == where[0]
+        assert own.any() and not own.all()
+        assert torch.equal(y[~own], want[~own]), (name, where)
+        assert not torch.isfinite(y[own]).all(1).any()
+        if name == "b":  # the column that it enters, and at most its block of 128
+            assert torch.isnan(y[own][:, where[2]]).all()
+            far = torch.arange(520, device="cuda") // 128 != where[2] // 128
+            assert torch.equal(y[own][:, far], want[own][:, far])
+
+
 @pytest.mark.parametrize("T,k,n,R,r", [(1, 8192, 8192, 4, 16), (64, 7168, 2048, 32, 16),
                                        (8192, 4096, 4096, 8, 32)])
 def test_large_sampled(heap, T, k, n, R, r):
