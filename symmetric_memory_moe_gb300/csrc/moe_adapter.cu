@@ -52,9 +52,11 @@ constexpr int kBM = 128, kBK = 64;
 constexpr int kThreads = 192;
 constexpr int kMaxStages = 12;
 constexpr uint32_t kATile = kBM * kBK * 2;
+// The product's ring.  (96 KB with few tokens, so that two CTAs fit on an SM and
+// one beside the first launch's, takes 21.6 us instead of 20.5 at 64 requests.)
 constexpr uint32_t kRingBytes = 200 * 1024;
 constexpr int kRankTokens = 128;  // tokens of a rank_kernel CTA, at most
-constexpr int kRankStages = 8;
+constexpr int kRankStages = 12;
 constexpr uint32_t kRankBytes = 98 * 1024;  // of its ring and sums, with two CTAs per SM
 
 struct AdapterArgs {
@@ -70,8 +72,8 @@ struct AdapterArgs {
   uint16_t* h;      // [T][2 r16]: high parts, then low parts
   uint64_t budget_ns;
   Control* ctl;
-  // rank_kernel: clusters per token block, stages, bytes of A and of a stage
-  uint32_t rk_share, rk_stages, rk_abytes, rk_stage;
+  // rank_kernel: clusters per token block, bytes of its ring and of A in a stage
+  uint32_t rk_share, rk_ring, rk_abytes;
 };
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
@@ -111,7 +113,7 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y
 __device__ __forceinline__ void dependents_may_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-__device__ __forceinline__ void wait_for_first_launch() {
+__device__ __forceinline__ void wait_for_earlier_launch() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -173,8 +175,8 @@ __global__ void __launch_bounds__(kThreads)
   using T = typename Elem<FMT>::T;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
-  // [stages] of A | x rows, 8 KB that the unused M rows may read, then the sums
-  float* sums = reinterpret_cast<float*>(smem + (size_t)a.rk_stages * a.rk_stage + 8192);
+  // the ring, 8 KB that the unused M rows may read, then the sums
+  float* sums = reinterpret_cast<float*>(smem + a.rk_ring + 8192);
   __shared__ uint64_t full[kRankStages], empty[kRankStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ __align__(16) uint32_t id_of[kRankTokens];  // by token
@@ -182,13 +184,12 @@ __global__ void __launch_bounds__(kThreads)
   __shared__ uint32_t sorted[kRankTokens];     // their ids
   __shared__ float scales[kRankTokens];        // their adapters' scales
   __shared__ uint32_t start[kRankTokens + 1];  // first position of each adapter's tokens
-  __shared__ uint32_t nitems;
+  __shared__ uint32_t nitems, most_rows;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), csize = cluster_size();
-  dependents_may_start();
 
   if (threadIdx.x == 0) {
-    for (uint32_t s = 0; s < a.rk_stages; ++s) {
+    for (uint32_t s = 0; s < kRankStages; ++s) {
       symm::mbar_init(&full[s], 1);
       symm::mbar_init(&empty[s], 1);
     }
@@ -200,6 +201,11 @@ __global__ void __launch_bounds__(kThreads)
     symm::fence_mbar_init();
   }
   if (warp == 5) symm::tmem_alloc(&tmem_slot, 256);
+  wait_for_earlier_launch();  // here: for whatever is before this call on the stream
+  // The second launch may start only now: it reads x and W at once, which that
+  // may have written; and its CTAs take TMEM, and hold it while they wait for
+  // this launch (warp 5 has this CTA's).
+  if (warp == 5) dependents_may_start();
 
   // this block's tokens, sorted by adapter (tokens without one last)
   const uint32_t group = blockIdx.x / csize, t0 = group / a.rk_share * kRankTokens;
@@ -224,7 +230,6 @@ __global__ void __launch_bounds__(kThreads)
     }
     order[pos] = (int)(t0 + mine);
     sorted[pos] = id;
-    scales[pos] = id < a.R ? a.scale[id] : 0.f;
   }
   __syncthreads();
   if (warp == 0) {
@@ -239,11 +244,20 @@ __global__ void __launch_bounds__(kThreads)
       valid += __popc(__ballot_sync(0xffffffffu, ok));
     }
     if (lane == 0) start[count] = valid, nitems = count;
+    __syncwarp();
+    uint32_t most = 16;  // rows of this cluster's largest adapter, in whole N steps
+    for (uint32_t i = share + a.rk_share * lane; i < count; i += a.rk_share * 32)
+      most = max(most, (start[i + 1] - start[i] + 15) / 16 * 16);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) most_rows = most;
   }
   symm::tc_fence_before();
   __syncthreads();
   symm::tc_fence_after();
   const uint32_t tmem = tmem_slot, items = nitems;
+  // stages of A | x rows, as many as the ring holds
+  const uint32_t stage_bytes = a.rk_abytes + most_rows * 128;
+  const uint32_t stages = min((uint32_t)kRankStages, a.rk_ring / stage_bytes);
   const uint32_t k0 = a.ktiles * crank / csize, k1 = a.ktiles * (crank + 1) / csize;
 
   if (warp == 0) {  // --------------------------------------- TMA producer
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kThreads)
           if (elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
           break;
         }
-        uint8_t* buf = smem + (size_t)st * a.rk_stage;
+        uint8_t* buf = smem + (size_t)st * stage_bytes;
         if (elected) {
           symm::mbar_arrive_expect_tx(&full[st], a.rk_abytes + rows16 * 128);
           for (uint32_t half = 0; half * 8192 < a.rk_abytes; ++half)
@@ -284,11 +298,11 @@ __global__ void __launch_bounds__(kThreads)
                         order[p0] + 16 * lane, &full[st]);
         } else if (q < rows16)
           tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
-        if (++st == a.rk_stages) st = 0, ph ^= 1;
+        if (++st == stages) st = 0, ph ^= 1;
       }
     }
-    for (uint32_t i = it > a.rk_stages ? it - a.rk_stages : 0; i < it; ++i)
-      symm::mbar_wait(&full[i % a.rk_stages], (i / a.rk_stages) & 1, a.budget_ns);
+    for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
+      symm::mbar_wait(&full[i % stages], (i / stages) & 1, a.budget_ns);
   } else if (warp == 1) {  // -------------------------------- MMA issuer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 0;
@@ -300,7 +314,7 @@ __global__ void __launch_bounds__(kThreads)
       for (uint32_t kt = k0; ok && kt < k1; ++kt) {
         if (!(ok = symm::mbar_wait_warp(&full[st], ph, a.budget_ns, a.ctl))) break;
         symm::tc_fence_after();
-        const uint8_t* tile = smem + (size_t)st * a.rk_stage;
+        const uint8_t* tile = smem + (size_t)st * stage_bytes;
         const uint64_t wd = symm::sw128_mnmajor_desc(tile);
         const uint64_t xd = symm::sw128_kmajor_desc(tile + a.rk_abytes);
         if (elected) {
@@ -310,7 +324,7 @@ __global__ void __launch_bounds__(kThreads)
                          kt != k0 || j != 0);
           symm::tc_commit(&empty[st]);
         }
-        if (++st == a.rk_stages) st = 0, ph ^= 1;
+        if (++st == stages) st = 0, ph ^= 1;
       }
       if (ok && elected) symm::tc_commit(&tfull[buf]);
     }
@@ -319,6 +333,8 @@ __global__ void __launch_bounds__(kThreads)
     symm::mbar_wait(&drain, 0, a.budget_ns);
   } else {  // ------------------------------------------- sums of this part
     const uint32_t q = (uint32_t)(warp & 3), row = 32 * q + lane;
+    for (uint32_t p = threadIdx.x - 64; p < kRankTokens; p += 128)
+      scales[p] = sorted[p] < a.R ? a.scale[sorted[p]] : 0.f;
     // B of these adapters on its way into L2, for the second launch
     for (uint32_t i = share; i < items; i += a.rk_share)
       for (uint32_t n0 = ((threadIdx.x - 64) * csize + crank) * 64; n0 < a.n;
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t k0 = a.slices * crank / C, k1 = a.slices * (crank + 1) / C;
   // The adapters come before the last ring's worth of a long part of K, where
   // the first launch is done and their loads hide behind W's; else at the end.
-  const uint32_t kp = k1 - k0 > 2 * a.stages ? k1 - a.stages : k1;
+  const uint32_t kp = k1 - k0 > 4 * a.stages ? k1 - a.stages : k1;
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
@@ -603,14 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::group_sync(1, 128);
         for (uint32_t i = me; i < 256; i += 128) {
           const uint32_t id = id_of[i];
-          bool seen = id >= a.R || (i && id_of[i - 1] == id);
-          for (uint32_t j = 0; j < (i | 31); j += 16) {  // the same for the warp's lanes
+          const uint32_t same = __match_any_sync(0xffffffffu, id);  // by every lane of the warp
+          bool seen = id >= a.R || (same & ((1u << lane) - 1)) != 0;
+          for (uint32_t j = 0; j < (i & ~31u); j += 16) {  // the same for the warp's lanes
             if (__all_sync(0xffffffffu, seen)) break;
 #pragma unroll
             for (uint32_t l = 0; l < 16; l += 4) {
               const uint4 v = *reinterpret_cast<const uint4*>(&id_of[j + l]);
-              seen |= (v.x == id && j + l < i) || (v.y == id && j + l + 1 < i) ||
-                      (v.z == id && j + l + 2 < i) || (v.w == id && j + l + 3 < i);
+              seen |= v.x == id || v.y == id || v.z == id || v.w == id;
             }
           }
           const uint32_t votes = __ballot_sync(0xffffffffu, !seen);
@@ -625,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         symm::group_sync(1, 128);
         if (me == 0) symm::mbar_arrive(&listed[buf]);
-        if (!waited) wait_for_first_launch(), waited = true;  // for h
+        if (!waited) wait_for_earlier_launch(), waited = true;  // for h
         any_spoilt = false;
         for (uint32_t i = me; i < 256; i += 128) spoilt[i] = 0;
         const uint32_t f0 = nlist[buf] * crank / C, f1 = nlist[buf] * (crank + 1) / C;
@@ -633,15 +649,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // this thread's 16-byte chunks of the piece (at most 16: bt 256, 8
           // chunks a row) and the adapters of their tokens
           const uint32_t width = (npieces == 1 ? 2 * a.r16 : piece_rows(a, p)) / 8;
+          const uint32_t wlog = 32 - __clz(width - 1);  // 2 to 8 chunks a row, in whole powers
           const uint32_t from = npieces == 1 ? 0 : (p & 1) * a.r16 + (p >> 1) * 64;
           uint4 v[16];
           uint32_t id[16], at[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const uint32_t i = me + 128 * c, tr = i / width, ch = i % width, t = t0 + tr;
+            const uint32_t tr = (me + 128 * c) >> wlog, ch = me & ((1u << wlog) - 1), t = t0 + tr;
+            const bool in = tr < a.bt && ch < width;
             id[c] = 0xffffffffu, v[c] = make_uint4(0, 0, 0, 0);
-            at[c] = tr < a.bt ? tr * 128 + ((ch ^ (tr & 7)) << 4) : 0xffffffffu;
-            if (tr < a.bt && t < a.T) {
+            at[c] = in ? tr * 128 + ((ch ^ (tr & 7)) << 4) : 0xffffffffu;
+            if (in && t < a.T) {
               id[c] = id_of[tr];
               if (id[c] < a.R)
                 v[c] = __ldcg(reinterpret_cast<const uint4*>(a.h + (size_t)t * 2 * a.r16 + from) +
@@ -650,16 +668,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           for (uint32_t i = f0; i < f1; ++i, ++it) {
             const uint32_t st = it % a.stages;
-            // not `empty`: whose phases this warp does not follow one by one
-            if (!symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl)) {
-              symm::record_error(a.ctl, symm::kErrTimedOut, -7);
-              ok = false;
-              break;
-            }
+            // not `empty`: whose phases this warp does not follow one by one.  A
+            // wait that gives up takes every thread to the barrier below first.
+            ok = symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl);
             phases ^= 1u << st;
             uint8_t* ring = smem + (size_t)st * stage_bytes + abytes;
             // B's tile: two boxes of 64 columns, from the start of the stage
-            bool bad = false;
+            bool bad = !ok;
             for (uint32_t v = me; v < 16 * min(64u, a.r16); v += 128) {
               const uint32_t half = v >= 8 * min(64u, a.r16);
               const uint4 x = *reinterpret_cast<const uint4*>(
@@ -676,6 +691,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             symm::fence_proxy_async_shared();  // h, for the MMAs
             bad = any_of(bad);
             if (bad) {
+              if (any_of(!ok)) {
+                if (me == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -7);
+                ok = false;
+                break;
+              }
               any_spoilt = true;
               for (uint32_t c = me; c < 256; c += 128)
                 if (id_of[c] == want) spoilt[c] = 1;
@@ -690,8 +710,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       it += k1 - kp;
-      if (!symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
-        symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+      ok = symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+      if (any_of(!ok)) {  // all threads leave, or none
+        if (me == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+        ok = false;
         break;
       }
       symm::tc_fence_after();
@@ -758,20 +780,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // How a call of these sizes is cut up.
 struct Plan {
   uint32_t bt, ntok, ncol, ktiles, deep, slices, stages, cluster, ctas, tmem_cols, r16;
-  uint32_t rk_share, rk_cluster, rk_blocks, rk_stages, rk_abytes, rk_stage, rk_bytes;
+  uint32_t rk_share, rk_cluster, rk_blocks, rk_ring, rk_abytes, rk_bytes;
 };
 
 size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
-// Clusters of c CTAs of the product that are resident at once (their ring
-// leaves one CTA per SM), once asked for each device.
+// Clusters of c CTAs of the product that are resident at once, asked once for
+// each device.
 int resident_clusters(int fmt, uint32_t c);
 
 // Tokens per tile and CTAs per tile: the pair with the least estimated time,
 // fitted to measured times.  A 64-deep K slice costs its loads, 16 KB of W and
 // 128 bytes a token at about 125 bytes a ns per SM, or what the roles need to
 // issue it; a round of tiles costs 2 us (filling the ring, the epilogue), and
-// sharing a tile 1 us and 5 ns a token.
+// sharing a tile 2 us and 5 ns a token.
 void choose_tiles(Plan& p, uint32_t T, int fmt) {
   double best = 0;
   for (uint32_t blocks = (T + 255) / 256, i = 0; i < 8; ++i, ++blocks) {
@@ -784,7 +806,7 @@ void choose_tiles(Plan& p, uint32_t T, int fmt) {
       const uint64_t rounds = (tiles + room - 1) / room;
       const double per = (double)((p.ktiles + c - 1) / c) * slice;
       const double t = c == 1 ? rounds * per + 2000 + 500 * (rounds - 1)
-                              : rounds * (per + 3000 + 5.0 * bt);
+                              : rounds * (per + 4000 + 5.0 * bt);
       if (best == 0 || t < best) best = t, p.bt = bt, p.ntok = ntok, p.cluster = c;
     }
     if (bt == 16) break;
@@ -815,11 +837,10 @@ Plan plan_of(int T, int k, int n, int r, int fmt) {
   p.rk_share = std::max(1u, std::min(std::min((uint32_t)T, (uint32_t)kRankTokens),
                                      2 * sms / (blocks * p.rk_cluster)));
   p.rk_abytes = r <= 64 ? 8192 : 16384;
-  p.rk_stage = p.rk_abytes + std::min<uint32_t>(kRankTokens, (uint32_t)up((size_t)T, 16)) * 128;
-  // two CTAs per SM while their sums leave room for it
+  // two CTAs per SM while their sums leave room for it; two stages at the least
   const uint32_t sums = std::min<uint32_t>(kRankTokens, (uint32_t)T) * (uint32_t)r * 4;
-  p.rk_stages = std::min<uint32_t>(kRankStages, (kRankBytes - std::min(sums, 32768u)) / p.rk_stage);
-  p.rk_bytes = 1024 + p.rk_stages * p.rk_stage + 8192 + sums;
+  p.rk_ring = (kRankBytes - std::min(sums, 32768u)) / 1024 * 1024;
+  p.rk_bytes = 1024 + p.rk_ring + 8192 + sums;
   return p;
 }
 
@@ -930,7 +951,7 @@ int launch(const Plan& p, const Maps& m, const AdapterArgs& a, cudaStream_t s) {
     cfg.gridDim = dim3(p.rk_blocks * p.rk_share * p.rk_cluster);
     cfg.dynamicSmemBytes = p.rk_bytes;
     attr[0].val.clusterDim.x = p.rk_cluster;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     rc = cuda_check(cudaLaunchKernelEx(&cfg, rank_kernel<FMT>, m.a, m.rows, m.rows16, m.b, a),
                     "moe_adapter_matmul: rank products");
     if (rc) return rc;
@@ -1007,8 +1028,7 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
     g.deep = p.deep, g.slices = p.slices;
     g.stages = p.stages, g.cluster = p.cluster, g.tmem_cols = p.tmem_cols;
     g.h = static_cast<uint16_t*>(workspace);
-    g.rk_share = p.rk_share, g.rk_stages = p.rk_stages, g.rk_abytes = p.rk_abytes;
-    g.rk_stage = p.rk_stage;
+    g.rk_share = p.rk_share, g.rk_ring = p.rk_ring, g.rk_abytes = p.rk_abytes;
     g.budget_ns = heap->spin_budget;
     g.ctl = reinterpret_cast<Control*>(heap->base);
     return fmt ? launch<1>(p, m, g, s) : launch<0>(p, m, g, s);

@@ -215,3 +215,28 @@ def test_graph_capture(heap):
 def test_no_tokens(heap):
     abi.moe_adapter_matmul(heap.handle, None, 8, None, 8, None, None, None, None, 1, 0, 8, 8, 0, 0,
                            None, 8, None)
+
+
+@pytest.mark.parametrize("T,k,n", [(3, 4096, 4096), (300, 512, 1024)])
+def test_inputs_written_just_before_on_the_stream(heap, T, k, n):
+    """What an earlier kernel of the stream still writes is read after it: x, W,
+    the adapters and the ids arrive by copies that take longer than a launch."""
+    a, b = (make(T, k, n, 3, 16, "bf16", s, "mixed") for s in (1, 2))
+    want = [run(heap, i, "bf16") for i in (a, b)]
+    live = {m: v.clone() for m, v in a.items()}
+    y = torch.empty(T, n, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(abi.moe_adapter_workspace(T, k, n, 16), dtype=torch.uint8, device="cuda")
+    slow = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    got = []
+    for j in range(6):
+        slow.add_(1)
+        for m in ("ids", "scale", "a", "b", "w", "x"):
+            live[m].copy_((a, b)[j % 2][m])
+        abi.moe_adapter_matmul(heap.handle, ptr(live["x"]), k, ptr(live["w"]), n, ptr(live["a"]),
+                               ptr(live["b"]), ptr(live["scale"]), ptr(live["ids"]), 1, T, k, n, 3,
+                               16, ptr(y), n, ws.data_ptr())
+        got.append(y.clone())
+    torch.cuda.synchronize()
+    assert abi.symm_check_error(heap.handle)[0] == abi.SYMM_OK
+    for j, g in enumerate(got):
+        assert torch.equal(g, want[j % 2]), j
