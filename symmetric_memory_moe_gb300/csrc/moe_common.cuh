@@ -60,6 +60,32 @@ __device__ __forceinline__ float block_sum_once(float v, float* red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
+// Programmatic dependent launch: a kernel launched by launch() may start while
+// the one before it on the stream ends; wait_for_earlier() holds it (before its
+// first access to memory) until that one's writes are visible.
+// let_next_start() is for a kernel whose own second launch follows.
+__device__ __forceinline__ void wait_for_earlier() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+int launch(const char* what, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+           cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return symm_host::cuda_check(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...), what);
+}
+
 inline size_t dtype_bytes(int dtype) { return dtype == SYMM_DTYPE_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) {
   return dtype == SYMM_DTYPE_F16 || dtype == SYMM_DTYPE_BF16 || dtype == SYMM_DTYPE_F32;

@@ -137,9 +137,6 @@ __device__ __forceinline__ void copy4(uint32_t smem, const void* src) {
 __device__ __forceinline__ void commit_group() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ void dependents_may_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 template <int N>
 __device__ __forceinline__ void wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -467,6 +464,7 @@ __global__ void __launch_bounds__(NT ? NT : kMaxThreads, CH == 4 ? 1 : blocks_of
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][kMaxWarps];
   Ring<T, CH, NT> ring(smem, a.D, DEPTH);
+  moe::wait_for_earlier();
   const int lane = threadIdx.x & 31;
   const float mean = 1.f / (float)a.D;
   const size_t step = gridDim.x;
@@ -573,7 +571,8 @@ __global__ void __launch_bounds__(NT ? NT : kMaxThreads, CH == 4 ? 1 : blocks_of
 
 template <typename T, bool ALIGNED, int CH>
 __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackArgs a) {
-  dependents_may_start();
+  moe::wait_for_earlier();
+  moe::let_next_start();
   __shared__ float red[kMaxWarps];
   __shared__ float dots[kMaxWarps][2 * SYMM_MOE_MAX_TOPK];  // <dn, Y_j>, <n, Y_j> per warp
   const Cols<T, ALIGNED> cols{a.D};
@@ -716,7 +715,8 @@ template <typename T, int CH, int NT>
 __global__ void __launch_bounds__(NT ? NT : kMaxThreads, blocks_of(512, NT))
     norm_back_stream_kernel(const NormBackArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  dependents_may_start();
+  moe::wait_for_earlier();
+  moe::let_next_start();
   __shared__ float red[2][kMaxWarps];
   __shared__ float dots[kMaxWarps][SYMM_MOE_MAX_TOPK];  // <dy / r1, Y_j> per warp
   Ring<T, CH, NT> ring(smem, a.D, 4 + a.k);
@@ -940,7 +940,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int i = blockIdx.x * 32 + lane;
   float* out = i < D ? dres : (i < 2 * D ? dw_post : (i < 3 * D ? dw_pre : nullptr));
   float s = 0.f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  moe::wait_for_earlier();
   if (out) {
     const int b1 = blocks * (warp + 1) / kJoinWarps;
 #pragma unroll 8
@@ -1109,9 +1109,11 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
       const auto kernel =
           depth == 7 ? norm_stream_kernel<E, CH, NT, 7> : norm_stream_kernel<E, CH, NT, 3>;
       rc = allow_smem((const void*)kernel, ring, "moe_block_norm: set-up");
-      if (!rc) kernel<<<(unsigned)grid_of(T, per_sm), sh.threads, ring, s>>>(a);
+      if (!rc)
+        rc = moe::launch("moe_block_norm: launch", kernel, (unsigned)grid_of(T, per_sm),
+                         (unsigned)sh.threads, ring, s, a);
     });
-    return rc ? rc : cuda_check(cudaGetLastError(), "moe_block_norm: launch");
+    return rc;
   });
 }
 
@@ -1175,24 +1177,17 @@ extern "C" int moe_block_norm_backward(
       if (ring) {
         rc = allow_smem((const void*)norm_back_stream_kernel<E, CH, NT>, ring,
                         "moe_block_norm_backward: set-up");
-        if (!rc) norm_back_stream_kernel<E, CH, NT><<<(unsigned)grid, sh.threads, ring, s>>>(a);
+        if (!rc)
+          rc = moe::launch("moe_block_norm_backward: launch", norm_back_stream_kernel<E, CH, NT>,
+                           (unsigned)grid, (unsigned)sh.threads, ring, s, a);
       } else {
-        norm_back_kernel<E, NT == 0, CH><<<(unsigned)grid, sh.threads, 0, s>>>(a);
+        rc = moe::launch("moe_block_norm_backward: launch", norm_back_kernel<E, NT == 0, CH>,
+                         (unsigned)grid, (unsigned)sh.threads, 0, s, a);
       }
     });
-    if (!rc) rc = cuda_check(cudaGetLastError(), "moe_block_norm_backward: launch");
     if (rc || (!dres && !dw_post && !dw_pre)) return rc;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((3 * D + 31) / 32));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_check(cudaLaunchKernelEx(&cfg, norm_join_kernel, (const float*)a.part, grid, D,
-                                         dres, dw_post, dw_pre),
-                      "moe_block_norm_backward: join");
+    return moe::launch("moe_block_norm_backward: join", norm_join_kernel,
+                       (unsigned)((3 * D + 31) / 32), 32 * kJoinWarps, 0, s, a.part, grid, D, dres,
+                       dw_post, dw_pre);
   });
 }

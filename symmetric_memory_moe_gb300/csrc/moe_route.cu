@@ -387,8 +387,9 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
   __shared__ int sn[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = blockIdx.x / a.blocks, b = blockIdx.x % a.blocks;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int e = threadIdx.x; e < a.E; e += kThreads) sc[e] = 0;
+  moe::wait_for_earlier();
+  moe::let_next_start();
   __syncthreads();
   float psum[V];
 #pragma unroll
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(kJoinThreads) route_join_kernel(const RouteArg
   const float* part = a.part + (size_t)g * a.blocks * step;
   const int width = (a.E + 31) / 32 * 32, ways = kJoinThreads / width;  // E <= 1024
   const int e = threadIdx.x % width, way = threadIdx.x / width;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  moe::wait_for_earlier();
   float p = 0.f, z = 0.f;
   int c = 0, n = 0;
   if (way < ways && e < a.E) {
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
 #pragma unroll
   for (int v = 0; v < V; ++v) add[lane + 32 * v] = 0.f;
   __syncwarp();
+  moe::wait_for_earlier();
   const float n = (float)max(a.tokens[g], 1);
   const float cb = a.dloss ? a.dloss[2 * g] * ((float)a.E / (float)a.k) / n / n : 0.f;
   const float cz = a.dloss ? 2.f * a.dloss[2 * g + 1] / n : 0.f;
@@ -718,23 +720,13 @@ extern "C" int moe_route(const void* logits, size_t ld, const uint8_t* mask, int
       for_width(E, [&](auto v) {
         constexpr int V = decltype(v)::value;
         for_vec(vectors(logits, ld, E, V, sizeof(t)), [&](auto vec) {
-          route_kernel<decltype(t), V, decltype(vec)::value>
-              <<<(unsigned)(G * a.blocks), kThreads, (kWarps + 1) * (size_t)E * 4, s>>>(a);
+          rc = moe::launch("moe_route: launch", route_kernel<decltype(t), V, decltype(vec)::value>,
+                           (unsigned)(G * a.blocks), kThreads, (kWarps + 1) * (size_t)E * 4, s, a);
         });
       });
     });
-    rc = cuda_check(cudaGetLastError(), "moe_route: launch");
     if (rc || a.blocks == 1) return rc;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)G);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cuda_check(cudaLaunchKernelEx(&cfg, route_join_kernel, a), "moe_route: join");
+    return moe::launch("moe_route: join", route_join_kernel, (unsigned)G, kJoinThreads, 0, s, a);
   });
 }
 
@@ -771,11 +763,12 @@ extern "C" int moe_route_backward(const void* logits, size_t ld, int dtype, int 
         const bool vec = vectors(logits, ld, E, V, sizeof(t)) &&
                          vectors(dlogits, ldd, E, V, sizeof(t));
         for_vec(vec, [&](auto w) {
-          route_back_kernel<decltype(t), V, decltype(w)::value>
-              <<<(unsigned)G * (unsigned)blocks, kThreads, kWarps * 32 * V * 4, s>>>(a);
+          rc = moe::launch("moe_route_backward: launch",
+                           route_back_kernel<decltype(t), V, decltype(w)::value>,
+                           (unsigned)G * (unsigned)blocks, kThreads, kWarps * 32 * V * 4, s, a);
         });
       });
     });
-    return cuda_check(cudaGetLastError(), "moe_route_backward: launch");
+    return rc;
   });
 }
