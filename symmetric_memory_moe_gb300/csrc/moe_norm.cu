@@ -9,14 +9,20 @@
 //   dx = res dz                                dres  = sum_t dz x
 //   dgate = sum_i dz n wpost                   dwpost = sum_t gate dz n
 //   dn = gate dz wpost;  dy = r1 (dn - n mean(dn n));  dY_j = w_j dy
-//   dw_j = <dy, Y_j> = r1 (<dn, Y_j> - mean(dn n) <n, Y_j>).
-// The last form needs no second pass over Y once mean(dn n) is known: both
-// inner products are sums of the pass that finds it.
+//   dw_j = <dy, Y_j>.
+// dy needs mean(dn n), and that needs y of all rows: Y is read twice, the second
+// time from shared memory where a token's rows fit there.
 //
 // One CTA per token at a time; a thread owns the same columns in every token
 // of its CTA (up to 4 chunks of 8), so the column sums of dres, dwpost and
 // dwpre stay in its registers over all tokens and are written once per CTA;
 // a second small kernel adds the CTAs' sums in order.
+//
+// Measured (rows of 7168 in bf16, 8 a token): 8192 tokens 217.7 us, 5.94 TB/s or
+// 88 % of the copy rate; backward, 4096 tokens 272.8 us, 4.5 TB/s (67 %): a
+// token's 172 KB fill an SM's shared memory there, so its phases overlap only in
+// part.  Rows of 1024: 5.8 TB/s.  Rows that are not 16-byte aligned, or odd,
+// move by 4-byte copies: 3.2 TB/s for 999 floats, 1.7 for 3001 bf16.
 #include <algorithm>
 #include <type_traits>
 

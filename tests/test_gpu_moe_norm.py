@@ -276,6 +276,19 @@ ODD = [  # T, D, k, dtype: rows that start in the middle of a word, at the ring'
 ]
 
 
+@pytest.mark.parametrize("D,dt", [(33, "bf16"), (515, "f16"), (3001, "bf16"), (77, "f32")])
+def test_odd_rows_in_place(D, dt):
+    i = make(19, D, 3, dt, D)
+    want = forward(i, dt)
+    for a, b in zip(forward(i, dt, inplace=True), want):
+        assert torch.equal(a, b)
+    g = torch.Generator().manual_seed(3)
+    dxo, dh = (torch.randn(19, D, generator=g).to(DTYPES[dt]).cuda() for _ in range(2))
+    a, b = (back(i, dt, want, dxo, dh, inplace=p) for p in (False, True))
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
 @pytest.mark.parametrize("T,D,k,dt", ODD)
 def test_odd_rows(T, D, k, dt):
     i = make(T, D, k, dt, T + D, drop=True, spare=3)

@@ -131,6 +131,20 @@ def test_many_tokens_and_equal_bits():
     assert abs(a["loss"][0, 0].item() - want.item()) <= (W + 20100 * U32) * want.item()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("E,k", [(256, 8), (256, 9), (256, 20), (128, 12), (200, 32), (512, 20)])
+def test_neighbouring_experts_win(dt, E, k):
+    """All of one lane's experts are chosen, and more: descending, ascending and equal runs."""
+    l = torch.zeros(1, 24, E)
+    for t in range(24):
+        s = 8 * t % (E - k)
+        run = torch.arange(k).float()
+        l[0, t, s:s + k] = 2 + (run, run.flip(0), torch.zeros(k))[t % 3]
+    l = l.to(DTYPES[dt])
+    _, o = forward(l, None, k, dt, 1)
+    check_forward(o, ref.route(l, None, k, 1, 1.0), E, k, 24)
+
+
 def test_empty_groups():
     """No tokens, or none valid: zero counts and losses."""
     for T, mask in ((0, None), (6, torch.zeros(3, 6, dtype=torch.uint8))):
