@@ -999,10 +999,12 @@ size_t ring_row(int D, size_t es, bool wide) {
 int forward_depth(int D, size_t es, bool wide) {
   return 7 * ring_row(D, es, wide) <= kSmemPerSm / 2 - 2048 ? 7 : 3;
 }
-// Bytes of shared memory of a token's rows in the backward pass; 0: too many.
+// Bytes of shared memory of a token's rows in the backward pass; 0: too many
+// (a Ring has 32 slots, a bit each).  Three more rows, filled a token ahead where
+// they fit, did not pay: 280 against 273 us at 4096 x 8 rows of 7168.
 size_t back_ring(int D, size_t es, int k, bool wide) {
   const size_t bytes = (size_t)(4 + k) * ring_row(D, es, wide);
-  return bytes <= kSmemPerSm - 8192 ? bytes : 0;
+  return 4 + k <= 32 && bytes <= kSmemPerSm - 8192 ? bytes : 0;
 }
 
 // Calls f with the element type, CH and NT (0: wide rows) as template arguments.

@@ -272,7 +272,8 @@ ODD = [  # T, D, k, dtype: rows that start in the middle of a word, at the ring'
     (5, 1, 2, "bf16"), (4, 31, 3, "f16"), (6, 63, 2, "bf16"), (3, 255, 8, "f16"),
     (7, 257, 4, "bf16"), (3, 511, 3, "f16"), (2, 2047, 8, "bf16"), (3, 2049, 2, "f16"),
     (2, 4097, 8, "bf16"), (2, 7167, 8, "bf16"), (2, 8191, 4, "f16"), (2, 16383, 3, "bf16"),
-    (5, 33, 2, "f32"), (3, 7167, 8, "f32"), (900, 65, 3, "bf16"),
+    (5, 33, 2, "f32"), (3, 7167, 8, "f32"), (900, 65, 3, "bf16"), (5, 37, 32, "bf16"),
+    (6, 129, 29, "f16"), (5, 40, 30, "bf16"), (400, 7168, 8, "bf16"), (400, 515, 5, "f16"),
 ]
 
 
