@@ -20,9 +20,9 @@
 // tokens, are joined per CTA in shared memory and across CTAs by a second
 // small kernel, in a fixed order, so equal inputs give equal bits.
 //
-// Bound by what can be issued: 469 instructions a token at 256 bf16 logits and
-// k = 8, half of them minima, maxima and selects, which issue at half rate (0.68
-// a cycle and scheduler).  8 x 4096 tokens take 26.0 us (2.8 would be HBM's), the
+// Bound by what can be issued: over 400 instructions a token at 256 bf16 logits
+// and k = 8, half of them minima, maxima and selects, which issue at half rate
+// (0.67 a cycle and scheduler).  8 x 4096 tokens take 24.1 us (2.8 would be HBM's), the
 // backward pass with 32-bit logits 17.2 (4.0 TB/s; 10.2 us at the copy rate), 8
 // tokens 6.1, of which the kernel is 3.4.  So exp, log and quotients are the
 // approximate instructions (2^-21 relatively): their error is of the size of
@@ -196,16 +196,21 @@ struct Choice {
 };
 
 // k rounds: `round(j, live)` takes the largest key left and moves the winner up
-// its list, of which no more than `live` keys can still matter; false: none left.
+// its list, of which no more than `live` keys can still matter.  Rounds after
+// the lists have run empty find "none" again.
 template <typename F>
 __device__ __forceinline__ void rounds(int k, F&& round) {
-  if (k <= 8) {
+  if (k == 8) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j >= k || !round(j, 8 - j)) break;
-  } else {
-    for (int j = 0; j < k && round(j, 9); ++j) {  // 9: a list may run empty
+    for (int j = 0; j < 8; ++j) round(j, 8 - j);
+  } else if (k < 8) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      if (j >= k) break;
+      round(j, 7 - j);
     }
+  } else {
+    for (int j = 0; j < k; ++j) round(j, 9);  // 9: a list may run empty
   }
 }
 // The winner of a lane's list moves up.
@@ -270,13 +275,11 @@ __device__ __forceinline__ Choice choose16(const Raw<T, V, VEC>& raw, int E, int
   uint32_t mine = 0, first = 0;
   rounds(k, [&](int j, int live) {
     const uint32_t m = __reduce_max_sync(kAll, key[0]);
-    if (m == 0) return false;
     if (j == 0) first = m;
     if (lane == j) mine = m;
     const bool win = key[0] == m;
     if constexpr (V == 1) key[0] = win ? 0u : key[0];
     else pop<V>(key, win, live);
-    return true;
   });
   auto value = [](uint32_t key) {
     const uint16_t bits = (uint16_t)unorder16(key >> 16);
@@ -306,13 +309,11 @@ __device__ __forceinline__ Choice choose32(const Raw<float, V, VEC>& raw, int E,
   int from = 0;
   rounds(k, [&](int j, int live) {
     const uint32_t m = __reduce_max_sync(kAll, key[0]);
-    if (m <= kNone) return false;
     const int src = __ffs(__ballot_sync(kAll, key[0] == m)) - 1;  // lowest lane: lowest experts
     if (j == 0) first = m;
     if (lane == j) mine = m, from = src;
     if constexpr (V == 1) key[0] = lane == src ? 0u : key[0];
     else pop<V>(key, lane == src, live);
-    return true;
   });
   auto value = [&](uint32_t m) {
     return m > kNone ? __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m) : -INFINITY;
@@ -400,22 +401,24 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
   float zsum = 0.f;
   int n = 0;
   const int step = a.blocks * kWarps;
-  const T* logits = static_cast<const T*>(a.logits) + (size_t)g * a.T * a.ld;
   int t = b * kWarps + warp;
+  size_t row = (size_t)g * a.T + t;
+  const T* next = static_cast<const T*>(a.logits) + row * a.ld;
+  const size_t next_step = (size_t)step * a.ld;
   Raw<T, V, VEC> raw;
   uint8_t mask = 1;
   if (t < a.T) {
-    raw.load(logits + (size_t)t * a.ld, a.E, lane);
-    if (a.mask) mask = a.mask[(size_t)g * a.T + t];
+    raw.load(next, a.E, lane);
+    if (a.mask) mask = a.mask[row];
   }
-  for (; t < a.T; t += step) {
+  for (; t < a.T; t += step, row += step) {
     const Raw<T, V, VEC> now = raw;
     const uint8_t on = mask;
+    next += next_step;
     if (t + step < a.T) {  // the next token's, on their way
-      raw.load(logits + (size_t)(t + step) * a.ld, a.E, lane);
-      if (a.mask) mask = a.mask[(size_t)g * a.T + t + step];
+      raw.load(next, a.E, lane);
+      if (a.mask) mask = a.mask[row + step];
     }
-    const size_t row = (size_t)g * a.T + t;
     Choice c{-1, -INFINITY, -INFINITY};
     float p[V];  // the logits, then their exponentials
     if (on) {
