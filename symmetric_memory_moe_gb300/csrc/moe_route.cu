@@ -20,9 +20,9 @@
 // tokens, are joined per CTA in shared memory and across CTAs by a second
 // small kernel, in a fixed order, so equal inputs give equal bits.
 //
-// Bound by what can be issued: over 400 instructions a token at 256 bf16 logits
+// Bound by what can be issued: 413 instructions a token at 256 bf16 logits
 // and k = 8, half of them minima, maxima and selects, which issue at half rate
-// (0.67 a cycle and scheduler).  8 x 4096 tokens take 24.1 us (2.8 would be HBM's), the
+// (0.66 a cycle and scheduler).  8 x 4096 tokens take 24.1 us (2.8 would be HBM's), the
 // backward pass with 32-bit logits 17.2 (4.0 TB/s; 10.2 us at the copy rate), 8
 // tokens 6.1, of which the kernel is 3.4.  So exp, log and quotients are the
 // approximate instructions (2^-21 relatively): their error is of the size of
