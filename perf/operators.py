@@ -28,40 +28,40 @@ EPS = 1e-6
 def listed():
     return [
         # the router of one decoding step: 8 tokens, latency only
-        dict(name="route decode", op="route", back=False, G=1, T=8, E=256, k=8,
+        dict(name="route, one decoding step", op="route", back=False, G=1, T=8, E=256, k=8,
              dtype="f32", renorm=True, holes=False),
         # a training step's router: 8 PEs of 4096 tokens, 256 experts
-        dict(name="route train", op="route", back=False, G=8, T=4096, E=256, k=8,
+        dict(name="route, training step", op="route", back=False, G=8, T=4096, E=256, k=8,
              dtype="bf16", renorm=True, holes=False),
         # its gradient, logits kept in 32 bits
-        dict(name="route train backward", op="route", back=True, G=8, T=4096, E=256, k=8,
+        dict(name="route, training step, backward", op="route", back=True, G=8, T=4096, E=256, k=8,
              dtype="f32", renorm=True, holes=False),
         # padded sequences of odd length, few experts, some of them closed
-        dict(name="route padded", op="route", back=False, G=3, T=1531, E=60, k=4,
+        dict(name="route, padded sequences", op="route", back=False, G=3, T=1531, E=60, k=4,
              dtype="f16", renorm=False, holes=True),
         # one decoding step: 16 tokens, each with 8 expert rows of 7168
-        dict(name="norm decode", op="norm", back=False, T=16, D=7168, k=8,
+        dict(name="norm, one decoding step", op="norm", back=False, T=16, D=7168, k=8,
              dtype="bf16", post=True, holes=False),
         # a training step: 8192 tokens and their 65,536 expert rows
-        dict(name="norm train", op="norm", back=False, T=8192, D=7168, k=8,
+        dict(name="norm, training step", op="norm", back=False, T=8192, D=7168, k=8,
              dtype="bf16", post=True, holes=False),
         # its gradients
-        dict(name="norm train backward", op="norm", back=True, T=4096, D=7168, k=8,
+        dict(name="norm, training step, backward", op="norm", back=True, T=4096, D=7168, k=8,
              dtype="bf16", post=True, holes=False),
         # odd width and count, dropped rows, 32 bits
-        dict(name="norm dropped backward", op="norm", back=True, T=1531, D=999, k=2,
+        dict(name="norm, dropped rows, backward", op="norm", back=True, T=1531, D=999, k=2,
              dtype="f32", post=True, holes=True),
         # one request, one token: the weight matrix is all there is to read
-        dict(name="adapter one token", op="adapter", T=1, K=8192, N=8192, R=4, r=16,
+        dict(name="adapters, one token", op="adapter", T=1, K=8192, N=8192, R=4, r=16,
              dtype="bf16", runs=1),
         # one token each of 64 requests
-        dict(name="adapter 64 requests", op="adapter", T=64, K=7168, N=2048, R=32, r=16,
+        dict(name="adapters, 64 requests", op="adapter", T=64, K=7168, N=2048, R=32, r=16,
              dtype="bf16", runs=64),
         # prompts of 8 requests, 8192 tokens in all
-        dict(name="adapter prompts", op="adapter", T=8192, K=4096, N=4096, R=8, r=32,
+        dict(name="adapters, prompts", op="adapter", T=8192, K=4096, N=4096, R=8, r=32,
              dtype="bf16", runs=8),
         # odd sizes, some requests without an adapter
-        dict(name="adapter odd", op="adapter", T=333, K=1000, N=2056, R=5, r=8,
+        dict(name="adapters, odd sizes", op="adapter", T=333, K=1000, N=2056, R=5, r=8,
              dtype="f16", runs=9),
     ]
 
