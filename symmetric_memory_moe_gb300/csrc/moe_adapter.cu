@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kThreads)
       const T hi = moe::from_f<T>(s);
       T* out = H + (size_t)order[pos] * 2 * a.r16 + c;
       out[0] = hi;
-      out[a.r16] = moe::from_f<T>(s - moe::to_f(hi));
+      // (what an infinity or NaN leaves would be NaN)
+      out[a.r16] = moe::from_f<T>(isfinite(moe::to_f(hi)) ? s - moe::to_f(hi) : 0.f);
     }
   }
   cluster_leave();  // no CTA leaves while another reads its sums
