@@ -551,9 +551,8 @@ int moe_adapter_workspace(int T, int k, int n, int r, size_t *bytes);
  *        means no adapter: y_t = x_t W.
  * y      device [T] rows of n, ldy elements apart.
  * x, w, a, b and y are of `dtype` (SYMM_DTYPE_F16 or _BF16).  Products are
- * summed in 32 bits and y is rounded once; scale_a x_t A_a enters the second
- * product as the sum of two values of `dtype` (16 significant bits of bf16, 21
- * of fp16, whose range it must not leave).  The order of the sums is fixed by
+ * summed in 32 bits and y is rounded once; scale_a x_t A_a keeps the 24
+ * significant bits and the range of a float.  The order of the sums is fixed by
  * the sizes.  A value that is not finite stays with its own tokens: in a or x
  * as in the formula; in b[a] it makes NaN of its block of 128 columns of y_t for
  * the tokens of adapter a.

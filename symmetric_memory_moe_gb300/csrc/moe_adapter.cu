@@ -6,9 +6,11 @@
 // which each adapter of a tile's tokens is a few more K columns: B_a under W,
 // and h (0 in the rows of the other adapters' tokens) beside x.  So any
 // mixture of adapters in any order of tokens is summed in the same 32-bit
-// accumulators before the one rounding.  h enters as the sum of two values of
-// the type, so that its rounding (2^-18 relatively in bf16, 2^-22 in fp16)
-// stays far below the output's.
+// accumulators before the one rounding.  h keeps the 24 bits and the range of
+// its 32-bit sum: it enters as three bf16 values of 8 bits each.  (Two take 7 us
+// less at the prompts below, but move as many outputs across a rounding
+// boundary as the whole sum over k does.)  With fp16 inputs, whose range and
+// bits h would leave, B becomes two bf16 values, 11 bits in all, on its way.
 //
 // The product is computed as y^T = W^T x^T: the M side of a tile is 128
 // columns of W (W as stored, k x n, is an M-major operand) and the N side BT
@@ -58,6 +60,7 @@ constexpr int kBM = 128, kBK = 64;
 constexpr int kThreads = 192;
 constexpr int kMaxStages = 12;
 constexpr uint32_t kATile = kBM * kBK * 2;
+constexpr uint32_t kParts = 3;  // bf16 values that make up an element of h
 // The product's ring.  (96 KB with few tokens, so that two CTAs fit on an SM and
 // one beside the first launch's, takes 21.6 us instead of 20.5 at 64 requests.)
 constexpr uint32_t kRingBytes = 200 * 1024;
@@ -68,6 +71,7 @@ constexpr uint32_t kRankBytes = 98 * 1024;  // of its ring and sums, with two CT
 struct AdapterArgs {
   const float* scale;
   const int32_t* ids;
+  const void* b;
   void* y;
   size_t ldy;
   uint32_t T, k, n, R, r, r16;  // r16: r in whole K steps of 16
@@ -75,7 +79,7 @@ struct AdapterArgs {
   uint32_t deep, slices;            // 64-deep K tiles per slice, slices of K
   uint32_t ktiles;                  // 64-deep K tiles (rank_kernel's slices)
   uint32_t cluster, tmem_cols;  // cluster: CTAs that share a tile
-  uint16_t* h;      // [T][2 r16]: high parts, then low parts
+  uint16_t* h;      // bf16 [T][r16 / 16][3][16]: of 16 ranks, their three parts
   uint64_t budget_ns;
   Control* ctl;
   // rank_kernel: clusters per token block, bytes of its ring and of A in a stage
@@ -172,13 +176,31 @@ __device__ __forceinline__ uint32_t mma_idesc(uint32_t fmt, uint32_t n) {
 constexpr uint64_t kWStep = (16 * 128) >> 4;  // 16 K rows of an M-major tile
 constexpr uint64_t kXStep = 32 >> 4;          // 16 K columns of a K-major tile
 
+// The adapters' columns of a tile come in pieces of one ring stage: up to 4
+// steps of 16 K columns of h as it lies in memory, step 3i + j the j-th part of
+// ranks 16i ..; and the 16 or 32 ranks of B that they multiply.
+__device__ __forceinline__ uint32_t pieces_of(const AdapterArgs& a) {
+  return (a.r16 / 16 * kParts + 3) / 4;
+}
+__device__ __forceinline__ uint32_t piece_steps(const AdapterArgs& a, uint32_t p) {
+  return min(4u, a.r16 / 16 * kParts - 4 * p);
+}
+__device__ __forceinline__ uint32_t piece_rank(uint32_t p) {  // the first one
+  return 4 * p / kParts * 16;
+}
+__host__ __device__ __forceinline__ uint32_t piece_rows(uint32_t r16) {  // of B
+  return r16 < 2 * 16 ? r16 : 2 * 16;
+}
+// With fp16 inputs, rows of a stage's B from its first (high) to its second
+// (low) bf16 part.
+constexpr uint32_t kLowRows = 32;
+
 // h of up to 128 tokens: see the head of the file.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
     rank_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_x16,
                 const __grid_constant__ CUtensorMap map_b, const AdapterArgs a) {
-  using T = typename Elem<FMT>::T;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   // the ring, 8 KB that the unused M rows may read, then the sums
@@ -345,7 +367,7 @@ __global__ void __launch_bounds__(kThreads)
     for (uint32_t i = share; i < items; i += a.rk_share)
       for (uint32_t n0 = ((threadIdx.x - 64) * csize + crank) * 64; n0 < a.n;
            n0 += 128 * csize * 64)
-        for (uint32_t r0 = 0; r0 < a.r; r0 += 64)
+        for (uint32_t r0 = 0; r0 < a.r; r0 += piece_rows(a.r16))
           prefetch_3d(&map_b, (int)n0, (int)r0, (int)sorted[start[i]]);
     for (uint32_t i = share, seg = 0; i < items; i += a.rk_share, ++seg) {
       const uint32_t p0 = start[i], rows = start[i + 1] - p0, buf = seg & 1;
@@ -375,7 +397,7 @@ __global__ void __launch_bounds__(kThreads)
     symm::tmem_dealloc(tmem, 256);
   }
   // each CTA of the cluster joins its share of the sums, CTAs in order
-  T* H = reinterpret_cast<T*>(a.h);
+  __nv_bfloat16* H = reinterpret_cast<__nv_bfloat16*>(a.h);
   for (uint32_t item = share; item < items; item += a.rk_share) {
     const uint32_t p0 = start[item], n = (start[item + 1] - p0) * a.r16;
     for (uint32_t i = crank * kThreads + threadIdx.x; i < n; i += csize * kThreads) {
@@ -390,31 +412,68 @@ __global__ void __launch_bounds__(kThreads)
         for (uint32_t b = 0; b < 8; ++b) s += v[b];
         s *= scales[pos];
       }
-      const T hi = moe::from_f<T>(s);
-      T* out = H + (size_t)order[pos] * 2 * a.r16 + c;
-      out[0] = hi;
-      // (what an infinity or NaN leaves would be NaN)
-      out[a.r16] = moe::from_f<T>(isfinite(moe::to_f(hi)) ? s - moe::to_f(hi) : 0.f);
+      // three parts of 8 bits, truncated; an infinity or NaN is all in the first
+      // (what it leaves would be NaN)
+      __nv_bfloat16* out = H + (size_t)order[pos] * kParts * a.r16 + c / 16 * (kParts * 16) + c % 16;
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const __nv_bfloat16 part = __float2bfloat16_rz(s);
+        out[16 * i] = part;
+        s = isfinite(s) ? s - moe::to_f(part) : 0.f;
+      }
     }
   }
   cluster_leave();  // no CTA leaves while another reads its sums
 }
 
-// The adapters' columns of a tile come in pieces of one ring stage: h's high
-// and low parts side by side while both fit into 64 K columns, else 64 ranks
-// of one part at a time.
-__device__ __forceinline__ uint32_t pieces_of(const AdapterArgs& a) {
-  return a.r16 <= 32 ? 1 : 2 * ((a.r16 + 63) / 64);
+// The larger magnitudes of 8 values and `most`, in both halves as they are; and
+// whether one of such a pair is an infinity or NaN.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t most, const uint4& x) {
+  const uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(most, __vmaxu2(x.x & m, x.y & m)), __vmaxu2(x.z & m, x.w & m));
 }
-__device__ __forceinline__ uint32_t piece_rows(const AdapterArgs& a, uint32_t p) {  // K rows of B
-  return min(64u, a.r16 - (p >> 1) * 64);
-}
-
-// Whether one of two values is an infinity or NaN.
 template <int FMT>
-__device__ __forceinline__ bool not_finite(uint32_t x) {
-  constexpr uint32_t kExp = FMT ? 0x7f80u : 0x7c00u;
-  return (x & kExp) == kExp || (x & (kExp << 16)) == (kExp << 16);
+__device__ __forceinline__ bool not_finite(uint32_t most) {
+  constexpr uint32_t kInf = FMT ? 0x7f80u : 0x7c00u;
+  return (most & 0xffffu) >= kInf || (most >> 16) >= kInf;
+}
+// 8 fp16 values as the sums of two bf16 values: the upper 8 of their 11 bits,
+// truncated (the upper half of the float), and the rest.
+__device__ __forceinline__ void two_parts(const uint4& x, uint4& hi, uint4& lo) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(in + i));
+    const uint32_t u = __float_as_uint(f.x), v = __float_as_uint(f.y);
+    const float g = f.x - __uint_as_float(u & 0xffff0000u);
+    const float k = f.y - __uint_as_float(v & 0xffff0000u);
+    h[i] = __byte_perm(u, v, 0x7632);
+    l[i] = __byte_perm(__float_as_uint(g), __float_as_uint(k), 0x7632);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// 8 bf16 values, 0 in the place of infinities and NaN.
+__device__ __forceinline__ uint4 only_finite(uint4 x) {
+  uint32_t* w = &x.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+  }
+  return x;
+}
+// What token t's infinities and NaN in h add to column n (fp16 inputs).
+__device__ __noinline__ float wild_sum(const AdapterArgs& a, uint32_t t, uint32_t id, uint32_t n) {
+  const __half* b = static_cast<const __half*>(a.b) + (size_t)id * a.r * a.n + n;
+  const uint16_t* h = a.h + (size_t)t * kParts * a.r16;
+  float s = 0.f;
+  for (uint32_t r = 0; r < a.r; ++r) {
+    const float v = __uint_as_float((uint32_t)h[r / 16 * (kParts * 16) + r % 16] << 16);
+    if (!isfinite(v)) s += v * __half2float(b[(size_t)r * a.n]);
+  }
+  return s;
 }
 // Whether p holds in any of the 128 threads of the epilogue (a barrier of theirs).
 __device__ __forceinline__ bool any_of(bool p) {
@@ -458,6 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t firsts[8], list[2][256], nlist[2];
   // a B tile that is not finite: whose tokens (by token), left out (by stage)
   __shared__ uint8_t spoilt[256], leave_out[kMaxStages];
+  // fp16 inputs: tokens with an h that is not finite, whether there are any
+  __shared__ uint8_t wild[256];
+  __shared__ uint32_t any_wild;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -526,9 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t i = f0; i < f1; ++i) {
             if (!(ok = symm::mbar_wait_warp(&empty[st], ph, a.budget_ns, a.ctl))) break;
             uint8_t* buf = smem + (size_t)st * stage_bytes;
-            const int id = (int)list[lb][i], row = (int)(p >> 1) * 64;
+            const int id = (int)list[lb][i], row = (int)piece_rank(p);
             if (elected) {
-              symm::mbar_arrive_expect_tx(&claimed[st], 256 * min(64u, a.r16));
+              symm::mbar_arrive_expect_tx(&claimed[st], 256 * piece_rows(a.r16));
               symm::tma_load_3d(buf, &map_b, n0, row, id, &claimed[st]);
               symm::tma_load_3d(buf + abytes / 2, &map_b, n0 + 64, row, id, &claimed[st]);
               symm::mbar_arrive(&full[st]);
@@ -544,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       symm::mbar_wait(&full[i % a.stages], (i / a.stages) & 1, a.budget_ns);
   } else if (warp == 1) {  // ---------------------------------- MMA issuer
     const bool elected = symm::elect_one();
-    const uint32_t idesc = mma_idesc(FMT, a.bt);
+    const uint32_t idesc = mma_idesc(FMT, a.bt), bf16_idesc = mma_idesc(1, a.bt);
     uint32_t st = 0, ph = 0, seg = 0;
     bool ok = true;
     auto next = [&]() {
@@ -581,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = symm::mbar_wait_warp(&listed[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
         const uint32_t mine = nlist[buf] * (crank + 1) / C - nlist[buf] * crank / C;
         for (uint32_t p = 0; ok && p < npieces; ++p) {
-          const uint32_t steps = piece_rows(a, p) / 16;
+          const uint32_t steps = piece_steps(a, p);
           for (uint32_t i = 0; i < mine; ++i) {
             if (!(ok = symm::mbar_wait_warp(&full[st], ph, a.budget_ns, a.ctl))) break;
             symm::tc_fence_after();
@@ -590,11 +652,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t xd = symm::sw128_kmajor_desc(ring + abytes);
             const uint32_t todo = leave_out[st] ? 0 : steps;
             if (elected) {
-              for (uint32_t j = 0; j < todo; ++j)
-                symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * j, idesc, 1);
-              if (npieces == 1)  // the low parts, beside the high ones
-                for (uint32_t j = 0; j < todo; ++j)
-                  symm::tc_mma(acc, wd + kWStep * j, xd + kXStep * (steps + j), idesc, 1);
+              for (uint32_t j = 0; j < todo; ++j) {
+                const uint64_t b = wd + kWStep * ((4 * p + j) / kParts - 4 * p / kParts);
+                symm::tc_mma(acc, b, xd + kXStep * j, bf16_idesc, 1);
+                if (FMT == 0)
+                  symm::tc_mma(acc, b + kWStep * (kLowRows / 16), xd + kXStep * j, bf16_idesc, 1);
+              }
               symm::tc_commit(&empty[st]);
             }
             next();
@@ -624,6 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t i = me; i < 256; i += 128)
           id_of[i] = i < a.bt && t0 + i < a.T ? (uint32_t)a.ids[t0 + i] : 0xffffffffu;
         symm::group_sync(1, 128);
+        any_spoilt = false;
+        for (uint32_t i = me; i < 256; i += 128) spoilt[i] = wild[i] = 0;
+        if (me == 0) any_wild = 0;
         for (uint32_t i = me; i < 256; i += 128) {
           const uint32_t id = id_of[i];
           const uint32_t same = __match_any_sync(0xffffffffu, id);  // by every lane of the warp
@@ -649,30 +715,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::group_sync(1, 128);
         if (me == 0) symm::mbar_arrive(&listed[buf]);
         if (!waited) wait_for_earlier_launch(), waited = true;  // for h
-        any_spoilt = false;
-        for (uint32_t i = me; i < 256; i += 128) spoilt[i] = 0;
         const uint32_t f0 = nlist[buf] * crank / C, f1 = nlist[buf] * (crank + 1) / C;
-        for (uint32_t p = 0; ok && f0 < f1 && p < npieces; ++p) {
-          // this thread's 16-byte chunks of the piece (at most 16: bt 256, 8
-          // chunks a row) and the adapters of their tokens
-          const uint32_t width = (npieces == 1 ? 2 * a.r16 : piece_rows(a, p)) / 8;
-          const uint32_t wlog = 32 - __clz(width - 1);  // 2 to 8 chunks a row, in whole powers
-          const uint32_t from = npieces == 1 ? 0 : (p & 1) * a.r16 + (p >> 1) * 64;
-          uint4 v[16];
-          uint32_t id[16], at[16];
+        // This thread's 16-byte chunks of a piece (at most 16: bt 256, 8 chunks a
+        // row), the next piece's on their way; chunk c is of token tr, the ch-th.
+        struct Chunk {
+          uint32_t tr, ch;
+        };
+        auto chunk = [&](uint32_t p, int c) {
+          const uint32_t wlog = 32 - __clz(2 * piece_steps(a, p) - 1);  // whole powers, 2 to 8 a row
+          return Chunk{(me + 128 * c) >> wlog, me & ((1u << wlog) - 1)};
+        };
+        // whether no thread has a chunk c or a later one (asked once: the others'
+        // accesses are to be issued together)
+        auto none = [&](uint32_t p, int c) {
+          return c == 4 && (128u * c) >> (32 - __clz(2 * piece_steps(a, p) - 1)) >= a.bt;
+        };
+        auto load = [&](uint32_t p, uint4 (&v)[16]) {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const uint32_t tr = (me + 128 * c) >> wlog, ch = me & ((1u << wlog) - 1), t = t0 + tr;
-            const bool in = tr < a.bt && ch < width;
-            id[c] = 0xffffffffu, v[c] = make_uint4(0, 0, 0, 0);
-            at[c] = in ? tr * 128 + ((ch ^ (tr & 7)) << 4) : 0xffffffffu;
-            if (in && t < a.T) {
-              id[c] = id_of[tr];
-              if (id[c] < a.R)
-                v[c] = __ldcg(reinterpret_cast<const uint4*>(a.h + (size_t)t * 2 * a.r16 + from) +
-                              ch);
-            }
+            if (none(p, c)) break;
+            const Chunk k = chunk(p, c);
+            v[c] = make_uint4(0, 0, 0, 0);
+            if (k.tr < a.bt && k.ch < 2 * piece_steps(a, p) && id_of[k.tr] < a.R)
+              v[c] = __ldcg(reinterpret_cast<const uint4*>(
+                                a.h + (size_t)(t0 + k.tr) * kParts * a.r16 + 64 * p) + k.ch);
           }
+        };
+        uint4 next[16] = {};
+        if (f0 < f1) load(0, next);
+        for (uint32_t p = 0; ok && f0 < f1 && p < npieces; ++p) {
+          uint4 v[16];
+          uint32_t id[16], at[16], most = 0, odd = 0;  // their tokens' adapters; odd: not finite
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            at[c] = id[c] = 0xffffffffu;
+            const Chunk k = chunk(p, c);
+            const bool in = k.tr < a.bt && k.ch < 2 * piece_steps(a, p);
+            v[c] = next[c];
+            if (in) id[c] = id_of[k.tr], at[c] = k.tr * 128 + ((k.ch ^ (k.tr & 7)) << 4);
+            if (FMT == 0) most = magnitudes(most, v[c]);
+          }
+          // B's second part may be 0: what is not finite is left to the epilogue
+          if (FMT == 0 && not_finite<1>(most))
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (not_finite<1>(magnitudes(0, v[c]))) odd |= 1u << c, v[c] = only_finite(v[c]);
+          if (p + 1 < npieces) load(p + 1, next);
           for (uint32_t i = f0; i < f1; ++i, ++it) {
             const uint32_t st = it % a.stages;
             // not `empty`: whose phases this warp does not follow one by one.  A
@@ -681,22 +769,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             phases ^= 1u << st;
             uint8_t* ring = smem + (size_t)st * stage_bytes + abytes;
             // B's tile: two boxes of 64 columns, from the start of the stage
-            bool bad = !ok;
-            for (uint32_t v = me; v < 16 * min(64u, a.r16); v += 128) {
-              const uint32_t half = v >= 8 * min(64u, a.r16);
-              const uint4 x = *reinterpret_cast<const uint4*>(
-                  ring - abytes + half * (abytes / 2) + (v - half * 8 * min(64u, a.r16)) * 16);
-              bad |= not_finite<FMT>(x.x) | not_finite<FMT>(x.y) | not_finite<FMT>(x.z) |
-                     not_finite<FMT>(x.w);
+            most = 0;
+            const uint32_t brows = piece_rows(a.r16);
+            uint4 x[4];  // of 8 vectors a row and box, 16 or 32 rows
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+              uint4* box = reinterpret_cast<uint4*>(ring - abytes + (u & 1) * (abytes / 2));
+              if (me + 128 * (u >> 1) < 8 * brows) x[u] = box[me + 128 * (u >> 1)];
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+              if (me + 128 * (u >> 1) >= 8 * brows) continue;
+              most = magnitudes(most, x[u]);
+              uint4* box = reinterpret_cast<uint4*>(ring - abytes + (u & 1) * (abytes / 2));
+              if (FMT == 0)
+                two_parts(x[u], box[me + 128 * (u >> 1)], box[me + 128 * (u >> 1) + kLowRows * 8]);
             }
             const uint32_t want = list[buf][i];
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < 16; ++c) {
+              if (none(p, c)) break;
               if (at[c] != 0xffffffffu)
                 *reinterpret_cast<uint4*>(ring + at[c]) =
                     id[c] == want ? v[c] : make_uint4(0, 0, 0, 0);
-            symm::fence_proxy_async_shared();  // h, for the MMAs
-            bad = any_of(bad);
+            }
+            if (FMT == 0 && odd)
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (((odd >> c) & 1) && id[c] == want)
+                  wild[chunk(p, c).tr] = 1, any_wild = 1;
+            symm::fence_proxy_async_shared();  // h (and B's parts), for the MMAs
+            const bool bad = any_of(!ok || not_finite<FMT>(most));
             if (bad) {
               if (any_of(!ok)) {
                 if (me == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -7);
@@ -740,6 +843,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             if (spoilt[c * 16 + j]) acc[j] = __uint_as_float(0x7fffffffu);
+        if (FMT == 0 && npieces && any_wild)
+#pragma unroll 1
+          for (int j = 0; j < 16; ++j)
+            if (wild[c * 16 + j]) {
+              const float more = wild_sum(a, t0 + c * 16 + j, id_of[c * 16 + j], min(n, a.n - 1));
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i == j) acc[i] += more;
+              __syncwarp();
+            }
         if (C == 1) {
           if (t0 + c * 16 < a.T) store16<FMT>(a, acc, t0 + c * 16, n);
         } else {  // the ring's loads have all been consumed: its memory takes the sums
@@ -852,7 +965,7 @@ Plan plan_of(int T, int k, int n, int r, int fmt) {
 }
 
 // Workspace: h.
-size_t h_bytes(int T, int r) { return up((size_t)T * 2 * up((size_t)r, 16) * 2, 256); }
+size_t h_bytes(int T, int r) { return up((size_t)T * kParts * up((size_t)r, 16) * 2, 256); }
 
 int check_adapter(const char* what, int T, int k, int n, int r) {
   if (T < 0 || T > (1 << 24) || k < 8 || n < 8 || k % 8 || n % 8 || k > (1 << 20) ||
@@ -1022,14 +1135,14 @@ extern "C" int moe_adapter_matmul(symm_heap_t* heap, const void* x, size_t ldx, 
       if (!rc) rc = make_map(&m.rows16, x, fmt, (uint64_t)k, (uint64_t)T, 0, ldx, 16);
       if (!rc)
         rc = make_map(&m.b, b, fmt, (uint64_t)n, (uint64_t)r, (uint64_t)R, (size_t)n,
-                      std::min(64u, p.r16));
+                      piece_rows(p.r16));
     }
     if (rc) return rc;
     cudaStream_t s = as_stream(stream);
     rc = ensure_ctrl(heap, s);
     if (rc) return rc;
     AdapterArgs g{};
-    g.scale = scale, g.ids = ids, g.y = y, g.ldy = ldy;
+    g.scale = scale, g.ids = ids, g.b = b, g.y = y, g.ldy = ldy;
     g.T = (uint32_t)T, g.k = (uint32_t)k, g.n = (uint32_t)n, g.R = (uint32_t)R, g.r = (uint32_t)r;
     g.r16 = p.r16, g.bt = p.bt, g.ntok = p.ntok, g.ncol = p.ncol, g.ktiles = p.ktiles;
     g.deep = p.deep, g.slices = p.slices;

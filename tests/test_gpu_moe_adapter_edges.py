@@ -6,7 +6,7 @@ import torch
 
 from moe_refs import DTYPES
 from symmetric_memory_moe_gb300.torch_heap import TorchSymmHeap
-from test_gpu_moe_adapter import make, run
+from test_gpu_moe_adapter import check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,56 @@ def test_an_infinite_sum_keeps_its_sign(heap, T, r, dt):
     y = run(heap, j, dt)
     assert (y[0] == math.inf).all() and torch.isfinite(y[1:]).all()
     assert y.dtype == DTYPES[dt]
+
+
+@pytest.mark.parametrize("r", [8, 16, 32, 40, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_the_rank_sums_keep_24_bits(heap, T, r, dt):
+    """What is left of scale x A after W has taken away its first two values of the type.
+    x picks one row of A, B is the identity and scale a power of two times a float of 24
+    bits, so h = scale A[0] is one rounded product; every further product and partial
+    sum is a multiple of h's last bit below 2 |h|, exact in 32 bits in any order.  h is
+    about 2^8, so that its last bit (2^-16) is well within fp16."""
+    k, n = 64, 136
+    g = torch.Generator(device="cuda").manual_seed(r + T)
+    x = torch.zeros(T, k, device="cuda")
+    x[:, :3] = 1
+    a = torch.zeros(2, k, r, device="cuda")
+    a[:, 0] = 1 + torch.randint(0, 128, (2, r), generator=g, device="cuda") / 128
+    scale = 128 + 64 * torch.rand(2, generator=g, device="cuda")
+    h = a[1, 0] * scale[1]                                  # in 32 bits
+    h1 = h.to(DTYPES[dt]).float()
+    h2 = (h - h1).to(DTYPES[dt]).float()
+    w = torch.zeros(k, n, device="cuda")
+    w[1, :r], w[2, :r] = -h1, -h2
+    b = torch.zeros(2, r, n, device="cuda")
+    b[:, :, :r] = torch.eye(r, device="cuda")
+    i = dict(x=x, w=w, a=a, b=b)
+    i = {m: v.to(DTYPES[dt]) for m, v in i.items()}
+    i.update(scale=scale, ids=torch.ones(T, dtype=torch.int32, device="cuda"))
+    y = run(heap, i, dt).float()
+    want = h - h1 - h2
+    assert (want != 0).sum() > r // 3 or dt == "f16"
+    assert (y[:, :r] == want).all() and not y[:, r:].any()
+
+
+@pytest.mark.parametrize("r", [8, 16, 64])
+@pytest.mark.parametrize("down", [6, 10, 14, 18])
+def test_small_rank_sums_in_half_precision(heap, r, down):
+    """A far below 1 and B above it: half precision has no bits there, the sums do."""
+    i = make(70, 256, 264, 3, r, "f16", 9, "mixed")
+    i["a"] = (i["a"].float() * 2.0 ** -down / 16).half()
+    i["b"] = (i["b"].float() * 2.0 ** min(10, down)).half()
+    i["w"] = (i["w"].float() * 2.0 ** -6).half()
+    check(i, run(heap, i, "f16"), "f16")
+
+
+def test_large_rank_sums_in_half_precision(heap):
+    """scale x A beyond 65504, which B brings back."""
+    i = make(70, 256, 264, 3, 16, "f16", 9, "mixed")
+    i["a"] = (i["a"].float() * 2.0 ** 12).half()
+    i["b"] = (i["b"].float() * 2.0 ** -14).half()
+    i["scale"] = i["scale"].abs() + 2
+    assert (i["x"].double() @ i["a"][1].double() * 2).abs().max() > 2e5
+    check(i, run(heap, i, "f16"), "f16")
