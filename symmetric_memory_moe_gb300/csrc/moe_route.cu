@@ -400,22 +400,23 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const RouteArgs a) {
   for (int v = 0; v < V; ++v) psum[v] = 0.f;
   float zsum = 0.f;
   int n = 0;
-  const int step = a.blocks * kWarps;
-  int t = b * kWarps + warp;
+  // unsigned: T < 2^31, but a step past it need not be
+  const unsigned T_ = (unsigned)a.T, step = (unsigned)(a.blocks * kWarps);
+  unsigned t = (unsigned)(b * kWarps + warp);
   size_t row = (size_t)g * a.T + t;
   const T* next = static_cast<const T*>(a.logits) + row * a.ld;
   const size_t next_step = (size_t)step * a.ld;
   Raw<T, V, VEC> raw;
   uint8_t mask = 1;
-  if (t < a.T) {
+  if (t < T_) {
     raw.load(next, a.E, lane);
     if (a.mask) mask = a.mask[row];
   }
-  for (; t < a.T; t += step, row += step) {
+  for (; t < T_; t += step, row += step) {
     const Raw<T, V, VEC> now = raw;
     const uint8_t on = mask;
     next += next_step;
-    if (t + step < a.T) {  // the next token's, on their way
+    if (t + step < T_) {  // the next token's, on their way
       raw.load(next, a.E, lane);
       if (a.mask) mask = a.mask[row + step];
     }
@@ -570,7 +571,8 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
     const int e = lane * V + v;
     base[v] = e < a.E && a.dloss ? cb * (float)a.counts[(size_t)g * a.E + e] : 0.f;
   }
-  const int step = a.blocks * kWarps;
+  // unsigned: T < 2^31, but a step past it need not be
+  const unsigned T_ = (unsigned)a.T, step = (unsigned)(a.blocks * kWarps);
   const size_t row0 = (size_t)g * a.T;
   const T* logits = static_cast<const T*>(a.logits) + row0 * a.ld;
   T* dlogits = static_cast<T*>(a.dlogits) + row0 * a.ldd;
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
     int at;
     float dw, m, s;
   } next;
-  auto load = [&](int t) {
+  auto load = [&](unsigned t) {
     next.raw.load(logits + (size_t)t * a.ld, a.E, lane);
     next.at = -1, next.dw = 0.f;
     if (lane < a.k) {
@@ -588,11 +590,11 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
     }
     next.m = a.stats[2 * (row0 + t)], next.s = a.stats[2 * (row0 + t) + 1];
   };
-  int t = b * kWarps + warp;
-  if (t < a.T) load(t);
-  for (; t < a.T; t += step) {
+  unsigned t = (unsigned)(b * kWarps + warp);
+  if (t < T_) load(t);
+  for (; t < T_; t += step) {
     const Next now = next;
-    if (t + step < a.T) load(t + step);  // (in place, a row is written after it is read: below)
+    if (t + step < T_) load(t + step);  // (in place, a row is written after it is read: below)
     T* dst = dlogits + (size_t)t * a.ldd;
     float d[V];
     if (__shfl_sync(kAll, now.at, 0) < 0) {  // an invalid token
@@ -660,9 +662,9 @@ void for_width(int E, F&& f) {
 // warp doubles the partial sums to join: 9.6 against 8.6 us at 3 x 1531 x 60; eight: 10.7.)
 int route_blocks(int G, int T) {
   const int sms = std::max(sm_count(), 1);
-  const int want = (T + 2 * kWarps - 1) / (2 * kWarps);
+  const int64_t want = ((int64_t)T + 2 * kWarps - 1) / (2 * kWarps);
   const int most = std::max(1, 4 * sms / std::max(G, 1));
-  return std::max(1, std::min(want, most));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, most));
 }
 
 // Whether a lane's V logits are whole aligned vectors in every row.
@@ -758,8 +760,9 @@ extern "C" int moe_route_backward(const void* logits, size_t ld, int dtype, int 
         !moe::aligned(counts, 4) || !moe::aligned(tokens, 4) || !moe::aligned(stats, 4) ||
         !moe::aligned(dweights, 4) || !moe::aligned(dloss, 4))
       return fail(SYMM_EINVAL, "moe_route_backward: a pointer is not aligned to its elements");
-    const int blocks = std::max(
-        1, std::min((T + kWarps - 1) / kWarps, std::max(sm_count(), 1) * 8 / std::min(G, 1 << 20)));
+    const int64_t want = ((int64_t)T + kWarps - 1) / kWarps;
+    const int most = std::max(sm_count(), 1) * 8 / std::min(G, 1 << 20);
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(want, most));
     RouteBackArgs a{logits, ld, G, T, E, k, renorm ? 1 : 0, scale, experts, counts, tokens, stats,
                     dweights, dloss, dlogits, ldd, blocks};
     cudaStream_t s = as_stream(stream);

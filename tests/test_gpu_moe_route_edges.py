@@ -1,0 +1,36 @@
+"""moe_route and moe_route_backward at the ends of their range."""
+import pytest
+import torch
+
+from moe_refs import U32
+from symmetric_memory_moe_gb300 import abi
+
+pytestmark = pytest.mark.gpu
+
+
+def test_the_largest_number_of_tokens():
+    """2^31 - 1 tokens of one expert: the last step of every warp's count leaves 31 bits.
+    Every logit is 1 but the last one's 2, so p = 1 and lse is the logit.  A warp adds
+    fewer than 2^20 ones and a CTA fewer than 2^23, exactly; joining at most 1024 CTAs
+    rounds 1024 times."""
+    T = (1 << 31) - 1
+    logits = torch.ones(T, dtype=torch.float16, device="cuda")
+    logits[-1] = 2
+    experts = torch.full((T,), 9, dtype=torch.int32, device="cuda")
+    weights, stats = torch.zeros(T, device="cuda"), torch.zeros(T, 2, device="cuda")
+    counts, tokens = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    loss = torch.zeros(2, device="cuda")
+    ws = torch.empty(abi.moe_route_workspace(1, T, 1), dtype=torch.uint8, device="cuda")
+    abi.moe_route(logits.data_ptr(), 1, None, abi.SYMM_DTYPE_F16, 1, T, 1, 1, 1, 1.0,
+                  *[t.data_ptr() for t in (experts, weights, counts, tokens, stats, loss)],
+                  ws.data_ptr())
+    assert int(counts) == T and int(tokens) == T
+    assert not experts.any() and bool((weights == 1).all())
+    assert bool((stats[:-1] == 1).all()) and stats[-1].tolist() == [2.0, 1.0]
+    assert abs(loss[0] - 1) <= 1024 * U32 and abs(loss[1] - 1) <= 1024 * U32
+    # dl = 2 lse / n dz with dz = n
+    dloss = torch.tensor([0.0, float(T)], device="cuda")
+    abi.moe_route_backward(logits.data_ptr(), 1, abi.SYMM_DTYPE_F16, 1, T, 1, 1, 1, 1.0,
+                           *[t.data_ptr() for t in (experts, counts, tokens, stats)], None,
+                           dloss.data_ptr(), logits.data_ptr(), 1)
+    assert bool((logits[:-1] == 2).all()) and float(logits[-1]) == 4
