@@ -24,6 +24,8 @@
 // part.  Rows of 1024: 5.8 TB/s.  Rows that are not 16-byte aligned, or odd,
 // move by 4-byte copies: 3.2 TB/s for 999 floats, 1.7 for 3001 bf16.
 #include <algorithm>
+#include <mutex>
+#include <set>
 #include <type_traits>
 
 #include "moe_common.cuh"
@@ -1057,11 +1059,25 @@ bool all_aligned(size_t a, std::initializer_list<const void*> ps) {
   return true;
 }
 
-// Lets kernel f use `bytes` of dynamic shared memory.
+// Lets kernel f use `bytes` of dynamic shared memory: all that an SM has, once
+// for each device.  The limit belongs to the kernel, whatever host thread
+// launches it, so it never goes by one call's size.
 int allow_smem(const void* f, size_t bytes, const char* what) {
   if (bytes <= 40 * 1024) return SYMM_OK;  // 48 KB with what the kernels hold statically
-  return cuda_check(
-      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes), what);
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), what);
+  if (rc) return rc;
+  static std::mutex mu;
+  static std::set<std::pair<const void*, int>> done;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({f, dev})) return SYMM_OK;
+  cudaFuncAttributes attr;
+  rc = cuda_check(cudaFuncGetAttributes(&attr, f), what);
+  if (!rc)
+    rc = cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(kSmemPerSm - attr.sharedSizeBytes)), what);
+  if (!rc) done.insert({f, dev});
+  return rc;
 }
 
 }  // namespace
