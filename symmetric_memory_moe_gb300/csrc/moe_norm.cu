@@ -1112,6 +1112,8 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
     if (!x || (y && !xo)) return fail(SYMM_EINVAL, "moe_block_norm: NULL x or xo");
     if (h && (h == x || h == xo || h == y))
       return fail(SYMM_EINVAL, "moe_block_norm: h must not be an input or xo");
+    if (xo && xo == y)  // other tokens' rows are still to be read
+      return fail(SYMM_EINVAL, "moe_block_norm: xo must not be y");
     const size_t es = moe::dtype_bytes(dtype);
     if (!all_aligned(es, {x, y, xo, h}) ||
         !all_aligned(4, {rows, weights, gate, res, w_post, w_pre, rstd}))
