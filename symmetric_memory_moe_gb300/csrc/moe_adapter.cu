@@ -716,51 +716,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (me == 0) symm::mbar_arrive(&listed[buf]);
         if (!waited) wait_for_earlier_launch(), waited = true;  // for h
         const uint32_t f0 = nlist[buf] * crank / C, f1 = nlist[buf] * (crank + 1) / C;
-        // This thread's 16-byte chunks of a piece (at most 16: bt 256, 8 chunks a
-        // row), the next piece's on their way; chunk c is of token tr, the ch-th.
-        struct Chunk {
-          uint32_t tr, ch;
-        };
-        auto chunk = [&](uint32_t p, int c) {
-          const uint32_t wlog = 32 - __clz(2 * piece_steps(a, p) - 1);  // whole powers, 2 to 8 a row
-          return Chunk{(me + 128 * c) >> wlog, me & ((1u << wlog) - 1)};
-        };
-        // whether no thread has a chunk c or a later one (asked once: the others'
-        // accesses are to be issued together)
-        auto none = [&](uint32_t p, int c) {
-          return c == 4 && (128u * c) >> (32 - __clz(2 * piece_steps(a, p) - 1)) >= a.bt;
-        };
-        auto load = [&](uint32_t p, uint4 (&v)[16]) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (none(p, c)) break;
-            const Chunk k = chunk(p, c);
-            v[c] = make_uint4(0, 0, 0, 0);
-            if (k.tr < a.bt && k.ch < 2 * piece_steps(a, p) && id_of[k.tr] < a.R)
-              v[c] = __ldcg(reinterpret_cast<const uint4*>(
-                                a.h + (size_t)(t0 + k.tr) * kParts * a.r16 + 64 * p) + k.ch);
-          }
-        };
-        uint4 next[16] = {};
-        if (f0 < f1) load(0, next);
         for (uint32_t p = 0; ok && f0 < f1 && p < npieces; ++p) {
+          // This thread's 16-byte chunks of the piece (at most 16: bt 256, 8 chunks a
+          // row) and the adapters of their tokens.  (The next piece's loaded ahead
+          // cost up to a tenth: 248 registers.)
+          const uint32_t width = 2 * piece_steps(a, p);
+          const uint32_t wlog = 32 - __clz(width - 1);  // 2 to 8 chunks a row, in whole powers
+          // whether no thread has chunk 4 or a later one (asked once: the others'
+          // accesses are to be issued together)
+          const bool few = (128u * 4) >> wlog >= a.bt;
           uint4 v[16];
-          uint32_t id[16], at[16], most = 0, odd = 0;  // their tokens' adapters; odd: not finite
+          uint32_t id[16], at[16], most = 0, odd = 0;  // odd: not finite
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            at[c] = id[c] = 0xffffffffu;
-            const Chunk k = chunk(p, c);
-            const bool in = k.tr < a.bt && k.ch < 2 * piece_steps(a, p);
-            v[c] = next[c];
-            if (in) id[c] = id_of[k.tr], at[c] = k.tr * 128 + ((k.ch ^ (k.tr & 7)) << 4);
-            if (FMT == 0) most = magnitudes(most, v[c]);
+            const uint32_t tr = (me + 128 * c) >> wlog, ch = me & ((1u << wlog) - 1);
+            id[c] = at[c] = 0xffffffffu, v[c] = make_uint4(0, 0, 0, 0);
+            if ((c >= 4 && few) || tr >= a.bt || ch >= width) continue;
+            id[c] = id_of[tr];
+            at[c] = tr * 128 + ((ch ^ (tr & 7)) << 4);
+            if (id[c] < a.R)
+              v[c] = __ldcg(reinterpret_cast<const uint4*>(
+                                a.h + (size_t)(t0 + tr) * kParts * a.r16 + 64 * p) + ch);
           }
+          if (FMT == 0)
+#pragma unroll
+            for (int c = 0; c < 16; ++c) most = magnitudes(most, v[c]);
           // B's second part may be 0: what is not finite is left to the epilogue
           if (FMT == 0 && not_finite<1>(most))
 #pragma unroll
             for (int c = 0; c < 16; ++c)
               if (not_finite<1>(magnitudes(0, v[c]))) odd |= 1u << c, v[c] = only_finite(v[c]);
-          if (p + 1 < npieces) load(p + 1, next);
           for (uint32_t i = f0; i < f1; ++i, ++it) {
             const uint32_t st = it % a.stages;
             // not `empty`: whose phases this warp does not follow one by one.  A
@@ -788,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t want = list[buf][i];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              if (none(p, c)) break;
+              if (c == 4 && few) break;
               if (at[c] != 0xffffffffu)
                 *reinterpret_cast<uint4*>(ring + at[c]) =
                     id[c] == want ? v[c] : make_uint4(0, 0, 0, 0);
@@ -797,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 16; ++c)
                 if (((odd >> c) & 1) && id[c] == want)
-                  wild[chunk(p, c).tr] = 1, any_wild = 1;
+                  wild[(me + 128 * c) >> wlog] = 1, any_wild = 1;
             symm::fence_proxy_async_shared();  // h (and B's parts), for the MMAs
             const bool bad = any_of(!ok || not_finite<FMT>(most));
             if (bad) {
