@@ -167,6 +167,12 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t remote) {
   return v;
 }
 
+// How long a CTA that gives up waits for its own copies and MMAs, which nothing
+// but the hardware holds up: a second, however short the heap's budget is.
+__device__ __forceinline__ uint64_t drain_ns(const AdapterArgs& a) {
+  return max(a.budget_ns, (uint64_t)1000000000);
+}
+
 // Instruction descriptor: fp32 accumulator, both operands of one type, the M
 // side M-major (bit 15), the N side K-major.
 __device__ __forceinline__ uint32_t mma_idesc(uint32_t fmt, uint32_t n) {
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
-      symm::mbar_wait(&full[i % stages], (i / stages) & 1, a.budget_ns);
+      symm::mbar_wait(&full[i % stages], (i / stages) & 1, drain_ns(a));
   } else if (warp == 1) {  // -------------------------------- MMA issuer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 0;
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
     if (elected) symm::tc_commit(&drain);
-    symm::mbar_wait(&drain, 0, a.budget_ns);
+    symm::mbar_wait(&drain, 0, drain_ns(a));
   } else {  // ------------------------------------------- sums of this part
     const uint32_t q = (uint32_t)(warp & 3), row = 32 * q + lane;
     for (uint32_t p = threadIdx.x - 64; p < kRankTokens; p += 128)
@@ -371,7 +377,8 @@ __global__ void __launch_bounds__(kThreads)
           prefetch_3d(&map_b, (int)n0, (int)r0, (int)sorted[start[i]]);
     for (uint32_t i = share, seg = 0; i < items; i += a.rk_share, ++seg) {
       const uint32_t p0 = start[i], rows = start[i + 1] - p0, buf = seg & 1;
-      if (!symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
+      // a warp gives up as one: tcgen05.ld wants all its lanes
+      if (!symm::mbar_wait_warp(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl)) {
         symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
       }
@@ -554,8 +561,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 1, it = 0;
+    uint32_t is_b = 0, b_phases = ~0u;  // stages whose last load is B's, phases of `claimed`
     bool ok = true;
-    auto next = [&]() {
+    auto next = [&](bool b) {
+      is_b = (is_b & ~(1u << st)) | ((uint32_t)b << st);
+      b_phases ^= (uint32_t)b << st;
       ++it;
       if (++st == a.stages) st = 0, ph ^= 1;
     };
@@ -576,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(buf + abytes + xbytes, &map_x, k + kBK, (int)(tb * a.bt), &full[st]);
             symm::mbar_arrive(&full[st]);
           }
-          next();
+          next(false);
         }
       };
       load_slices(k0, kp);
@@ -595,15 +605,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               symm::tma_load_3d(buf + abytes / 2, &map_b, n0 + 64, row, id, &claimed[st]);
               symm::mbar_arrive(&full[st]);
             }
-            next();
+            next(true);
           }
       }
       load_slices(kp, k1);
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-    // every load issued lands before the CTA may leave (bounded)
-    for (uint32_t i = it > a.stages ? it - a.stages : 0; i < it; ++i)
-      symm::mbar_wait(&full[i % a.stages], (i / a.stages) & 1, a.budget_ns);
+    // every load issued lands before the CTA may leave (bounded): of B on
+    // `claimed` (nobody may be left to complete `full`), else on `full`
+    for (uint32_t i = it > a.stages ? it - a.stages : 0; i < it; ++i) {
+      const uint32_t s = i % a.stages;
+      if ((is_b >> s) & 1) symm::mbar_wait(&claimed[s], (b_phases >> s) & 1, drain_ns(a));
+      else symm::mbar_wait(&full[s], (i / a.stages) & 1, drain_ns(a));
+    }
   } else if (warp == 1) {  // ---------------------------------- MMA issuer
     const bool elected = symm::elect_one();
     const uint32_t idesc = mma_idesc(FMT, a.bt), bf16_idesc = mma_idesc(1, a.bt);
@@ -669,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
     if (elected) symm::tc_commit(&drain);  // every MMA is complete before TMEM is freed
-    symm::mbar_wait(&drain, 0, a.budget_ns);
+    symm::mbar_wait(&drain, 0, drain_ns(a));
   } else {  // ------------------------------------------ h, and the epilogue
     const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q + 31
     const uint32_t row = 32 * q + lane;       // this thread's column of W in the tile
@@ -750,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t st = it % a.stages;
             // not `empty`: whose phases this warp does not follow one by one.  A
             // wait that gives up takes every thread to the barrier below first.
-            ok = symm::mbar_wait_ab(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl);
+            ok = symm::mbar_wait_warp(&claimed[st], (phases >> st) & 1, a.budget_ns, a.ctl);
             phases ^= 1u << st;
             uint8_t* ring = smem + (size_t)st * stage_bytes + abytes;
             // B's tile: two boxes of 64 columns, from the start of the stage
@@ -805,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       it += k1 - kp;
-      ok = symm::mbar_wait_ab(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+      ok = symm::mbar_wait_warp(&tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
       if (any_of(!ok)) {  // all threads leave, or none
         if (me == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         ok = false;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from moe_refs import DTYPES
+from symmetric_memory_moe_gb300 import abi
 from symmetric_memory_moe_gb300.torch_heap import TorchSymmHeap
 from test_gpu_moe_adapter import check, make, run
 
@@ -88,3 +89,25 @@ def test_large_rank_sums_in_half_precision(heap):
     i["scale"] = i["scale"].abs() + 2
     assert (i["x"].double() @ i["a"][1].double() * 2).abs().max() > 2e5
     check(i, run(heap, i, "f16"), "f16")
+
+
+@pytest.mark.parametrize("T,k,n,r", [(1, 4096, 4096, 16), (70, 1024, 264, 72), (600, 512, 2048, 32)])
+def test_a_budget_of_a_nanosecond(heap, T, k, n, r):
+    """Every wait that is not over at once may give up: the call ends, writes nothing but y,
+    and says so or is right; the next one, with time again, is right."""
+    i = make(T, k, n, 3, r, "bf16", 2, "mixed")
+    x, w = i["x"], i["w"]
+    y = torch.full((T + 1, n), 7.0, dtype=x.dtype, device="cuda")
+    ws = torch.empty(abi.moe_adapter_workspace(T, k, n, r), dtype=torch.uint8, device="cuda")
+    abi.symm_set_spin_budget(heap.handle, 1)
+    try:
+        abi.moe_adapter_matmul(heap.handle, x.data_ptr(), k, w.data_ptr(), n, i["a"].data_ptr(),
+                               i["b"].data_ptr(), i["scale"].data_ptr(), i["ids"].data_ptr(),
+                               abi.SYMM_DTYPE_BF16, T, k, n, 3, r, y.data_ptr(), n, ws.data_ptr())
+        code = abi.symm_check_error(heap.handle)[0]
+    finally:
+        abi.symm_set_spin_budget(heap.handle, 2_000_000_000)
+    assert code in (abi.SYMM_OK, abi.SYMM_ETIMEDOUT) and (y[T] == 7).all()
+    if code == abi.SYMM_OK:
+        check(i, y[:T], "bf16")
+    check(i, run(heap, i, "bf16"), "bf16")
