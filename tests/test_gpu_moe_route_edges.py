@@ -2,8 +2,10 @@
 import pytest
 import torch
 
-from moe_refs import U32
+import moe_refs as ref
+from moe_refs import DTYPES, U32
 from symmetric_memory_moe_gb300 import abi
+from test_gpu_moe_route import check_forward, forward
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +36,15 @@ def test_the_largest_number_of_tokens():
                            *[t.data_ptr() for t in (experts, counts, tokens, stats)], None,
                            dloss.data_ptr(), logits.data_ptr(), 1)
     assert bool((logits[:-1] == 2).all()) and float(logits[-1]) == 4
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("E", [30, 64, 100, 256, 300])
+def test_subnormal_logits_keep_their_order(dt, E):
+    """Numbers below the type's smallest normal one, of both signs, and zeros of both signs."""
+    g = torch.Generator().manual_seed(E)
+    bits = torch.randint(0, 128 if dt == "bf16" else 1024, (2, 40, E), generator=g)
+    sign = torch.randint(0, 2, bits.shape, generator=g) << 15
+    l = (bits | sign).to(torch.int32).to(torch.int16).view(DTYPES[dt])
+    _, o = forward(l, None, 8, dt, 1)
+    check_forward(o, ref.route(l, None, 8, 1, 1.0), E, 8, 40)

@@ -6,6 +6,8 @@ import pytest
 import torch
 
 from symmetric_memory_moe_gb300 import abi
+from symmetric_memory_moe_gb300.torch_heap import TorchSymmHeap
+from test_gpu_moe_adapter import make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +72,30 @@ def test_norms_of_different_sizes_from_two_threads(what):
         sys.setswitchinterval(interval)
     torch.cuda.synchronize()
     assert not bad, bad[0]
+
+
+def test_adapter_calls_in_flight_on_three_streams():
+    """Each call's second launch holds tensor memory that another call's first one may be
+    waiting for; all of them end, with the bits that each has alone."""
+    heap = TorchSymmHeap(1, 0)
+    cases = [(3000, 512, 1024, 6, 16, "bf16"), (64, 4096, 2048, 32, 16, "bf16"),
+             (700, 264, 520, 5, 72, "f16")]
+    inputs = [make(T, k, n, R, r, dt, T, "mixed") for T, k, n, R, r, dt in cases]
+    want = [run(heap, i, c[-1]) for i, c in zip(inputs, cases)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    out = [torch.empty_like(w) for w in want]
+    ws = [torch.empty(abi.moe_adapter_workspace(c[0], c[1], c[2], c[4]), dtype=torch.uint8,
+                      device="cuda") for c in cases]
+    codes = {"f16": abi.SYMM_DTYPE_F16, "bf16": abi.SYMM_DTYPE_BF16}
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for (T, k, n, R, r, dt), i, y, w, s in zip(cases, inputs, out, ws, streams):
+            abi.moe_adapter_matmul(heap.handle, i["x"].data_ptr(), k, i["w"].data_ptr(), n,
+                                   i["a"].data_ptr(), i["b"].data_ptr(), i["scale"].data_ptr(),
+                                   i["ids"].data_ptr(), codes[dt], T, k, n, R, r, y.data_ptr(), n,
+                                   w.data_ptr(), stream=s)
+    torch.cuda.synchronize()
+    assert abi.symm_check_error(heap.handle)[0] == abi.SYMM_OK
+    for y, w in zip(out, want):
+        assert torch.equal(y, w)
+    heap.close()
