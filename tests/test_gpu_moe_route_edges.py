@@ -5,7 +5,7 @@ import torch
 import moe_refs as ref
 from moe_refs import DTYPES, U32
 from symmetric_memory_moe_gb300 import abi
-from test_gpu_moe_route import check_forward, forward
+from test_gpu_moe_route import check_forward, forward, make
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,12 @@ def test_subnormal_logits_keep_their_order(dt, E):
     l = (bits | sign).to(torch.int32).to(torch.int16).view(DTYPES[dt])
     _, o = forward(l, None, 8, dt, 1)
     check_forward(o, ref.route(l, None, 8, 1, 1.0), E, 8, 40)
+
+
+@pytest.mark.parametrize("k", range(1, 12))
+@pytest.mark.parametrize("E,dt", [(40, "f16"), (256, "bf16"), (256, "f32"), (20, "f32")])
+@pytest.mark.parametrize("kind", ["ties", "holes"])
+def test_every_number_of_choices(k, E, dt, kind):
+    l, mask = make(2, 25, E, dt, k + E, kind)
+    _, o = forward(l, mask, k, dt, 1)
+    check_forward(o, ref.route(l, mask, k, 1, 1.0), E, k, 25)
