@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
     const int at = now.at < a.E ? now.at : -1;
     const float dw = at >= 0 ? a.scale * now.dw : 0.f;
     const float m = now.m, inv = __fdividef(1.f, now.s);
-    const float lz = cz * (m + __logf(now.s));
+    const float lse = m + __logf(now.s);
     float p[V];
     float dot = 0.f;
 #pragma unroll
@@ -641,8 +641,11 @@ __global__ void __launch_bounds__(kThreads) route_back_kernel(const RouteBackArg
     __syncwarp();
     if (a.dweights && at >= 0) add[at] = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      d[v] = a.renorm ? fmaf(p[v], base[v] - dot + lz, d[v]) : p[v] * (base[v] + d[v] - dot + lz);
+    for (int v = 0; v < V; ++v) {
+      d[v] = a.renorm ? fmaf(p[v], base[v] - dot, d[v]) : p[v] * (base[v] + d[v] - dot);
+      // p first: lse may be the largest float, and p 0
+      d[v] = fmaf(p[v] * cz, lse, d[v]);
+    }
     Raw<T, V, VEC>::store(dst, a.E, lane, d);
   }
 }

@@ -1,11 +1,13 @@
 """moe_route and moe_route_backward at the ends of their range."""
+import math
+
 import pytest
 import torch
 
 import moe_refs as ref
 from moe_refs import DTYPES, U32
 from symmetric_memory_moe_gb300 import abi
-from test_gpu_moe_route import check_forward, forward, make
+from test_gpu_moe_route import W, back, check_forward, forward, make
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +59,22 @@ def test_every_number_of_choices(k, E, dt, kind):
     l, mask = make(2, 25, E, dt, k + E, kind)
     _, o = forward(l, mask, k, dt, 1)
     check_forward(o, ref.route(l, mask, k, 1, 1.0), E, k, 25)
+
+
+@pytest.mark.parametrize("renorm", [1, 0])
+@pytest.mark.parametrize("E", [8, 100, 300])
+def test_z_gradient_of_the_largest_and_lowest_logits(E, renorm):
+    """2 p lse dz / n with lse at either end of a float's range: infinite only where the
+    gradient itself is, and 0 where p is."""
+    top = torch.finfo(torch.float32).max
+    l = torch.randn(2, 1, E, generator=torch.Generator().manual_seed(E))
+    l[0, 0, 3] = math.inf
+    l[1] = -top
+    buf, f = forward(l, None, 2, "f32", renorm)
+    dl = torch.tensor([[0.0, 1.0], [0.0, 2.0]], device="cuda")
+    d = back(l, f, 2, "f32", renorm, 1.0, torch.zeros(2, 1, 2, device="cuda"), dl, buf=buf)
+    d = d.view(2, E).double().cpu()
+    want = torch.zeros(E, dtype=torch.float64)
+    want[3] = math.inf                       # 2 FLT_MAX
+    assert torch.equal(d[0], want)
+    assert ((d[1] + 4 * top / E).abs() <= 2 * W * 4 * top / E).all()
