@@ -28,8 +28,8 @@
 // tile: each takes a part of K and of the adapters, and the parts are joined in
 // rank order through distributed shared memory, each CTA storing its share of
 // the tokens.  The second launch starts while the first runs (programmatic
-// dependent launch) and waits for its results only where it needs them.  Every wait is bounded; a role that gives up records
-// the error in the heap's header.
+// dependent launch) and waits for its results only where it needs them.  Every
+// wait is bounded; a role that gives up records the error in the heap's header.
 //
 // rank_kernel: h^T = A_a^T x^T the same way (A as stored, k x r, is an M-major
 // operand, rows r to 127 of the tile unused).  Per block of 128 tokens, a CTA
@@ -120,12 +120,6 @@ __device__ __forceinline__ void prefetch_3d(const CUtensorMap* map, int x, int y
                "r"(x), "r"(y), "r"(z)
                : "memory");
 }
-__device__ __forceinline__ void dependents_may_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_earlier_launch() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t v;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(v));
@@ -204,7 +198,8 @@ constexpr uint32_t kLowRows = 32;
 // h of up to 128 tokens: see the head of the file.
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
-    rank_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_x,
+    rank_kernel(const __grid_constant__ CUtensorMap map_a,
+                const __grid_constant__ CUtensorMap map_x,
                 const __grid_constant__ CUtensorMap map_x16,
                 const __grid_constant__ CUtensorMap map_b, const AdapterArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -235,15 +230,15 @@ __global__ void __launch_bounds__(kThreads)
     symm::fence_mbar_init();
   }
   if (warp == 5) symm::tmem_alloc(&tmem_slot, 256);
-  wait_for_earlier_launch();  // here: for whatever is before this call on the stream
+  moe::wait_for_earlier();  // here: for whatever is before this call on the stream
   // The second launch may start only now: it reads x and W at once, which that
   // may have written; and its CTAs take TMEM, and hold it while they wait for
   // this launch (warp 5 has this CTA's).
-  if (warp == 5) dependents_may_start();
+  if (warp == 5) moe::let_next_start();
 
   // this block's tokens, sorted by adapter (tokens without one last)
   const uint32_t group = blockIdx.x / csize, t0 = group / a.rk_share * kRankTokens;
-  const uint32_t share = group % a.rk_share;  // this cluster's adapters: share, share + rk_share, ..
+  const uint32_t share = group % a.rk_share;  // its adapters: share, share + rk_share, ..
   const uint32_t mine = threadIdx.x;
   if (mine < kRankTokens) {
     const uint32_t t = t0 + mine;
@@ -421,7 +416,8 @@ __global__ void __launch_bounds__(kThreads)
       }
       // three parts of 8 bits, truncated; an infinity or NaN is all in the first
       // (what it leaves would be NaN)
-      __nv_bfloat16* out = H + (size_t)order[pos] * kParts * a.r16 + c / 16 * (kParts * 16) + c % 16;
+      __nv_bfloat16* out =
+          H + (size_t)order[pos] * kParts * a.r16 + c / 16 * (kParts * 16) + c % 16;
 #pragma unroll
       for (int i = 0; i < kParts; ++i) {
         const __nv_bfloat16 part = __float2bfloat16_rz(s);
@@ -728,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         symm::group_sync(1, 128);
         if (me == 0) symm::mbar_arrive(&listed[buf]);
-        if (!waited) wait_for_earlier_launch(), waited = true;  // for h
+        if (!waited) moe::wait_for_earlier(), waited = true;  // for h
         const uint32_t f0 = nlist[buf] * crank / C, f1 = nlist[buf] * (crank + 1) / C;
         for (uint32_t p = 0; ok && f0 < f1 && p < npieces; ++p) {
           // This thread's 16-byte chunks of the piece (at most 16: bt 256, 8 chunks a
@@ -993,7 +989,7 @@ int make_map(CUtensorMap* map, const void* base, int fmt, uint64_t inner, uint64
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(SYMM_ECUDA,
-                "moe_adapter_matmul: tensor map rejected (CUresult " + std::to_string((int)r) + ")");
+                "moe_adapter_matmul: tensor map rejected (CUresult " + std::to_string(r) + ")");
   return SYMM_OK;
 }
 
@@ -1001,7 +997,8 @@ struct Maps {
   CUtensorMap w, x, a, rows, rows16, b;
 };
 
-constexpr size_t kRankSmemMax = 1024 + kRankBytes + 8192 + (size_t)kRankTokens * SYMM_MOE_MAX_RANK * 4;
+constexpr size_t kRankSmemMax =
+    1024 + kRankBytes + 8192 + (size_t)kRankTokens * SYMM_MOE_MAX_RANK * 4;
 
 // Once per device: both kernels may use more than 48 KB of shared memory.
 template <int FMT>

@@ -714,11 +714,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackAr
     }
 }
 
-// The backward pass, when shared memory holds a whole token: (2k + 5) rows through HBM a token, and Y read twice from shared memory
-// only -- for y, and for the inner products with it.  Every row has its own
-// place there (dh, z, dxo, x, Y_0 ..): the first four are copied in one group
-// for the next token as soon as they are used up, and row j of Y when this
-// token's is.
+// The backward pass, when shared memory holds a whole token: (2k + 5) rows
+// through HBM a token, and Y read twice from shared memory only -- for y, and
+// for the inner products with it.  Every row has its own place there (dh, z,
+// dxo, x, Y_0 ..): the first four are copied in one group for the next token as
+// soon as they are used up, and row j of Y when this token's is.
 template <typename T, int CH, int NT>
 __global__ void __launch_bounds__(NT ? NT : kMaxThreads, blocks_of(512, NT))
     norm_back_stream_kernel(const NormBackArgs a) {
@@ -1105,7 +1105,8 @@ extern "C" int moe_block_norm(const void* x, size_t ld, const void* y, size_t ld
     if (!(eps > 0.f) || isinf(eps)) return fail(SYMM_EINVAL, "moe_block_norm: eps must be > 0");
     if (!y && (rows || weights || gate || res || w_post || xo))
       return fail(SYMM_EINVAL,
-                  "moe_block_norm: without y, rows, weights, gate, res, w_post and xo must be NULL");
+                  "moe_block_norm: without y, rows, weights, gate, res, w_post and xo must be "
+                  "NULL");
     if (!y && !h) return fail(SYMM_EINVAL, "moe_block_norm: neither y nor h given");
     if (!h != !w_pre) return fail(SYMM_EINVAL, "moe_block_norm: h and w_pre go together");
     if (T == 0) return SYMM_OK;

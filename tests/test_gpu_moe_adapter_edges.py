@@ -91,7 +91,8 @@ def test_large_rank_sums_in_half_precision(heap):
     check(i, run(heap, i, "f16"), "f16")
 
 
-@pytest.mark.parametrize("T,k,n,r", [(1, 4096, 4096, 16), (70, 1024, 264, 72), (600, 512, 2048, 32)])
+@pytest.mark.parametrize("T,k,n,r", [(1, 4096, 4096, 16), (70, 1024, 264, 72),
+                                     (600, 512, 2048, 32)])
 def test_a_budget_of_a_nanosecond(heap, T, k, n, r):
     """Every wait that is not over at once may give up: the call ends, writes nothing but y,
     and says so or is right; the next one, with time again, is right."""
