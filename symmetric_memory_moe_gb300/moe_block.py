@@ -28,6 +28,14 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _plain(t, dtype, *shape):
+    """t as the library takes it: dense rows of the type, on the GPU."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor of {dtype}, {shape}, got {t.dtype}, "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.contiguous()
+
+
 class MoeBlock:
     """W PEs of T tokens, width D, E experts (E / W per PE), k choices, R adapters of rank r."""
 
@@ -68,6 +76,9 @@ class MoeBlock:
         """x [W, T, D] bf16, mask [W, T] uint8 (0: padding), ids [W, T] int32 adapters
         (-1: none), gate [W, T]: (residual stream, next input), [W, T, D] each."""
         W, T, D, E, k, o = self.W, self.T, self.D, self.E, self.k, self.o
+        x = _plain(x, BF16, W, T, D)
+        mask = _plain(mask.byte() if mask.dtype == torch.bool else mask, torch.uint8, W, T)
+        ids, gate = _plain(ids, torch.int32, W, T), _plain(gate, torch.float32, W, T)
         self.x, self.gate = x, gate
         h = torch.empty_like(x)
         for w in range(W):
@@ -129,6 +140,8 @@ class MoeBlock:
         """Gradients of what ``forward`` left: dx (through the residual stream), drows (of the
         rows that came back and the shared rows), dlogits, and the vectors' gradients."""
         W, T, D, E, k, o = self.W, self.T, self.D, self.E, self.k, self.o
+        dxo, dnext = _plain(dxo, BF16, W, T, D), _plain(dnext, BF16, W, T, D)
+        dloss = _plain(dloss, torch.float32, W, 2)
         back = self._rows(self.back, self.back_rows)
         dx, drows = torch.empty_like(dxo), torch.zeros_like(back)
         dweights, dgate = torch.empty_like(self.weights), torch.empty_like(self.gate)
