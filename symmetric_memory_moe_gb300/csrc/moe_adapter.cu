@@ -38,11 +38,11 @@
 // rank order through distributed shared memory.  A block's adapters are dealt
 // out to several clusters while there are few blocks.
 //
-// Measured (bf16): 8192 tokens, k = n = 4096, 8 adapters of rank 32: 191.8 us, of
-// which the product is 165 (1.67 PFLOP/s, 86 % of the burst rate); one token, k =
-// n = 8192: 23.8 us, 5.7 TB/s or 84 % of the copy rate; 64 tokens with 32 adapters
-// of rank 16, 7168 x 2048: 22.1 us, 7.8 without adapters (the rank products, 9 us,
-// are two rounds of memory latency long).
+// Measured (bf16): 8192 tokens, k = n = 4096, 8 adapters of rank 32: 199 us, of
+// which the product without adapters is 165 (1.67 PFLOP/s, 88 % of the burst
+// rate); one token, k = n = 8192: 23.3 us, 5.8 TB/s or 85 % of the copy rate; 64
+// tokens with 32 adapters of rank 16, 7168 x 2048: 21.4 us, 7.8 without adapters
+// (the rank products, 9 us, are two rounds of memory latency long).
 #include <algorithm>
 #include <string>
 

@@ -18,11 +18,13 @@
 // dwpre stay in its registers over all tokens and are written once per CTA;
 // a second small kernel adds the CTAs' sums in order.
 //
-// Measured (rows of 7168 in bf16, 8 a token): 8192 tokens 217.7 us, 5.94 TB/s or
-// 88 % of the copy rate; backward, 4096 tokens 272.8 us, 4.5 TB/s (67 %): a
+// Measured (rows of 7168 in bf16, 8 a token): 8192 tokens 216 us, 6.0 TB/s or
+// 88 % of the copy rate; backward, 4096 tokens 273 us, 4.5 TB/s (67 %): a
 // token's 172 KB fill an SM's shared memory there, so its phases overlap only in
 // part.  Rows of 1024: 5.8 TB/s.  Rows that are not 16-byte aligned, or odd,
-// move by 4-byte copies: 3.2 TB/s for 999 floats, 1.7 for 3001 bf16.
+// move by 4-byte copies: 3.2 TB/s for 999 floats, 1.7 for 3001 bf16.  A token
+// that does not fit into shared memory goes through norm_back_kernel: 753 us for
+// the same rows in 32 bits (3.3 TB/s, 48 %).
 #include <algorithm>
 #include <mutex>
 #include <set>
@@ -577,6 +579,11 @@ __global__ void __launch_bounds__(NT ? NT : kMaxThreads, CH == 4 ? 1 : blocks_of
   wait_groups<0>();
 }
 
+// The backward pass, when shared memory does not hold a token: Y and the rows
+// of dh and z are read twice, nothing ahead of its use, so it is bound by the
+// latency of each token's loads and sums (2.1 times the bytes' time at 4096 x 8
+// rows of 7168 floats; 4.9 times at 2048 x 4 rows of 16384 bf16, where four
+// chunks a thread spill).
 template <typename T, bool ALIGNED, int CH>
 __global__ void __launch_bounds__(kMaxThreads) norm_back_kernel(const NormBackArgs a) {
   moe::wait_for_earlier();
