@@ -566,6 +566,60 @@ int moe_adapter_matmul(symm_heap_t *heap, const void *x, size_t ldx, const void 
                        int dtype, int T, int k, int n, int R, int r, void *y, size_t ldy,
                        void *workspace, void *stream);
 
+/* Activations of the experts: x sigma(x), and x Phi(x) with the normal
+ * distribution's Phi (the exact form). */
+#define SYMM_ACT_SILU 0
+#define SYMM_ACT_GELU 1
+
+/* Bytes of device workspace (256-byte aligned) of moe_expert_ffn, or with
+ * backward != 0 of moe_expert_ffn_backward.
+ * Errors: SYMM_EINVAL (sizes as for the call). */
+int moe_expert_workspace(int n, int E, int D, int F, int backward, size_t *bytes);
+
+/* The experts' gated feed-forward on rows grouped by expert: for each row r of
+ * expert e, with g and u the first and the last F columns of x_r Wgu_e,
+ *     y_r = (act(g) * u) Wd_e.
+ * heap    supplies the spin budget and records errors (symm_check_error); the
+ *         tensors need not lie in it.
+ * x       device [n] rows of D, ldx elements apart: expert 0's rows, then
+ *         expert 1's, and so on.
+ * counts  device int32 [E], read by the kernels: rows of each expert (NULL
+ *         with E = 1: all n).  Their sum may be below n: rows behind the last
+ *         expert's are not read, and those of y and gu left as they were.  A
+ *         negative count, or a sum above n, is found on the device: nothing is
+ *         written and symm_check_error() reports SYMM_ERANGE.
+ * w_gu    device [E][D][2F], dense: Wg beside Wu; w_d device [E][F][D], dense.
+ * gu      device [n][2F], dense (NULL allowed): g and u, for the backward pass.
+ * y       device [n] rows of D, ldy elements apart.
+ * x, weights, gu and y are of `dtype` (SYMM_DTYPE_F16 or _BF16).  Products are
+ * summed in 32 bits in an order fixed by the sizes and counts; act(g) * u, of
+ * the unrounded g and u, is rounded to `dtype` once, as the second product's
+ * operand.  Rows do not mix: an infinity or NaN stays with its row.
+ * 0 <= n <= 2^24, 1 <= E <= SYMM_MOE_MAX_EXPERTS, D and F multiples of 8 in
+ * [8, 2^17], ldx a multiple of 8; x and weights 16-byte aligned.  n = 0 is a
+ * no-op.
+ * Errors: SYMM_EINVAL, SYMM_ECUDA; SYMM_ERANGE, SYMM_ETIMEDOUT by
+ * symm_check_error(). */
+int moe_expert_ffn(symm_heap_t *heap, const void *x, size_t ldx, const int32_t *counts,
+                   const void *w_gu, const void *w_d, int act, int dtype, int n, int E, int D,
+                   int F, void *gu, void *y, size_t ldy, void *workspace, void *stream);
+
+/* Gradients of moe_expert_ffn: dy [n] rows of D, lddy apart (a multiple of 8,
+ * 16-byte aligned), those of y; x, counts, w_gu, w_d as in the call, gu what it
+ * saved.  With dh = dy Wd_e^T, dg = dh * u * act'(g), du = dh * act(g):
+ *   dx     [n] rows of D, lddx apart: [dg | du] Wgu_e^T (rows behind the last
+ *          expert's left as they were);
+ *   dw_gu  [E][D][2F]: x_e^T [dg | du]_e, dw_d [E][F][D]: (act(g) * u)_e^T dy_e,
+ *          over the expert's rows; 0 of an expert without rows.
+ * Each of the three may be NULL.  dg, du and act(g) * u are rounded to `dtype`
+ * once, as operands.  Rows behind the last expert's are not read into any
+ * gradient.  n = 0 writes zero weight gradients.  Errors: as moe_expert_ffn. */
+int moe_expert_ffn_backward(symm_heap_t *heap, const void *dy, size_t lddy, const void *x,
+                            size_t ldx, const void *gu, const int32_t *counts, const void *w_gu,
+                            const void *w_d, int act, int dtype, int n, int E, int D, int F,
+                            void *dx, size_t lddx, void *dw_gu, void *dw_d, void *workspace,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -90,6 +90,10 @@ _SIGS = {
                                [_P] * 9,
     "moe_adapter_workspace": [_I] * 4 + [ctypes.POINTER(_SZ)],
     "moe_adapter_matmul": [_P, _P, _SZ, _P, _SZ] + [_P] * 4 + [_I] * 6 + [_P, _SZ, _P, _P],
+    "moe_expert_workspace": [_I] * 5 + [ctypes.POINTER(_SZ)],
+    "moe_expert_ffn": [_P, _P, _SZ] + [_P] * 3 + [_I] * 6 + [_P, _P, _SZ, _P, _P],
+    "moe_expert_ffn_backward": [_P, _P, _SZ, _P, _SZ] + [_P] * 4 + [_I] * 6 +
+                               [_P, _SZ] + [_P] * 4,
 }
 
 _lock = threading.Lock()
@@ -378,3 +382,29 @@ def moe_adapter_matmul(heap, x, ldx, w, ldw, a, b, scale, ids, dtype, T, k, n, R
     include/symm_a2a.h."""
     _check(lib().moe_adapter_matmul(heap, x, ldx, w, ldw, a, b, scale, ids, dtype, T, k, n, R, r,
                                     y, ldy, workspace, _stream(stream)), "moe_adapter_matmul")
+
+
+SYMM_ACT_SILU = 0
+SYMM_ACT_GELU = 1
+
+
+def moe_expert_workspace(n: int, E: int, D: int, F: int, backward: bool = False) -> int:
+    b = _SZ(0)
+    _check(lib().moe_expert_workspace(n, E, D, F, int(backward), ctypes.byref(b)),
+           "moe_expert_workspace")
+    return b.value
+
+
+def moe_expert_ffn(heap, x, ldx, counts, w_gu, w_d, act, dtype, n, E, D, F, gu, y, ldy, workspace,
+                   stream=None):
+    """The experts' gated feed-forward on rows grouped by expert; see
+    include/symm_a2a.h."""
+    _check(lib().moe_expert_ffn(heap, x, ldx, counts, w_gu, w_d, act, dtype, n, E, D, F, gu, y,
+                                ldy, workspace, _stream(stream)), "moe_expert_ffn")
+
+
+def moe_expert_ffn_backward(heap, dy, lddy, x, ldx, gu, counts, w_gu, w_d, act, dtype, n, E, D, F,
+                            dx, lddx, dw_gu, dw_d, workspace, stream=None):
+    _check(lib().moe_expert_ffn_backward(heap, dy, lddy, x, ldx, gu, counts, w_gu, w_d, act, dtype,
+                                         n, E, D, F, dx, lddx, dw_gu, dw_d, workspace,
+                                         _stream(stream)), "moe_expert_ffn_backward")

@@ -86,15 +86,6 @@ struct AdapterArgs {
   uint32_t rk_share, rk_ring, rk_abytes;
 };
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(symm::smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(symm::smem_addr(bar))
-      : "memory");
-}
-
 template <int FMT>
 struct Elem {
   using T = __half;
@@ -323,7 +314,7 @@ __global__ void __launch_bounds__(kThreads)
         __syncwarp();
         if (run) {
           if (16 * lane < rows16)
-            tma_load_2d(buf + a.rk_abytes + lane * 2048, &map_x16, (int)(kt * kBK),
+            symm::tma_load_2d(buf + a.rk_abytes + lane * 2048, &map_x16, (int)(kt * kBK),
                         order[p0] + 16 * lane, &full[st]);
         } else if (q < rows16)
           tma_gather4(buf + a.rk_abytes + q * 128, &map_x, (int)(kt * kBK), r, &full[st]);
@@ -575,11 +566,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elected) {
             symm::mbar_arrive_expect_tx(&full[st], stage_bytes);
             const int k = (int)(kt * a.deep * kBK);
-            tma_load_2d(buf, &map_w, n0, k, &full[st]);
-            tma_load_2d(buf + abytes / 2, &map_w, n0 + 64, k, &full[st]);
-            tma_load_2d(buf + abytes, &map_x, k, (int)(tb * a.bt), &full[st]);
+            symm::tma_load_2d(buf, &map_w, n0, k, &full[st]);
+            symm::tma_load_2d(buf + abytes / 2, &map_w, n0 + 64, k, &full[st]);
+            symm::tma_load_2d(buf + abytes, &map_x, k, (int)(tb * a.bt), &full[st]);
             if (a.deep == 2)
-              tma_load_2d(buf + abytes + xbytes, &map_x, k + kBK, (int)(tb * a.bt), &full[st]);
+              symm::tma_load_2d(buf + abytes + xbytes, &map_x, k + kBK, (int)(tb * a.bt), &full[st]);
             symm::mbar_arrive(&full[st]);
           }
           next(false);

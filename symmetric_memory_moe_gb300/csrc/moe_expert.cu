@@ -1,0 +1,721 @@
+// moe_expert.cu -- the experts' gated feed-forward and its gradients on rows
+// grouped by expert: y = (act(x Wg_e) * (x Wu_e)) Wd_e for the rows of expert e.
+//
+// With gu = x Wgu_e (its first F columns g, the others u), h = act(g) u:
+//   forward    gu, h  (one launch: both projections, the activation, the product)
+//              y = h Wd_e
+//   backward   dh = dy Wd_e^T;  dg = dh u act'(g), du = dh act(g), and h again,
+//              in that launch's epilogue;
+//              dx = [dg | du] Wgu_e^T;  dWd_e = h_e^T dy_e;  dWgu_e = x_e^T [dg | du]_e
+// h and [dg | du] are rounded to the inputs' type between launches: they are
+// operands of 16-bit tensor-core products, and one rounding of 2^-9 (bf16) is what
+// the outputs have anyway.  All sums are in 32 bits, in TMEM.
+//
+// rows_kernel: a product of an expert's rows with its weights, computed as
+// y^T = W^T x^T: the M side of a tile is 128 features (the weights as they are
+// stored, M-major or K-major), the N side 16 to 256 of the expert's rows, as
+// evenly cut as steps of 16 allow, so that an expert with few rows costs no
+// more than their loads and MMAs.  How many rows each expert has is read on the
+// device; every CTA lays out the same table of tiles and takes every
+// gridDim-th.
+//   warp 0     TMA producer: 64-deep slices of K of both sides, 128-byte
+//              swizzled, into a ring of stages; 128 deep when no tile has more
+//              than 64 rows (a slice costs each role some 250 cycles beside its MMAs)
+//   warp 1     MMA issuer: tcgen05.mma kind::f16, two accumulators in TMEM
+//   warps 2-5  epilogue: tcgen05.ld, activation or gradient, rounding, stores (a
+//              warp's 32 lanes are 32 features of a row)
+// The gated product's tile is 64 columns of Wg over the same 64 of Wu: g and u of
+// an element are then 64 TMEM lanes apart, in two warps, which exchange halves
+// of them through shared memory, each finishing half of the rows.
+//
+// grad_kernel: a gradient of weights, dW_e = a_e^T b_e: 128 x 256 tiles, K the
+// expert's rows, both operands as stored (M- and N-major).  Rows of the next
+// expert that share the last 16-row step are zeroed in shared memory, in both
+// operands, before its MMAs: what they hold may be an infinity.
+#include <algorithm>
+#include <string>
+
+#include "moe_experts.cuh"
+
+using namespace experts;
+using namespace symm_host;
+
+namespace {
+
+constexpr uint32_t kBK = 64;
+constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
+constexpr uint32_t kRingBytes = 192 * 1024;              // four stages of 128 x 256 tiles
+constexpr uint32_t kMaxStages = 8;
+constexpr uint32_t kExchange = 2 * 2 * 16 * 64 * 4;      // two chunks, two halves of 16 x 64
+constexpr uint32_t kSmemBytes = 1024 + kRingBytes + kExchange;
+constexpr uint32_t kAccCols = 256;
+
+enum Kind { kGated, kDown, kDh, kDx };
+
+struct ExpertArgs {
+  const int32_t* counts;
+  uint32_t n, E;
+  uint32_t m, k;       // features out (kGated: F), contraction
+  uint32_t ncol;       // column blocks
+  uint32_t F;          // offset of u in gu
+  int act;
+  const void* gu_in;   // kDh
+  void *gu, *h, *out;  // kGated: gu (NULL allowed), h; kDh: gu is [dg | du], h; else out
+  size_t ldo;
+  uint64_t budget_ns;
+  Control* ctl;
+};
+
+// Instruction descriptor: fp32 accumulator, both operands of one type; bits 15
+// and 16: the M and the N side are M- and N-major.
+__device__ __forceinline__ uint32_t mma_idesc(uint32_t fmt, uint32_t n, bool m_major,
+                                              bool n_major) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)m_major << 15) |
+         ((uint32_t)n_major << 16) | ((n >> 3) << 17) | ((kBM >> 4) << 24);
+}
+constexpr uint64_t kMajorStep = (16 * 128) >> 4;  // 16 K rows of an M- or N-major tile
+constexpr uint64_t kKStep = 32 >> 4;              // 16 K columns of a K-major tile
+
+template <int FMT>
+struct Elem {
+  using T = __half;
+};
+template <>
+struct Elem<1> {
+  using T = __nv_bfloat16;
+};
+
+// The ring of a launch whose largest tile copies `rows` rows.
+struct Ring {
+  uint32_t deep, stages, stage_bytes;
+};
+__device__ __forceinline__ Ring ring_of(uint32_t rows) {
+  Ring r;
+  r.deep = rows <= 64 ? 2 : 1;
+  r.stage_bytes = r.deep * (kATile + rows * 128);
+  r.stages = min(kMaxStages, kRingBytes / r.stage_bytes);
+  return r;
+}
+
+struct Barriers {
+  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+};
+// Barriers and TMEM, before the launch before this one has ended.
+__device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < kMaxStages; ++s) symm::mbar_init(&b.full[s], 1), symm::mbar_init(&b.empty[s], 1);
+    for (int i = 0; i < 2; ++i) symm::mbar_init(&b.tfull[i], 1), symm::mbar_init(&b.tempty[i], 128);
+    symm::mbar_init(&b.drain, 1);
+    symm::fence_mbar_init();
+  }
+  if (warp == 1) symm::tmem_alloc(&b.tmem, 2 * kAccCols);
+  symm::tc_fence_before();
+  __syncthreads();
+  symm::tc_fence_after();
+}
+__device__ __forceinline__ void leave_cta(Barriers& b, int warp) {
+  __syncwarp();
+  symm::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    symm::tc_fence_after();
+    symm::tmem_dealloc(b.tmem, 2 * kAccCols);
+  }
+}
+
+// ------------------------------------------------------------- epilogues --
+// 16 rows from `row` on, `valid` of them there, feature f of each.
+template <int FMT>
+__device__ __forceinline__ void store16(const ExpertArgs& a, const uint32_t (&v)[16], uint32_t row,
+                                        uint32_t valid, uint32_t f) {
+  using T = typename Elem<FMT>::T;
+  if (f >= a.m) return;
+  T* y = static_cast<T*>(a.out) + (size_t)row * a.ldo + f;
+#pragma unroll
+  for (uint32_t j = 0; j < 16; ++j)
+    if (j < valid) y[j * a.ldo] = moe::from_f<T>(__uint_as_float(v[j]));
+}
+template <int FMT>
+__device__ __forceinline__ void grad16(const ExpertArgs& a, const uint32_t (&v)[16], uint32_t row,
+                                       uint32_t valid, uint32_t f) {
+  using T = typename Elem<FMT>::T;
+  if (f >= a.m) return;
+  const T* gu = static_cast<const T*>(a.gu_in) + (size_t)row * 2 * a.F + f;
+  T* dgu = static_cast<T*>(a.gu) + (size_t)row * 2 * a.F + f;
+  T* h = static_cast<T*>(a.h) + (size_t)row * a.F + f;
+  T g[16], u[16];
+#pragma unroll
+  for (uint32_t j = 0; j < 16; ++j)
+    if (j < valid) g[j] = gu[(size_t)j * 2 * a.F], u[j] = gu[(size_t)j * 2 * a.F + a.F];
+#pragma unroll
+  for (uint32_t j = 0; j < 16; ++j)
+    if (j < valid) {
+      float act, slope;
+      activate_both(a.act, moe::to_f(g[j]), act, slope);
+      const float dh = __uint_as_float(v[j]), up = moe::to_f(u[j]);
+      dgu[(size_t)j * 2 * a.F] = moe::from_f<T>(dh * up * slope);
+      dgu[(size_t)j * 2 * a.F + a.F] = moe::from_f<T>(dh * act);
+      h[(size_t)j * a.F] = moe::from_f<T>(act * up);
+    }
+}
+// Rows of the gated product: g and u of feature f, 16 rows from `row` on.
+template <int FMT>
+__device__ __forceinline__ void gated16(const ExpertArgs& a, const float (&g)[16],
+                                        const float (&u)[16], uint32_t row, uint32_t valid,
+                                        uint32_t f) {
+  using T = typename Elem<FMT>::T;
+  if (f >= a.m) return;
+  T* h = static_cast<T*>(a.h) + (size_t)row * a.F + f;
+#pragma unroll
+  for (uint32_t j = 0; j < 16; ++j)
+    if (j < valid) h[(size_t)j * a.F] = moe::from_f<T>(activate(a.act, g[j]) * u[j]);
+  if (!a.gu) return;
+  T* gu = static_cast<T*>(a.gu) + (size_t)row * 2 * a.F + f;
+#pragma unroll
+  for (uint32_t j = 0; j < 16; ++j)
+    if (j < valid) {
+      gu[(size_t)j * 2 * a.F] = moe::from_f<T>(g[j]);
+      gu[(size_t)j * 2 * a.F + a.F] = moe::from_f<T>(u[j]);
+    }
+}
+
+// ------------------------------------------------------------ rows_kernel --
+template <int FMT, int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_kernel(const __grid_constant__ CUtensorMap map_w,
+                const __grid_constant__ CUtensorMap map_x64,
+                const __grid_constant__ CUtensorMap map_x16, const ExpertArgs a) {
+  constexpr bool kMMajor = KIND == kGated || KIND == kDown;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
+  __shared__ Barriers bar;
+  __shared__ Table table;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  set_up_cta(bar, warp);
+  moe::let_next_start();
+  moe::wait_for_earlier();
+  const bool good = lay_out(table, a.counts, a.E, a.n);
+  if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
+  const uint32_t tiles = good ? table.blocks[a.E] * a.ncol : 0;
+  const Ring ring = ring_of(good ? copied_rows(table.most) : 16);
+  const uint32_t slices = (a.k + ring.deep * kBK - 1) / (ring.deep * kBK);
+  const uint32_t tmem = bar.tmem, abytes = ring.deep * kATile;
+
+  if (warp == 0) {  // ----------------------------------------- TMA producer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 1, it = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t rows = copied_rows(t.bt), xbytes = rows * 128;
+      for (uint32_t s = 0; s < slices; ++s) {
+        if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
+        uint8_t* buf = smem + st * ring.stage_bytes;
+        uint64_t* full = &bar.full[st];
+        if (elected) {
+          symm::mbar_arrive_expect_tx(full, abytes + ring.deep * xbytes);
+          for (uint32_t d = 0; d < ring.deep; ++d) {
+            const int k = (int)((s * ring.deep + d) * kBK);
+            if (kMMajor) {
+              const int x = KIND == kGated ? (int)(t.col * 64) : (int)(t.col * kBM);
+              const int x2 = KIND == kGated ? x + (int)a.F : x + 64;
+              symm::tma_load_3d(buf + d * (kATile / 2), &map_w, x, k, (int)t.e, full);
+              symm::tma_load_3d(buf + abytes / 2 + d * (kATile / 2), &map_w, x2, k, (int)t.e, full);
+            } else {
+              symm::tma_load_3d(buf + d * kATile, &map_w, k, (int)(t.col * kBM), (int)t.e, full);
+            }
+            uint8_t* x = buf + abytes + d * xbytes;
+            if (t.bt <= 48)
+              for (uint32_t r = 0; r < rows; r += 16)
+                symm::tma_load_2d(x + r * 128, &map_x16, k, (int)(t.row + r), full);
+            else
+              for (uint32_t r = 0; r < rows; r += 64)
+                symm::tma_load_2d(x + r * 128, &map_x64, k, (int)(t.row + r), full);
+          }
+        }
+        ++it;
+        if (++st == ring.stages) st = 0, ph ^= 1;
+      }
+    }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+    // every load issued lands before the CTA may leave (bounded)
+    for (uint32_t i = it > ring.stages ? it - ring.stages : 0; i < it; ++i)
+      symm::mbar_wait(&bar.full[i % ring.stages], (i / ring.stages) & 1, drain_ns(a.budget_ns));
+  } else if (warp == 1) {  // ---------------------------------- MMA issuer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 0, seg = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t xbytes = copied_rows(t.bt) * 128, buf = seg & 1;
+      const uint32_t idesc = mma_idesc(FMT, t.bt, kMMajor, false);
+      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+        break;
+      symm::tc_fence_after();
+      const uint32_t acc = tmem + buf * kAccCols;
+      for (uint32_t s = 0; s < slices; ++s) {
+        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        symm::tc_fence_after();
+        const uint8_t* at = smem + st * ring.stage_bytes;
+        if (elected) {
+          for (uint32_t d = 0; d < ring.deep; ++d) {
+            const uint64_t wd = kMMajor
+                                    ? symm::sw128_mnmajor_desc(at + d * (kATile / 2), abytes / 2)
+                                    : symm::sw128_kmajor_desc(at + d * kATile);
+            const uint64_t xd = symm::sw128_kmajor_desc(at + abytes + d * xbytes);
+#pragma unroll
+            for (uint32_t j = 0; j < kBK / 16; ++j)
+              symm::tc_mma(acc, wd + (kMMajor ? kMajorStep : kKStep) * j, xd + kKStep * j, idesc,
+                           (s | d | j) != 0);
+          }
+          symm::tc_commit(&bar.empty[st]);
+        }
+        if (++st == ring.stages) st = 0, ph ^= 1;
+      }
+      if (ok && elected) symm::tc_commit(&bar.tfull[buf]);
+    }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+    if (elected) symm::tc_commit(&bar.drain);  // every MMA is complete before TMEM is freed
+    symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+  } else {  // -------------------------------------------------- epilogue
+    const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q + 31
+    float* exchange = reinterpret_cast<float*>(smem + kRingBytes);
+    uint32_t seg = 0, chunk = 0;
+    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t buf = seg & 1;
+      const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+      if (any_of(!ok)) {  // all threads leave, or none
+        if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+        break;
+      }
+      symm::tc_fence_after();
+      const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
+      if (KIND == kGated) {
+        // Chunks of 32 rows: the warps of g finish the first 16, those of u the others.
+        const uint32_t f = t.col * 64 + 32 * (q & 1) + lane, mine = q >> 1;
+        for (uint32_t c = 0; c < t.rows; c += 32, ++chunk) {
+          uint32_t v[32];
+          symm::tmem_ld32(taddr + c, v);
+          if (c + 32 >= t.rows) {  // the accumulator is free for the next tile
+            symm::tc_fence_before();
+            symm::mbar_arrive(&bar.tempty[buf]);
+          }
+          // half 0: g of the last 16 rows, half 1: u of the first 16
+          float* there = exchange + (chunk & 1) * (2 * 16 * 64) + 32 * (q & 1) + lane;
+          float own[16], other[16];
+#pragma unroll
+          for (uint32_t j = 0; j < 16; ++j) {
+            there[mine * (16 * 64) + j * 64] = __uint_as_float(mine ? v[j] : v[16 + j]);
+            own[j] = __uint_as_float(mine ? v[16 + j] : v[j]);
+          }
+          symm::group_sync(2 + (int)(q & 1), 64);  // this pair of warps
+#pragma unroll
+          for (uint32_t j = 0; j < 16; ++j) other[j] = there[(mine ^ 1) * (16 * 64) + j * 64];
+          const uint32_t r = c + 16 * mine;
+          if (r < t.rows) {
+            if (mine) gated16<FMT>(a, other, own, t.row + r, t.rows - r, f);
+            else gated16<FMT>(a, own, other, t.row + r, t.rows - r, f);
+          }
+        }
+      } else {
+        const uint32_t f = t.col * kBM + 32 * q + lane;
+        for (uint32_t c = 0; c < t.rows; c += 16) {
+          uint32_t v[16];
+          symm::tmem_ld16(taddr + c, v);
+          if (c + 16 >= t.rows) {
+            symm::tc_fence_before();
+            symm::mbar_arrive(&bar.tempty[buf]);
+          }
+          if (KIND == kDh) grad16<FMT>(a, v, t.row + c, t.rows - c, f);
+          else store16<FMT>(a, v, t.row + c, t.rows - c, f);
+        }
+      }
+    }
+  }
+  leave_cta(bar, warp);
+}
+
+// ------------------------------------------------------------ grad_kernel --
+struct GradArgs {
+  const int32_t* counts;
+  uint32_t n, E, m, nf;  // out [E][m][nf]
+  uint32_t mb, nb;       // blocks of 128 and of 256
+  void* out;
+  uint64_t budget_ns;
+  Control* ctl;
+};
+constexpr uint32_t kGradStage = 6 * 64 * 128;  // two boxes of A, four of B: 64 rows x 64 features
+constexpr uint32_t kGradStages = kRingBytes / kGradStage;
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+    grad_kernel(const __grid_constant__ CUtensorMap map_a,
+                const __grid_constant__ CUtensorMap map_b, const GradArgs a) {
+  using T = typename Elem<FMT>::T;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
+  __shared__ Barriers bar;
+  __shared__ Table table;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  set_up_cta(bar, warp);
+  moe::let_next_start();
+  moe::wait_for_earlier();
+  const bool good = lay_out(table, a.counts, a.E, a.n);
+  if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
+  const uint32_t per = a.mb * a.nb, tiles = good ? a.E * per : 0;
+  const uint32_t tmem = bar.tmem;
+  // Tile i: an expert's blocks of 256 columns one after another, then the next 128 rows.
+
+  if (warp == 0) {  // ----------------------------------------- TMA producer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 1, it = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      const uint32_t e = i / per, m0 = i % per / a.nb * kBM, n0 = i % a.nb * 256;
+      const uint32_t r0 = table.off[e], r1 = table.off[e + 1];
+      for (uint32_t r = r0; r < r1; r += 64) {
+        if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
+        uint8_t* buf = smem + st * kGradStage;
+        if (elected) {
+          symm::mbar_arrive_expect_tx(&bar.full[st], kGradStage);
+#pragma unroll
+          for (uint32_t b = 0; b < 2; ++b)
+            symm::tma_load_2d(buf + b * 8192, &map_a, (int)(m0 + 64 * b), (int)r, &bar.full[st]);
+#pragma unroll
+          for (uint32_t b = 0; b < 4; ++b)
+            symm::tma_load_2d(buf + (2 + b) * 8192, &map_b, (int)(n0 + 64 * b), (int)r,
+                              &bar.full[st]);
+        }
+        ++it;
+        if (++st == kGradStages) st = 0, ph ^= 1;
+      }
+    }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+    for (uint32_t i = it > kGradStages ? it - kGradStages : 0; i < it; ++i)
+      symm::mbar_wait(&bar.full[i % kGradStages], (i / kGradStages) & 1, drain_ns(a.budget_ns));
+  } else if (warp == 1) {  // ---------------------------------- MMA issuer
+    const bool elected = symm::elect_one();
+    const uint32_t idesc = mma_idesc(FMT, 256, true, true);
+    uint32_t st = 0, ph = 0, seg = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      const uint32_t e = i / per, r0 = table.off[e], r1 = table.off[e + 1];
+      if (r0 == r1) continue;  // the epilogue writes zeros
+      const uint32_t buf = seg & 1;
+      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+        break;
+      symm::tc_fence_after();
+      const uint32_t acc = tmem + buf * kAccCols;
+      for (uint32_t r = r0; r < r1; r += 64) {
+        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        uint8_t* at = smem + st * kGradStage;
+        const uint32_t left = min(64u, r1 - r), steps = (left + 15) / 16;
+        if (left % 16) {  // the next expert's rows in the last step
+          const uint32_t zero = steps * 16 - left;
+          for (uint32_t c = lane; c < 6 * 8 * zero; c += 32) {
+            const uint32_t box = c / (8 * zero), w = c % (8 * zero);
+            *reinterpret_cast<uint4*>(at + box * 8192 + left * 128 + w * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          symm::fence_proxy_async_shared();
+          __syncwarp();
+        }
+        symm::tc_fence_after();
+        const uint64_t ad = symm::sw128_mnmajor_desc(at), bd = symm::sw128_mnmajor_desc(at + 16384);
+        if (elected) {
+          for (uint32_t j = 0; j < steps; ++j)
+            symm::tc_mma(acc, ad + kMajorStep * j, bd + kMajorStep * j, idesc, r != r0 || j != 0);
+          symm::tc_commit(&bar.empty[st]);
+        }
+        if (++st == kGradStages) st = 0, ph ^= 1;
+      }
+      if (ok && elected) symm::tc_commit(&bar.tfull[buf]);
+      ++seg;
+    }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+    if (elected) symm::tc_commit(&bar.drain);
+    symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+  } else {  // -------------------------------------------------- epilogue
+    const uint32_t q = (uint32_t)(warp & 3);
+    uint32_t seg = 0;
+    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+      const uint32_t e = i / per, n0 = i % a.nb * 256;
+      const uint32_t m = i % per / a.nb * kBM + 32 * q + lane, buf = seg & 1;
+      const bool any = table.off[e] != table.off[e + 1];
+      if (any) {
+        const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+        if (any_of(!ok)) {  // all threads leave, or none
+          if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+          break;
+        }
+        symm::tc_fence_after();
+        ++seg;
+      }
+      const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
+      T* out = static_cast<T*>(a.out) + ((size_t)e * a.m + m) * a.nf + n0;
+      const uint32_t cols = min(256u, a.nf - n0);  // a multiple of 8
+      for (uint32_t c = 0; c < 256; c += 32) {
+        uint32_t v[32];
+        if (any) {
+          symm::tmem_ld32(taddr + c, v);
+          if (c == 224) {
+            symm::tc_fence_before();
+            symm::mbar_arrive(&bar.tempty[buf]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0;
+        }
+        if (m >= a.m) continue;
+#pragma unroll
+        for (uint32_t j = 0; j < 32; j += 8)
+          if (c + j < cols) {
+            uint4 p;
+            uint32_t* w = &p.x;
+#pragma unroll
+            for (int l = 0; l < 4; ++l)
+              w[l] = symm::pack2<FMT>(__uint_as_float(v[j + 2 * l]), __uint_as_float(v[j + 2 * l + 1]));
+            *reinterpret_cast<uint4*>(out + c + j) = p;
+          }
+      }
+    }
+  }
+  leave_cta(bar, warp);
+}
+
+// ------------------------------------------------------------------- host --
+size_t up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+int check_sizes(const char* what, int n, int E, int D, int F) {
+  if (n < 0 || n > (1 << 24) || E < 1 || E > SYMM_MOE_MAX_EXPERTS)
+    return fail(SYMM_EINVAL, std::string(what) + ": n must be in [0, 2^24], E in [1, 1024]");
+  if (D < 8 || F < 8 || D % 8 || F % 8 || D > (1 << 17) || F > (1 << 17))
+    return fail(SYMM_EINVAL, std::string(what) + ": D and F must be multiples of 8 (16-byte rows) "
+                                                 "in [8, 2^17]");
+  return SYMM_OK;
+}
+size_t h_bytes(int n, int F) { return up((size_t)n * F * 2, 256); }
+
+// [depth][rows][inner] elements of 16 bits, rows `ld` apart, planes rows * ld;
+// boxes of 64 x box_rows, 128-byte swizzled; depth 0: a 2-d map.
+int make_map(const char* what, CUtensorMap* map, const void* base, int fmt, uint64_t inner,
+             uint64_t rows, uint64_t depth, size_t ld, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(SYMM_ECUDA, std::string(what) + ": no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {inner, rows, depth};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * rows * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, fmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+         depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(SYMM_ECUDA,
+                std::string(what) + ": tensor map rejected (CUresult " + std::to_string(r) + ")");
+  return SYMM_OK;
+}
+
+// Once per device: the kernels may use more than 48 KB of shared memory.
+template <int FMT>
+int set_up() {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "moe_expert_ffn: device");
+  if (rc) return rc;
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev >= 0 && dev < 64 && done[dev]) return SYMM_OK;
+  for (const void* f : {(const void*)rows_kernel<FMT, kGated>, (const void*)rows_kernel<FMT, kDown>,
+                        (const void*)rows_kernel<FMT, kDh>, (const void*)rows_kernel<FMT, kDx>,
+                        (const void*)grad_kernel<FMT>})
+    if (!rc)
+      rc = cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)kSmemBytes),
+                      "moe_expert_ffn: kernel set-up");
+  if (!rc && dev >= 0 && dev < 64) done[dev] = true;
+  return rc;
+}
+
+// One product of the rows x [n][k] (ldx apart) with the experts' weights, stored
+// [E][wrows][wcols].
+template <int FMT, int KIND>
+int rows_product(const char* what, const void* x, size_t ldx, const void* w, uint32_t wrows,
+                 uint32_t wcols, ExpertArgs a, cudaStream_t s) {
+  constexpr bool kMMajor = KIND == kGated || KIND == kDown;
+  CUtensorMap mw, m64, m16;
+  int rc = make_map(what, &mw, w, FMT, wcols, wrows, a.E, wcols, kMMajor ? kBK : kBM);
+  if (!rc) rc = make_map(what, &m64, x, FMT, a.k, a.n, 0, ldx, 64);
+  if (!rc) rc = make_map(what, &m16, x, FMT, a.k, a.n, 0, ldx, 16);
+  if (rc) return rc;
+  a.ncol = (a.m + (KIND == kGated ? 63 : 127)) / (KIND == kGated ? 64 : 128);
+  // at most one partly filled block of rows for each expert that has rows
+  const uint64_t most = (uint64_t)a.ncol * std::min<uint64_t>(a.n, a.n / kMaxRows + a.E);
+  const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), most);
+  return moe::launch(what, rows_kernel<FMT, KIND>, grid, kThreads, kSmemBytes, s, mw, m64, m16, a);
+}
+
+// dW [E][m][nf] = a_e^T b_e of the rows a [n][m] and b [n][nf].
+template <int FMT>
+int weight_grad(const char* what, const void* a, size_t lda, const void* b, size_t ldb, void* out,
+                uint32_t m, uint32_t nf, const ExpertArgs& x, cudaStream_t s) {
+  CUtensorMap ma, mb;
+  int rc = make_map(what, &ma, a, FMT, m, x.n, 0, lda, 64);
+  if (!rc) rc = make_map(what, &mb, b, FMT, nf, x.n, 0, ldb, 64);
+  if (rc) return rc;
+  GradArgs g{};
+  g.counts = x.counts, g.n = x.n, g.E = x.E, g.m = m, g.nf = nf, g.out = out;
+  g.mb = (m + kBM - 1) / kBM, g.nb = (nf + 255) / 256;
+  g.budget_ns = x.budget_ns, g.ctl = x.ctl;
+  const uint64_t tiles = (uint64_t)x.E * g.mb * g.nb;
+  const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), tiles);
+  return moe::launch(what, grad_kernel<FMT>, grid, kThreads, kSmemBytes, s, ma, mb, g);
+}
+
+// What both entry points check of their sizes, weights and type.
+int check_common(const char* what, const symm_heap_t* heap, const int32_t* counts,
+                 const void* w_gu, const void* w_d, int act, int dtype, int n, int E, int D,
+                 int F) {
+  if (!heap) return fail(SYMM_EINVAL, std::string(what) + ": NULL heap");
+  if (dtype != SYMM_DTYPE_F16 && dtype != SYMM_DTYPE_BF16)
+    return fail(SYMM_EINVAL, std::string(what) + ": dtype must be SYMM_DTYPE_F16 or _BF16");
+  if (act != SYMM_ACT_SILU && act != SYMM_ACT_GELU)
+    return fail(SYMM_EINVAL, std::string(what) + ": act must be SYMM_ACT_SILU or _GELU");
+  const int rc = check_sizes(what, n, E, D, F);
+  if (rc) return rc;
+  if (!counts && E != 1)
+    return fail(SYMM_EINVAL, std::string(what) + ": counts may be NULL with one expert only");
+  if (!w_gu || !w_d) return fail(SYMM_EINVAL, std::string(what) + ": NULL weights");
+  if (!moe::aligned(w_gu, 16) || !moe::aligned(w_d, 16) || !moe::aligned(counts, 4))
+    return fail(SYMM_EINVAL, std::string(what) + ": weights must be 16-byte aligned, counts to "
+                                                 "their elements");
+  return SYMM_OK;
+}
+bool bad_ld(size_t ld, int width) {
+  return ld < (size_t)width || ld % 8 || ld > (1ull << 36);
+}
+
+template <int FMT>
+int forward(const char* what, const void* x, size_t ldx, const void* w_gu, const void* w_d, int D,
+            int F, void* gu, void* y, size_t ldy, void* h, ExpertArgs a, cudaStream_t s) {
+  int rc = set_up<FMT>();
+  if (rc) return rc;
+  a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu = gu, a.h = h;
+  rc = rows_product<FMT, kGated>(what, x, ldx, w_gu, D, 2 * F, a, s);
+  if (rc) return rc;
+  a.m = (uint32_t)D, a.k = (uint32_t)F, a.out = y, a.ldo = ldy;
+  return rows_product<FMT, kDown>(what, h, F, w_d, F, D, a, s);
+}
+
+template <int FMT>
+int backward(const char* what, const void* dy, size_t lddy, const void* x, size_t ldx,
+             const void* gu, const void* w_gu, const void* w_d, int D, int F, void* dx,
+             size_t lddx, void* dw_gu, void* dw_d, void* h, void* dgu, ExpertArgs a,
+             cudaStream_t s) {
+  int rc = set_up<FMT>();
+  if (!rc && a.n) {
+    a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu_in = gu, a.gu = dgu, a.h = h;
+    rc = rows_product<FMT, kDh>(what, dy, lddy, w_d, F, D, a, s);
+    if (!rc && dx) {
+      a.m = (uint32_t)D, a.k = 2 * (uint32_t)F, a.out = dx, a.ldo = lddx;
+      rc = rows_product<FMT, kDx>(what, dgu, 2 * (size_t)F, w_gu, D, 2 * F, a, s);
+    }
+  }
+  if (!rc && dw_d) rc = weight_grad<FMT>(what, h, F, dy, lddy, dw_d, F, D, a, s);
+  if (!rc && dw_gu) rc = weight_grad<FMT>(what, x, ldx, dgu, 2 * (size_t)F, dw_gu, D, 2 * F, a, s);
+  return rc;
+}
+
+}  // namespace
+
+extern "C" int moe_expert_workspace(int n, int E, int D, int F, int backward, size_t* bytes) {
+  return moe::entry("moe_expert_workspace", [&]() -> int {
+    if (!bytes) return fail(SYMM_EINVAL, "moe_expert_workspace: NULL bytes");
+    const int rc = check_sizes("moe_expert_workspace", n, E, D, F);
+    if (rc) return rc;
+    *bytes = h_bytes(n, F) + (backward ? h_bytes(n, 2 * F) : 0);
+    return SYMM_OK;
+  });
+}
+
+extern "C" int moe_expert_ffn(symm_heap_t* heap, const void* x, size_t ldx, const int32_t* counts,
+                              const void* w_gu, const void* w_d, int act, int dtype, int n, int E,
+                              int D, int F, void* gu, void* y, size_t ldy, void* workspace,
+                              void* stream) {
+  return moe::entry("moe_expert_ffn", [&]() -> int {
+    const char* what = "moe_expert_ffn";
+    int rc = check_common(what, heap, counts, w_gu, w_d, act, dtype, n, E, D, F);
+    if (rc) return rc;
+    if (bad_ld(ldx, D) || ldy < (size_t)D || ldy > (1ull << 36))
+      return fail(SYMM_EINVAL, "moe_expert_ffn: ldx >= D (a multiple of 8), ldy >= D");
+    if (n == 0) return SYMM_OK;
+    if (!x || !y || !workspace) return fail(SYMM_EINVAL, "moe_expert_ffn: NULL x, y or workspace");
+    if (!moe::aligned(x, 16) || !moe::aligned(y, 2) || !moe::aligned(gu, 2) ||
+        !moe::aligned(workspace, 256))
+      return fail(SYMM_EINVAL, "moe_expert_ffn: x must be 16-byte aligned, workspace 256-byte, "
+                               "y and gu to their elements");
+    if (y == x || y == w_gu || y == w_d || y == gu || (gu && (gu == x || gu == w_gu || gu == w_d)))
+      return fail(SYMM_EINVAL, "moe_expert_ffn: outputs must not be inputs or each other");
+    cudaStream_t s = as_stream(stream);
+    rc = ensure_ctrl(heap, s);
+    if (rc) return rc;
+    ExpertArgs a{};
+    a.counts = counts, a.n = (uint32_t)n, a.E = (uint32_t)E, a.F = (uint32_t)F, a.act = act;
+    a.budget_ns = heap->spin_budget, a.ctl = reinterpret_cast<Control*>(heap->base);
+    return dtype == SYMM_DTYPE_BF16
+               ? forward<1>(what, x, ldx, w_gu, w_d, D, F, gu, y, ldy, workspace, a, s)
+               : forward<0>(what, x, ldx, w_gu, w_d, D, F, gu, y, ldy, workspace, a, s);
+  });
+}
+
+extern "C" int moe_expert_ffn_backward(symm_heap_t* heap, const void* dy, size_t lddy,
+                                       const void* x, size_t ldx, const void* gu,
+                                       const int32_t* counts, const void* w_gu, const void* w_d,
+                                       int act, int dtype, int n, int E, int D, int F, void* dx,
+                                       size_t lddx, void* dw_gu, void* dw_d, void* workspace,
+                                       void* stream) {
+  return moe::entry("moe_expert_ffn_backward", [&]() -> int {
+    const char* what = "moe_expert_ffn_backward";
+    int rc = check_common(what, heap, counts, w_gu, w_d, act, dtype, n, E, D, F);
+    if (rc) return rc;
+    if (bad_ld(lddy, D) || bad_ld(ldx, D) || (dx && (lddx < (size_t)D || lddx > (1ull << 36))))
+      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: lddy, ldx >= D (multiples of 8), "
+                               "lddx >= D");
+    if (n && (!dy || !x || !gu || !workspace))
+      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: NULL dy, x, gu or workspace");
+    if (!moe::aligned(dy, 16) || !moe::aligned(x, 16) || !moe::aligned(gu, 2) ||
+        !moe::aligned(dx, 2) || !moe::aligned(dw_gu, 16) || !moe::aligned(dw_d, 16) ||
+        !moe::aligned(workspace, 256))
+      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: dy, x, dw_gu and dw_d must be 16-byte "
+                               "aligned, workspace 256-byte, gu and dx to their elements");
+    const void* in[] = {dy, x, gu, w_gu, w_d};
+    const void* out[] = {dx, dw_gu, dw_d};
+    for (int i = 0; i < 3; ++i)
+      for (int j = 0; out[i] && j < 5 + i; ++j)
+        if (out[i] == (j < 5 ? in[j] : out[j - 5]))
+          return fail(SYMM_EINVAL,
+                      "moe_expert_ffn_backward: outputs must not be inputs or each other");
+    cudaStream_t s = as_stream(stream);
+    rc = ensure_ctrl(heap, s);
+    if (rc) return rc;
+    if (n == 0) {  // no rows: gradients of zero
+      const size_t half = (size_t)E * D * F * 2;
+      if (dw_gu) rc = cuda_check(cudaMemsetAsync(dw_gu, 0, 2 * half, s), what);
+      if (!rc && dw_d) rc = cuda_check(cudaMemsetAsync(dw_d, 0, half, s), what);
+      return rc;
+    }
+    ExpertArgs a{};
+    a.counts = counts, a.n = (uint32_t)n, a.E = (uint32_t)E, a.F = (uint32_t)F, a.act = act;
+    a.budget_ns = heap->spin_budget, a.ctl = reinterpret_cast<Control*>(heap->base);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    void* dgu = ws + h_bytes(n, F);
+    return dtype == SYMM_DTYPE_BF16
+               ? backward<1>(what, dy, lddy, x, ldx, gu, w_gu, w_d, D, F, dx, lddx, dw_gu, dw_d,
+                             ws, dgu, a, s)
+               : backward<0>(what, dy, lddy, x, ldx, gu, w_gu, w_d, D, F, dx, lddx, dw_gu, dw_d,
+                             ws, dgu, a, s);
+  });
+}

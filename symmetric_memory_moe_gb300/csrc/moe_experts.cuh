@@ -1,0 +1,160 @@
+// moe_experts.cuh -- what the experts' products share: where each expert's rows
+// lie, how they are cut into tiles, and how a tile's operands reach shared memory.
+#pragma once
+
+#include "moe_common.cuh"
+#include "symm_device.cuh"
+#include "symm_tcgen05.cuh"
+
+namespace experts {
+
+using symm::Control;
+
+constexpr uint32_t kThreads = 192;     // TMA producer, MMA issuer, four warps of epilogue
+constexpr uint32_t kBM = 128;          // features of a tile: the M side
+constexpr uint32_t kMaxRows = 256;     // rows of a tile: the N side
+constexpr uint32_t kMaxExperts = SYMM_MOE_MAX_EXPERTS;
+enum { kErrRange = -5 };
+
+// Expert e's rows are off[e] .. off[e + 1] - 1, its blocks of rows are numbered
+// blocks[e] .. blocks[e + 1] - 1 among all experts' (times the column blocks:
+// its tiles).
+struct Table {
+  uint32_t off[kMaxExperts + 1], blocks[kMaxExperts + 1];
+  uint32_t warp_rows[kThreads / 32], warp_blocks[kThreads / 32], warp_most[kThreads / 32];
+  uint32_t most;  // rows of the largest tile, in whole steps of 16
+};
+
+__device__ __forceinline__ uint32_t blocks_of(uint32_t rows) {
+  return (rows + kMaxRows - 1) / kMaxRows;
+}
+// Rows of each of an expert's blocks (the last one may have fewer, never none),
+// as even as whole steps of 16 allow.
+__device__ __forceinline__ uint32_t block_rows(uint32_t rows) {
+  const uint32_t nb = blocks_of(rows);
+  return nb ? ((rows + nb - 1) / nb + 15) / 16 * 16 : 0;
+}
+
+// Fills the table from the counts (NULL: one expert with all n rows), by all
+// threads of the block.  False where a count is negative or they exceed n.
+__device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_t E, uint32_t n) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t per = (E + kThreads - 1) / kThreads, first = threadIdx.x * per;
+  uint64_t sum = 0;  // of at most 1024 counts of at most n <= 2^24 each
+  uint32_t blocks = 0, most = 0;
+  bool bad = false;
+  for (uint32_t e = first; e < min(E, first + per); ++e) {
+    const int32_t c = counts ? counts[e] : (int32_t)n;
+    if (c < 0 || (uint32_t)c > n) {
+      bad = true;
+      continue;
+    }
+    sum += (uint32_t)c;
+    blocks += blocks_of((uint32_t)c);
+    most = max(most, block_rows((uint32_t)c));
+  }
+  bad |= sum > n;
+  uint32_t rows = (uint32_t)min(sum, (uint64_t)n + 1);  // the whole sum stays below 2^33
+  const uint32_t own_rows = rows, own_blocks = blocks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t r = __shfl_up_sync(0xffffffffu, rows, o);
+    const uint32_t b = __shfl_up_sync(0xffffffffu, blocks, o);
+    if (lane >= (uint32_t)o) rows = min(rows + r, n + 1), blocks += b;
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  if (lane == 31) t.warp_rows[warp] = rows, t.warp_blocks[warp] = blocks, t.warp_most[warp] = most;
+  __syncthreads();
+  uint32_t at = rows - own_rows, bt = blocks - own_blocks, all = 0, largest = 0;
+  for (uint32_t w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) at += t.warp_rows[w], bt += t.warp_blocks[w];
+    all = min(all + t.warp_rows[w], n + 1);
+    largest = max(largest, t.warp_most[w]);
+  }
+  bad |= all > n;
+  if (__syncthreads_or(bad)) return false;
+  for (uint32_t e = first; e < min(E, first + per); ++e) {
+    t.off[e] = at, t.blocks[e] = bt;
+    const uint32_t c = counts ? (uint32_t)counts[e] : n;
+    at += c, bt += blocks_of(c);
+    if (e == E - 1) t.off[E] = at, t.blocks[E] = bt, t.most = largest;
+  }
+  __syncthreads();
+  return true;
+}
+
+// The expert whose blocks hold number b (below blocks[E]): the last one with
+// blocks[e] <= b.
+__device__ __forceinline__ uint32_t expert_of(const Table& t, uint32_t b, uint32_t E) {
+  uint32_t lo = 0, hi = E;  // blocks[lo] <= b < blocks[hi]
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (t.blocks[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct Tile {
+  uint32_t e, row, rows, bt, col;  // rows: that are there, of bt
+};
+// Tile i of ncol column blocks.  Up to eight blocks of rows share a column
+// block's weights one after another, then the next column block shares theirs:
+// what the SMs work on at a time is about as many rows as columns, which L2 holds.
+__device__ __forceinline__ Tile tile_at(const Table& t, uint32_t i, uint32_t E, uint32_t ncol) {
+  Tile o;
+  o.e = expert_of(t, i / ncol, E);
+  const uint32_t c = t.off[o.e + 1] - t.off[o.e], nb = blocks_of(c);
+  o.bt = block_rows(c);
+  const uint32_t local = i - t.blocks[o.e] * ncol, group = local / (8 * ncol);
+  const uint32_t in = min(8u, nb - 8 * group), r = local - 8 * group * ncol;
+  const uint32_t b = 8 * group + r % in;
+  o.col = r / in;
+  o.row = t.off[o.e] + b * o.bt;
+  o.rows = min(o.bt, c - b * o.bt);
+  return o;
+}
+
+// Rows that a tile's copies bring: boxes of 16 up to 48 rows, else of 64.
+__device__ __forceinline__ uint32_t copied_rows(uint32_t bt) {
+  return bt <= 48 ? bt : (bt + 63) / 64 * 64;
+}
+
+// How long a CTA that gives up waits for its own copies and MMAs, which nothing
+// but the hardware holds up: a second, however short the heap's budget is.
+__device__ __forceinline__ uint64_t drain_ns(uint64_t budget_ns) {
+  return max(budget_ns, (uint64_t)1000000000);
+}
+
+// Whether p holds in any of the 128 threads of the epilogue (a barrier of theirs).
+__device__ __forceinline__ bool any_of(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p)
+      : "memory");
+  return r != 0;
+}
+
+// act(g) and its derivative: g sigma(g), or g Phi(g) with the normal
+// distribution's Phi.  The exponential and the quotient are the approximate
+// instructions, 2 to 3 ulp of 24 bits, before a rounding to 16 bits or fewer.
+__device__ __forceinline__ float activate(int act, float g) {
+  if (act == SYMM_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
+  return g * normcdff(g);
+}
+__device__ __forceinline__ void activate_both(int act, float g, float& a, float& da) {
+  if (act == SYMM_ACT_SILU) {
+    const float p = __fdividef(1.f, 1.f + __expf(-g));
+    a = g * p;
+    da = p * (1.f + g * (1.f - p));
+  } else {
+    const float p = normcdff(g);
+    a = g * p;
+    da = p + g * 0.3989422804014327f * __expf(-0.5f * g * g);
+  }
+}
+
+}  // namespace experts
