@@ -568,6 +568,7 @@ int moe_adapter_matmul(symm_heap_t *heap, const void *x, size_t ldx, const void 
 
 /* Activations of the experts: x sigma(x), and x Phi(x) with the normal
  * distribution's Phi (the exact form). */
+#define SYMM_ACT_NONE (-1) /* moe_fp4_quantize alone: rows as they are */
 #define SYMM_ACT_SILU 0
 #define SYMM_ACT_GELU 1
 
@@ -619,6 +620,66 @@ int moe_expert_ffn_backward(symm_heap_t *heap, const void *dy, size_t lddy, cons
                             const void *w_d, int act, int dtype, int n, int E, int D, int F,
                             void *dx, size_t lddx, void *dw_gu, void *dw_d, void *workspace,
                             void *stream);
+
+/* Microscaled 4-bit floating point: e2m1 codes (sign, two bits of exponent, one
+ * of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the even element in the
+ * low half, and a scale for each block of a row:
+ *   SYMM_FP4_MX  blocks of 32, scales e8m0 (byte b: 2^(b - 127), 255: NaN)
+ *   SYMM_FP4_NV  blocks of 16, scales e4m3, times a 32-bit number of the tensor's
+ * A packed row is k / 2 bytes of codes and, in a buffer of its own, a row of
+ * scales, one byte each in the blocks' order; the row strides ldc and lds are in
+ * bytes, multiples of 16. */
+#define SYMM_FP4_MX 0
+#define SYMM_FP4_NV 1
+
+/* Rows to 4 bits.  With t the largest magnitude of a block and g = gscale[0]:
+ *   MX  s = the smallest power of two with t <= 6 s (at least 2^-127)
+ *   NV  s = t / (6 g), at most 448, rounded to e4m3 (products and quotients
+ *       rounded to 32 bits); the values' unit is s g rounded to 32 bits
+ *   code = x / unit rounded to the nearest e2m1, ties to the even code, at most
+ *       6; 0 where the unit is 0.
+ * A block that holds an infinity or NaN gets the scale NaN and codes 0.
+ * x       device [n] rows, ldx elements apart (a multiple of 8), of `dtype`
+ *         (SYMM_DTYPE_F16, _BF16 or _F32).  act SYMM_ACT_NONE: rows of k.
+ *         Else rows of 2k, and what is packed is act(first k) * (last k) in 32
+ *         bits: gu of the feed-forward becomes its second product's operand.
+ * gscale  device float [1], positive (NULL allowed = 1; not read with MX).
+ * codes, scales  device, 16-byte aligned as x; of a scale row, the k / 32 or
+ *         k / 16 bytes are written.
+ * 0 <= n <= 2^24, k a multiple of 32 in [32, 2^17].  n = 0 is a no-op.
+ * Errors: SYMM_EINVAL, SYMM_ECUDA. */
+int moe_fp4_quantize(const void *x, size_t ldx, int act, int dtype, int fmt, const float *gscale,
+                     int n, int k, void *codes, size_t ldc, void *scales, size_t lds,
+                     void *stream);
+
+/* And back: y [n] rows of k, ldy elements apart (a multiple of 8, 16-byte
+ * aligned), of `dtype`: code * (s * gscale[0]) (gscale NULL allowed = 1, with
+ * either format), rounded once.  Errors: SYMM_EINVAL, SYMM_ECUDA. */
+int moe_fp4_dequantize(const void *codes, size_t ldc, const void *scales, size_t lds, int fmt,
+                       const float *gscale, int n, int k, int dtype, void *y, size_t ldy,
+                       void *stream);
+
+/* The experts' projection of packed rows with packed weights, rows grouped by
+ * expert as for moe_expert_ffn: for each row r of expert e and feature f < m,
+ *     y_rf = gx[0] gw[e] sum_i x_ri w_efi.
+ * xc, xs  the rows' codes and scales, n rows, ldxc and ldxs bytes apart.
+ * wc, ws  the weights', E * m rows of k (an expert's features one after another:
+ *         the matrix transposed, as its contraction is what the blocks divide),
+ *         ldwc and ldws bytes apart.
+ * counts  device int32 [E], as moe_expert_ffn (NULL with E = 1: all n).
+ * gx      device float [1], gw device float [E] (each NULL allowed = 1): the
+ *         tensors' own scales.
+ * y       device [n] rows of m, ldy elements apart, of `dtype` (SYMM_DTYPE_F16 or
+ *         _BF16); rows behind the last expert's are left as they were.
+ * Sums are in 32 bits, gx gw_e and y rounded once each.  n, k as for moe_fp4_quantize,
+ * 1 <= E <= SYMM_MOE_MAX_EXPERTS, 1 <= m <= 2^20; codes and scales 16-byte
+ * aligned.  n = 0 is a no-op.
+ * Errors: as moe_expert_ffn. */
+int moe_fp4_expert_matmul(symm_heap_t *heap, const void *xc, size_t ldxc, const void *xs,
+                          size_t ldxs, const void *wc, size_t ldwc, const void *ws, size_t ldws,
+                          const int32_t *counts, const float *gx, const float *gw, int fmt,
+                          int dtype, int n, int E, int k, int m, void *y, size_t ldy,
+                          void *stream);
 
 #ifdef __cplusplus
 }

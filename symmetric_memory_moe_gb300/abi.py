@@ -94,6 +94,9 @@ _SIGS = {
     "moe_expert_ffn": [_P, _P, _SZ] + [_P] * 3 + [_I] * 6 + [_P, _P, _SZ, _P, _P],
     "moe_expert_ffn_backward": [_P, _P, _SZ, _P, _SZ] + [_P] * 4 + [_I] * 6 +
                                [_P, _SZ] + [_P] * 4,
+    "moe_fp4_quantize": [_P, _SZ] + [_I] * 3 + [_P, _I, _I] + [_P, _SZ] * 2 + [_P],
+    "moe_fp4_dequantize": [_P, _SZ] * 2 + [_I, _P] + [_I] * 3 + [_P, _SZ, _P],
+    "moe_fp4_expert_matmul": [_P] + [_P, _SZ] * 4 + [_P] * 3 + [_I] * 6 + [_P, _SZ, _P],
 }
 
 _lock = threading.Lock()
@@ -384,6 +387,7 @@ def moe_adapter_matmul(heap, x, ldx, w, ldw, a, b, scale, ids, dtype, T, k, n, R
                                     y, ldy, workspace, _stream(stream)), "moe_adapter_matmul")
 
 
+SYMM_ACT_NONE = -1
 SYMM_ACT_SILU = 0
 SYMM_ACT_GELU = 1
 
@@ -408,3 +412,27 @@ def moe_expert_ffn_backward(heap, dy, lddy, x, ldx, gu, counts, w_gu, w_d, act, 
     _check(lib().moe_expert_ffn_backward(heap, dy, lddy, x, ldx, gu, counts, w_gu, w_d, act, dtype,
                                          n, E, D, F, dx, lddx, dw_gu, dw_d, workspace,
                                          _stream(stream)), "moe_expert_ffn_backward")
+
+
+SYMM_FP4_MX = 0
+SYMM_FP4_NV = 1
+
+
+def moe_fp4_quantize(x, ldx, act, dtype, fmt, gscale, n, k, codes, ldc, scales, lds, stream=None):
+    """Rows to microscaled 4-bit floating point; see include/symm_a2a.h."""
+    _check(lib().moe_fp4_quantize(x, ldx, act, dtype, fmt, gscale, n, k, codes, ldc, scales, lds,
+                                  _stream(stream)), "moe_fp4_quantize")
+
+
+def moe_fp4_dequantize(codes, ldc, scales, lds, fmt, gscale, n, k, dtype, y, ldy, stream=None):
+    _check(lib().moe_fp4_dequantize(codes, ldc, scales, lds, fmt, gscale, n, k, dtype, y, ldy,
+                                    _stream(stream)), "moe_fp4_dequantize")
+
+
+def moe_fp4_expert_matmul(heap, xc, ldxc, xs, ldxs, wc, ldwc, ws, ldws, counts, gx, gw, fmt, dtype,
+                          n, E, k, m, y, ldy, stream=None):
+    """The experts' projection of 4-bit rows with 4-bit weights; see
+    include/symm_a2a.h."""
+    _check(lib().moe_fp4_expert_matmul(heap, xc, ldxc, xs, ldxs, wc, ldwc, ws, ldws, counts, gx,
+                                       gw, fmt, dtype, n, E, k, m, y, ldy, _stream(stream)),
+           "moe_fp4_expert_matmul")

@@ -19,7 +19,7 @@ LIB_NAME = "libsymm_a2a.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["heap.cu", "a2a.cu", "pc_noalloc.cu", "collectives.cu", "two_phase.cu",
            "ag_gemm.cu", "host_pipe.cu", "moe_route.cu", "moe_norm.cu",
-           "moe_adapter.cu", "moe_expert.cu"]
+           "moe_adapter.cu", "moe_expert.cu", "moe_fp4.cu"]
 HEADERS = ["symm_device.cuh", "symm_internal.h", "symm_tcgen05.cuh", "moe_common.cuh",
            "moe_experts.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -42,6 +42,8 @@ using namespace symm_host;
 
 namespace {
 
+constexpr uint32_t kThreads = 192;
+constexpr uint32_t kMaxRows = 256;                       // rows of a tile: the N side
 constexpr uint32_t kBK = 64;
 constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
 constexpr uint32_t kRingBytes = 192 * 1024;              // four stages of 128 x 256 tiles
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table table;
+  __shared__ Table<kMaxRows> table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
   moe::let_next_start();
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table table;
+  __shared__ Table<kMaxRows> table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
   moe::let_next_start();

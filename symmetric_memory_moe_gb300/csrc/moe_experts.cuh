@@ -10,36 +10,40 @@ namespace experts {
 
 using symm::Control;
 
-constexpr uint32_t kThreads = 192;     // TMA producer, MMA issuer, four warps of epilogue
 constexpr uint32_t kBM = 128;          // features of a tile: the M side
-constexpr uint32_t kMaxRows = 256;     // rows of a tile: the N side
+constexpr uint32_t kMaxWarps = 10;     // of a block
 constexpr uint32_t kMaxExperts = SYMM_MOE_MAX_EXPERTS;
 enum { kErrRange = -5 };
 
 // Expert e's rows are off[e] .. off[e + 1] - 1, its blocks of rows are numbered
 // blocks[e] .. blocks[e + 1] - 1 among all experts' (times the column blocks:
-// its tiles).
+// its tiles).  A block has at most MAX rows.
+template <uint32_t MAX>
 struct Table {
   uint32_t off[kMaxExperts + 1], blocks[kMaxExperts + 1];
-  uint32_t warp_rows[kThreads / 32], warp_blocks[kThreads / 32], warp_most[kThreads / 32];
-  uint32_t most;  // rows of the largest tile, in whole steps of 16
+  uint32_t warp_rows[kMaxWarps], warp_blocks[kMaxWarps], warp_most[kMaxWarps];
+  uint32_t most;  // rows of the largest block, in whole steps of 16
 };
 
+template <uint32_t MAX>
 __device__ __forceinline__ uint32_t blocks_of(uint32_t rows) {
-  return (rows + kMaxRows - 1) / kMaxRows;
+  return (rows + MAX - 1) / MAX;
 }
-// Rows of each of an expert's blocks (the last one may have fewer, never none),
-// as even as whole steps of 16 allow.
+// Rows of each of an expert's blocks (the last one may have fewer, never none), as
+// even as whole steps of 16 allow.
+template <uint32_t MAX>
 __device__ __forceinline__ uint32_t block_rows(uint32_t rows) {
-  const uint32_t nb = blocks_of(rows);
+  const uint32_t nb = blocks_of<MAX>(rows);
   return nb ? ((rows + nb - 1) / nb + 15) / 16 * 16 : 0;
 }
 
 // Fills the table from the counts (NULL: one expert with all n rows), by all
 // threads of the block.  False where a count is negative or they exceed n.
-__device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_t E, uint32_t n) {
+template <uint32_t MAX>
+__device__ __forceinline__ bool lay_out(Table<MAX>& t, const int32_t* counts, uint32_t E,
+                                        uint32_t n) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t per = (E + kThreads - 1) / kThreads, first = threadIdx.x * per;
+  const uint32_t per = (E + blockDim.x - 1) / blockDim.x, first = threadIdx.x * per;
   uint64_t sum = 0;  // of at most 1024 counts of at most n <= 2^24 each
   uint32_t blocks = 0, most = 0;
   bool bad = false;
@@ -50,8 +54,8 @@ __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_
       continue;
     }
     sum += (uint32_t)c;
-    blocks += blocks_of((uint32_t)c);
-    most = max(most, block_rows((uint32_t)c));
+    blocks += blocks_of<MAX>((uint32_t)c);
+    most = max(most, block_rows<MAX>((uint32_t)c));
   }
   bad |= sum > n;
   uint32_t rows = (uint32_t)min(sum, (uint64_t)n + 1);  // the whole sum stays below 2^33
@@ -66,7 +70,7 @@ __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_
   if (lane == 31) t.warp_rows[warp] = rows, t.warp_blocks[warp] = blocks, t.warp_most[warp] = most;
   __syncthreads();
   uint32_t at = rows - own_rows, bt = blocks - own_blocks, all = 0, largest = 0;
-  for (uint32_t w = 0; w < kThreads / 32; ++w) {
+  for (uint32_t w = 0; w < blockDim.x / 32; ++w) {
     if (w < warp) at += t.warp_rows[w], bt += t.warp_blocks[w];
     all = min(all + t.warp_rows[w], n + 1);
     largest = max(largest, t.warp_most[w]);
@@ -76,7 +80,7 @@ __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_
   for (uint32_t e = first; e < min(E, first + per); ++e) {
     t.off[e] = at, t.blocks[e] = bt;
     const uint32_t c = counts ? (uint32_t)counts[e] : n;
-    at += c, bt += blocks_of(c);
+    at += c, bt += blocks_of<MAX>(c);
     if (e == E - 1) t.off[E] = at, t.blocks[E] = bt, t.most = largest;
   }
   __syncthreads();
@@ -85,7 +89,8 @@ __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_
 
 // The expert whose blocks hold number b (below blocks[E]): the last one with
 // blocks[e] <= b.
-__device__ __forceinline__ uint32_t expert_of(const Table& t, uint32_t b, uint32_t E) {
+template <uint32_t MAX>
+__device__ __forceinline__ uint32_t expert_of(const Table<MAX>& t, uint32_t b, uint32_t E) {
   uint32_t lo = 0, hi = E;  // blocks[lo] <= b < blocks[hi]
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) / 2;
@@ -101,11 +106,13 @@ struct Tile {
 // Tile i of ncol column blocks.  Up to eight blocks of rows share a column
 // block's weights one after another, then the next column block shares theirs:
 // what the SMs work on at a time is about as many rows as columns, which L2 holds.
-__device__ __forceinline__ Tile tile_at(const Table& t, uint32_t i, uint32_t E, uint32_t ncol) {
+template <uint32_t MAX>
+__device__ __forceinline__ Tile tile_at(const Table<MAX>& t, uint32_t i, uint32_t E,
+                                        uint32_t ncol) {
   Tile o;
   o.e = expert_of(t, i / ncol, E);
-  const uint32_t c = t.off[o.e + 1] - t.off[o.e], nb = blocks_of(c);
-  o.bt = block_rows(c);
+  const uint32_t c = t.off[o.e + 1] - t.off[o.e], nb = blocks_of<MAX>(c);
+  o.bt = block_rows<MAX>(c);
   const uint32_t local = i - t.blocks[o.e] * ncol, group = local / (8 * ncol);
   const uint32_t in = min(8u, nb - 8 * group), r = local - 8 * group * ncol;
   const uint32_t b = 8 * group + r % in;

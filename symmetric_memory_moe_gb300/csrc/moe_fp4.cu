@@ -1,0 +1,708 @@
+// moe_fp4.cu -- rows in microscaled 4-bit floating point (e2m1: 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6 and their negatives) and the experts' product of such rows with
+// such weights.
+//
+// A block of values shares a scale s, in 8 bits; with a tensor's own scale g:
+//   MX  blocks of 32, s the smallest power of two with max |x| <= 6 s: no value of
+//       a block is cut off (the power below would cut those above 6 s, up to a
+//       quarter of them, for half the step)
+//   NV  blocks of 16, s = max |x| / (6 g) rounded to e4m3
+//   code = x / (s g) rounded to the nearest e2m1, ties to the even code
+// The quotient is CUDA's correctly rounded one (MX: a product with a power of two,
+// exact): a value next to a border of two codes goes where it belongs.
+//
+// quantize_kernel, dequantize_kernel: one pass; a lane has 8 values (16 bytes), 2
+// or 4 neighbouring lanes a block.  With an activation the values are act(g) u
+// of a row's halves, in 32 bits.
+//
+// fp4_kernel: y_r = gx gw_e sum_b sx_rb sw_b sum_i x_ri w_i, as y^T = W^T x^T on the
+// block-scaled tensor cores: the M side 128 features of an expert, the N side 16
+// to 192 of its rows.  A slice of K is 256 values, one 128-byte swizzled row.
+//   warp 0     TMA producer: codes and scales of both sides into a ring
+//   warp 1     MMA issuer: copies a slice's scales from shared memory into TMEM
+//              (tcgen05.cp, two slots) and issues its four tcgen05.mma, K 64
+//   warps 2-5  epilogue
+//   warps 6-9  scales as they lie beside the codes (a row's one after another) into
+//              the order that TMEM takes: 4 scales of each of 128 rows, row r at
+//              word r / 32 of 16-byte line r % 32
+// 192 rows, not 256: two accumulators and two slots of scales fill 480 of TMEM's 512
+// columns.
+#include <algorithm>
+#include <string>
+
+#include "moe_experts.cuh"
+
+using namespace experts;
+using namespace symm_host;
+
+namespace {
+
+// ------------------------------------------------------- rows to codes --
+constexpr uint32_t kQuantThreads = 256;
+
+struct QuantArgs {
+  const void* x;
+  size_t ldx;       // elements
+  uint8_t *codes, *scales;
+  size_t ldc, lds;  // bytes
+  const float* g;
+  uint64_t vectors;  // of 8 values
+  uint32_t k, kv;    // values and vectors of a row
+  int act;
+};
+
+template <typename T>
+struct Vec8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T* p) {
+  Vec8<T> r;
+#pragma unroll
+  for (size_t i = 0; i < sizeof(T) / 2; ++i)
+    r.v[i] = symm::ld16_ro(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void floats(const Vec8<T>& r, float (&f)[8]) {
+  const T* t = reinterpret_cast<const T*>(&r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = moe::to_f(t[i]);
+}
+
+// 8 codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t to_codes(const float (&q)[8]) {
+  uint32_t c;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(c)
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return c;
+}
+__device__ __forceinline__ void from_codes(uint32_t c, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(h + i));
+    v[2 * i] = f.x, v[2 * i + 1] = f.y;
+  }
+}
+// e4m3 of a value that is not negative, at most 448, to the nearest, and back.
+__device__ __forceinline__ uint32_t to_e4m3(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(v));
+  return r & 0xffu;
+}
+__device__ __forceinline__ float from_e4m3(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
+  return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+}
+__device__ __forceinline__ float power_of_two(int e) {  // -127 <= e <= 127
+  return __uint_as_float(e == -127 ? 0x400000u : (uint32_t)(e + 127) << 23);
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
+  constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;  // of a block
+  moe::let_next_start();
+  moe::wait_for_earlier();
+  const float g = a.g ? *a.g : 1.f;
+  const uint64_t step = (uint64_t)gridDim.x * kQuantThreads;
+  const uint64_t first = (uint64_t)blockIdx.x * kQuantThreads + threadIdx.x;
+  const uint64_t step_row = step / a.kv;
+  const uint32_t step_col = (uint32_t)(step % a.kv);
+  uint64_t row = first / a.kv;
+  uint32_t col = (uint32_t)(first % a.kv);
+  // whole warps go round: a block's lanes are of one row, and there or not together
+  for (uint64_t v = first; v - (threadIdx.x & 31) < a.vectors; v += step) {
+    float f[8];
+    if (v < a.vectors) {
+      const T* x = static_cast<const T*>(a.x) + row * a.ldx + 8 * col;
+      const Vec8<T> r = load8(x);
+      floats(r, f);
+      if (a.act != SYMM_ACT_NONE) {
+        const Vec8<T> r2 = load8(x + a.k);
+        float u[8];
+        floats(r2, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = activate(a.act, f[i]) * u[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    }
+    uint32_t top = 0;  // magnitudes compare as whole numbers, NaN above infinity
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+#pragma unroll
+    for (uint32_t o = 1; o < kLanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const bool finite = top < 0x7f800000u;
+    uint32_t byte, code = 0;
+    if (FMT == SYMM_FP4_MX) {
+      // top = m 2^e with 1 <= m < 2: 6 2^(e - 2) reaches it up to m = 1.5
+      int e = (int)(top >> 23) - 127;
+      if (e == -127) e = -1000;  // below 2^-126 the smallest scale reaches anything
+      e = max(-127, min(127, e - 2 + ((top & 0x7fffffu) > 0x400000u)));
+      byte = finite ? (uint32_t)(e + 127) : 0xffu;
+      if (finite) {
+        // 2^-e in two factors, neither of which leaves the range
+        const float s1 = power_of_two(-e / 2), s2 = power_of_two(-e - -e / 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f[i] * s1 * s2;
+        code = to_codes(f);
+      }
+    } else {
+      byte = finite ? to_e4m3(fminf(__fdiv_rn(__uint_as_float(top), __fmul_rn(6.f, g)), 448.f))
+                    : 0x7fu;
+      const float unit = __fmul_rn(from_e4m3(byte), g);
+      if (finite && unit > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], unit);
+        code = to_codes(f);
+      }
+    }
+    if (v < a.vectors) {
+      *reinterpret_cast<uint32_t*>(a.codes + row * a.ldc + 4 * col) = code;
+      if (threadIdx.x % kLanes == 0) a.scales[row * a.lds + col / kLanes] = (uint8_t)byte;
+    }
+    row += step_row, col += step_col;
+    if (col >= a.kv) col -= a.kv, ++row;
+  }
+}
+
+struct DequantArgs {
+  const uint8_t *codes, *scales;
+  size_t ldc, lds;  // bytes
+  const float* g;
+  void* y;
+  size_t ldy;  // elements
+  uint64_t vectors;
+  uint32_t kv;
+};
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const DequantArgs a) {
+  constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;
+  moe::let_next_start();
+  moe::wait_for_earlier();
+  const float g = a.g ? *a.g : 1.f;
+  const uint64_t step = (uint64_t)gridDim.x * kQuantThreads;
+  const uint64_t first = (uint64_t)blockIdx.x * kQuantThreads + threadIdx.x;
+  const uint64_t step_row = step / a.kv;
+  const uint32_t step_col = (uint32_t)(step % a.kv);
+  uint64_t row = first / a.kv;
+  uint32_t col = (uint32_t)(first % a.kv);
+  for (uint64_t v = first; v < a.vectors; v += step) {
+    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(a.codes + row * a.ldc) + col);
+    const uint32_t byte = __ldg(a.scales + row * a.lds + col / kLanes);
+    float unit;
+    if (FMT == SYMM_FP4_MX)
+      unit = byte == 0xffu ? __uint_as_float(0x7fffffffu) : power_of_two((int)byte - 127);
+    else
+      unit = from_e4m3(byte);
+    if (a.g) unit = __fmul_rn(unit, g);
+    float f[8];
+    from_codes(code, f);
+    __align__(16) T out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = moe::from_f<T>(__fmul_rn(f[i], unit));
+    uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.ldy + 8 * col);
+#pragma unroll
+    for (size_t i = 0; i < sizeof(T) / 2; ++i) y[i] = reinterpret_cast<const uint4*>(out)[i];
+    row += step_row, col += step_col;
+    if (col >= a.kv) col -= a.kv, ++row;
+  }
+}
+
+// ------------------------------------------------------------ fp4_kernel --
+constexpr uint32_t kThreads = 320;
+constexpr uint32_t kMaxRows = 192;
+constexpr uint32_t kSlice = 256;                     // values of K: a row of 128 bytes
+constexpr uint32_t kATile = kBM * 128;               // 16 KB
+constexpr uint32_t kARaw = kBM * 16;                 // its scales, 16 bytes a row
+constexpr uint32_t kRingBytes = 208 * 1024;          // four stages of 128 x 192 tiles
+constexpr uint32_t kMaxStages = 9;
+constexpr uint32_t kSmemBytes = 1024 + kRingBytes;
+constexpr uint32_t kAccCols = 192;
+constexpr uint32_t kScaleCols = 2 * kAccCols;        // first column of the scales' slots
+
+template <int FMT>
+struct Scales {
+  // 512-byte tiles of a slice: 4 scales of 128 rows, the K of one MMA (NV) or two (MX)
+  static constexpr uint32_t kTiles = FMT == SYMM_FP4_MX ? 2 : 4;
+  static constexpr uint32_t kPerSlice = kTiles * 4;      // scales of a row
+  static constexpr uint32_t kSlotCols = kTiles * 4 * 3;  // one row block of A, two of B
+};
+
+struct Fp4Args {
+  const int32_t* counts;
+  const float *gx, *gw;
+  uint32_t n, E, m, k, ncol;
+  void* y;
+  size_t ldy;
+  uint64_t budget_ns;
+  Control* ctl;
+};
+
+struct Barriers {
+  uint64_t full[kMaxStages], placed[kMaxStages], empty[kMaxStages];
+  uint64_t tfull[2], tempty[2], sfree[2], drain;
+  uint32_t tmem;
+};
+
+// 32 lines of 16 bytes into 4 TMEM columns of all four quarters of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, const void* tile) {
+  const uint64_t desc = ((symm::smem_addr(tile) & 0x3FFFFull) >> 4) | ((128ull >> 4) << 32) |
+                        (1ull << 46);  // no swizzle, 8 lines 128 bytes apart, version 1
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+template <int FMT>
+__device__ __forceinline__ void scaled_mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc,
+                                           uint32_t sa, uint32_t sb, uint32_t accumulate) {
+  if (FMT == SYMM_FP4_MX)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: e2m1 on both sides (1 at bits 7 and 10), N, the scales'
+// type (bit 23: ue8m0), M, and which of a column's scales are meant (bits 4, 29).
+template <int FMT>
+__device__ __forceinline__ uint32_t fp4_idesc(uint32_t n, uint32_t which) {
+  return (which << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) |
+         ((uint32_t)(FMT == SYMM_FP4_MX) << 23) | ((kBM >> 4) << 24) | (which << 29);
+}
+
+template <typename T>
+__device__ __forceinline__ void store16(const Fp4Args& a, const uint32_t (&v)[16], float scale,
+                                        uint32_t row, uint32_t valid, uint32_t f) {
+  if (f >= a.m) return;
+  T* y = static_cast<T*>(a.y) + (size_t)row * a.ldy + f;
+#pragma unroll
+  for (uint32_t j = 0; j < 16; ++j)
+    if (j < valid) y[j * a.ldy] = moe::from_f<T>(__uint_as_float(v[j]) * scale);
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
+               const __grid_constant__ CUtensorMap map_x64,
+               const __grid_constant__ CUtensorMap map_xs64,
+               const __grid_constant__ CUtensorMap map_x16,
+               const __grid_constant__ CUtensorMap map_xs16, const Fp4Args a) {
+  using S = Scales<FMT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
+  __shared__ Barriers bar;
+  __shared__ Table<kMaxRows> table;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < kMaxStages; ++s) {
+      symm::mbar_init(&bar.full[s], 1);
+      symm::mbar_init(&bar.placed[s], 128);
+      symm::mbar_init(&bar.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      symm::mbar_init(&bar.tfull[i], 1);
+      symm::mbar_init(&bar.tempty[i], 128);
+      symm::mbar_init(&bar.sfree[i], 1);
+    }
+    symm::mbar_init(&bar.drain, 1);
+    symm::fence_mbar_init();
+  }
+  if (warp == 1) symm::tmem_alloc(&bar.tmem, 512);
+  symm::tc_fence_before();
+  __syncthreads();
+  symm::tc_fence_after();
+  moe::let_next_start();
+  moe::wait_for_earlier();
+  const bool good = lay_out(table, a.counts, a.E, a.n);
+  if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
+  const uint32_t tiles = good ? table.blocks[a.E] * a.ncol : 0, tmem = bar.tmem;
+  const uint32_t slices = (a.k + kSlice - 1) / kSlice;
+  // A stage: codes of A and B, their scales as loaded (A, B), and as TMEM takes them.
+  const uint32_t most = good ? copied_rows(table.most) : 16;
+  const uint32_t raw = kATile + most * 128, tiled = raw + kARaw + most * 16;
+  const uint32_t stage_bytes = (tiled + S::kTiles * 512 * 3 + 1023) / 1024 * 1024;
+  const uint32_t stages = min(kMaxStages, kRingBytes / stage_bytes);
+
+  if (warp == 0) {  // ----------------------------------------- TMA producer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 1, it = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t rows = copied_rows(t.bt);
+      for (uint32_t s = 0; s < slices; ++s) {
+        if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
+        uint8_t* buf = smem + st * stage_bytes;
+        uint64_t* full = &bar.full[st];
+        if (elected) {
+          symm::mbar_arrive_expect_tx(full, kATile + kARaw + rows * (128 + 16));
+          // 16 bytes of scales: this slice's, or with MX of this and its neighbour
+          const int k = (int)(s * 128), b = (int)(s * S::kPerSlice / 16 * 16);
+          symm::tma_load_3d(buf, &map_w, k, (int)(t.col * kBM), (int)t.e, full);
+          symm::tma_load_3d(buf + raw, &map_ws, b, (int)(t.col * kBM), (int)t.e, full);
+          const uint32_t box = t.bt <= 48 ? 16 : 64;
+          const CUtensorMap* mx = t.bt <= 48 ? &map_x16 : &map_x64;
+          const CUtensorMap* ms = t.bt <= 48 ? &map_xs16 : &map_xs64;
+          for (uint32_t r = 0; r < rows; r += box) {
+            symm::tma_load_2d(buf + kATile + r * 128, mx, k, (int)(t.row + r), full);
+            symm::tma_load_2d(buf + raw + kARaw + r * 16, ms, b, (int)(t.row + r), full);
+          }
+        }
+        ++it;
+        if (++st == stages) st = 0, ph ^= 1;
+      }
+    }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
+    for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
+      symm::mbar_wait(&bar.full[i % stages], (i / stages) & 1, drain_ns(a.budget_ns));
+  } else if (warp == 1) {  // ---------------------------------- MMA issuer
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 0, seg = 0, g = 0;  // g: slices so far
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t buf = seg & 1;
+      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+        break;
+      symm::tc_fence_after();
+      const uint32_t acc = tmem + buf * kAccCols;
+      for (uint32_t s = 0; s < slices; ++s, ++g) {
+        const uint32_t slot = g & 1, sa = tmem + kScaleCols + slot * S::kSlotCols;
+        const uint32_t sb = sa + S::kTiles * 4;
+        ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl) &&
+             symm::mbar_wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl) &&
+             symm::mbar_wait_warp(&bar.sfree[slot], ((g >> 1) & 1) ^ 1u, a.budget_ns, a.ctl);
+        if (!ok) break;
+        symm::tc_fence_after();
+        const uint8_t* at = smem + st * stage_bytes;
+        const uint64_t wd = symm::sw128_kmajor_desc(at);
+        const uint64_t xd = symm::sw128_kmajor_desc(at + kATile);
+        if (elected) {
+          // A's tiles in K order; B's two row blocks side by side, in K order
+#pragma unroll
+          for (uint32_t c = 0; c < S::kTiles; ++c)
+            copy_scales(sa + 4 * c, at + tiled + 512 * c);
+          for (uint32_t c = 0; c < 2 * S::kTiles; ++c)
+            if (c % 2 == 0 || t.bt > 128)
+              copy_scales(sb + 4 * c, at + tiled + 512 * (S::kTiles + c));
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint32_t c = j * S::kTiles / 4, which = FMT == SYMM_FP4_MX ? 2 * (j & 1) : 0;
+            scaled_mma<FMT>(acc, wd + 2 * j, xd + 2 * j, fp4_idesc<FMT>(t.bt, which), sa + 4 * c,
+                            sb + 8 * c, (s | j) != 0);
+          }
+          symm::tc_commit(&bar.sfree[slot]);
+          symm::tc_commit(&bar.empty[st]);
+        }
+        if (++st == stages) st = 0, ph ^= 1;
+      }
+      if (ok && elected) symm::tc_commit(&bar.tfull[buf]);
+    }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
+    if (elected) symm::tc_commit(&bar.drain);
+    symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+  } else if (warp < 6) {  // ------------------------------------ epilogue
+    const uint32_t q = (uint32_t)(warp & 3);
+    const float gx = a.gx ? *a.gx : 1.f;
+    uint32_t seg = 0;
+    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t buf = seg & 1;
+      const float scale = a.gw ? gx * a.gw[t.e] : gx;
+      const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+      if (any_of(!ok)) {  // all threads leave, or none
+        if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
+        break;
+      }
+      symm::tc_fence_after();
+      const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
+      const uint32_t f = t.col * kBM + 32 * q + lane;
+      for (uint32_t c = 0; c < t.rows; c += 16) {
+        uint32_t v[16];
+        symm::tmem_ld16(taddr + c, v);
+        if (c + 16 >= t.rows) {  // the accumulator is free for the next tile
+          symm::tc_fence_before();
+          symm::mbar_arrive(&bar.tempty[buf]);
+        }
+        store16<T>(a, v, scale, t.row + c, t.rows - c, f);
+      }
+    }
+  } else {  // ---------------------------------------------- scales' order
+    // Lane l of warp w takes row 32 (l % 4) + 8 w + l / 4 of a block of 128: its
+    // words are neighbours of the other lanes' in the tile.
+    const uint32_t w = (uint32_t)warp - 6, r = 32 * (lane % 4) + 8 * w + lane / 4;
+    uint32_t st = 0, ph = 0;
+    bool ok = true;
+    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+      const Tile t = tile_at(table, i, a.E, a.ncol);
+      const uint32_t rows = copied_rows(t.bt);
+      for (uint32_t s = 0; s < slices; ++s) {
+        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        uint8_t* at = smem + st * stage_bytes;
+        const uint4* from = reinterpret_cast<const uint4*>(at + raw);
+        uint32_t* to = reinterpret_cast<uint32_t*>(at + tiled);
+        const uint32_t word = 4 * (8 * w + lane / 4) + lane % 4;
+        const bool odd = FMT == SYMM_FP4_MX && (s & 1);  // the second 8 bytes
+#pragma unroll
+        for (uint32_t b = 0; b < 3; ++b) {  // A's rows, B's first 128, B's others
+          const uint32_t row = b == 2 ? 128 + r : r;
+          if (b && row >= rows) continue;
+          const uint4 v = from[b ? 128 + row : row];
+          const uint32_t x[4] = {odd ? v.z : v.x, odd ? v.w : v.y, v.z, v.w};
+#pragma unroll
+          for (uint32_t c = 0; c < S::kTiles; ++c)
+            to[128 * (b ? S::kTiles + 2 * c + b - 1 : c) + word] = x[c];
+        }
+        symm::fence_proxy_async_shared();
+        symm::mbar_arrive(&bar.placed[st]);
+        if (++st == stages) st = 0, ph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -7);
+  }
+  __syncwarp();
+  symm::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    symm::tc_fence_after();
+    symm::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+int check_rows(const char* what, int fmt, int n, int k) {
+  if (fmt != SYMM_FP4_MX && fmt != SYMM_FP4_NV)
+    return fail(SYMM_EINVAL, std::string(what) + ": fmt must be SYMM_FP4_MX or _NV");
+  if (n < 0 || n > (1 << 24) || k < 32 || k % 32 || k > (1 << 17))
+    return fail(SYMM_EINVAL, std::string(what) + ": n must be in [0, 2^24], k a multiple of 32 in "
+                                                 "[32, 2^17]");
+  return SYMM_OK;
+}
+size_t scale_bytes(int fmt, int k) { return (size_t)k / (fmt == SYMM_FP4_MX ? 32 : 16); }
+bool bad_packed(size_t ldc, size_t lds, int fmt, int k) {
+  return ldc < (size_t)k / 2 || ldc % 16 || ldc > (1ull << 36) || lds < scale_bytes(fmt, k) ||
+         lds % 16 || lds > (1ull << 36);
+}
+
+unsigned quant_grid(uint64_t vectors) {
+  // as many blocks as are resident at once, 2048 threads an SM
+  const uint64_t room = (uint64_t)std::max(sm_count(), 1) * (2048 / kQuantThreads);
+  return (unsigned)std::min<uint64_t>(room, (vectors + kQuantThreads - 1) / kQuantThreads);
+}
+
+// Bytes [depth][rows][inner], rows ld and planes rows * ld apart; boxes of box_inner
+// x box_rows; depth 0: a 2-d map.
+int make_map(const char* what, CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
+             uint64_t depth, size_t ld, uint32_t box_inner, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return fail(SYMM_ECUDA, std::string(what) + ": no cuTensorMapEncodeTiled");
+  const cuuint64_t dims[3] = {inner, rows, depth};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld * rows};
+  const cuuint32_t box[3] = {box_inner, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, depth ? 3 : 2, const_cast<void*>(base), dims, strides,
+         box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         box_inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(SYMM_ECUDA,
+                std::string(what) + ": tensor map rejected (CUresult " + std::to_string(r) + ")");
+  return SYMM_OK;
+}
+
+struct Maps {
+  CUtensorMap w, ws, x64, xs64, x16, xs16;
+};
+
+template <typename T, int FMT>
+int launch_product(const Maps& m, const Fp4Args& a, cudaStream_t s) {
+  static std::mutex mu;
+  static bool done[64] = {};
+  int dev = 0;
+  int rc = cuda_check(cudaGetDevice(&dev), "moe_fp4_expert_matmul: device");
+  if (rc) return rc;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+      rc = cuda_check(cudaFuncSetAttribute((const void*)fp4_kernel<T, FMT>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)kSmemBytes),
+                      "moe_fp4_expert_matmul: kernel set-up");
+      if (rc) return rc;
+      if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+  }
+  // at most one partly filled block of rows for each expert that has rows
+  const uint64_t most = (uint64_t)a.ncol * std::min<uint64_t>(a.n, a.n / kMaxRows + a.E);
+  const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), most);
+  return moe::launch("moe_fp4_expert_matmul", fp4_kernel<T, FMT>, grid, kThreads, kSmemBytes, s,
+                     m.w, m.ws, m.x64, m.xs64, m.x16, m.xs16, a);
+}
+
+template <typename T>
+int launch_quantize(int fmt, const QuantArgs& a, cudaStream_t s) {
+  return moe::launch("moe_fp4_quantize",
+                     fmt == SYMM_FP4_MX ? quantize_kernel<T, SYMM_FP4_MX>
+                                        : quantize_kernel<T, SYMM_FP4_NV>,
+                     quant_grid(a.vectors), kQuantThreads, 0, s, a);
+}
+template <typename T>
+int launch_dequantize(int fmt, const DequantArgs& a, cudaStream_t s) {
+  return moe::launch("moe_fp4_dequantize",
+                     fmt == SYMM_FP4_MX ? dequantize_kernel<T, SYMM_FP4_MX>
+                                        : dequantize_kernel<T, SYMM_FP4_NV>,
+                     quant_grid(a.vectors), kQuantThreads, 0, s, a);
+}
+
+}  // namespace
+
+extern "C" int moe_fp4_quantize(const void* x, size_t ldx, int act, int dtype, int fmt,
+                                const float* gscale, int n, int k, void* codes, size_t ldc,
+                                void* scales, size_t lds, void* stream) {
+  return moe::entry("moe_fp4_quantize", [&]() -> int {
+    const char* what = "moe_fp4_quantize";
+    int rc = check_rows(what, fmt, n, k);
+    if (rc) return rc;
+    if (!moe::dtype_ok(dtype))
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: dtype must be SYMM_DTYPE_F16, _BF16 or _F32");
+    if (act != SYMM_ACT_NONE && act != SYMM_ACT_SILU && act != SYMM_ACT_GELU)
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: act must be SYMM_ACT_NONE, _SILU or _GELU");
+    const size_t width = act == SYMM_ACT_NONE ? (size_t)k : 2 * (size_t)k;
+    if (ldx < width || ldx % 8 || ldx > (1ull << 36) || bad_packed(ldc, lds, fmt, k))
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: ldx must hold a row (k, or 2k with an "
+                               "activation) in whole eights, ldc k / 2 bytes and lds a row's "
+                               "scales in whole sixteens");
+    if (n == 0) return SYMM_OK;
+    if (!x || !codes || !scales)
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: NULL x, codes or scales");
+    if (!moe::aligned(x, 16) || !moe::aligned(codes, 16) || !moe::aligned(scales, 16) ||
+        !moe::aligned(gscale, 4))
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: x, codes and scales must be 16-byte aligned, "
+                               "gscale 4-byte");
+    if (codes == x || scales == x || codes == scales)
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: outputs must not be inputs or each other");
+    QuantArgs a{};
+    a.x = x, a.ldx = ldx, a.codes = static_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint8_t*>(scales), a.ldc = ldc, a.lds = lds, a.g = gscale;
+    a.k = (uint32_t)k, a.kv = (uint32_t)k / 8, a.vectors = (uint64_t)n * a.kv, a.act = act;
+    if (fmt == SYMM_FP4_MX) a.g = nullptr;
+    cudaStream_t s = as_stream(stream);
+    return dtype == SYMM_DTYPE_F32    ? launch_quantize<float>(fmt, a, s)
+           : dtype == SYMM_DTYPE_BF16 ? launch_quantize<__nv_bfloat16>(fmt, a, s)
+                                      : launch_quantize<__half>(fmt, a, s);
+  });
+}
+
+extern "C" int moe_fp4_dequantize(const void* codes, size_t ldc, const void* scales, size_t lds,
+                                  int fmt, const float* gscale, int n, int k, int dtype, void* y,
+                                  size_t ldy, void* stream) {
+  return moe::entry("moe_fp4_dequantize", [&]() -> int {
+    const char* what = "moe_fp4_dequantize";
+    int rc = check_rows(what, fmt, n, k);
+    if (rc) return rc;
+    if (!moe::dtype_ok(dtype))
+      return fail(SYMM_EINVAL, "moe_fp4_dequantize: dtype must be SYMM_DTYPE_F16, _BF16 or _F32");
+    if (ldy < (size_t)k || ldy % 8 || ldy > (1ull << 36) || bad_packed(ldc, lds, fmt, k))
+      return fail(SYMM_EINVAL, "moe_fp4_dequantize: ldy >= k in whole eights, ldc k / 2 bytes and "
+                               "lds a row's scales in whole sixteens");
+    if (n == 0) return SYMM_OK;
+    if (!codes || !scales || !y)
+      return fail(SYMM_EINVAL, "moe_fp4_dequantize: NULL codes, scales or y");
+    if (!moe::aligned(codes, 16) || !moe::aligned(scales, 16) || !moe::aligned(y, 16) ||
+        !moe::aligned(gscale, 4))
+      return fail(SYMM_EINVAL, "moe_fp4_dequantize: codes, scales and y must be 16-byte aligned, "
+                               "gscale 4-byte");
+    if (y == codes || y == scales)
+      return fail(SYMM_EINVAL, "moe_fp4_dequantize: y must not be an input");
+    DequantArgs a{};
+    a.codes = static_cast<const uint8_t*>(codes), a.scales = static_cast<const uint8_t*>(scales);
+    a.ldc = ldc, a.lds = lds, a.g = gscale, a.y = y, a.ldy = ldy;
+    a.kv = (uint32_t)k / 8, a.vectors = (uint64_t)n * a.kv;
+    cudaStream_t s = as_stream(stream);
+    return dtype == SYMM_DTYPE_F32    ? launch_dequantize<float>(fmt, a, s)
+           : dtype == SYMM_DTYPE_BF16 ? launch_dequantize<__nv_bfloat16>(fmt, a, s)
+                                      : launch_dequantize<__half>(fmt, a, s);
+  });
+}
+
+extern "C" int moe_fp4_expert_matmul(symm_heap_t* heap, const void* xc, size_t ldxc,
+                                     const void* xs, size_t ldxs, const void* wc, size_t ldwc,
+                                     const void* ws, size_t ldws, const int32_t* counts,
+                                     const float* gx, const float* gw, int fmt, int dtype, int n,
+                                     int E, int k, int m, void* y, size_t ldy, void* stream) {
+  return moe::entry("moe_fp4_expert_matmul", [&]() -> int {
+    const char* what = "moe_fp4_expert_matmul";
+    if (!heap) return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: NULL heap");
+    int rc = check_rows(what, fmt, n, k);
+    if (rc) return rc;
+    if (dtype != SYMM_DTYPE_F16 && dtype != SYMM_DTYPE_BF16)
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: dtype must be SYMM_DTYPE_F16 or _BF16");
+    if (E < 1 || E > SYMM_MOE_MAX_EXPERTS || m < 1 || m > (1 << 20))
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: E must be in [1, 1024], m in [1, 2^20]");
+    if (bad_packed(ldxc, ldxs, fmt, k) || bad_packed(ldwc, ldws, fmt, k) || ldy < (size_t)m ||
+        ldy > (1ull << 36))
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: ldxc and ldwc must hold k / 2 bytes, ldxs "
+                               "and ldws a row's scales, in whole sixteens; ldy >= m");
+    if (!counts && E != 1)
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: counts may be NULL with one expert only");
+    if (n == 0) return SYMM_OK;
+    if (!xc || !xs || !wc || !ws || !y)
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: NULL codes, scales or y");
+    if (!moe::aligned(xc, 16) || !moe::aligned(xs, 16) || !moe::aligned(wc, 16) ||
+        !moe::aligned(ws, 16) || !moe::aligned(y, 2) || !moe::aligned(counts, 4) ||
+        !moe::aligned(gx, 4) || !moe::aligned(gw, 4))
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: codes and scales must be 16-byte aligned, "
+                               "the rest to their elements");
+    if (y == xc || y == xs || y == wc || y == ws)
+      return fail(SYMM_EINVAL, "moe_fp4_expert_matmul: y must not be an input");
+    const size_t sb = scale_bytes(fmt, k);
+    Maps mp{};
+    rc = make_map(what, &mp.w, wc, k / 2, m, E, ldwc, 128, kBM);
+    if (!rc) rc = make_map(what, &mp.ws, ws, sb, m, E, ldws, 16, kBM);
+    if (!rc) rc = make_map(what, &mp.x64, xc, k / 2, n, 0, ldxc, 128, 64);
+    if (!rc) rc = make_map(what, &mp.xs64, xs, sb, n, 0, ldxs, 16, 64);
+    if (!rc) rc = make_map(what, &mp.x16, xc, k / 2, n, 0, ldxc, 128, 16);
+    if (!rc) rc = make_map(what, &mp.xs16, xs, sb, n, 0, ldxs, 16, 16);
+    if (rc) return rc;
+    cudaStream_t s = as_stream(stream);
+    rc = ensure_ctrl(heap, s);
+    if (rc) return rc;
+    Fp4Args a{};
+    a.counts = counts, a.gx = gx, a.gw = gw, a.n = (uint32_t)n, a.E = (uint32_t)E;
+    a.m = (uint32_t)m, a.k = (uint32_t)k, a.ncol = ((uint32_t)m + kBM - 1) / kBM;
+    a.y = y, a.ldy = ldy, a.budget_ns = heap->spin_budget;
+    a.ctl = reinterpret_cast<Control*>(heap->base);
+    const bool bf = dtype == SYMM_DTYPE_BF16;
+    if (fmt == SYMM_FP4_MX)
+      return bf ? launch_product<__nv_bfloat16, SYMM_FP4_MX>(mp, a, s)
+                : launch_product<__half, SYMM_FP4_MX>(mp, a, s);
+    return bf ? launch_product<__nv_bfloat16, SYMM_FP4_NV>(mp, a, s)
+              : launch_product<__half, SYMM_FP4_NV>(mp, a, s);
+  });
+}

@@ -92,3 +92,66 @@ def ffn_grad(dy, x, gu, counts, w_gu, w_d, name, u_out, tiny):
             o["e" + name_].append(ev)
     cat = {k: torch.cat(v) if k.endswith("dx") else torch.stack(v) for k, v in o.items()}
     return cat
+
+
+# ------------------------------------------------------------ 4-bit rows --
+GRID = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+BLOCK = {"mx": 32, "nv": 16}
+
+
+def nearest(q):
+    """Codes 0 .. 7 of magnitudes q in 64 bits: the nearest value, ties to the even code."""
+    grid = GRID.to(q.device)
+    lo = (torch.bucketize(q, grid, right=True) - 1).clamp(0, 7)
+    hi = (lo + 1).clamp(max=7)
+    down, up = q - grid[lo], grid[hi] - q
+    return torch.where((up < down) | ((up == down) & (lo % 2 == 1)), hi, lo)
+
+
+def unit_of(scale, fmt, g):
+    """What a block's scale byte stands for, with the tensor's own scale g (None: 1)."""
+    if fmt == "mx":
+        u = torch.ldexp(torch.ones(scale.shape, dtype=torch.float64), scale.cpu().int() - 127)
+        u[scale.cpu() == 255] = math.nan
+        u = u.to(scale.device)
+        return u if g is None else (u.float() * g).double()
+    u = scale.contiguous().view(torch.float8_e4m3fn).float()
+    return (u if g is None else u * g).double()
+
+
+def quantize(x, fmt, g):
+    """Codes [n, k] uint8 (sign in bit 3) and scales [n, k / block] uint8 of x in 64 bits."""
+    b = x.double().unflatten(-1, (-1, BLOCK[fmt]))
+    top = b.abs().amax(-1)
+    bad = ~torch.isfinite(b).all(-1)
+    top = torch.where(bad, 0.0, top)
+    if fmt == "mx":
+        s = torch.full_like(top, -127, dtype=torch.int64)
+        for e in range(-126, 128):  # the smallest that reaches the largest value
+            s = torch.where(top > 6 * 2.0 ** (e - 1), e, s)
+        scale = (s + 127).to(torch.uint8)
+        scale[bad] = 255
+    else:
+        six = 6 * (torch.ones(1, device=x.device) if g is None else g)
+        scale = (top.float() / six).clamp(max=448).to(torch.float8_e4m3fn).view(torch.uint8)
+        scale = torch.where(bad, torch.full_like(scale, 0x7f), scale)
+    unit = unit_of(scale, fmt, None if fmt == "mx" else g)[..., None]
+    q = (b / unit).float().double()  # the quotient is rounded to 32 bits
+    code = nearest(torch.where((unit > 0) & ~bad[..., None], q.abs(), 0.0))
+    code = torch.where(torch.signbit(b) & ~bad[..., None] & (unit > 0), code + 8, code)
+    return code.flatten(-2).to(torch.uint8), scale
+
+
+def values(code, scale, fmt, g):
+    """What codes and scales stand for, in 64 bits."""
+    v = GRID.to(code.device)[(code & 7).long()] * torch.where(code > 7, -1.0, 1.0)
+    return (v.unflatten(-1, (-1, BLOCK[fmt])) * unit_of(scale, fmt, g)[..., None]).flatten(-2)
+
+
+def pack(code):
+    c = code.unflatten(-1, (-1, 2))
+    return c[..., 0] | (c[..., 1] << 4)
+
+
+def unpack(codes):
+    return torch.stack([codes & 15, codes >> 4], -1).flatten(-2)

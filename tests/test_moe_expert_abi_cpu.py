@@ -75,3 +75,55 @@ def test_workspace_refuses():
     for bad in ((-1, 1, 8, 8), (1, 0, 8, 8), (1, 1, 12, 8), (1, 1, 8, 4)):
         assert code(abi.moe_expert_workspace, *bad) == E
     assert abi.lib().moe_expert_workspace(1, 1, 8, 8, 0, ctypes.POINTER(ctypes.c_size_t)()) == E
+
+
+QUANT = dict(x=P, ldx=64, act=-1, dtype=BF16, fmt=0, gscale=P, n=4, k=64, codes=2 * P, ldc=32,
+             scales=3 * P, lds=16, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(act=2), dict(act=-2), dict(dtype=3), dict(dtype=-1), dict(fmt=2), dict(fmt=-1),
+    dict(n=-1), dict(n=(1 << 24) + 1), dict(k=0), dict(k=48),
+    dict(k=(1 << 17) + 32, ldx=1 << 18, ldc=1 << 17, lds=1 << 14),
+    dict(ldx=56), dict(ldx=68), dict(ldx=1 << 37), dict(act=0), dict(ldc=16), dict(ldc=40),
+    dict(ldc=1 << 37), dict(lds=0), dict(lds=8), dict(lds=24), dict(lds=1 << 37), dict(x=None),
+    dict(codes=None), dict(scales=None), dict(x=P + 8), dict(codes=P + 8), dict(scales=P + 8),
+    dict(gscale=P + 2), dict(codes=P), dict(scales=P), dict(scales=2 * P)])
+def test_quantize_refuses(bad):
+    assert code(abi.moe_fp4_quantize, **dict(QUANT, **bad)) == E
+
+
+DEQ = dict(codes=P, ldc=32, scales=2 * P, lds=16, fmt=1, gscale=None, n=4, k=64, dtype=BF16,
+           y=3 * P, ldy=64, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(fmt=2), dict(dtype=3), dict(n=-1), dict(n=(1 << 24) + 1), dict(k=0), dict(k=40),
+    dict(ldc=16), dict(ldc=33), dict(lds=0), dict(lds=20), dict(ldy=56), dict(ldy=65),
+    dict(ldy=1 << 37), dict(codes=None), dict(scales=None), dict(y=None), dict(codes=P + 4),
+    dict(scales=P + 4), dict(y=P + 8), dict(gscale=P + 1), dict(y=P), dict(y=2 * P)])
+def test_dequantize_refuses(bad):
+    assert code(abi.moe_fp4_dequantize, **dict(DEQ, **bad)) == E
+
+
+MM = dict(xc=P, ldxc=32, xs=2 * P, ldxs=16, wc=3 * P, ldwc=32, ws=4 * P, ldws=16, counts=P,
+          gx=None, gw=P, fmt=1, dtype=BF16, n=4, E=2, k=64, m=40, y=5 * P, ldy=40, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(heap=None), dict(fmt=2), dict(dtype=2), dict(n=-1), dict(n=(1 << 24) + 1), dict(E=0),
+    dict(E=1025), dict(k=0), dict(k=48), dict(m=0), dict(m=(1 << 20) + 1, ldy=1 << 21),
+    dict(ldxc=16), dict(ldxc=40), dict(ldxs=0), dict(ldxs=8), dict(ldwc=16), dict(ldwc=40),
+    dict(ldws=0), dict(ldws=8), dict(ldy=39), dict(ldy=1 << 37), dict(counts=None), dict(xc=None),
+    dict(xs=None), dict(wc=None), dict(ws=None), dict(y=None), dict(xc=P + 8), dict(xs=P + 8),
+    dict(wc=P + 8), dict(ws=P + 8), dict(y=P + 1), dict(counts=P + 2), dict(gx=P + 2),
+    dict(gw=P + 2), dict(y=P), dict(y=2 * P), dict(y=3 * P), dict(y=4 * P)])
+def test_product_refuses(heap, bad):
+    assert code(abi.moe_fp4_expert_matmul, **dict(MM, **dict(dict(heap=heap), **bad))) == E
+
+
+def test_fp4_of_no_rows(heap):
+    abi.moe_fp4_quantize(**dict(QUANT, n=0, x=None, codes=None, scales=None))
+    abi.moe_fp4_dequantize(**dict(DEQ, n=0, codes=None, scales=None, y=None))
+    abi.moe_fp4_expert_matmul(**dict(MM, heap=heap, n=0, xc=None, xs=None, wc=None, ws=None,
+                                     y=None))
