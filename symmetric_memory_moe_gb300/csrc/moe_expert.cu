@@ -43,10 +43,10 @@ using namespace symm_host;
 namespace {
 
 constexpr uint32_t kThreads = 192;
-constexpr uint32_t kMaxRows = 256;                       // rows of a tile: the N side
+constexpr uint32_t kMaxRows = 256, kStep = 32;           // rows of a tile: the N side of a pair
 constexpr uint32_t kBK = 64;
 constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
-constexpr uint32_t kRingBytes = 192 * 1024;              // four stages of 128 x 256 tiles
+constexpr uint32_t kRingBytes = 192 * 1024;              // six stages of 128 features, 128 rows
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kExchange = 2 * 2 * 16 * 64 * 4;      // two chunks, two halves of 16 x 64
 constexpr uint32_t kSmemBytes = 1024 + kRingBytes + kExchange;
@@ -58,7 +58,7 @@ struct ExpertArgs {
   const int32_t* counts;
   uint32_t n, E;
   uint32_t m, k;       // features out (kGated: F), contraction
-  uint32_t ncol;       // column blocks
+  uint32_t npair;      // pairs of column blocks
   uint32_t F;          // offset of u in gu
   int act;
   const void* gu_in;   // kDh
@@ -73,7 +73,7 @@ struct ExpertArgs {
 __device__ __forceinline__ uint32_t mma_idesc(uint32_t fmt, uint32_t n, bool m_major,
                                               bool n_major) {
   return (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)m_major << 15) |
-         ((uint32_t)n_major << 16) | ((n >> 3) << 17) | ((kBM >> 4) << 24);
+         ((uint32_t)n_major << 16) | ((n >> 3) << 17) | ((2 * kBM >> 4) << 24);
 }
 constexpr uint64_t kMajorStep = (16 * 128) >> 4;  // 16 K rows of an M- or N-major tile
 constexpr uint64_t kKStep = 32 >> 4;              // 16 K columns of a K-major tile
@@ -87,42 +87,52 @@ struct Elem<1> {
   using T = __nv_bfloat16;
 };
 
-// The ring of a launch whose largest tile copies `rows` rows.
+// The ring of a launch in which a CTA copies at most `rows` rows of a tile.
 struct Ring {
   uint32_t deep, stages, stage_bytes;
 };
 __device__ __forceinline__ Ring ring_of(uint32_t rows) {
   Ring r;
-  r.deep = rows <= 64 ? 2 : 1;
+  r.deep = rows <= 32 ? 2 : 1;
   r.stage_bytes = r.deep * (kATile + rows * 128);
   r.stages = min(kMaxStages, kRingBytes / r.stage_bytes);
   return r;
 }
 
 struct Barriers {
-  uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];  // ready: the second CTA's half
+  uint64_t tfull[2], tempty[2], drain;
   uint32_t tmem;
 };
 // Barriers and TMEM, before the launch before this one has ended.
 __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
   if (threadIdx.x == 0) {
-    for (uint32_t s = 0; s < kMaxStages; ++s) symm::mbar_init(&b.full[s], 1), symm::mbar_init(&b.empty[s], 1);
-    for (int i = 0; i < 2; ++i) symm::mbar_init(&b.tfull[i], 1), symm::mbar_init(&b.tempty[i], 128);
+    for (uint32_t s = 0; s < kMaxStages; ++s) {
+      symm::mbar_init(&b.full[s], 1);
+      symm::mbar_init(&b.ready[s], 1);
+      symm::mbar_init(&b.empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      symm::mbar_init(&b.tfull[i], 1);
+      symm::mbar_init(&b.tempty[i], 256);  // both CTAs' epilogues
+    }
     symm::mbar_init(&b.drain, 1);
     symm::fence_mbar_init();
   }
-  if (warp == 1) symm::tmem_alloc(&b.tmem, 2 * kAccCols);
+  if (warp == 1) pair_tmem_alloc(&b.tmem, 2 * kAccCols);
   symm::tc_fence_before();
   __syncthreads();
+  pair_sync();
   symm::tc_fence_after();
 }
 __device__ __forceinline__ void leave_cta(Barriers& b, int warp) {
   __syncwarp();
   symm::tc_fence_before();
   __syncthreads();
+  pair_sync();  // the other CTA's MMAs, arrivals and reads of TMEM are over too
   if (warp == 1) {
     symm::tc_fence_after();
-    symm::tmem_dealloc(b.tmem, 2 * kAccCols);
+    pair_tmem_dealloc(b.tmem, 2 * kAccCols);
   }
 }
 
@@ -192,25 +202,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<kMaxRows> table;
+  __shared__ Table<kMaxRows, kStep> table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
   moe::let_next_start();
   moe::wait_for_earlier();
   const bool good = lay_out(table, a.counts, a.E, a.n);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
-  const uint32_t tiles = good ? table.blocks[a.E] * a.ncol : 0;
-  const Ring ring = ring_of(good ? copied_rows(table.most) : 16);
+  const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0;
+  const Ring ring = ring_of(good ? copied_rows(table.most / 2) : 16);
   const uint32_t slices = (a.k + ring.deep * kBK - 1) / (ring.deep * kBK);
   const uint32_t tmem = bar.tmem, abytes = ring.deep * kATile;
+  const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 1, it = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
-      const uint32_t rows = copied_rows(t.bt), xbytes = rows * 128;
+    for (uint32_t i = first; ok && i < tiles; i += step) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
+      const uint32_t half = t.bt / 2, rows = copied_rows(half), xbytes = rows * 128;
+      const uint32_t col = 2 * t.col + rank, row = t.row + rank * half;
       for (uint32_t s = 0; s < slices; ++s) {
         if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * ring.stage_bytes;
@@ -220,20 +232,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t d = 0; d < ring.deep; ++d) {
             const int k = (int)((s * ring.deep + d) * kBK);
             if (kMMajor) {
-              const int x = KIND == kGated ? (int)(t.col * 64) : (int)(t.col * kBM);
+              const int x = KIND == kGated ? (int)(col * 64) : (int)(col * kBM);
               const int x2 = KIND == kGated ? x + (int)a.F : x + 64;
               symm::tma_load_3d(buf + d * (kATile / 2), &map_w, x, k, (int)t.e, full);
               symm::tma_load_3d(buf + abytes / 2 + d * (kATile / 2), &map_w, x2, k, (int)t.e, full);
             } else {
-              symm::tma_load_3d(buf + d * kATile, &map_w, k, (int)(t.col * kBM), (int)t.e, full);
+              symm::tma_load_3d(buf + d * kATile, &map_w, k, (int)(col * kBM), (int)t.e, full);
             }
             uint8_t* x = buf + abytes + d * xbytes;
-            if (t.bt <= 48)
+            if (half <= 48)
               for (uint32_t r = 0; r < rows; r += 16)
-                symm::tma_load_2d(x + r * 128, &map_x16, k, (int)(t.row + r), full);
+                symm::tma_load_2d(x + r * 128, &map_x16, k, (int)(row + r), full);
             else
               for (uint32_t r = 0; r < rows; r += 64)
-                symm::tma_load_2d(x + r * 128, &map_x64, k, (int)(t.row + r), full);
+                symm::tma_load_2d(x + r * 128, &map_x64, k, (int)(row + r), full);
           }
         }
         ++it;
@@ -241,23 +253,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-    // every load issued lands before the CTA may leave (bounded)
-    for (uint32_t i = it > ring.stages ? it - ring.stages : 0; i < it; ++i)
-      symm::mbar_wait(&bar.full[i % ring.stages], (i / ring.stages) & 1, drain_ns(a.budget_ns));
+    drain_ring(bar.full, bar.empty, ring.stages, it, ok, a.budget_ns);
+  } else if (warp == 1 && rank) {  // -------- tells the first CTA what is here
+    const bool elected = symm::elect_one();
+    uint32_t st = 0, ph = 0;
+    bool ok = true;
+    for (uint32_t i = first; ok && i < tiles; i += step)
+      for (uint32_t s = 0; s < slices; ++s) {
+        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        if (elected) arrive_first(&bar.ready[st]);
+        if (++st == ring.stages) st = 0, ph ^= 1;
+      }
+    if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -4);
   } else if (warp == 1) {  // ---------------------------------- MMA issuer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 0, seg = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++seg) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
-      const uint32_t xbytes = copied_rows(t.bt) * 128, buf = seg & 1;
+    for (uint32_t i = first; ok && i < tiles; i += step, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
+      const uint32_t xbytes = copied_rows(t.bt / 2) * 128, buf = seg & 1;
       const uint32_t idesc = mma_idesc(FMT, t.bt, kMMajor, false);
-      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+      if (!(ok = wait_pair_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
       for (uint32_t s = 0; s < slices; ++s) {
-        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl) &&
+             wait_pair_warp(&bar.ready[st], ph, a.budget_ns, a.ctl);
+        if (!ok) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * ring.stage_bytes;
         if (elected) {
@@ -268,24 +291,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t xd = symm::sw128_kmajor_desc(at + abytes + d * xbytes);
 #pragma unroll
             for (uint32_t j = 0; j < kBK / 16; ++j)
-              symm::tc_mma(acc, wd + (kMMajor ? kMajorStep : kKStep) * j, xd + kKStep * j, idesc,
-                           (s | d | j) != 0);
+              pair_mma(acc, wd + (kMMajor ? kMajorStep : kKStep) * j, xd + kKStep * j, idesc,
+                       (s | d | j) != 0);
           }
-          symm::tc_commit(&bar.empty[st]);
+          pair_commit(&bar.empty[st]);
         }
         if (++st == ring.stages) st = 0, ph ^= 1;
       }
-      if (ok && elected) symm::tc_commit(&bar.tfull[buf]);
+      if (ok && elected) pair_commit(&bar.tfull[buf]);
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-    if (elected) symm::tc_commit(&bar.drain);  // every MMA is complete before TMEM is freed
+    if (elected) pair_commit_own(&bar.drain);  // every MMA is complete before TMEM is freed
     symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
   } else {  // -------------------------------------------------- epilogue
     const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q + 31
     float* exchange = reinterpret_cast<float*>(smem + kRingBytes);
     uint32_t seg = 0, chunk = 0;
-    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, ++seg) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
+    for (uint32_t i = first; i < tiles; i += step, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t buf = seg & 1;
       const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
       if (any_of(!ok)) {  // all threads leave, or none
@@ -296,13 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
       if (KIND == kGated) {
         // Chunks of 32 rows: the warps of g finish the first 16, those of u the others.
-        const uint32_t f = t.col * 64 + 32 * (q & 1) + lane, mine = q >> 1;
+        const uint32_t f = (2 * t.col + rank) * 64 + 32 * (q & 1) + lane, mine = q >> 1;
         for (uint32_t c = 0; c < t.rows; c += 32, ++chunk) {
           uint32_t v[32];
           symm::tmem_ld32(taddr + c, v);
           if (c + 32 >= t.rows) {  // the accumulator is free for the next tile
             symm::tc_fence_before();
-            symm::mbar_arrive(&bar.tempty[buf]);
+            arrive_first(&bar.tempty[buf]);
           }
           // half 0: g of the last 16 rows, half 1: u of the first 16
           float* there = exchange + (chunk & 1) * (2 * 16 * 64) + 32 * (q & 1) + lane;
@@ -322,13 +345,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        const uint32_t f = t.col * kBM + 32 * q + lane;
+        const uint32_t f = (2 * t.col + rank) * kBM + 32 * q + lane;
         for (uint32_t c = 0; c < t.rows; c += 16) {
           uint32_t v[16];
           symm::tmem_ld16(taddr + c, v);
           if (c + 16 >= t.rows) {
             symm::tc_fence_before();
-            symm::mbar_arrive(&bar.tempty[buf]);
+            arrive_first(&bar.tempty[buf]);
           }
           if (KIND == kDh) grad16<FMT>(a, v, t.row + c, t.rows - c, f);
           else store16<FMT>(a, v, t.row + c, t.rows - c, f);
@@ -343,12 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct GradArgs {
   const int32_t* counts;
   uint32_t n, E, m, nf;  // out [E][m][nf]
-  uint32_t mb, nb;       // blocks of 128 and of 256
+  uint32_t mb, nb;       // blocks of 256
   void* out;
   uint64_t budget_ns;
   Control* ctl;
 };
-constexpr uint32_t kGradStage = 6 * 64 * 128;  // two boxes of A, four of B: 64 rows x 64 features
+constexpr uint32_t kGradStage = 4 * 64 * 128;  // two boxes of A, two of B: 64 rows x 64 features
 constexpr uint32_t kGradStages = kRingBytes / kGradStage;
 
 template <int FMT>
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<kMaxRows> table;
+  __shared__ Table<kMaxRows, kStep> table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
   moe::let_next_start();
@@ -368,14 +391,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   const uint32_t per = a.mb * a.nb, tiles = good ? a.E * per : 0;
   const uint32_t tmem = bar.tmem;
-  // Tile i: an expert's blocks of 256 columns one after another, then the next 128 rows.
+  const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
+  // Tile i: an expert's blocks of 256 columns one after another, then the next 256 rows.
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 1, it = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-      const uint32_t e = i / per, m0 = i % per / a.nb * kBM, n0 = i % a.nb * 256;
+    for (uint32_t i = first; ok && i < tiles; i += step) {
+      const uint32_t e = i / per, m0 = i % per / a.nb * 256 + rank * kBM;
+      const uint32_t n0 = i % a.nb * 256 + rank * 128;
       const uint32_t r0 = table.off[e], r1 = table.off[e + 1];
       for (uint32_t r = r0; r < r1; r += 64) {
         if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
@@ -386,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t b = 0; b < 2; ++b)
             symm::tma_load_2d(buf + b * 8192, &map_a, (int)(m0 + 64 * b), (int)r, &bar.full[st]);
 #pragma unroll
-          for (uint32_t b = 0; b < 4; ++b)
+          for (uint32_t b = 0; b < 2; ++b)
             symm::tma_load_2d(buf + (2 + b) * 8192, &map_b, (int)(n0 + 64 * b), (int)r,
                               &bar.full[st]);
         }
@@ -395,18 +420,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-    for (uint32_t i = it > kGradStages ? it - kGradStages : 0; i < it; ++i)
-      symm::mbar_wait(&bar.full[i % kGradStages], (i / kGradStages) & 1, drain_ns(a.budget_ns));
-  } else if (warp == 1) {  // ---------------------------------- MMA issuer
+    drain_ring(bar.full, bar.empty, kGradStages, it, ok, a.budget_ns);
+  } else if (warp == 1) {  // ------ MMA issuer, or tells the first CTA what is here
     const bool elected = symm::elect_one();
     const uint32_t idesc = mma_idesc(FMT, 256, true, true);
     uint32_t st = 0, ph = 0, seg = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+    for (uint32_t i = first; ok && i < tiles; i += step) {
       const uint32_t e = i / per, r0 = table.off[e], r1 = table.off[e + 1];
       if (r0 == r1) continue;  // the epilogue writes zeros
       const uint32_t buf = seg & 1;
-      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+      if (!rank &&
+          !(ok = wait_pair_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
@@ -416,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t left = min(64u, r1 - r), steps = (left + 15) / 16;
         if (left % 16) {  // the next expert's rows in the last step
           const uint32_t zero = steps * 16 - left;
-          for (uint32_t c = lane; c < 6 * 8 * zero; c += 32) {
+          for (uint32_t c = lane; c < 4 * 8 * zero; c += 32) {
             const uint32_t box = c / (8 * zero), w = c % (8 * zero);
             *reinterpret_cast<uint4*>(at + box * 8192 + left * 128 + w * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -424,27 +449,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           symm::fence_proxy_async_shared();
           __syncwarp();
         }
-        symm::tc_fence_after();
-        const uint64_t ad = symm::sw128_mnmajor_desc(at), bd = symm::sw128_mnmajor_desc(at + 16384);
-        if (elected) {
-          for (uint32_t j = 0; j < steps; ++j)
-            symm::tc_mma(acc, ad + kMajorStep * j, bd + kMajorStep * j, idesc, r != r0 || j != 0);
-          symm::tc_commit(&bar.empty[st]);
+        if (rank) {
+          if (elected) arrive_first(&bar.ready[st]);
+        } else {
+          if (!(ok = wait_pair_warp(&bar.ready[st], ph, a.budget_ns, a.ctl))) break;
+          symm::tc_fence_after();
+          const uint64_t ad = symm::sw128_mnmajor_desc(at);
+          const uint64_t bd = symm::sw128_mnmajor_desc(at + 16384);
+          if (elected) {
+            for (uint32_t j = 0; j < steps; ++j)
+              pair_mma(acc, ad + kMajorStep * j, bd + kMajorStep * j, idesc, r != r0 || j != 0);
+            pair_commit(&bar.empty[st]);
+          }
         }
         if (++st == kGradStages) st = 0, ph ^= 1;
       }
-      if (ok && elected) symm::tc_commit(&bar.tfull[buf]);
+      if (ok && elected && !rank) pair_commit(&bar.tfull[buf]);
       ++seg;
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-    if (elected) symm::tc_commit(&bar.drain);
-    symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+    if (!rank) {
+      if (elected) pair_commit_own(&bar.drain);
+      symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+    }
   } else {  // -------------------------------------------------- epilogue
     const uint32_t q = (uint32_t)(warp & 3);
     uint32_t seg = 0;
-    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x) {
+    for (uint32_t i = first; i < tiles; i += step) {
       const uint32_t e = i / per, n0 = i % a.nb * 256;
-      const uint32_t m = i % per / a.nb * kBM + 32 * q + lane, buf = seg & 1;
+      const uint32_t m = i % per / a.nb * 256 + rank * kBM + 32 * q + lane, buf = seg & 1;
       const bool any = table.off[e] != table.off[e + 1];
       if (any) {
         const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
@@ -464,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           symm::tmem_ld32(taddr + c, v);
           if (c == 224) {
             symm::tc_fence_before();
-            symm::mbar_arrive(&bar.tempty[buf]);
+            arrive_first(&bar.tempty[buf]);
           }
         } else {
 #pragma unroll
@@ -521,16 +554,21 @@ int make_map(const char* what, CUtensorMap* map, const void* base, int fmt, uint
   return SYMM_OK;
 }
 
-// Once per device: the kernels may use more than 48 KB of shared memory.
+// Once per device: the kernels may use more than 48 KB of shared memory.  *pairs:
+// CTA pairs that are resident at once (all kernels have the same resources).
 template <int FMT>
-int set_up() {
+int set_up(unsigned* pairs) {
   static std::mutex mu;
-  static bool done[64] = {};
+  static unsigned known[64] = {};
   int dev = 0;
   int rc = cuda_check(cudaGetDevice(&dev), "moe_expert_ffn: device");
   if (rc) return rc;
   std::lock_guard<std::mutex> lock(mu);
-  if (dev >= 0 && dev < 64 && done[dev]) return SYMM_OK;
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && known[dev]) {
+    *pairs = known[dev];
+    return SYMM_OK;
+  }
   for (const void* f : {(const void*)rows_kernel<FMT, kGated>, (const void*)rows_kernel<FMT, kDown>,
                         (const void*)rows_kernel<FMT, kDh>, (const void*)rows_kernel<FMT, kDx>,
                         (const void*)grad_kernel<FMT>})
@@ -538,43 +576,45 @@ int set_up() {
       rc = cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)kSmemBytes),
                       "moe_expert_ffn: kernel set-up");
-  if (!rc && dev >= 0 && dev < 64) done[dev] = true;
-  return rc;
+  if (rc) return rc;
+  *pairs = resident_pairs((const void*)rows_kernel<FMT, kGated>, kThreads, kSmemBytes);
+  if (keep) known[dev] = *pairs;
+  return SYMM_OK;
 }
 
 // One product of the rows x [n][k] (ldx apart) with the experts' weights, stored
 // [E][wrows][wcols].
 template <int FMT, int KIND>
 int rows_product(const char* what, const void* x, size_t ldx, const void* w, uint32_t wrows,
-                 uint32_t wcols, ExpertArgs a, cudaStream_t s) {
+                 uint32_t wcols, ExpertArgs a, unsigned pairs, cudaStream_t s) {
   constexpr bool kMMajor = KIND == kGated || KIND == kDown;
   CUtensorMap mw, m64, m16;
   int rc = make_map(what, &mw, w, FMT, wcols, wrows, a.E, wcols, kMMajor ? kBK : kBM);
   if (!rc) rc = make_map(what, &m64, x, FMT, a.k, a.n, 0, ldx, 64);
   if (!rc) rc = make_map(what, &m16, x, FMT, a.k, a.n, 0, ldx, 16);
   if (rc) return rc;
-  a.ncol = (a.m + (KIND == kGated ? 63 : 127)) / (KIND == kGated ? 64 : 128);
+  a.npair = (a.m + (KIND == kGated ? 127 : 255)) / (KIND == kGated ? 128 : 256);
   // at most one partly filled block of rows for each expert that has rows
-  const uint64_t most = (uint64_t)a.ncol * std::min<uint64_t>(a.n, a.n / kMaxRows + a.E);
-  const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), most);
-  return moe::launch(what, rows_kernel<FMT, KIND>, grid, kThreads, kSmemBytes, s, mw, m64, m16, a);
+  const uint64_t most = (uint64_t)a.npair * std::min<uint64_t>(a.n, a.n / kMaxRows + a.E);
+  return launch_pairs(what, rows_kernel<FMT, KIND>, (unsigned)std::min<uint64_t>(pairs, most),
+                      kThreads, kSmemBytes, s, mw, m64, m16, a);
 }
 
 // dW [E][m][nf] = a_e^T b_e of the rows a [n][m] and b [n][nf].
 template <int FMT>
 int weight_grad(const char* what, const void* a, size_t lda, const void* b, size_t ldb, void* out,
-                uint32_t m, uint32_t nf, const ExpertArgs& x, cudaStream_t s) {
+                uint32_t m, uint32_t nf, const ExpertArgs& x, unsigned pairs, cudaStream_t s) {
   CUtensorMap ma, mb;
   int rc = make_map(what, &ma, a, FMT, m, x.n, 0, lda, 64);
   if (!rc) rc = make_map(what, &mb, b, FMT, nf, x.n, 0, ldb, 64);
   if (rc) return rc;
   GradArgs g{};
   g.counts = x.counts, g.n = x.n, g.E = x.E, g.m = m, g.nf = nf, g.out = out;
-  g.mb = (m + kBM - 1) / kBM, g.nb = (nf + 255) / 256;
+  g.mb = (m + 255) / 256, g.nb = (nf + 255) / 256;
   g.budget_ns = x.budget_ns, g.ctl = x.ctl;
   const uint64_t tiles = (uint64_t)x.E * g.mb * g.nb;
-  const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), tiles);
-  return moe::launch(what, grad_kernel<FMT>, grid, kThreads, kSmemBytes, s, ma, mb, g);
+  return launch_pairs(what, grad_kernel<FMT>, (unsigned)std::min<uint64_t>(pairs, tiles), kThreads,
+                      kSmemBytes, s, ma, mb, g);
 }
 
 // What both entry points check of their sizes, weights and type.
@@ -603,13 +643,14 @@ bool bad_ld(size_t ld, int width) {
 template <int FMT>
 int forward(const char* what, const void* x, size_t ldx, const void* w_gu, const void* w_d, int D,
             int F, void* gu, void* y, size_t ldy, void* h, ExpertArgs a, cudaStream_t s) {
-  int rc = set_up<FMT>();
+  unsigned pairs = 0;
+  int rc = set_up<FMT>(&pairs);
   if (rc) return rc;
   a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu = gu, a.h = h;
-  rc = rows_product<FMT, kGated>(what, x, ldx, w_gu, D, 2 * F, a, s);
+  rc = rows_product<FMT, kGated>(what, x, ldx, w_gu, D, 2 * F, a, pairs, s);
   if (rc) return rc;
   a.m = (uint32_t)D, a.k = (uint32_t)F, a.out = y, a.ldo = ldy;
-  return rows_product<FMT, kDown>(what, h, F, w_d, F, D, a, s);
+  return rows_product<FMT, kDown>(what, h, F, w_d, F, D, a, pairs, s);
 }
 
 template <int FMT>
@@ -617,17 +658,18 @@ int backward(const char* what, const void* dy, size_t lddy, const void* x, size_
              const void* gu, const void* w_gu, const void* w_d, int D, int F, void* dx,
              size_t lddx, void* dw_gu, void* dw_d, void* h, void* dgu, ExpertArgs a,
              cudaStream_t s) {
-  int rc = set_up<FMT>();
+  unsigned pairs = 0;
+  int rc = set_up<FMT>(&pairs);
   if (!rc && a.n) {
     a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu_in = gu, a.gu = dgu, a.h = h;
-    rc = rows_product<FMT, kDh>(what, dy, lddy, w_d, F, D, a, s);
+    rc = rows_product<FMT, kDh>(what, dy, lddy, w_d, F, D, a, pairs, s);
     if (!rc && dx) {
       a.m = (uint32_t)D, a.k = 2 * (uint32_t)F, a.out = dx, a.ldo = lddx;
-      rc = rows_product<FMT, kDx>(what, dgu, 2 * (size_t)F, w_gu, D, 2 * F, a, s);
+      rc = rows_product<FMT, kDx>(what, dgu, 2 * (size_t)F, w_gu, D, 2 * F, a, pairs, s);
     }
   }
-  if (!rc && dw_d) rc = weight_grad<FMT>(what, h, F, dy, lddy, dw_d, F, D, a, s);
-  if (!rc && dw_gu) rc = weight_grad<FMT>(what, x, ldx, dgu, 2 * (size_t)F, dw_gu, D, 2 * F, a, s);
+  if (!rc && dw_d) rc = weight_grad<FMT>(what, h, F, dy, lddy, dw_d, F, D, a, pairs, s);
+  if (!rc && dw_gu) rc = weight_grad<FMT>(what, x, ldx, dgu, 2 * (size_t)F, dw_gu, D, 2 * F, a, pairs, s);
   return rc;
 }
 

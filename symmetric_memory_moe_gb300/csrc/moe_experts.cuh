@@ -17,12 +17,12 @@ enum { kErrRange = -5 };
 
 // Expert e's rows are off[e] .. off[e + 1] - 1, its blocks of rows are numbered
 // blocks[e] .. blocks[e + 1] - 1 among all experts' (times the column blocks:
-// its tiles).  A block has at most MAX rows.
-template <uint32_t MAX>
+// its tiles).  A block has at most MAX rows, in whole steps of STEP.
+template <uint32_t MAX, uint32_t STEP>
 struct Table {
   uint32_t off[kMaxExperts + 1], blocks[kMaxExperts + 1];
   uint32_t warp_rows[kMaxWarps], warp_blocks[kMaxWarps], warp_most[kMaxWarps];
-  uint32_t most;  // rows of the largest block, in whole steps of 16
+  uint32_t most;  // rows of the largest block, in whole steps
 };
 
 template <uint32_t MAX>
@@ -30,17 +30,17 @@ __device__ __forceinline__ uint32_t blocks_of(uint32_t rows) {
   return (rows + MAX - 1) / MAX;
 }
 // Rows of each of an expert's blocks (the last one may have fewer, never none), as
-// even as whole steps of 16 allow.
-template <uint32_t MAX>
+// even as whole steps allow.
+template <uint32_t MAX, uint32_t STEP>
 __device__ __forceinline__ uint32_t block_rows(uint32_t rows) {
   const uint32_t nb = blocks_of<MAX>(rows);
-  return nb ? ((rows + nb - 1) / nb + 15) / 16 * 16 : 0;
+  return nb ? ((rows + nb - 1) / nb + STEP - 1) / STEP * STEP : 0;
 }
 
 // Fills the table from the counts (NULL: one expert with all n rows), by all
 // threads of the block.  False where a count is negative or they exceed n.
-template <uint32_t MAX>
-__device__ __forceinline__ bool lay_out(Table<MAX>& t, const int32_t* counts, uint32_t E,
+template <uint32_t MAX, uint32_t STEP>
+__device__ __forceinline__ bool lay_out(Table<MAX, STEP>& t, const int32_t* counts, uint32_t E,
                                         uint32_t n) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t per = (E + blockDim.x - 1) / blockDim.x, first = threadIdx.x * per;
@@ -55,7 +55,7 @@ __device__ __forceinline__ bool lay_out(Table<MAX>& t, const int32_t* counts, ui
     }
     sum += (uint32_t)c;
     blocks += blocks_of<MAX>((uint32_t)c);
-    most = max(most, block_rows<MAX>((uint32_t)c));
+    most = max(most, block_rows<MAX, STEP>((uint32_t)c));
   }
   bad |= sum > n;
   uint32_t rows = (uint32_t)min(sum, (uint64_t)n + 1);  // the whole sum stays below 2^33
@@ -89,8 +89,8 @@ __device__ __forceinline__ bool lay_out(Table<MAX>& t, const int32_t* counts, ui
 
 // The expert whose blocks hold number b (below blocks[E]): the last one with
 // blocks[e] <= b.
-template <uint32_t MAX>
-__device__ __forceinline__ uint32_t expert_of(const Table<MAX>& t, uint32_t b, uint32_t E) {
+template <uint32_t MAX, uint32_t STEP>
+__device__ __forceinline__ uint32_t expert_of(const Table<MAX, STEP>& t, uint32_t b, uint32_t E) {
   uint32_t lo = 0, hi = E;  // blocks[lo] <= b < blocks[hi]
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) / 2;
@@ -106,13 +106,13 @@ struct Tile {
 // Tile i of ncol column blocks.  Up to eight blocks of rows share a column
 // block's weights one after another, then the next column block shares theirs:
 // what the SMs work on at a time is about as many rows as columns, which L2 holds.
-template <uint32_t MAX>
-__device__ __forceinline__ Tile tile_at(const Table<MAX>& t, uint32_t i, uint32_t E,
+template <uint32_t MAX, uint32_t STEP>
+__device__ __forceinline__ Tile tile_at(const Table<MAX, STEP>& t, uint32_t i, uint32_t E,
                                         uint32_t ncol) {
   Tile o;
   o.e = expert_of(t, i / ncol, E);
   const uint32_t c = t.off[o.e + 1] - t.off[o.e], nb = blocks_of<MAX>(c);
-  o.bt = block_rows<MAX>(c);
+  o.bt = block_rows<MAX, STEP>(c);
   const uint32_t local = i - t.blocks[o.e] * ncol, group = local / (8 * ncol);
   const uint32_t in = min(8u, nb - 8 * group), r = local - 8 * group * ncol;
   const uint32_t b = 8 * group + r % in;
@@ -143,6 +143,142 @@ __device__ __forceinline__ bool any_of(bool p) {
       : "r"((uint32_t)p)
       : "memory");
   return r != 0;
+}
+
+// ------------------------------------------------------------- CTA pairs --
+// Two CTAs of a cluster share a tile of twice 128 features (cta_group::2): each
+// holds its own 128 features of the M side and half of the N side's rows in its
+// shared memory, and its own features' accumulators in its TMEM; the first one
+// issues the MMAs of both.  An SM then loads and reads half of the N side: alone,
+// 96 bytes a cycle of operands and 94 of copies at N 256 exceed the 128 that its
+// shared memory moves.
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t v;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(v));
+  return v;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// One warp of each CTA of the pair calls these, with the same number of columns.
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   symm::smem_addr(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA issued so far by this thread is done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(symm::smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// The same on this CTA's alone.
+__device__ __forceinline__ void pair_commit_own(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          symm::smem_addr(bar))
+      : "memory");
+}
+// Arrives on `bar` of the pair's first CTA, and waits there (for both CTAs' writes).
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  uint32_t remote;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(symm::smem_addr(bar)));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
+               : "memory");
+}
+__device__ __forceinline__ bool try_wait_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(symm::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+static __device__ __noinline__ bool wait_pair_slow(uint64_t* bar, uint32_t parity,
+                                                   uint64_t budget_ns, const Control* ctl) {
+  const uint64_t t0 = symm::globaltimer_ns(), max_iters = budget_ns / 32 + (1u << 20);
+  for (uint64_t it = 0;; ++it) {
+    if (try_wait_pair(bar, parity)) return true;
+    if ((it & 255) == 255 && (symm::ld_relaxed_u32(&ctl->abort) ||
+                              symm::globaltimer_ns() - t0 > budget_ns || it > max_iters))
+      return false;
+  }
+}
+__device__ __forceinline__ bool wait_pair_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                               const Control* ctl) {
+  return __all_sync(0xffffffffu, try_wait_pair(bar, parity)) ||
+         __all_sync(0xffffffffu, wait_pair_slow(bar, parity, budget_ns, ctl));
+}
+// Before a CTA of a pair may leave: its copies have landed (`full`; whether or not
+// anything used them), and what uses them has released them (`empty`: arrivals
+// from the other CTA, which must find this one's shared memory).  Bounded.
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint64_t* empty, uint32_t stages,
+                                           uint32_t loads, bool ok, uint64_t budget_ns) {
+  const uint32_t first = loads > stages ? loads - stages : 0;
+  for (uint32_t i = first; i < loads; ++i)
+    symm::mbar_wait(&full[i % stages], (i / stages) & 1, drain_ns(budget_ns));
+  for (uint32_t i = first; ok && i < loads; ++i)
+    ok = symm::mbar_wait(&empty[i % stages], (i / stages) & 1, drain_ns(budget_ns));
+}
+// Launches clusters of two CTAs, as moe::launch.
+template <typename... P, typename... A>
+int launch_pairs(const char* what, void (*kernel)(P...), unsigned pairs, unsigned block,
+                 size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return symm_host::cuda_check(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...), what);
+}
+// Pairs of such CTAs that are resident at once (a kernel needs its shared memory allowed
+// before); SMs / 2 where the driver does not say.
+inline unsigned resident_pairs(const void* kernel, unsigned block, size_t smem) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    n = symm_host::sm_count() / 2;
+  }
+  return (unsigned)(n < 1 ? 1 : n);
 }
 
 // act(g) and its derivative: g sigma(g), or g Phi(g) with the normal
