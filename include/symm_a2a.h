@@ -597,17 +597,17 @@ int moe_expert_workspace(int n, int E, int D, int F, int backward, size_t *bytes
  * the unrounded g and u, is rounded to `dtype` once, as the second product's
  * operand.  Rows do not mix: an infinity or NaN stays with its row.
  * 0 <= n <= 2^24, 1 <= E <= SYMM_MOE_MAX_EXPERTS, D and F multiples of 8 in
- * [8, 2^17], ldx a multiple of 8; x and weights 16-byte aligned.  n = 0 is a
- * no-op.
+ * [8, 2^17], ldx and ldy multiples of 8; x, weights, gu and y 16-byte aligned.
+ * n = 0 is a no-op.
  * Errors: SYMM_EINVAL, SYMM_ECUDA; SYMM_ERANGE, SYMM_ETIMEDOUT by
  * symm_check_error(). */
 int moe_expert_ffn(symm_heap_t *heap, const void *x, size_t ldx, const int32_t *counts,
                    const void *w_gu, const void *w_d, int act, int dtype, int n, int E, int D,
                    int F, void *gu, void *y, size_t ldy, void *workspace, void *stream);
 
-/* Gradients of moe_expert_ffn: dy [n] rows of D, lddy apart (a multiple of 8,
- * 16-byte aligned), those of y; x, counts, w_gu, w_d as in the call, gu what it
- * saved.  With dh = dy Wd_e^T, dg = dh * u * act'(g), du = dh * act(g):
+/* Gradients of moe_expert_ffn: dy [n] rows of D, lddy apart, those of y; x,
+ * counts, w_gu, w_d as in the call, gu what it saved; strides multiples of 8, all
+ * tensors 16-byte aligned.  With dh = dy Wd_e^T, dg = dh * u * act'(g), du = dh * act(g):
  *   dx     [n] rows of D, lddx apart: [dg | du] Wgu_e^T (rows behind the last
  *          expert's left as they were);
  *   dw_gu  [E][D][2F]: x_e^T [dg | du]_e, dw_d [E][F][D]: (act(g) * u)_e^T dy_e,

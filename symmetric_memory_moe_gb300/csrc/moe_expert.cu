@@ -22,7 +22,7 @@
 //              swizzled, into a ring of stages; 128 deep when no tile has more
 //              than 64 rows (a slice costs each role some 250 cycles beside its MMAs)
 //   warp 1     MMA issuer: tcgen05.mma kind::f16, two accumulators in TMEM
-//   warps 2-5  epilogue: tcgen05.ld, activation or gradient, rounding, stores (a
+//   warps 2-9  epilogue: tcgen05.ld, activation or gradient, rounding, stores (a
 //              warp's 32 lanes are 32 features of a row)
 // The gated product's tile is 64 columns of Wg over the same 64 of Wu: g and u of
 // an element are then 64 TMEM lanes apart, in two warps, which exchange halves
@@ -42,14 +42,14 @@ using namespace symm_host;
 
 namespace {
 
-constexpr uint32_t kThreads = 192;
+constexpr uint32_t kThreads = 320, kEpilogue = 256;
 constexpr uint32_t kMaxRows = 256, kStep = 32;           // rows of a tile: the N side of a pair
 constexpr uint32_t kBK = 64;
 constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
 constexpr uint32_t kRingBytes = 192 * 1024;              // six stages of 128 features, 128 rows
 constexpr uint32_t kMaxStages = 8;
-constexpr uint32_t kExchange = 2 * 2 * 16 * 64 * 4;      // two chunks, two halves of 16 x 64
-constexpr uint32_t kSmemBytes = 1024 + kRingBytes + kExchange;
+constexpr uint32_t kStageWarp = 32 * kLine;              // where a warp of the epilogue stages rows
+constexpr uint32_t kSmemBytes = 1024 + kRingBytes + 8 * kStageWarp;
 constexpr uint32_t kAccCols = 256;
 
 enum Kind { kGated, kDown, kDh, kDx };
@@ -114,7 +114,7 @@ __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
     }
     for (int i = 0; i < 2; ++i) {
       symm::mbar_init(&b.tfull[i], 1);
-      symm::mbar_init(&b.tempty[i], 256);  // both CTAs' epilogues
+      symm::mbar_init(&b.tempty[i], 2 * kEpilogue);  // both CTAs'
     }
     symm::mbar_init(&b.drain, 1);
     symm::fence_mbar_init();
@@ -137,59 +137,51 @@ __device__ __forceinline__ void leave_cta(Barriers& b, int warp) {
 }
 
 // ------------------------------------------------------------- epilogues --
-// 16 rows from `row` on, `valid` of them there, feature f of each.
+// Fragments of 16 rows (columns of TMEM) and this warp's 32 features, as
+// tmem_frags leaves them, packed in pairs of neighbouring rows.
 template <int FMT>
-__device__ __forceinline__ void store16(const ExpertArgs& a, const uint32_t (&v)[16], uint32_t row,
-                                        uint32_t valid, uint32_t f) {
-  using T = typename Elem<FMT>::T;
-  if (f >= a.m) return;
-  T* y = static_cast<T*>(a.out) + (size_t)row * a.ldo + f;
+__device__ __forceinline__ void pack_frags(const uint32_t (&v)[2][8], uint32_t (&p)[2][4]) {
 #pragma unroll
-  for (uint32_t j = 0; j < 16; ++j)
-    if (j < valid) y[j * a.ldo] = moe::from_f<T>(__uint_as_float(v[j]));
+  for (uint32_t t = 0; t < 2; ++t)
+#pragma unroll
+    for (uint32_t o = 0; o < 4; ++o)
+      p[t][o] = symm::pack2<FMT>(__uint_as_float(v[o / 2][4 * t + 2 * (o % 2)]),
+                                 __uint_as_float(v[o / 2][4 * t + 2 * (o % 2) + 1]));
 }
+// 16 rows of 32 features through `stage` to global memory.
 template <int FMT>
-__device__ __forceinline__ void grad16(const ExpertArgs& a, const uint32_t (&v)[16], uint32_t row,
-                                       uint32_t valid, uint32_t f) {
+__device__ __forceinline__ void put_rows(uint8_t* stage, const uint32_t (&p)[2][4], void* to,
+                                         size_t ld, uint32_t row, uint32_t f, uint32_t valid,
+                                         uint32_t width) {
   using T = typename Elem<FMT>::T;
-  if (f >= a.m) return;
-  const T* gu = static_cast<const T*>(a.gu_in) + (size_t)row * 2 * a.F + f;
-  T* dgu = static_cast<T*>(a.gu) + (size_t)row * 2 * a.F + f;
-  T* h = static_cast<T*>(a.h) + (size_t)row * a.F + f;
-  T g[16], u[16];
-#pragma unroll
-  for (uint32_t j = 0; j < 16; ++j)
-    if (j < valid) g[j] = gu[(size_t)j * 2 * a.F], u[j] = gu[(size_t)j * 2 * a.F + a.F];
-#pragma unroll
-  for (uint32_t j = 0; j < 16; ++j)
-    if (j < valid) {
-      float act, slope;
-      activate_both(a.act, moe::to_f(g[j]), act, slope);
-      const float dh = __uint_as_float(v[j]), up = moe::to_f(u[j]);
-      dgu[(size_t)j * 2 * a.F] = moe::from_f<T>(dh * up * slope);
-      dgu[(size_t)j * 2 * a.F + a.F] = moe::from_f<T>(dh * act);
-      h[(size_t)j * a.F] = moe::from_f<T>(act * up);
-    }
+  stage_rows(stage, p);
+  __syncwarp();
+  store_rows(stage, static_cast<T*>(to) + (size_t)row * ld + f, ld, valid, width, true);
+  __syncwarp();
 }
-// Rows of the gated product: g and u of feature f, 16 rows from `row` on.
+// Two packed values of 16 bits.
 template <int FMT>
-__device__ __forceinline__ void gated16(const ExpertArgs& a, const float (&g)[16],
-                                        const float (&u)[16], uint32_t row, uint32_t valid,
-                                        uint32_t f) {
-  using T = typename Elem<FMT>::T;
-  if (f >= a.m) return;
-  T* h = static_cast<T*>(a.h) + (size_t)row * a.F + f;
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if (FMT == 1) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// What a lane stages of 16 rows: two vectors of 8 features; zeros where there are none.
+__device__ __forceinline__ void fetch_rows(uint4 (&v)[2], const void* from, size_t ld, uint32_t row,
+                                           uint32_t f, uint32_t valid, uint32_t width) {
+  const uint32_t lane = threadIdx.x & 31, c = 8 * (lane & 3);
 #pragma unroll
-  for (uint32_t j = 0; j < 16; ++j)
-    if (j < valid) h[(size_t)j * a.F] = moe::from_f<T>(activate(a.act, g[j]) * u[j]);
-  if (!a.gu) return;
-  T* gu = static_cast<T*>(a.gu) + (size_t)row * 2 * a.F + f;
+  for (uint32_t i = 0; i < 2; ++i) {
+    const uint32_t r = 8 * i + lane / 4;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < valid && c < width)
+      v[i] = symm::ld16_ro(static_cast<const uint16_t*>(from) + (size_t)(row + r) * ld + f + c);
+  }
+}
+__device__ __forceinline__ void drop_rows(uint8_t* stage, const uint4 (&v)[2]) {
+  const uint32_t lane = threadIdx.x & 31;
 #pragma unroll
-  for (uint32_t j = 0; j < 16; ++j)
-    if (j < valid) {
-      gu[(size_t)j * 2 * a.F] = moe::from_f<T>(g[j]);
-      gu[(size_t)j * 2 * a.F + a.F] = moe::from_f<T>(u[j]);
-    }
+  for (uint32_t i = 0; i < 2; ++i)
+    *reinterpret_cast<uint4*>(stage + (8 * i + lane / 4) * kLine + (lane & 3) * 16) = v[i];
 }
 
 // ------------------------------------------------------------ rows_kernel --
@@ -273,13 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t xbytes = copied_rows(t.bt / 2) * 128, buf = seg & 1;
       const uint32_t idesc = mma_idesc(FMT, t.bt, kMMajor, false);
-      if (!(ok = wait_pair_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
       for (uint32_t s = 0; s < slices; ++s) {
         ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl) &&
-             wait_pair_warp(&bar.ready[st], ph, a.budget_ns, a.ctl);
+             symm::mbar_wait_warp(&bar.ready[st], ph, a.budget_ns, a.ctl);
         if (!ok) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * ring.stage_bytes;
@@ -304,14 +296,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elected) pair_commit_own(&bar.drain);  // every MMA is complete before TMEM is freed
     symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
   } else {  // -------------------------------------------------- epilogue
-    const uint32_t q = (uint32_t)(warp & 3);  // TMEM lanes 32q .. 32q + 31
-    float* exchange = reinterpret_cast<float*>(smem + kRingBytes);
-    uint32_t seg = 0, chunk = 0;
+    // Two warps to each 32 TMEM lanes, which take turns at the chunks of rows.
+    const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
+    uint8_t* mine = smem + kRingBytes + (warp - 2) * kStageWarp;
+    uint32_t seg = 0;
     for (uint32_t i = first; i < tiles; i += step, ++seg) {
       const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t buf = seg & 1;
+      const uint32_t f = KIND == kGated ? (2 * t.col + rank) * 64 + 32 * (q & 1)
+                                        : (2 * t.col + rank) * kBM + 32 * q;
+      const uint32_t width = f < a.m ? a.m - f : 0;  // features from f on that are there
+      uint4 g[2], u[2];                              // kDh: of the next chunk
+      if (KIND == kDh && 16 * turn < t.rows) {
+        const uint32_t r = 16 * turn;
+        fetch_rows(g, a.gu_in, 2 * a.F, t.row + r, f, t.rows - r, width);
+        fetch_rows(u, a.gu_in, 2 * a.F, t.row + r, a.F + f, t.rows - r, width);
+      }
       const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
-      if (any_of(!ok)) {  // all threads leave, or none
+      if (any_of(!ok, kEpilogue)) {  // all threads leave, or none
         if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
       }
@@ -319,44 +321,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
       if (KIND == kGated) {
         // Chunks of 32 rows: the warps of g finish the first 16, those of u the others.
-        const uint32_t f = (2 * t.col + rank) * 64 + 32 * (q & 1) + lane, mine = q >> 1;
-        for (uint32_t c = 0; c < t.rows; c += 32, ++chunk) {
-          uint32_t v[32];
-          symm::tmem_ld32(taddr + c, v);
-          if (c + 32 >= t.rows) {  // the accumulator is free for the next tile
-            symm::tc_fence_before();
-            arrive_first(&bar.tempty[buf]);
-          }
-          // half 0: g of the last 16 rows, half 1: u of the first 16
-          float* there = exchange + (chunk & 1) * (2 * 16 * 64) + 32 * (q & 1) + lane;
-          float own[16], other[16];
+        const uint32_t up = q >> 1;
+        uint8_t* theirs = smem + kRingBytes + ((warp - 2) ^ 2) * kStageWarp;
+        for (uint32_t c = 32 * turn; c < t.rows; c += 64) {
+          uint32_t own[2][8], other[2][8];
+          tmem_frags(taddr + c + 16 * (up ^ 1), other);
+          tmem_frags(taddr + c + 16 * up, own);
+          // the same lane of the other warp has the same elements' other half
 #pragma unroll
-          for (uint32_t j = 0; j < 16; ++j) {
-            there[mine * (16 * 64) + j * 64] = __uint_as_float(mine ? v[j] : v[16 + j]);
-            own[j] = __uint_as_float(mine ? v[16 + j] : v[j]);
-          }
-          symm::group_sync(2 + (int)(q & 1), 64);  // this pair of warps
+          for (uint32_t j = 0; j < 4; ++j)
+            reinterpret_cast<uint4*>(theirs)[32 * j + lane] =
+                make_uint4(other[j / 2][4 * (j % 2)], other[j / 2][4 * (j % 2) + 1],
+                           other[j / 2][4 * (j % 2) + 2], other[j / 2][4 * (j % 2) + 3]);
+          symm::group_sync(2 + (int)(2 * turn + (q & 1)), 64);  // this pair of warps
 #pragma unroll
-          for (uint32_t j = 0; j < 16; ++j) other[j] = there[(mine ^ 1) * (16 * 64) + j * 64];
-          const uint32_t r = c + 16 * mine;
+          for (uint32_t j = 0; j < 4; ++j) {
+            const uint4 v = reinterpret_cast<const uint4*>(mine)[32 * j + lane];
+            other[j / 2][4 * (j % 2)] = v.x, other[j / 2][4 * (j % 2) + 1] = v.y;
+            other[j / 2][4 * (j % 2) + 2] = v.z, other[j / 2][4 * (j % 2) + 3] = v.w;
+          }
+          __syncwarp();  // before what is read is staged over
+          const uint32_t r = c + 16 * up;
           if (r < t.rows) {
-            if (mine) gated16<FMT>(a, other, own, t.row + r, t.rows - r, f);
-            else gated16<FMT>(a, own, other, t.row + r, t.rows - r, f);
+            uint32_t p[2][4], h[2][8];
+#pragma unroll
+            for (uint32_t x = 0; x < 2; ++x)
+#pragma unroll
+              for (uint32_t j = 0; j < 8; ++j) {
+                const float gate = __uint_as_float(up ? other[x][j] : own[x][j]);
+                const float value = __uint_as_float(up ? own[x][j] : other[x][j]);
+                h[x][j] = __float_as_uint(activate(a.act, gate) * value);
+              }
+            pack_frags<FMT>(h, p);
+            put_rows<FMT>(mine, p, a.h, a.F, t.row + r, f, t.rows - r, width);
+            if (a.gu) {
+              pack_frags<FMT>(own, p);
+              put_rows<FMT>(mine, p, a.gu, 2 * a.F, t.row + r, f + (up ? a.F : 0), t.rows - r,
+                            width);
+              pack_frags<FMT>(other, p);
+              put_rows<FMT>(mine, p, a.gu, 2 * a.F, t.row + r, f + (up ? 0 : a.F), t.rows - r,
+                            width);
+            }
           }
+          symm::group_sync(2 + (int)(2 * turn + (q & 1)), 64);
         }
       } else {
-        const uint32_t f = (2 * t.col + rank) * kBM + 32 * q + lane;
-        for (uint32_t c = 0; c < t.rows; c += 16) {
-          uint32_t v[16];
-          symm::tmem_ld16(taddr + c, v);
-          if (c + 16 >= t.rows) {
-            symm::tc_fence_before();
-            arrive_first(&bar.tempty[buf]);
+        for (uint32_t c = 16 * turn; c < t.rows; c += 32) {
+          uint32_t v[2][8], p[2][4];
+          const uint32_t row = t.row + c, valid = t.rows - c;
+          if (KIND == kDh) {
+            uint8_t* mine2 = mine + 16 * kLine;
+            drop_rows(mine, g), drop_rows(mine2, u);
+            __syncwarp();
+            if (c + 32 < t.rows) {
+              fetch_rows(g, a.gu_in, 2 * a.F, row + 32, f, valid - 32, width);
+              fetch_rows(u, a.gu_in, 2 * a.F, row + 32, a.F + f, valid - 32, width);
+            }
+            uint32_t pg[2][4], pu[2][4];
+            unstage_rows(mine, pg);
+            unstage_rows(mine2, pu);
+            tmem_frags(taddr + c, v);
+            uint32_t dg[2][4], du[2][4];
+#pragma unroll
+            for (uint32_t x = 0; x < 2; ++x)
+#pragma unroll
+              for (uint32_t o = 0; o < 4; ++o) {
+                const float2 gate = unpack2<FMT>(pg[x][o]), value = unpack2<FMT>(pu[x][o]);
+                const float d0 = __uint_as_float(v[o / 2][4 * x + 2 * (o % 2)]);
+                const float d1 = __uint_as_float(v[o / 2][4 * x + 2 * (o % 2) + 1]);
+                float a0, a1, s0, s1;
+                activate_both(a.act, gate.x, a0, s0);
+                activate_both(a.act, gate.y, a1, s1);
+                p[x][o] = symm::pack2<FMT>(a0 * value.x, a1 * value.y);
+                dg[x][o] = symm::pack2<FMT>(d0 * value.x * s0, d1 * value.y * s1);
+                du[x][o] = symm::pack2<FMT>(d0 * a0, d1 * a1);
+              }
+            __syncwarp();
+            stage_rows(mine2, du);
+            put_rows<FMT>(mine, dg, a.gu, 2 * a.F, row, f, valid, width);
+            store_rows(mine2, static_cast<typename Elem<FMT>::T*>(a.gu) +
+                                  (size_t)row * 2 * a.F + a.F + f,
+                       2 * (size_t)a.F, valid, width, true);
+            put_rows<FMT>(mine, p, a.h, a.F, row, f, valid, width);
+          } else {
+            tmem_frags(taddr + c, v);
+            pack_frags<FMT>(v, p);
+            put_rows<FMT>(mine, p, a.out, a.ldo, row, f, valid, width);
           }
-          if (KIND == kDh) grad16<FMT>(a, v, t.row + c, t.rows - c, f);
-          else store16<FMT>(a, v, t.row + c, t.rows - c, f);
         }
       }
+      symm::tc_fence_before();
+      arrive_first(&bar.tempty[buf]);  // the accumulator is free for the next tile
     }
   }
   leave_cta(bar, warp);
@@ -431,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (r0 == r1) continue;  // the epilogue writes zeros
       const uint32_t buf = seg & 1;
       if (!rank &&
-          !(ok = wait_pair_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+          !(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
@@ -452,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank) {
           if (elected) arrive_first(&bar.ready[st]);
         } else {
-          if (!(ok = wait_pair_warp(&bar.ready[st], ph, a.budget_ns, a.ctl))) break;
+          if (!(ok = symm::mbar_wait_warp(&bar.ready[st], ph, a.budget_ns, a.ctl))) break;
           symm::tc_fence_after();
           const uint64_t ad = symm::sw128_mnmajor_desc(at);
           const uint64_t bd = symm::sw128_mnmajor_desc(at + 16384);
@@ -473,15 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
     }
   } else {  // -------------------------------------------------- epilogue
-    const uint32_t q = (uint32_t)(warp & 3);
+    const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
+    uint8_t* mine = smem + kRingBytes + (warp - 2) * kStageWarp;
     uint32_t seg = 0;
     for (uint32_t i = first; i < tiles; i += step) {
-      const uint32_t e = i / per, n0 = i % a.nb * 256;
-      const uint32_t m = i % per / a.nb * 256 + rank * kBM + 32 * q + lane, buf = seg & 1;
+      const uint32_t e = i / per, n0 = i % a.nb * 256, buf = seg & 1;
+      const uint32_t m0 = i % per / a.nb * 256 + rank * kBM + 32 * q;
       const bool any = table.off[e] != table.off[e + 1];
       if (any) {
         const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
-        if (any_of(!ok)) {  // all threads leave, or none
+        if (any_of(!ok, kEpilogue)) {  // all threads leave, or none
           if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
           break;
         }
@@ -489,31 +545,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
       }
       const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
-      T* out = static_cast<T*>(a.out) + ((size_t)e * a.m + m) * a.nf + n0;
-      const uint32_t cols = min(256u, a.nf - n0);  // a multiple of 8
-      for (uint32_t c = 0; c < 256; c += 32) {
-        uint32_t v[32];
+      const uint32_t valid = m0 < a.m ? a.m - m0 : 0, cols = min(256u, a.nf - n0);
+      T* out = static_cast<T*>(a.out) + ((size_t)e * a.m + m0) * a.nf + n0;
+      for (uint32_t c = 32 * turn; c < cols; c += 64) {
+        // matrices of 8 lanes (rows of the gradient) x 8 columns, as they are: 16
+        // bytes of a line each
+        const uint32_t at = symm::smem_addr(mine) + (lane & 7) * kLine + (lane >> 3) * 16;
+        uint32_t v[2][8], w[2][8];
         if (any) {
-          symm::tmem_ld32(taddr + c, v);
-          if (c == 224) {
-            symm::tc_fence_before();
-            arrive_first(&bar.tempty[buf]);
-          }
+          tmem_frags(taddr + c, v);
+          tmem_frags(taddr + c + 16, w);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0;
+          for (int j = 0; j < 8; ++j) v[0][j] = v[1][j] = w[0][j] = w[1][j] = 0;
         }
-        if (m >= a.m) continue;
 #pragma unroll
-        for (uint32_t j = 0; j < 32; j += 8)
-          if (c + j < cols) {
-            uint4 p;
-            uint32_t* w = &p.x;
-#pragma unroll
-            for (int l = 0; l < 4; ++l)
-              w[l] = symm::pack2<FMT>(__uint_as_float(v[j + 2 * l]), __uint_as_float(v[j + 2 * l + 1]));
-            *reinterpret_cast<uint4*>(out + c + j) = p;
-          }
+        for (uint32_t o = 0; o < 4; ++o) {  // lanes 8 o .., four times 8 columns
+          const uint32_t h = o / 2, k = 2 * (o % 2);
+          auto two = [&](const uint32_t (&x)[2][8], uint32_t t) {
+            return symm::pack2<FMT>(__uint_as_float(x[h][4 * t + k]),
+                                    __uint_as_float(x[h][4 * t + k + 1]));
+          };
+          stmatrix(at + 8 * o * kLine, two(v, 0), two(v, 1), two(w, 0), two(w, 1));
+        }
+        __syncwarp();
+        store_rows(mine, out + c, a.nf, valid, cols - c, true);
+        if (valid > 16)
+          store_rows(mine + 16 * kLine, out + (size_t)16 * a.nf + c, a.nf, valid - 16, cols - c,
+                     true);
+        __syncwarp();
+      }
+      if (any) {
+        symm::tc_fence_before();
+        arrive_first(&bar.tempty[buf]);
       }
     }
   }
@@ -693,14 +757,14 @@ extern "C" int moe_expert_ffn(symm_heap_t* heap, const void* x, size_t ldx, cons
     const char* what = "moe_expert_ffn";
     int rc = check_common(what, heap, counts, w_gu, w_d, act, dtype, n, E, D, F);
     if (rc) return rc;
-    if (bad_ld(ldx, D) || ldy < (size_t)D || ldy > (1ull << 36))
-      return fail(SYMM_EINVAL, "moe_expert_ffn: ldx >= D (a multiple of 8), ldy >= D");
+    if (bad_ld(ldx, D) || bad_ld(ldy, D))
+      return fail(SYMM_EINVAL, "moe_expert_ffn: ldx, ldy >= D (multiples of 8)");
     if (n == 0) return SYMM_OK;
     if (!x || !y || !workspace) return fail(SYMM_EINVAL, "moe_expert_ffn: NULL x, y or workspace");
-    if (!moe::aligned(x, 16) || !moe::aligned(y, 2) || !moe::aligned(gu, 2) ||
+    if (!moe::aligned(x, 16) || !moe::aligned(y, 16) || !moe::aligned(gu, 16) ||
         !moe::aligned(workspace, 256))
-      return fail(SYMM_EINVAL, "moe_expert_ffn: x must be 16-byte aligned, workspace 256-byte, "
-                               "y and gu to their elements");
+      return fail(SYMM_EINVAL, "moe_expert_ffn: x, y and gu must be 16-byte aligned, workspace "
+                               "256-byte");
     if (y == x || y == w_gu || y == w_d || y == gu || (gu && (gu == x || gu == w_gu || gu == w_d)))
       return fail(SYMM_EINVAL, "moe_expert_ffn: outputs must not be inputs or each other");
     cudaStream_t s = as_stream(stream);
@@ -725,16 +789,15 @@ extern "C" int moe_expert_ffn_backward(symm_heap_t* heap, const void* dy, size_t
     const char* what = "moe_expert_ffn_backward";
     int rc = check_common(what, heap, counts, w_gu, w_d, act, dtype, n, E, D, F);
     if (rc) return rc;
-    if (bad_ld(lddy, D) || bad_ld(ldx, D) || (dx && (lddx < (size_t)D || lddx > (1ull << 36))))
-      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: lddy, ldx >= D (multiples of 8), "
-                               "lddx >= D");
+    if (bad_ld(lddy, D) || bad_ld(ldx, D) || (dx && bad_ld(lddx, D)))
+      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: lddy, ldx, lddx >= D (multiples of 8)");
     if (n && (!dy || !x || !gu || !workspace))
       return fail(SYMM_EINVAL, "moe_expert_ffn_backward: NULL dy, x, gu or workspace");
-    if (!moe::aligned(dy, 16) || !moe::aligned(x, 16) || !moe::aligned(gu, 2) ||
-        !moe::aligned(dx, 2) || !moe::aligned(dw_gu, 16) || !moe::aligned(dw_d, 16) ||
+    if (!moe::aligned(dy, 16) || !moe::aligned(x, 16) || !moe::aligned(gu, 16) ||
+        !moe::aligned(dx, 16) || !moe::aligned(dw_gu, 16) || !moe::aligned(dw_d, 16) ||
         !moe::aligned(workspace, 256))
-      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: dy, x, dw_gu and dw_d must be 16-byte "
-                               "aligned, workspace 256-byte, gu and dx to their elements");
+      return fail(SYMM_EINVAL, "moe_expert_ffn_backward: the tensors must be 16-byte aligned, "
+                               "workspace 256-byte");
     const void* in[] = {dy, x, gu, w_gu, w_d};
     const void* out[] = {dx, dw_gu, dw_d};
     for (int i = 0; i < 3; ++i)

@@ -133,16 +133,109 @@ __device__ __forceinline__ uint64_t drain_ns(uint64_t budget_ns) {
   return max(budget_ns, (uint64_t)1000000000);
 }
 
-// Whether p holds in any of the 128 threads of the epilogue (a barrier of theirs).
-__device__ __forceinline__ bool any_of(bool p) {
+// Whether p holds in any thread of the epilogue (a barrier of its `threads`).
+__device__ __forceinline__ bool any_of(bool p, uint32_t threads) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p)
+      : "r"((uint32_t)p), "r"(threads)
       : "memory");
   return r != 0;
+}
+
+// --------------------------------------------------------- the epilogue --
+// A warp reads its 32 TMEM lanes (features) in fragments of 8 lanes x 8 columns, in
+// which a thread has two neighbouring columns of lane T / 4.  stmatrix and ldmatrix
+// move such fragments to and from shared memory, with .trans as rows of
+// features: what global memory holds, 64 bytes of a row for a warp.  (A lane for
+// a feature and 2-byte stores took 25 thousand cycles a 128 x 256 tile; the
+// gradients' reads beside them 90 thousand.)
+constexpr uint32_t kLine = 80;  // bytes of 32 staged 16-bit values: 8 lines meet all banks
+
+// 16 TMEM lanes x 16 columns: v[4 t + 2 o + i] is lane 8 o + T / 4, column
+// 8 t + 2 (T % 4) + i.
+__device__ __forceinline__ void tmem_frag16(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for them; names the registers, so that no use comes before.
+__device__ __forceinline__ void tmem_wait(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                 "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
+}
+// The warp's 32 lanes x 16 columns: v[h] lanes 16 h ..
+__device__ __forceinline__ void tmem_frags(uint32_t taddr, uint32_t (&v)[2][8]) {
+  tmem_frag16(taddr, v[0]);
+  tmem_frag16(taddr + (16u << 16), v[1]);
+  tmem_wait(v[0], v[1]);
+}
+// Four 8 x 8 matrices: the lines of 16 bytes of matrix m at the addresses of lanes 8 m ..
+__device__ __forceinline__ void stmatrix_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                           uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                         uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c,
+                                           uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+// Packed fragments p[t][o] (columns 8 t .., lanes 8 o ..) of 16 columns to 16 lines of
+// `stage`, and back.
+__device__ __forceinline__ void stage_rows(uint8_t* stage, const uint32_t (&p)[2][4]) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t at = symm::smem_addr(stage) + (lane & 7) * kLine + (lane >> 3) * 16;
+#pragma unroll
+  for (uint32_t t = 0; t < 2; ++t)
+    stmatrix_t(at + 8 * t * kLine, p[t][0], p[t][1], p[t][2], p[t][3]);
+}
+__device__ __forceinline__ void unstage_rows(const uint8_t* stage, uint32_t (&p)[2][4]) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint32_t at = symm::smem_addr(stage) + (lane & 7) * kLine + (lane >> 3) * 16;
+#pragma unroll
+  for (uint32_t t = 0; t < 2; ++t)
+    ldmatrix_t(at + 8 * t * kLine, p[t][0], p[t][1], p[t][2], p[t][3]);
+}
+// 16 staged lines to the rows at y (first row, first feature), `valid` rows and
+// `width` features of 32 there; 16 bytes at a time where `vec` (rows 16-byte aligned).
+template <typename T>
+__device__ __forceinline__ void store_rows(const uint8_t* stage, T* y, size_t ld, uint32_t valid,
+                                           uint32_t width, bool vec) {
+  const uint32_t lane = threadIdx.x & 31, f = 8 * (lane & 3);
+#pragma unroll
+  for (uint32_t i = 0; i < 2; ++i) {
+    const uint32_t r = 8 * i + lane / 4;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kLine + (lane & 3) * 16);
+    if (r >= valid || f >= width) continue;
+    T* to = y + r * ld + f;
+    if (vec && f + 8 <= width) {
+      *reinterpret_cast<uint4*>(to) = v;
+    } else {
+      const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+      for (uint32_t j = 0; j < 8; ++j)
+        if (f + j < width) to[j] = e[j];
+    }
+  }
 }
 
 // ------------------------------------------------------------- CTA pairs --
@@ -197,38 +290,13 @@ __device__ __forceinline__ void pair_commit_own(uint64_t* bar) {
           symm::smem_addr(bar))
       : "memory");
 }
-// Arrives on `bar` of the pair's first CTA, and waits there (for both CTAs' writes).
+// Arrives on `bar` of the pair's first CTA.  What it tells of are copies and
+// tcgen05.ld that are complete and writes behind a proxy fence: no release of
+// cluster scope, which waits for all of the SM's stores (2000 cycles a slice).
 __device__ __forceinline__ void arrive_first(uint64_t* bar) {
   uint32_t remote;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(symm::smem_addr(bar)));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote)
-               : "memory");
-}
-__device__ __forceinline__ bool try_wait_pair(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(symm::smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-static __device__ __noinline__ bool wait_pair_slow(uint64_t* bar, uint32_t parity,
-                                                   uint64_t budget_ns, const Control* ctl) {
-  const uint64_t t0 = symm::globaltimer_ns(), max_iters = budget_ns / 32 + (1u << 20);
-  for (uint64_t it = 0;; ++it) {
-    if (try_wait_pair(bar, parity)) return true;
-    if ((it & 255) == 255 && (symm::ld_relaxed_u32(&ctl->abort) ||
-                              symm::globaltimer_ns() - t0 > budget_ns || it > max_iters))
-      return false;
-  }
-}
-__device__ __forceinline__ bool wait_pair_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
-                                               const Control* ctl) {
-  return __all_sync(0xffffffffu, try_wait_pair(bar, parity)) ||
-         __all_sync(0xffffffffu, wait_pair_slow(bar, parity, budget_ns, ctl));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 // Before a CTA of a pair may leave: its copies have landed (`full`; whether or not
 // anything used them), and what uses them has released them (`empty`: arrivals

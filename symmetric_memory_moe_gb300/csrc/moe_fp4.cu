@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t buf = seg & 1;
       const float scale = a.gw ? gx * a.gw[t.e] : gx;
       const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
-      if (any_of(!ok)) {  // all threads leave, or none
+      if (any_of(!ok, 128)) {  // all threads leave, or none
         if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
       }

@@ -33,10 +33,10 @@ FFN = dict(x=P, ldx=64, counts=P, w_gu=2 * P, w_d=3 * P, act=0, dtype=BF16, n=4,
     dict(heap=None), dict(act=2), dict(act=-1), dict(dtype=2), dict(dtype=-1), dict(n=-1),
     dict(n=(1 << 24) + 1), dict(E=0), dict(E=1025), dict(D=0), dict(D=60), dict(D=4),
     dict(D=(1 << 17) + 8, ldx=1 << 18, ldy=1 << 18), dict(F=0), dict(F=12), dict(F=(1 << 17) + 8),
-    dict(ldx=56), dict(ldx=68), dict(ldx=1 << 37), dict(ldy=63), dict(ldy=1 << 37),
+    dict(ldx=56), dict(ldx=68), dict(ldx=1 << 37), dict(ldy=63), dict(ldy=68), dict(ldy=1 << 37),
     dict(counts=None), dict(x=None), dict(w_gu=None), dict(w_d=None), dict(y=None),
     dict(workspace=None), dict(x=P + 2), dict(w_gu=P + 8), dict(w_d=P + 8), dict(counts=P + 2),
-    dict(gu=P + 1), dict(y=P + 1), dict(workspace=P + 128), dict(y=P), dict(y=2 * P),
+    dict(gu=P + 8), dict(y=P + 8), dict(workspace=P + 128), dict(y=P), dict(y=2 * P),
     dict(y=3 * P), dict(y=4 * P), dict(gu=P), dict(gu=2 * P), dict(gu=3 * P)])
 def test_forward_refuses(heap, bad):
     assert code(abi.moe_expert_ffn, **dict(FFN, **dict(dict(heap=heap), **bad))) == E
@@ -54,9 +54,9 @@ BACK = dict(dy=P, lddy=64, x=2 * P, ldx=64, gu=3 * P, counts=P, w_gu=4 * P, w_d=
 @pytest.mark.parametrize("bad", [
     dict(heap=None), dict(act=2), dict(dtype=2), dict(n=-1), dict(n=(1 << 24) + 1), dict(E=0),
     dict(E=1025), dict(D=60), dict(F=12), dict(lddy=56), dict(lddy=68), dict(ldx=56), dict(ldx=68),
-    dict(lddx=63), dict(lddx=1 << 37), dict(counts=None), dict(dy=None), dict(x=None),
+    dict(lddx=63), dict(lddx=68), dict(lddx=1 << 37), dict(counts=None), dict(dy=None), dict(x=None),
     dict(gu=None), dict(w_gu=None), dict(w_d=None), dict(workspace=None), dict(dy=P + 2),
-    dict(x=P + 2), dict(gu=P + 1), dict(dx=P + 1), dict(dw_gu=P + 2), dict(dw_d=P + 2),
+    dict(x=P + 2), dict(gu=P + 8), dict(dx=P + 8), dict(dw_gu=P + 2), dict(dw_d=P + 2),
     dict(workspace=P + 16), dict(dx=P), dict(dx=2 * P), dict(dx=3 * P), dict(dw_gu=4 * P),
     dict(dw_d=5 * P), dict(dw_gu=6 * P), dict(dw_d=6 * P), dict(dw_d=7 * P)])
 def test_backward_refuses(heap, bad):
