@@ -494,13 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* at = smem + st * kGradStage;
         const uint32_t left = min(64u, r1 - r), steps = (left + 15) / 16;
-        if (left % 16) {  // the next expert's rows in the last step
-          const uint32_t zero = steps * 16 - left;
-          for (uint32_t c = lane; c < 4 * 8 * zero; c += 32) {
-            const uint32_t box = c / (8 * zero), w = c % (8 * zero);
-            *reinterpret_cast<uint4*>(at + box * 8192 + left * 128 + w * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
+        if (left % 16) {  // the next expert's rows in the last step: a line of all four boxes a turn
+          uint8_t* line = at + (lane / 8) * 8192 + (lane % 8) * 16;
+          for (uint32_t z = left; z < steps * 16; ++z)
+            *reinterpret_cast<uint4*>(line + z * 128) = make_uint4(0, 0, 0, 0);
           symm::fence_proxy_async_shared();
           __syncwarp();
         }
@@ -512,8 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t ad = symm::sw128_mnmajor_desc(at);
           const uint64_t bd = symm::sw128_mnmajor_desc(at + 16384);
           if (elected) {
-            for (uint32_t j = 0; j < steps; ++j)
-              pair_mma(acc, ad + kMajorStep * j, bd + kMajorStep * j, idesc, r != r0 || j != 0);
+#pragma unroll
+            for (uint32_t j = 0; j < 4; ++j)
+              if (j < steps)
+                pair_mma(acc, ad + kMajorStep * j, bd + kMajorStep * j, idesc, r != r0 || j != 0);
             pair_commit(&bar.empty[st]);
           }
         }
