@@ -49,7 +49,9 @@ constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
 constexpr uint32_t kRingBytes = 192 * 1024;              // six stages of 128 features, 128 rows
 constexpr uint32_t kMaxStages = 8;
 constexpr uint32_t kStageWarp = 32 * kLine;              // where a warp of the epilogue stages rows
+constexpr uint32_t kGradBox = 16 * 128;                  // where it stages 16 rows of a gradient
 constexpr uint32_t kSmemBytes = 1024 + kRingBytes + 8 * kStageWarp;
+static_assert(kGradBox <= kStageWarp, "both stagings in one size");
 constexpr uint32_t kAccCols = 256;
 
 enum Kind { kGated, kDown, kDh, kDx };
@@ -418,11 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ grad_kernel --
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {  // shared memory may be written again
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 struct GradArgs {
   const int32_t* counts;
   uint32_t n, E, m, nf;  // out [E][m][nf]
   uint32_t mb, nb;       // blocks of 256
-  void* out;
   uint64_t budget_ns;
   Control* ctl;
 };
@@ -432,8 +443,8 @@ constexpr uint32_t kGradStages = kRingBytes / kGradStage;
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     grad_kernel(const __grid_constant__ CUtensorMap map_a,
-                const __grid_constant__ CUtensorMap map_b, const GradArgs a) {
-  using T = typename Elem<FMT>::T;
+                const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_out, const GradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
@@ -528,11 +539,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {  // -------------------------------------------------- epilogue
     const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
-    uint8_t* mine = smem + kRingBytes + (warp - 2) * kStageWarp;
+    // 16 rows of the gradient and 64 columns go out by one copy: whole lines of 128
+    // bytes, swizzled.  Gradients of 16 experts of 2048 x 2816, 32 rows each: 56 us;
+    // stores from registers, 64 or 128 bytes a row, 71 and 59; three boxes a warp of 8
+    // rows (twice the proxy fences) 66, of 16 rows with a ring stage less 53, but then
+    // 500 rows an expert took 435 us instead of 390.
+    uint8_t* mine = smem + kGradStages * kGradStage + (warp - 2) * kGradBox;
+    const bool elected = symm::elect_one();
     uint32_t seg = 0;
     for (uint32_t i = first; i < tiles; i += step) {
       const uint32_t e = i / per, n0 = i % a.nb * 256, buf = seg & 1;
-      const uint32_t m0 = i % per / a.nb * 256 + rank * kBM + 32 * q;
+      const uint32_t m0 = i % per / a.nb * 256 + rank * kBM + 32 * q + 16 * turn;
       const bool any = table.off[e] != table.off[e + 1];
       if (any) {
         const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
@@ -543,42 +560,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::tc_fence_after();
         ++seg;
       }
-      const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
-      const uint32_t valid = m0 < a.m ? a.m - m0 : 0, cols = min(256u, a.nf - n0);
-      T* out = static_cast<T*>(a.out) + ((size_t)e * a.m + m0) * a.nf + n0;
-      for (uint32_t c = 32 * turn; c < cols; c += 64) {
-        // matrices of 8 lanes (rows of the gradient) x 8 columns, as they are: 16
-        // bytes of a line each
-        const uint32_t at = symm::smem_addr(mine) + (lane & 7) * kLine + (lane >> 3) * 16;
-        uint32_t v[2][8], w[2][8];
+      const uint32_t taddr = tmem + ((32 * q + 16 * turn) << 16) + buf * kAccCols;
+      for (uint32_t c = 0; c < 256 && n0 + c < a.nf; c += 64) {
+        uint32_t v[4][8];
         if (any) {
-          tmem_frags(taddr + c, v);
-          tmem_frags(taddr + c + 16, w);
+#pragma unroll
+          for (uint32_t j = 0; j < 4; ++j) tmem_frag16(taddr + c + 16 * j, v[j]);
+          tmem_wait(v[0], v[1]);
+          tmem_wait(v[2], v[3]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[0][j] = v[1][j] = w[0][j] = w[1][j] = 0;
+          for (int j = 0; j < 8; ++j) v[0][j] = v[1][j] = v[2][j] = v[3][j] = 0;
         }
+        if (m0 >= a.m) continue;
+        uint32_t pk[2][8];
 #pragma unroll
-        for (uint32_t o = 0; o < 4; ++o) {  // lanes 8 o .., four times 8 columns
-          const uint32_t h = o / 2, k = 2 * (o % 2);
-          auto two = [&](const uint32_t (&x)[2][8], uint32_t t) {
-            return symm::pack2<FMT>(__uint_as_float(x[h][4 * t + k]),
-                                    __uint_as_float(x[h][4 * t + k + 1]));
-          };
-          stmatrix(at + 8 * o * kLine, two(v, 0), two(v, 1), two(w, 0), two(w, 1));
+        for (uint32_t o = 0; o < 2; ++o)
+#pragma unroll
+          for (uint32_t j = 0; j < 8; ++j)
+            pk[o][j] = symm::pack2<FMT>(__uint_as_float(v[j / 2][4 * (j % 2) + 2 * o]),
+                                        __uint_as_float(v[j / 2][4 * (j % 2) + 2 * o + 1]));
+        if (elected) bulk_wait_read();  // the copy before
+        __syncwarp();
+        // matrices of 8 rows x 8 columns, as they are: 16 bytes of a line each
+#pragma unroll
+        for (uint32_t o = 0; o < 2; ++o)
+#pragma unroll
+          for (uint32_t j = 0; j < 4; j += 2) {
+            const uint32_t at = (lane & 7) * 128 + (((2 * j + (lane >> 3)) ^ (lane & 7)) << 4);
+            stmatrix(symm::smem_addr(mine) + 1024 * o + at, pk[o][2 * j], pk[o][2 * j + 1],
+                     pk[o][2 * j + 2], pk[o][2 * j + 3]);
+          }
+        symm::fence_proxy_async_shared();
+        __syncwarp();
+        if (elected) {
+          symm::tma_store_3d(&map_out, mine, (int)(n0 + c), (int)m0, (int)e);
+          bulk_commit();
         }
-        __syncwarp();
-        store_rows(mine, out + c, a.nf, valid, cols - c, true);
-        if (valid > 16)
-          store_rows(mine + 16 * kLine, out + (size_t)16 * a.nf + c, a.nf, valid - 16, cols - c,
-                     true);
-        __syncwarp();
       }
       if (any) {
         symm::tc_fence_before();
         arrive_first(&bar.tempty[buf]);
       }
     }
+    if (elected) bulk_wait();
   }
   leave_cta(bar, warp);
 }
@@ -667,17 +692,18 @@ int rows_product(const char* what, const void* x, size_t ldx, const void* w, uin
 template <int FMT>
 int weight_grad(const char* what, const void* a, size_t lda, const void* b, size_t ldb, void* out,
                 uint32_t m, uint32_t nf, const ExpertArgs& x, unsigned pairs, cudaStream_t s) {
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, mo;
   int rc = make_map(what, &ma, a, FMT, m, x.n, 0, lda, 64);
+  if (!rc) rc = make_map(what, &mo, out, FMT, nf, m, x.E, nf, 16);
   if (!rc) rc = make_map(what, &mb, b, FMT, nf, x.n, 0, ldb, 64);
   if (rc) return rc;
   GradArgs g{};
-  g.counts = x.counts, g.n = x.n, g.E = x.E, g.m = m, g.nf = nf, g.out = out;
+  g.counts = x.counts, g.n = x.n, g.E = x.E, g.m = m, g.nf = nf;
   g.mb = (m + 255) / 256, g.nb = (nf + 255) / 256;
   g.budget_ns = x.budget_ns, g.ctl = x.ctl;
   const uint64_t tiles = (uint64_t)x.E * g.mb * g.nb;
   return launch_pairs(what, grad_kernel<FMT>, (unsigned)std::min<uint64_t>(pairs, tiles), kThreads,
-                      kSmemBytes, s, ma, mb, g);
+                      kSmemBytes, s, ma, mb, mo, g);
 }
 
 // What both entry points check of their sizes, weights and type.

@@ -11,7 +11,7 @@ namespace experts {
 using symm::Control;
 
 constexpr uint32_t kBM = 128;          // features of a tile: the M side
-constexpr uint32_t kMaxWarps = 10;     // of a block
+constexpr uint32_t kMaxWarps = 14;     // of a block
 constexpr uint32_t kMaxExperts = SYMM_MOE_MAX_EXPERTS;
 enum { kErrRange = -5 };
 

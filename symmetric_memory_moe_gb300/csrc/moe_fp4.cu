@@ -21,8 +21,8 @@
 //   warp 0     TMA producer: codes and scales of both sides into a ring
 //   warp 1     MMA issuer: copies a slice's scales from shared memory into TMEM
 //              (tcgen05.cp, two slots) and issues its four tcgen05.mma, K 64
-//   warps 2-5  epilogue
-//   warps 6-9  scales as they lie beside the codes (a row's one after another) into
+//   warps 2-9  epilogue
+//   warps 10-13  scales as they lie beside the codes (a row's one after another) into
 //              the order that TMEM takes: 4 scales of each of 128 rows, row r at
 //              word r / 32 of 16-byte line r % 32
 // 192 rows, not 256: two accumulators and two slots of scales fill 480 of TMEM's 512
@@ -46,9 +46,23 @@ struct QuantArgs {
   uint8_t *codes, *scales;
   size_t ldc, lds;  // bytes
   const float* g;
-  uint64_t vectors;  // of 8 values
-  uint32_t k, kv;    // values and vectors of a row
+  uint32_t n, k, kv;  // rows, values and vectors of 8 values of a row
   int act;
+};
+
+// Vectors of rows [n][kv] in turn: this thread's next one is `step` vectors on.
+struct Walk {
+  uint32_t row, col, step_row, step_col, kv;
+  __device__ __forceinline__ explicit Walk(uint32_t kv_) : kv(kv_) {
+    const uint32_t step = gridDim.x * kQuantThreads;
+    const uint32_t first = blockIdx.x * kQuantThreads + threadIdx.x;
+    row = first / kv, col = first % kv;
+    step_row = step / kv, step_col = step % kv;
+  }
+  __device__ __forceinline__ void next() {
+    row += step_row, col += step_col;
+    if (col >= kv) col -= kv, ++row;
+  }
 };
 
 template <typename T>
@@ -114,72 +128,111 @@ __device__ __forceinline__ float power_of_two(int e) {  // -127 <= e <= 127
   return __uint_as_float(e == -127 ? 0x400000u : (uint32_t)(e + 127) << 23);
 }
 
-template <typename T, int FMT>
+// The largest magnitude of 8 values, as the bits of a float (a NaN's are the largest).
+template <typename T>
+__device__ __forceinline__ uint32_t top_of(const Vec8<T>& r) {
+  uint32_t m = 0;
+  if (sizeof(T) == 4) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+  }
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  const uint16_t t = (uint16_t)max(m & 0xffffu, m >> 16);
+  return __float_as_uint(moe::to_f(*reinterpret_cast<const T*>(&t)));
+}
+// Codes and the scale's byte of a lane's 8 values and their block's largest magnitude.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode(float (&f)[8], uint32_t top, float g, uint32_t& byte) {
+  const bool finite = top < 0x7f800000u;
+  if (FMT == SYMM_FP4_MX) {
+    // top = m 2^e with 1 <= m < 2: 6 2^(e - 2) reaches it up to m = 1.5
+    int e = (int)(top >> 23) - 127;
+    if (e == -127) e = -1000;  // below 2^-126 the smallest scale reaches anything
+    e = max(-127, min(127, e - 2 + ((top & 0x7fffffu) > 0x400000u)));
+    byte = finite ? (uint32_t)(e + 127) : 0xffu;
+    const float s = power_of_two(-e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= s;
+  } else {
+    byte = finite ? to_e4m3(fminf(__fdiv_rn(__uint_as_float(top), __fmul_rn(6.f, g)), 448.f))
+                  : 0x7fu;
+    const float unit = __fmul_rn(from_e4m3(byte), g);
+    if (!(unit > 0.f)) return 0;
+    if (unit > 0x1p-100f && unit < 0x1p100f) {
+      // Markstein's theorem (1990): with y = RN(1 / b), q a neighbour of a / b and r = a -
+      // q b (exact by fma), RN(q + r y) is the correctly rounded a / b.  (Of a tiny a, r
+      // may underflow: its code is 0 either way.  -0 would become 0.)
+      const float y = __frcp_rn(unit);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = f[i] * y;
+        f[i] = copysignf(fmaf(fmaf(-q, unit, f[i]), y, q), f[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], unit);
+    }
+  }
+  return finite ? to_codes(f) : 0;
+}
+
+// Four vectors (two with an activation, whose rows are two) in flight a thread: one
+// left a third of the bandwidth unused (188 us for 32768 x 7168 in bf16; now see the head).
+template <typename T, int FMT, bool GATED>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
   constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;  // of a block
+  constexpr int kFlight = GATED || sizeof(T) == 4 ? 2 : 4;
   moe::let_next_start();
   moe::wait_for_earlier();
   const float g = a.g ? *a.g : 1.f;
-  const uint64_t step = (uint64_t)gridDim.x * kQuantThreads;
-  const uint64_t first = (uint64_t)blockIdx.x * kQuantThreads + threadIdx.x;
-  const uint64_t step_row = step / a.kv;
-  const uint32_t step_col = (uint32_t)(step % a.kv);
-  uint64_t row = first / a.kv;
-  uint32_t col = (uint32_t)(first % a.kv);
+  Walk w(a.kv);
   // whole warps go round: a block's lanes are of one row, and there or not together
-  for (uint64_t v = first; v - (threadIdx.x & 31) < a.vectors; v += step) {
-    float f[8];
-    if (v < a.vectors) {
-      const T* x = static_cast<const T*>(a.x) + row * a.ldx + 8 * col;
-      const Vec8<T> r = load8(x);
-      floats(r, f);
-      if (a.act != SYMM_ACT_NONE) {
-        const Vec8<T> r2 = load8(x + a.k);
+  while (__any_sync(0xffffffffu, w.row < a.n)) {
+    Vec8<T> r[kFlight], r2[GATED ? kFlight : 1];
+    uint32_t row[kFlight], col[kFlight];
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      row[i] = w.row, col[i] = w.col;
+      r[i] = Vec8<T>();
+      if (GATED) r2[i] = Vec8<T>();
+      if (w.row < a.n) {
+        const T* x = static_cast<const T*>(a.x) + (size_t)w.row * a.ldx + 8 * w.col;
+        r[i] = load8(x);
+        if (GATED) r2[i] = load8(x + a.k);
+      }
+      w.next();
+    }
+#pragma unroll
+    for (int i = 0; i < kFlight; ++i) {
+      if (i && !__any_sync(0xffffffffu, row[i] < a.n)) break;
+      float f[8];
+      floats(r[i], f);
+      uint32_t top = 0, byte;
+      if (GATED) {
         float u[8];
-        floats(r2, u);
+        floats(r2[i], u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = activate(a.act, f[i]) * u[i];
+        for (int j = 0; j < 8; ++j) {
+          f[j] = activate(a.act, f[j]) * u[j];
+          top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+        }
+      } else {
+        top = top_of(r[i]);
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.f;
-    }
-    uint32_t top = 0;  // magnitudes compare as whole numbers, NaN above infinity
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-#pragma unroll
-    for (uint32_t o = 1; o < kLanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool finite = top < 0x7f800000u;
-    uint32_t byte, code = 0;
-    if (FMT == SYMM_FP4_MX) {
-      // top = m 2^e with 1 <= m < 2: 6 2^(e - 2) reaches it up to m = 1.5
-      int e = (int)(top >> 23) - 127;
-      if (e == -127) e = -1000;  // below 2^-126 the smallest scale reaches anything
-      e = max(-127, min(127, e - 2 + ((top & 0x7fffffu) > 0x400000u)));
-      byte = finite ? (uint32_t)(e + 127) : 0xffu;
-      if (finite) {
-        // 2^-e in two factors, neither of which leaves the range
-        const float s1 = power_of_two(-e / 2), s2 = power_of_two(-e - -e / 2);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * s1 * s2;
-        code = to_codes(f);
-      }
-    } else {
-      byte = finite ? to_e4m3(fminf(__fdiv_rn(__uint_as_float(top), __fmul_rn(6.f, g)), 448.f))
-                    : 0x7fu;
-      const float unit = __fmul_rn(from_e4m3(byte), g);
-      if (finite && unit > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], unit);
-        code = to_codes(f);
+      for (uint32_t o = 1; o < kLanes; o *= 2)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t code = encode<FMT>(f, top, g, byte);
+      if (row[i] < a.n) {
+        *reinterpret_cast<uint32_t*>(a.codes + row[i] * a.ldc + 4 * col[i]) = code;
+        if (threadIdx.x % kLanes == 0)
+          a.scales[row[i] * a.lds + col[i] / kLanes] = (uint8_t)byte;
       }
     }
-    if (v < a.vectors) {
-      *reinterpret_cast<uint32_t*>(a.codes + row * a.ldc + 4 * col) = code;
-      if (threadIdx.x % kLanes == 0) a.scales[row * a.lds + col / kLanes] = (uint8_t)byte;
-    }
-    row += step_row, col += step_col;
-    if (col >= a.kv) col -= a.kv, ++row;
   }
 }
 
@@ -189,8 +242,7 @@ struct DequantArgs {
   const float* g;
   void* y;
   size_t ldy;  // elements
-  uint64_t vectors;
-  uint32_t kv;
+  uint32_t n, kv;
 };
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const DequantArgs a) {
@@ -198,15 +250,10 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const Dequant
   moe::let_next_start();
   moe::wait_for_earlier();
   const float g = a.g ? *a.g : 1.f;
-  const uint64_t step = (uint64_t)gridDim.x * kQuantThreads;
-  const uint64_t first = (uint64_t)blockIdx.x * kQuantThreads + threadIdx.x;
-  const uint64_t step_row = step / a.kv;
-  const uint32_t step_col = (uint32_t)(step % a.kv);
-  uint64_t row = first / a.kv;
-  uint32_t col = (uint32_t)(first % a.kv);
-  for (uint64_t v = first; v < a.vectors; v += step) {
-    const uint32_t code = __ldg(reinterpret_cast<const uint32_t*>(a.codes + row * a.ldc) + col);
-    const uint32_t byte = __ldg(a.scales + row * a.lds + col / kLanes);
+  for (Walk w(a.kv); w.row < a.n; w.next()) {
+    const uint32_t code =
+        __ldg(reinterpret_cast<const uint32_t*>(a.codes + w.row * a.ldc) + w.col);
+    const uint32_t byte = __ldg(a.scales + w.row * a.lds + w.col / kLanes);
     float unit;
     if (FMT == SYMM_FP4_MX)
       unit = byte == 0xffu ? __uint_as_float(0x7fffffffu) : power_of_two((int)byte - 127);
@@ -218,23 +265,22 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const Dequant
     __align__(16) T out[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = moe::from_f<T>(__fmul_rn(f[i], unit));
-    uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(a.y) + row * a.ldy + 8 * col);
+    uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(a.y) + w.row * a.ldy + 8 * w.col);
 #pragma unroll
     for (size_t i = 0; i < sizeof(T) / 2; ++i) y[i] = reinterpret_cast<const uint4*>(out)[i];
-    row += step_row, col += step_col;
-    if (col >= a.kv) col -= a.kv, ++row;
   }
 }
 
 // ------------------------------------------------------------ fp4_kernel --
-constexpr uint32_t kThreads = 320;
+constexpr uint32_t kThreads = 448, kEpilogue = 256;
 constexpr uint32_t kMaxRows = 192;
 constexpr uint32_t kSlice = 256;                     // values of K: a row of 128 bytes
 constexpr uint32_t kATile = kBM * 128;               // 16 KB
 constexpr uint32_t kARaw = kBM * 16;                 // its scales, 16 bytes a row
-constexpr uint32_t kRingBytes = 208 * 1024;          // four stages of 128 x 192 tiles
+constexpr uint32_t kRingBytes = 204 * 1024;          // four stages of 128 x 192 tiles
 constexpr uint32_t kMaxStages = 9;
-constexpr uint32_t kSmemBytes = 1024 + kRingBytes;
+constexpr uint32_t kStageWarp = 16 * kLine;          // where a warp of the epilogue stages rows
+constexpr uint32_t kSmemBytes = 1024 + kRingBytes + 8 * kStageWarp;
 constexpr uint32_t kAccCols = 192;
 constexpr uint32_t kScaleCols = 2 * kAccCols;        // first column of the scales' slots
 
@@ -252,6 +298,7 @@ struct Fp4Args {
   uint32_t n, E, m, k, ncol;
   void* y;
   size_t ldy;
+  int vec;  // rows of y are 16-byte aligned
   uint64_t budget_ns;
   Control* ctl;
 };
@@ -296,14 +343,13 @@ __device__ __forceinline__ uint32_t fp4_idesc(uint32_t n, uint32_t which) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store16(const Fp4Args& a, const uint32_t (&v)[16], float scale,
-                                        uint32_t row, uint32_t valid, uint32_t f) {
-  if (f >= a.m) return;
-  T* y = static_cast<T*>(a.y) + (size_t)row * a.ldy + f;
-#pragma unroll
-  for (uint32_t j = 0; j < 16; ++j)
-    if (j < valid) y[j * a.ldy] = moe::from_f<T>(__uint_as_float(v[j]) * scale);
-}
+struct Fmt {
+  static constexpr int k = 0;
+};
+template <>
+struct Fmt<__nv_bfloat16> {
+  static constexpr int k = 1;
+};
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -326,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       symm::mbar_init(&bar.tfull[i], 1);
-      symm::mbar_init(&bar.tempty[i], 128);
+      symm::mbar_init(&bar.tempty[i], kEpilogue);
       symm::mbar_init(&bar.sfree[i], 1);
     }
     symm::mbar_init(&bar.drain, 1);
@@ -426,36 +472,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
     if (elected) symm::tc_commit(&bar.drain);
     symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
-  } else if (warp < 6) {  // ------------------------------------ epilogue
-    const uint32_t q = (uint32_t)(warp & 3);
+  } else if (warp < 10) {  // ----------------------------------- epilogue
+    // Two warps to each 32 TMEM lanes, which take turns at the chunks of rows.
+    const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
+    uint8_t* mine = smem + kRingBytes + (warp - 2) * kStageWarp;
     const float gx = a.gx ? *a.gx : 1.f;
     uint32_t seg = 0;
     for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, ++seg) {
       const Tile t = tile_at(table, i, a.E, a.ncol);
-      const uint32_t buf = seg & 1;
+      const uint32_t buf = seg & 1, f = t.col * kBM + 32 * q;
+      const uint32_t width = f < a.m ? a.m - f : 0;  // features from f on that are there
       const float scale = a.gw ? gx * a.gw[t.e] : gx;
       const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
-      if (any_of(!ok, 128)) {  // all threads leave, or none
+      if (any_of(!ok, kEpilogue)) {  // all threads leave, or none
         if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
       }
       symm::tc_fence_after();
       const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
-      const uint32_t f = t.col * kBM + 32 * q + lane;
-      for (uint32_t c = 0; c < t.rows; c += 16) {
-        uint32_t v[16];
-        symm::tmem_ld16(taddr + c, v);
-        if (c + 16 >= t.rows) {  // the accumulator is free for the next tile
-          symm::tc_fence_before();
-          symm::mbar_arrive(&bar.tempty[buf]);
-        }
-        store16<T>(a, v, scale, t.row + c, t.rows - c, f);
+      for (uint32_t c = 16 * turn; c < t.rows; c += 32) {
+        uint32_t v[2][8], p[2][4];
+        tmem_frags(taddr + c, v);
+#pragma unroll
+        for (uint32_t x = 0; x < 2; ++x)
+#pragma unroll
+          for (uint32_t o = 0; o < 4; ++o)
+            p[x][o] = symm::pack2<Fmt<T>::k>(
+                __uint_as_float(v[o / 2][4 * x + 2 * (o % 2)]) * scale,
+                __uint_as_float(v[o / 2][4 * x + 2 * (o % 2) + 1]) * scale);
+        stage_rows(mine, p);
+        __syncwarp();
+        store_rows(mine, static_cast<T*>(a.y) + (size_t)(t.row + c) * a.ldy + f, a.ldy,
+                   t.rows - c, width, a.vec);
+        __syncwarp();
       }
+      symm::tc_fence_before();
+      symm::mbar_arrive(&bar.tempty[buf]);  // the accumulator is free for the next tile
     }
   } else {  // ---------------------------------------------- scales' order
     // Lane l of warp w takes row 32 (l % 4) + 8 w + l / 4 of a block of 128: its
     // words are neighbours of the other lanes' in the tile.
-    const uint32_t w = (uint32_t)warp - 6, r = 32 * (lane % 4) + 8 * w + lane / 4;
+    const uint32_t w = (uint32_t)warp - 10, r = 32 * (lane % 4) + 8 * w + lane / 4;
     uint32_t st = 0, ph = 0;
     bool ok = true;
     for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
@@ -509,8 +566,9 @@ bool bad_packed(size_t ldc, size_t lds, int fmt, int k) {
          lds % 16 || lds > (1ull << 36);
 }
 
-unsigned quant_grid(uint64_t vectors) {
-  // as many blocks as are resident at once, 2048 threads an SM
+unsigned quant_grid(uint32_t n, uint32_t kv) {
+  // as many blocks as are resident at once at most, 2048 threads an SM
+  const uint64_t vectors = (uint64_t)n * kv;
   const uint64_t room = (uint64_t)std::max(sm_count(), 1) * (2048 / kQuantThreads);
   return (unsigned)std::min<uint64_t>(room, (vectors + kQuantThreads - 1) / kQuantThreads);
 }
@@ -565,19 +623,24 @@ int launch_product(const Maps& m, const Fp4Args& a, cudaStream_t s) {
                      m.w, m.ws, m.x64, m.xs64, m.x16, m.xs16, a);
 }
 
+template <typename T, int FMT>
+int launch_quantize(const QuantArgs& a, cudaStream_t s) {
+  return moe::launch("moe_fp4_quantize",
+                     a.act == SYMM_ACT_NONE ? quantize_kernel<T, FMT, false>
+                                            : quantize_kernel<T, FMT, true>,
+                     quant_grid(a.n, a.kv), kQuantThreads, 0, s, a);
+}
 template <typename T>
 int launch_quantize(int fmt, const QuantArgs& a, cudaStream_t s) {
-  return moe::launch("moe_fp4_quantize",
-                     fmt == SYMM_FP4_MX ? quantize_kernel<T, SYMM_FP4_MX>
-                                        : quantize_kernel<T, SYMM_FP4_NV>,
-                     quant_grid(a.vectors), kQuantThreads, 0, s, a);
+  return fmt == SYMM_FP4_MX ? launch_quantize<T, SYMM_FP4_MX>(a, s)
+                            : launch_quantize<T, SYMM_FP4_NV>(a, s);
 }
 template <typename T>
 int launch_dequantize(int fmt, const DequantArgs& a, cudaStream_t s) {
   return moe::launch("moe_fp4_dequantize",
                      fmt == SYMM_FP4_MX ? dequantize_kernel<T, SYMM_FP4_MX>
                                         : dequantize_kernel<T, SYMM_FP4_NV>,
-                     quant_grid(a.vectors), kQuantThreads, 0, s, a);
+                     quant_grid(a.n, a.kv), kQuantThreads, 0, s, a);
 }
 
 }  // namespace
@@ -610,7 +673,7 @@ extern "C" int moe_fp4_quantize(const void* x, size_t ldx, int act, int dtype, i
     QuantArgs a{};
     a.x = x, a.ldx = ldx, a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales), a.ldc = ldc, a.lds = lds, a.g = gscale;
-    a.k = (uint32_t)k, a.kv = (uint32_t)k / 8, a.vectors = (uint64_t)n * a.kv, a.act = act;
+    a.n = (uint32_t)n, a.k = (uint32_t)k, a.kv = (uint32_t)k / 8, a.act = act;
     if (fmt == SYMM_FP4_MX) a.g = nullptr;
     cudaStream_t s = as_stream(stream);
     return dtype == SYMM_DTYPE_F32    ? launch_quantize<float>(fmt, a, s)
@@ -643,7 +706,7 @@ extern "C" int moe_fp4_dequantize(const void* codes, size_t ldc, const void* sca
     DequantArgs a{};
     a.codes = static_cast<const uint8_t*>(codes), a.scales = static_cast<const uint8_t*>(scales);
     a.ldc = ldc, a.lds = lds, a.g = gscale, a.y = y, a.ldy = ldy;
-    a.kv = (uint32_t)k / 8, a.vectors = (uint64_t)n * a.kv;
+    a.n = (uint32_t)n, a.kv = (uint32_t)k / 8;
     cudaStream_t s = as_stream(stream);
     return dtype == SYMM_DTYPE_F32    ? launch_dequantize<float>(fmt, a, s)
            : dtype == SYMM_DTYPE_BF16 ? launch_dequantize<__nv_bfloat16>(fmt, a, s)
@@ -696,7 +759,8 @@ extern "C" int moe_fp4_expert_matmul(symm_heap_t* heap, const void* xc, size_t l
     Fp4Args a{};
     a.counts = counts, a.gx = gx, a.gw = gw, a.n = (uint32_t)n, a.E = (uint32_t)E;
     a.m = (uint32_t)m, a.k = (uint32_t)k, a.ncol = ((uint32_t)m + kBM - 1) / kBM;
-    a.y = y, a.ldy = ldy, a.budget_ns = heap->spin_budget;
+    a.y = y, a.ldy = ldy, a.vec = ldy % 8 == 0 && moe::aligned(y, 16);
+    a.budget_ns = heap->spin_budget;
     a.ctl = reinterpret_cast<Control*>(heap->base);
     const bool bf = dtype == SYMM_DTYPE_BF16;
     if (fmt == SYMM_FP4_MX)
