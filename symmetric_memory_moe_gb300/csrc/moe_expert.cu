@@ -116,7 +116,7 @@ __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
     }
     for (int i = 0; i < 2; ++i) {
       symm::mbar_init(&b.tfull[i], 1);
-      symm::mbar_init(&b.tempty[i], 2 * kEpilogue);  // both CTAs'
+      symm::mbar_init(&b.tempty[i], 2 * kEpilogue / 32);  // both CTAs' warps
     }
     symm::mbar_init(&b.drain, 1);
     symm::fence_mbar_init();
@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       symm::tc_fence_before();
-      arrive_first(&bar.tempty[buf]);  // the accumulator is free for the next tile
+      __syncwarp();
+      if (lane == 0) arrive_first(&bar.tempty[buf]);  // the accumulator is free again
     }
   }
   leave_cta(bar, warp);
@@ -600,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (any) {
         symm::tc_fence_before();
-        arrive_first(&bar.tempty[buf]);
+        __syncwarp();
+        if (lane == 0) arrive_first(&bar.tempty[buf]);
       }
     }
     if (elected) bulk_wait();

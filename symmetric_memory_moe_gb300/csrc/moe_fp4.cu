@@ -20,13 +20,12 @@
 // to 192 of its rows.  A slice of K is 256 values, one 128-byte swizzled row.
 //   warp 0     TMA producer: codes and scales of both sides into a ring
 //   warp 1     MMA issuer: copies a slice's scales from shared memory into TMEM
-//              (tcgen05.cp, two slots) and issues its four tcgen05.mma, K 64
+//              (tcgen05.cp) and issues its four tcgen05.mma, K 64
 //   warps 2-9  epilogue
 //   warps 10-13  scales as they lie beside the codes (a row's one after another) into
 //              the order that TMEM takes: 4 scales of each of 128 rows, row r at
 //              word r / 32 of 16-byte line r % 32
-// 192 rows, not 256: two accumulators and two slots of scales fill 480 of TMEM's 512
-// columns.
+// 192 rows (NV: 160), not 256: two accumulators and four stages' scales fill TMEM.
 #include <algorithm>
 #include <string>
 
@@ -273,7 +272,6 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const Dequant
 
 // ------------------------------------------------------------ fp4_kernel --
 constexpr uint32_t kThreads = 448, kEpilogue = 256;
-constexpr uint32_t kMaxRows = 192;
 constexpr uint32_t kSlice = 256;                     // values of K: a row of 128 bytes
 constexpr uint32_t kATile = kBM * 128;               // 16 KB
 constexpr uint32_t kARaw = kBM * 16;                 // its scales, 16 bytes a row
@@ -281,15 +279,16 @@ constexpr uint32_t kRingBytes = 204 * 1024;          // four stages of 128 x 192
 constexpr uint32_t kMaxStages = 9;
 constexpr uint32_t kStageWarp = 16 * kLine;          // where a warp of the epilogue stages rows
 constexpr uint32_t kSmemBytes = 1024 + kRingBytes + 8 * kStageWarp;
-constexpr uint32_t kAccCols = 192;
-constexpr uint32_t kScaleCols = 2 * kAccCols;        // first column of the scales' slots
+constexpr uint32_t kTmemCols = 512;
 
 template <int FMT>
 struct Scales {
   // 512-byte tiles of a slice: 4 scales of 128 rows, the K of one MMA (NV) or two (MX)
   static constexpr uint32_t kTiles = FMT == SYMM_FP4_MX ? 2 : 4;
   static constexpr uint32_t kPerSlice = kTiles * 4;      // scales of a row
-  static constexpr uint32_t kSlotCols = kTiles * 4 * 3;  // one row block of A, two of B
+  // most rows of a tile: TMEM holds two accumulators and the scales of four stages
+  static constexpr uint32_t kMaxRows = FMT == SYMM_FP4_MX ? 192 : 160;
+  static_assert(2 * kMaxRows + 4 * kTiles * 4 * 3 <= kTmemCols, "TMEM");
 };
 
 struct Fp4Args {
@@ -305,14 +304,16 @@ struct Fp4Args {
 
 struct Barriers {
   uint64_t full[kMaxStages], placed[kMaxStages], empty[kMaxStages];
-  uint64_t tfull[2], tempty[2], sfree[2], drain;
+  uint64_t tfull[2], tempty[2], drain;
   uint32_t tmem;
 };
 
-// 32 lines of 16 bytes into 4 TMEM columns of all four quarters of the lanes.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, const void* tile) {
-  const uint64_t desc = ((symm::smem_addr(tile) & 0x3FFFFull) >> 4) | ((128ull >> 4) << 32) |
-                        (1ull << 46);  // no swizzle, 8 lines 128 bytes apart, version 1
+// Descriptor of 32 lines of 16 bytes: no swizzle, 8 lines 128 bytes apart, version 1.
+__device__ __forceinline__ uint64_t scales_desc(const void* tile) {
+  return ((symm::smem_addr(tile) & 0x3FFFFull) >> 4) | ((128ull >> 4) << 32) | (1ull << 46);
+}
+// Such lines into 4 TMEM columns of all four quarters of the lanes.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                : "memory");
 }
@@ -355,30 +356,29 @@ template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
                const __grid_constant__ CUtensorMap map_x64,
-               const __grid_constant__ CUtensorMap map_xs64,
                const __grid_constant__ CUtensorMap map_x16,
-               const __grid_constant__ CUtensorMap map_xs16, const Fp4Args a) {
+               const __grid_constant__ CUtensorMap map_xs,
+               const __grid_constant__ CUtensorMap map_xs48, const Fp4Args a) {
   using S = Scales<FMT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<kMaxRows, 16> table;
+  __shared__ Table<S::kMaxRows, 16> table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
       symm::mbar_init(&bar.full[s], 1);
-      symm::mbar_init(&bar.placed[s], 128);
+      symm::mbar_init(&bar.placed[s], 4);
       symm::mbar_init(&bar.empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       symm::mbar_init(&bar.tfull[i], 1);
-      symm::mbar_init(&bar.tempty[i], kEpilogue);
-      symm::mbar_init(&bar.sfree[i], 1);
+      symm::mbar_init(&bar.tempty[i], kEpilogue / 32);
     }
     symm::mbar_init(&bar.drain, 1);
     symm::fence_mbar_init();
   }
-  if (warp == 1) symm::tmem_alloc(&bar.tmem, 512);
+  if (warp == 1) symm::tmem_alloc(&bar.tmem, kTmemCols);
   symm::tc_fence_before();
   __syncthreads();
   symm::tc_fence_after();
@@ -390,9 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t slices = (a.k + kSlice - 1) / kSlice;
   // A stage: codes of A and B, their scales as loaded (A, B), and as TMEM takes them.
   const uint32_t most = good ? copied_rows(table.most) : 16;
-  const uint32_t raw = kATile + most * 128, tiled = raw + kARaw + most * 16;
+  const uint32_t raw = kATile + most * 128, tiled = raw + kARaw + (most <= 48 ? 48 : S::kMaxRows) * 16;
   const uint32_t stage_bytes = (tiled + S::kTiles * 512 * 3 + 1023) / 1024 * 1024;
-  const uint32_t stages = min(kMaxStages, kRingBytes / stage_bytes);
+  // In TMEM two accumulators, then a place for each stage's scales: what frees the
+  // stage frees it too.
+  const uint32_t acc_cols = good ? table.most : 16, row_blocks = acc_cols > 128 ? 2 : 1;
+  const uint32_t scale_cols = S::kTiles * 4 * (1 + row_blocks);
+  const uint32_t stages = min(min(kMaxStages, kRingBytes / stage_bytes),
+                              (kTmemCols - 2 * acc_cols) / scale_cols);
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
@@ -401,23 +406,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       const Tile t = tile_at(table, i, a.E, a.ncol);
       const uint32_t rows = copied_rows(t.bt);
+      const bool few = t.bt <= 48;
       for (uint32_t s = 0; s < slices; ++s) {
         if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * stage_bytes;
         uint64_t* full = &bar.full[st];
         if (elected) {
-          symm::mbar_arrive_expect_tx(full, kATile + kARaw + rows * (128 + 16));
+          symm::mbar_arrive_expect_tx(full, kATile + kARaw + rows * 128 + (few ? 48 : S::kMaxRows) * 16);
           // 16 bytes of scales: this slice's, or with MX of this and its neighbour
           const int k = (int)(s * 128), b = (int)(s * S::kPerSlice / 16 * 16);
           symm::tma_load_3d(buf, &map_w, k, (int)(t.col * kBM), (int)t.e, full);
           symm::tma_load_3d(buf + raw, &map_ws, b, (int)(t.col * kBM), (int)t.e, full);
-          const uint32_t box = t.bt <= 48 ? 16 : 64;
-          const CUtensorMap* mx = t.bt <= 48 ? &map_x16 : &map_x64;
-          const CUtensorMap* ms = t.bt <= 48 ? &map_xs16 : &map_xs64;
-          for (uint32_t r = 0; r < rows; r += box) {
-            symm::tma_load_2d(buf + kATile + r * 128, mx, k, (int)(t.row + r), full);
-            symm::tma_load_2d(buf + raw + kARaw + r * 16, ms, b, (int)(t.row + r), full);
-          }
+          // the rows' scales by one copy of all that a tile may have, few rows' by 48
+          symm::tma_load_2d(buf + raw + kARaw, few ? &map_xs48 : &map_xs, b, (int)t.row, full);
+          if (few)
+            for (uint32_t r = 0; r < rows; r += 16)
+              symm::tma_load_2d(buf + kATile + r * 128, &map_x16, k, (int)(t.row + r), full);
+          else
+            for (uint32_t r = 0; r < rows; r += 64)
+              symm::tma_load_2d(buf + kATile + r * 128, &map_x64, k, (int)(t.row + r), full);
         }
         ++it;
         if (++st == stages) st = 0, ph ^= 1;
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       symm::mbar_wait(&bar.full[i % stages], (i / stages) & 1, drain_ns(a.budget_ns));
   } else if (warp == 1) {  // ---------------------------------- MMA issuer
     const bool elected = symm::elect_one();
-    uint32_t st = 0, ph = 0, seg = 0, g = 0;  // g: slices so far
+    uint32_t st = 0, ph = 0, seg = 0;
     bool ok = true;
     for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++seg) {
       const Tile t = tile_at(table, i, a.E, a.ncol);
@@ -436,33 +443,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
-      const uint32_t acc = tmem + buf * kAccCols;
-      for (uint32_t s = 0; s < slices; ++s, ++g) {
-        const uint32_t slot = g & 1, sa = tmem + kScaleCols + slot * S::kSlotCols;
+      const uint32_t acc = tmem + buf * acc_cols;
+      const uint32_t idesc = fp4_idesc<FMT>(t.bt, 0), idesc_odd = fp4_idesc<FMT>(t.bt, 2);
+      for (uint32_t s = 0; s < slices; ++s) {
+        const uint32_t sa = tmem + 2 * acc_cols + st * scale_cols;
         const uint32_t sb = sa + S::kTiles * 4;
-        ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl) &&
-             symm::mbar_wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl) &&
-             symm::mbar_wait_warp(&bar.sfree[slot], ((g >> 1) & 1) ^ 1u, a.budget_ns, a.ctl);
-        if (!ok) break;
+        // whoever placed the scales has seen the copies land
+        if (!(ok = symm::mbar_wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl))) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * stage_bytes;
         const uint64_t wd = symm::sw128_kmajor_desc(at);
         const uint64_t xd = symm::sw128_kmajor_desc(at + kATile);
         if (elected) {
-          // A's tiles in K order; B's two row blocks side by side, in K order
+          // A's tiles in K order; B's row blocks, one or two, side by side in K order
+          const uint64_t sd = scales_desc(at + tiled);
 #pragma unroll
-          for (uint32_t c = 0; c < S::kTiles; ++c)
-            copy_scales(sa + 4 * c, at + tiled + 512 * c);
-          for (uint32_t c = 0; c < 2 * S::kTiles; ++c)
-            if (c % 2 == 0 || t.bt > 128)
-              copy_scales(sb + 4 * c, at + tiled + 512 * (S::kTiles + c));
+          for (uint32_t c = 0; c < S::kTiles; ++c) copy_scales(sa + 4 * c, sd + 32 * c);
+          if (row_blocks == 1) {
+#pragma unroll
+            for (uint32_t c = 0; c < S::kTiles; ++c)
+              copy_scales(sb + 4 * c, sd + 32 * (S::kTiles + 2 * c));
+          } else {
+#pragma unroll
+            for (uint32_t c = 0; c < 2 * S::kTiles; ++c)
+              copy_scales(sb + 4 * c, sd + 32 * (S::kTiles + c));
+          }
 #pragma unroll
           for (uint32_t j = 0; j < 4; ++j) {
-            const uint32_t c = j * S::kTiles / 4, which = FMT == SYMM_FP4_MX ? 2 * (j & 1) : 0;
-            scaled_mma<FMT>(acc, wd + 2 * j, xd + 2 * j, fp4_idesc<FMT>(t.bt, which), sa + 4 * c,
-                            sb + 8 * c, (s | j) != 0);
+            const uint32_t c = j * S::kTiles / 4;
+            scaled_mma<FMT>(acc, wd + 2 * j, xd + 2 * j,
+                            FMT == SYMM_FP4_MX && (j & 1) ? idesc_odd : idesc, sa + 4 * c,
+                            sb + 4 * row_blocks * c, (s | j) != 0);
           }
-          symm::tc_commit(&bar.sfree[slot]);
           symm::tc_commit(&bar.empty[st]);
         }
         if (++st == stages) st = 0, ph ^= 1;
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       symm::tc_fence_after();
-      const uint32_t taddr = tmem + ((32 * q) << 16) + buf * kAccCols;
+      const uint32_t taddr = tmem + ((32 * q) << 16) + buf * acc_cols;
       for (uint32_t c = 16 * turn; c < t.rows; c += 32) {
         uint32_t v[2][8], p[2][4];
         tmem_frags(taddr + c, v);
@@ -507,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       symm::tc_fence_before();
-      symm::mbar_arrive(&bar.tempty[buf]);  // the accumulator is free for the next tile
+      __syncwarp();
+      if (lane == 0) symm::mbar_arrive(&bar.tempty[buf]);  // the accumulator is free again
     }
   } else {  // ---------------------------------------------- scales' order
     // Lane l of warp w takes row 32 (l % 4) + 8 w + l / 4 of a block of 128: its
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       const Tile t = tile_at(table, i, a.E, a.ncol);
-      const uint32_t rows = copied_rows(t.bt);
+      const uint32_t rows = t.bt;
       for (uint32_t s = 0; s < slices; ++s) {
         if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* at = smem + st * stage_bytes;
@@ -536,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             to[128 * (b ? S::kTiles + 2 * c + b - 1 : c) + word] = x[c];
         }
         symm::fence_proxy_async_shared();
-        symm::mbar_arrive(&bar.placed[st]);
+        __syncwarp();
+        if (lane == 0) symm::mbar_arrive(&bar.placed[st]);
         if (++st == stages) st = 0, ph ^= 1;
       }
     }
@@ -547,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     symm::tc_fence_after();
-    symm::tmem_dealloc(tmem, 512);
+    symm::tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -595,7 +609,7 @@ int make_map(const char* what, CUtensorMap* map, const void* base, uint64_t inne
 }
 
 struct Maps {
-  CUtensorMap w, ws, x64, xs64, x16, xs16;
+  CUtensorMap w, ws, x64, x16, xs, xs48;
 };
 
 template <typename T, int FMT>
@@ -617,10 +631,10 @@ int launch_product(const Maps& m, const Fp4Args& a, cudaStream_t s) {
     }
   }
   // at most one partly filled block of rows for each expert that has rows
-  const uint64_t most = (uint64_t)a.ncol * std::min<uint64_t>(a.n, a.n / kMaxRows + a.E);
+  const uint64_t most = (uint64_t)a.ncol * std::min<uint64_t>(a.n, a.n / Scales<FMT>::kMaxRows + a.E);
   const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), most);
   return moe::launch("moe_fp4_expert_matmul", fp4_kernel<T, FMT>, grid, kThreads, kSmemBytes, s,
-                     m.w, m.ws, m.x64, m.xs64, m.x16, m.xs16, a);
+                     m.w, m.ws, m.x64, m.x16, m.xs, m.xs48, a);
 }
 
 template <typename T, int FMT>
@@ -749,9 +763,12 @@ extern "C" int moe_fp4_expert_matmul(symm_heap_t* heap, const void* xc, size_t l
     rc = make_map(what, &mp.w, wc, k / 2, m, E, ldwc, 128, kBM);
     if (!rc) rc = make_map(what, &mp.ws, ws, sb, m, E, ldws, 16, kBM);
     if (!rc) rc = make_map(what, &mp.x64, xc, k / 2, n, 0, ldxc, 128, 64);
-    if (!rc) rc = make_map(what, &mp.xs64, xs, sb, n, 0, ldxs, 16, 64);
     if (!rc) rc = make_map(what, &mp.x16, xc, k / 2, n, 0, ldxc, 128, 16);
-    if (!rc) rc = make_map(what, &mp.xs16, xs, sb, n, 0, ldxs, 16, 16);
+    if (!rc)
+      rc = make_map(what, &mp.xs, xs, sb, n, 0, ldxs, 16,
+                    fmt == SYMM_FP4_MX ? Scales<SYMM_FP4_MX>::kMaxRows
+                                       : Scales<SYMM_FP4_NV>::kMaxRows);
+    if (!rc) rc = make_map(what, &mp.xs48, xs, sb, n, 0, ldxs, 16, 48);
     if (rc) return rc;
     cudaStream_t s = as_stream(stream);
     rc = ensure_ctrl(heap, s);
