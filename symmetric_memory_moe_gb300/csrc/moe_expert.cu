@@ -102,7 +102,7 @@ __device__ __forceinline__ Ring ring_of(uint32_t rows) {
 }
 
 struct Barriers {
-  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];  // ready: the second CTA's half
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2], drain;
   uint32_t tmem;
 };
@@ -110,8 +110,8 @@ struct Barriers {
 __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
-      symm::mbar_init(&b.full[s], 1);
-      symm::mbar_init(&b.ready[s], 1);
+      // the first CTA's: its own copies, and the second one's word that its are there
+      symm::mbar_init(&b.full[s], pair_rank() ? 1 : 2);
       symm::mbar_init(&b.empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -204,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool good = lay_out(table, a.counts, a.E, a.n);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0;
-  const Ring ring = ring_of(good ? copied_rows(table.most / 2) : 16);
+  const Ring ring = ring_of(uniform(good ? table.most / 2 : 16));
   const uint32_t slices = (a.k + ring.deep * kBK - 1) / (ring.deep * kBK);
-  const uint32_t tmem = bar.tmem, abytes = ring.deep * kATile;
+  const uint32_t tmem = uniform(bar.tmem), abytes = ring.deep * kATile;
   const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t i = first; ok && i < tiles; i += step) {
       const Tile t = tile_at(table, i, a.E, a.npair);
-      const uint32_t half = t.bt / 2, rows = copied_rows(half), xbytes = rows * 128;
+      const uint32_t half = t.bt / 2, xbytes = half * 128;
       const uint32_t col = 2 * t.col + rank, row = t.row + rank * half;
       for (uint32_t s = 0; s < slices; ++s) {
         if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
@@ -233,13 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               symm::tma_load_3d(buf + d * kATile, &map_w, k, (int)(col * kBM), (int)t.e, full);
             }
-            uint8_t* x = buf + abytes + d * xbytes;
-            if (half <= 48)
-              for (uint32_t r = 0; r < rows; r += 16)
-                symm::tma_load_2d(x + r * 128, &map_x16, k, (int)(row + r), full);
-            else
-              for (uint32_t r = 0; r < rows; r += 64)
-                symm::tma_load_2d(x + r * 128, &map_x64, k, (int)(row + r), full);
+            load_lines(buf + abytes + d * xbytes, &map_x64, &map_x16, k, row, half, full);
           }
         }
         ++it;
@@ -255,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = first; ok && i < tiles; i += step)
       for (uint32_t s = 0; s < slices; ++s) {
         if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
-        if (elected) arrive_first(&bar.ready[st]);
+        if (elected) arrive_first(&bar.full[st]);
         if (++st == ring.stages) st = 0, ph ^= 1;
       }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -4);
@@ -265,16 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t i = first; ok && i < tiles; i += step, ++seg) {
       const Tile t = tile_at(table, i, a.E, a.npair);
-      const uint32_t xbytes = copied_rows(t.bt / 2) * 128, buf = seg & 1;
-      const uint32_t idesc = mma_idesc(FMT, t.bt, kMMajor, false);
+      const uint32_t bt = uniform(t.bt), xbytes = bt / 2 * 128, buf = seg & 1;
+      const uint32_t idesc = mma_idesc(FMT, bt, kMMajor, false);
       if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
       for (uint32_t s = 0; s < slices; ++s) {
-        ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl) &&
-             symm::mbar_wait_warp(&bar.ready[st], ph, a.budget_ns, a.ctl);
-        if (!ok) break;
+        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * ring.stage_bytes;
         if (elected) {
@@ -457,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool good = lay_out(table, a.counts, a.E, a.n);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   const uint32_t per = a.mb * a.nb, tiles = good ? a.E * per : 0;
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = uniform(bar.tmem);
   const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
   // Tile i: an expert's blocks of 256 columns one after another, then the next 256 rows.
 
@@ -497,9 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t e = i / per, r0 = table.off[e], r1 = table.off[e + 1];
       if (r0 == r1) continue;  // the epilogue writes zeros
       const uint32_t buf = seg & 1;
-      if (!rank &&
-          !(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
-        break;
+      const uint32_t phase = ((seg >> 1) & 1) ^ 1u;
+      if (!rank && !(ok = symm::mbar_wait_warp(&bar.tempty[buf], phase, a.budget_ns, a.ctl))) break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
       for (uint32_t r = r0; r < r1; r += 64) {
@@ -514,9 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (rank) {
-          if (elected) arrive_first(&bar.ready[st]);
+          if (elected) arrive_first(&bar.full[st]);
         } else {
-          if (!(ok = symm::mbar_wait_warp(&bar.ready[st], ph, a.budget_ns, a.ctl))) break;
           symm::tc_fence_after();
           const uint64_t ad = symm::sw128_mnmajor_desc(at);
           const uint64_t bd = symm::sw128_mnmajor_desc(at + 16384);
@@ -760,7 +750,8 @@ int backward(const char* what, const void* dy, size_t lddy, const void* x, size_
     }
   }
   if (!rc && dw_d) rc = weight_grad<FMT>(what, h, F, dy, lddy, dw_d, F, D, a, pairs, s);
-  if (!rc && dw_gu) rc = weight_grad<FMT>(what, x, ldx, dgu, 2 * (size_t)F, dw_gu, D, 2 * F, a, pairs, s);
+  if (!rc && dw_gu)
+    rc = weight_grad<FMT>(what, x, ldx, dgu, 2 * (size_t)F, dw_gu, D, 2 * F, a, pairs, s);
   return rc;
 }
 

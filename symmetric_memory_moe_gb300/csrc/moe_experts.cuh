@@ -11,7 +11,7 @@ namespace experts {
 using symm::Control;
 
 constexpr uint32_t kBM = 128;          // features of a tile: the M side
-constexpr uint32_t kMaxWarps = 14;     // of a block
+constexpr uint32_t kMaxWarps = 18;     // of a block
 constexpr uint32_t kMaxExperts = SYMM_MOE_MAX_EXPERTS;
 enum { kErrRange = -5 };
 
@@ -122,9 +122,14 @@ __device__ __forceinline__ Tile tile_at(const Table<MAX, STEP>& t, uint32_t i, u
   return o;
 }
 
-// Rows that a tile's copies bring: boxes of 16 up to 48 rows, else of 64.
-__device__ __forceinline__ uint32_t copied_rows(uint32_t bt) {
-  return bt <= 48 ? bt : (bt + 63) / 64 * 64;
+// `rows` rows (whole steps of 16) from `row` on, 128 bytes of each from x on, to lines
+// of 128 bytes at `to`: boxes of 64 rows, then of 16.
+__device__ __forceinline__ void load_lines(uint8_t* to, const CUtensorMap* map64,
+                                           const CUtensorMap* map16, int x, uint32_t row,
+                                           uint32_t rows, uint64_t* bar) {
+  uint32_t r = 0;
+  for (; r + 64 <= rows; r += 64) symm::tma_load_2d(to + r * 128, map64, x, (int)(row + r), bar);
+  for (; r < rows; r += 16) symm::tma_load_2d(to + r * 128, map16, x, (int)(row + r), bar);
 }
 
 // How long a CTA that gives up waits for its own copies and MMAs, which nothing
@@ -239,6 +244,11 @@ __device__ __forceinline__ void store_rows(const uint8_t* stage, T* y, size_t ld
 }
 
 // ------------------------------------------------------------- CTA pairs --
+// A value that is the same in the whole warp, where the compiler sees that it is and
+// keeps it in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
 // Two CTAs of a cluster share a tile of twice 128 features (cta_group::2): each
 // holds its own 128 features of the M side and half of the N side's rows in its
 // shared memory, and its own features' accumulators in its TMEM; the first one
@@ -266,6 +276,7 @@ __device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
+// D (both CTAs' TMEM) (+)= A B^T, kind::f16, issued by one thread of the first CTA.
 __device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(

@@ -16,16 +16,21 @@
 // of a row's halves, in 32 bits.
 //
 // fp4_kernel: y_r = gx gw_e sum_b sx_rb sw_b sum_i x_ri w_i, as y^T = W^T x^T on the
-// block-scaled tensor cores: the M side 128 features of an expert, the N side 16
-// to 192 of its rows.  A slice of K is 256 values, one 128-byte swizzled row.
+// block-scaled tensor cores, by CTA pairs (cta_group::2): the M side 256 features of
+// an expert, the N side 32 to 192 of its rows.  A slice of K is 256 values, one
+// 128-byte swizzled row; a CTA loads its own 128 features, half of the rows, and the
+// scales of both (all of the rows': either half of the product needs them).
 //   warp 0     TMA producer: codes and scales of both sides into a ring
-//   warp 1     MMA issuer: copies a slice's scales from shared memory into TMEM
-//              (tcgen05.cp) and issues its four tcgen05.mma, K 64
-//   warps 2-9  epilogue
-//   warps 10-13  scales as they lie beside the codes (a row's one after another) into
+//   warp 1     MMA issuer (first CTA): copies a slice's scales from shared memory
+//              into TMEM (tcgen05.cp) and issues its four tcgen05.mma, K 64
+//   warps 2-9  epilogue, as in moe_expert.cu
+//   warps 10-17  scales as they lie beside the codes (a row's one after another) into
 //              the order that TMEM takes: 4 scales of each of 128 rows, row r at
-//              word r / 32 of 16-byte line r % 32
-// 192 rows (NV: 160), not 256: two accumulators and four stages' scales fill TMEM.
+//              word r / 32 of 16-byte line r % 32.  Four warps to a stage, in turns.
+// 192 rows (NV: 160), not 256: two accumulators and four slots of scales fill TMEM.
+// What bounds it is the way of a stage around its ring (copies, placing, MMAs and back,
+// some 3000 cycles for 4 or 5 stages), then the issue of a slice (12 or 6 tcgen05.cp
+// and 4 MMAs from one thread, 450 cycles); the MMAs of a slice are 330.
 #include <algorithm>
 #include <string>
 
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const Dequant
 }
 
 // ------------------------------------------------------------ fp4_kernel --
-constexpr uint32_t kThreads = 448, kEpilogue = 256;
+constexpr uint32_t kThreads = 576, kEpilogue = 256;
 constexpr uint32_t kSlice = 256;                     // values of K: a row of 128 bytes
 constexpr uint32_t kATile = kBM * 128;               // 16 KB
 constexpr uint32_t kARaw = kBM * 16;                 // its scales, 16 bytes a row
@@ -294,7 +299,7 @@ struct Scales {
 struct Fp4Args {
   const int32_t* counts;
   const float *gx, *gw;
-  uint32_t n, E, m, k, ncol;
+  uint32_t n, E, m, k, npair;
   void* y;
   size_t ldy;
   int vec;  // rows of y are 16-byte aligned
@@ -304,7 +309,7 @@ struct Fp4Args {
 
 struct Barriers {
   uint64_t full[kMaxStages], placed[kMaxStages], empty[kMaxStages];
-  uint64_t tfull[2], tempty[2], drain;
+  uint64_t tfull[2], tempty[2], sfree[kMaxStages], drain;
   uint32_t tmem;
 };
 
@@ -314,7 +319,7 @@ __device__ __forceinline__ uint64_t scales_desc(const void* tile) {
 }
 // Such lines into 4 TMEM columns of all four quarters of the lanes.
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                : "memory");
 }
 template <int FMT>
@@ -323,14 +328,14 @@ __device__ __forceinline__ void scaled_mma(uint32_t d, uint64_t ad, uint64_t bd,
   if (FMT == SYMM_FP4_MX)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
         "[%5], p;\n\t}" ::"r"(d),
         "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
   else
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, "
         "[%4], [%5], p;\n\t}" ::"r"(d),
         "l"(ad), "l"(bd), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
@@ -340,7 +345,7 @@ __device__ __forceinline__ void scaled_mma(uint32_t d, uint64_t ad, uint64_t bd,
 template <int FMT>
 __device__ __forceinline__ uint32_t fp4_idesc(uint32_t n, uint32_t which) {
   return (which << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) |
-         ((uint32_t)(FMT == SYMM_FP4_MX) << 23) | ((kBM >> 4) << 24) | (which << 29);
+         ((uint32_t)(FMT == SYMM_FP4_MX) << 23) | ((2 * kBM >> 4) << 24) | (which << 29);
 }
 
 template <typename T>
@@ -354,102 +359,108 @@ struct Fmt<__nv_bfloat16> {
 
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
-    fp4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_ws,
+    fp4_kernel(const __grid_constant__ CUtensorMap map_w,
+               const __grid_constant__ CUtensorMap map_ws,
                const __grid_constant__ CUtensorMap map_x64,
                const __grid_constant__ CUtensorMap map_x16,
                const __grid_constant__ CUtensorMap map_xs,
-               const __grid_constant__ CUtensorMap map_xs48, const Fp4Args a) {
+               const __grid_constant__ CUtensorMap map_xs32, const Fp4Args a) {
   using S = Scales<FMT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<S::kMaxRows, 16> table;
+  __shared__ Table<S::kMaxRows, 32> table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
       symm::mbar_init(&bar.full[s], 1);
-      symm::mbar_init(&bar.placed[s], 4);
+      symm::mbar_init(&bar.placed[s], 8);  // of the first CTA: by the four warps of either
       symm::mbar_init(&bar.empty[s], 1);
+      symm::mbar_init(&bar.sfree[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       symm::mbar_init(&bar.tfull[i], 1);
-      symm::mbar_init(&bar.tempty[i], kEpilogue / 32);
+      symm::mbar_init(&bar.tempty[i], 2 * kEpilogue / 32);  // both CTAs' warps
     }
     symm::mbar_init(&bar.drain, 1);
     symm::fence_mbar_init();
   }
-  if (warp == 1) symm::tmem_alloc(&bar.tmem, kTmemCols);
+  if (warp == 1) pair_tmem_alloc(&bar.tmem, kTmemCols);
   symm::tc_fence_before();
   __syncthreads();
+  pair_sync();
   symm::tc_fence_after();
   moe::let_next_start();
   moe::wait_for_earlier();
   const bool good = lay_out(table, a.counts, a.E, a.n);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
-  const uint32_t tiles = good ? table.blocks[a.E] * a.ncol : 0, tmem = bar.tmem;
+  const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0, tmem = uniform(bar.tmem);
+  const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
   const uint32_t slices = (a.k + kSlice - 1) / kSlice;
   // A stage: codes of A and B, their scales as loaded (A, B), and as TMEM takes them.
-  const uint32_t most = good ? copied_rows(table.most) : 16;
-  const uint32_t raw = kATile + most * 128, tiled = raw + kARaw + (most <= 48 ? 48 : S::kMaxRows) * 16;
+  const uint32_t most = uniform(good ? table.most / 2 : 16);
+  const uint32_t raw = kATile + most * 128;
+  const uint32_t tiled = raw + kARaw + (most <= 16 ? 32 : S::kMaxRows) * 16;
   const uint32_t stage_bytes = (tiled + S::kTiles * 512 * 3 + 1023) / 1024 * 1024;
-  // In TMEM two accumulators, then a place for each stage's scales: what frees the
-  // stage frees it too.
-  const uint32_t acc_cols = good ? table.most : 16, row_blocks = acc_cols > 128 ? 2 : 1;
+  // In TMEM two accumulators, then slots of a slice's scales: one for each stage, which
+  // is free when the stage is, or as many as fit, each with a barrier of its own.
+  const uint32_t acc_cols = 2 * most, row_blocks = acc_cols > 128 ? 2 : 1;
   const uint32_t scale_cols = S::kTiles * 4 * (1 + row_blocks);
-  const uint32_t stages = min(min(kMaxStages, kRingBytes / stage_bytes),
-                              (kTmemCols - 2 * acc_cols) / scale_cols);
+  const uint32_t stages = min(kMaxStages, kRingBytes / stage_bytes);
+  const uint32_t slots = min(stages, (kTmemCols - 2 * acc_cols) / scale_cols);
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 1, it = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
-      const uint32_t rows = copied_rows(t.bt);
-      const bool few = t.bt <= 48;
+    for (uint32_t i = first; ok && i < tiles; i += step) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
+      const uint32_t half = t.bt / 2;
+      const uint32_t col = 2 * t.col + rank, row = t.row + rank * half;
+      const bool few = t.bt == 32;
       for (uint32_t s = 0; s < slices; ++s) {
         if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * stage_bytes;
         uint64_t* full = &bar.full[st];
         if (elected) {
-          symm::mbar_arrive_expect_tx(full, kATile + kARaw + rows * 128 + (few ? 48 : S::kMaxRows) * 16);
+          symm::mbar_arrive_expect_tx(
+              full, kATile + kARaw + half * 128 + (few ? 32 : S::kMaxRows) * 16);
           // 16 bytes of scales: this slice's, or with MX of this and its neighbour
           const int k = (int)(s * 128), b = (int)(s * S::kPerSlice / 16 * 16);
-          symm::tma_load_3d(buf, &map_w, k, (int)(t.col * kBM), (int)t.e, full);
-          symm::tma_load_3d(buf + raw, &map_ws, b, (int)(t.col * kBM), (int)t.e, full);
-          // the rows' scales by one copy of all that a tile may have, few rows' by 48
-          symm::tma_load_2d(buf + raw + kARaw, few ? &map_xs48 : &map_xs, b, (int)t.row, full);
-          if (few)
-            for (uint32_t r = 0; r < rows; r += 16)
-              symm::tma_load_2d(buf + kATile + r * 128, &map_x16, k, (int)(t.row + r), full);
-          else
-            for (uint32_t r = 0; r < rows; r += 64)
-              symm::tma_load_2d(buf + kATile + r * 128, &map_x64, k, (int)(t.row + r), full);
+          symm::tma_load_3d(buf, &map_w, k, (int)(col * kBM), (int)t.e, full);
+          symm::tma_load_3d(buf + raw, &map_ws, b, (int)(col * kBM), (int)t.e, full);
+          // all the rows' scales, which both CTAs need, by one copy of what a tile has at
+          // most (or of 32 rows)
+          symm::tma_load_2d(buf + raw + kARaw, few ? &map_xs32 : &map_xs, b, (int)t.row, full);
+          load_lines(buf + kATile, &map_x64, &map_x16, k, row, half, full);
         }
         ++it;
         if (++st == stages) st = 0, ph ^= 1;
       }
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -3);
-    for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
-      symm::mbar_wait(&bar.full[i % stages], (i / stages) & 1, drain_ns(a.budget_ns));
-  } else if (warp == 1) {  // ---------------------------------- MMA issuer
+    drain_ring(bar.full, bar.empty, stages, it, ok, a.budget_ns);
+  } else if (warp == 1 && rank == 0) {  // --------------------- MMA issuer
     const bool elected = symm::elect_one();
-    uint32_t st = 0, ph = 0, seg = 0;
+    uint32_t st = 0, ph = 0, seg = 0, slot = 0, sph = 1;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x, ++seg) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
+    for (uint32_t i = first; ok && i < tiles; i += step, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t buf = seg & 1;
       if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * acc_cols;
-      const uint32_t idesc = fp4_idesc<FMT>(t.bt, 0), idesc_odd = fp4_idesc<FMT>(t.bt, 2);
+      const uint32_t bt = uniform(t.bt);
+      const uint32_t idesc = fp4_idesc<FMT>(bt, 0), idesc_odd = fp4_idesc<FMT>(bt, 2);
       for (uint32_t s = 0; s < slices; ++s) {
-        const uint32_t sa = tmem + 2 * acc_cols + st * scale_cols;
+        const uint32_t sa = tmem + 2 * acc_cols + slot * scale_cols;
         const uint32_t sb = sa + S::kTiles * 4;
-        // whoever placed the scales has seen the copies land
-        if (!(ok = symm::mbar_wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl))) break;
+        // whoever placed the scales, here and in the other CTA, has seen the copies land
+        ok = symm::mbar_wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl) &&
+             (slots == stages ||
+              symm::mbar_wait_warp(&bar.sfree[slot], sph, a.budget_ns, a.ctl));
+        if (!ok) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * stage_bytes;
         const uint64_t wd = symm::sw128_kmajor_desc(at);
@@ -475,24 +486,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                             FMT == SYMM_FP4_MX && (j & 1) ? idesc_odd : idesc, sa + 4 * c,
                             sb + 4 * row_blocks * c, (s | j) != 0);
           }
-          symm::tc_commit(&bar.empty[st]);
+          if (slots != stages) pair_commit_own(&bar.sfree[slot]);
+          pair_commit(&bar.empty[st]);
         }
         if (++st == stages) st = 0, ph ^= 1;
+        if (++slot == slots) slot = 0, sph ^= 1;
       }
-      if (ok && elected) symm::tc_commit(&bar.tfull[buf]);
+      if (ok && elected) pair_commit(&bar.tfull[buf]);
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-    if (elected) symm::tc_commit(&bar.drain);
+    if (elected) pair_commit_own(&bar.drain);
     symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
-  } else if (warp < 10) {  // ----------------------------------- epilogue
+  } else if (warp >= 2 && warp < 10) {  // ---------------------- epilogue
     // Two warps to each 32 TMEM lanes, which take turns at the chunks of rows.
     const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
     uint8_t* mine = smem + kRingBytes + (warp - 2) * kStageWarp;
     const float gx = a.gx ? *a.gx : 1.f;
     uint32_t seg = 0;
-    for (uint32_t i = blockIdx.x; i < tiles; i += gridDim.x, ++seg) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
-      const uint32_t buf = seg & 1, f = t.col * kBM + 32 * q;
+    for (uint32_t i = first; i < tiles; i += step, ++seg) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
+      const uint32_t buf = seg & 1, f = (2 * t.col + rank) * kBM + 32 * q;
       const uint32_t width = f < a.m ? a.m - f : 0;  // features from f on that are there
       const float scale = a.gw ? gx * a.gw[t.e] : gx;
       const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
@@ -520,20 +533,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       symm::tc_fence_before();
       __syncwarp();
-      if (lane == 0) symm::mbar_arrive(&bar.tempty[buf]);  // the accumulator is free again
+      if (lane == 0) arrive_first(&bar.tempty[buf]);  // the accumulator is free again
     }
-  } else {  // ---------------------------------------------- scales' order
+  } else if (warp >= 10) {  // ------------------------------ scales' order
     // Lane l of warp w takes row 32 (l % 4) + 8 w + l / 4 of a block of 128: its
     // words are neighbours of the other lanes' in the tile.
-    const uint32_t w = (uint32_t)warp - 10, r = 32 * (lane % 4) + 8 * w + lane / 4;
+    const uint32_t turn = (uint32_t)(warp - 10) / 4, w = (uint32_t)(warp - 10) % 4;
+    const uint32_t r = 32 * (lane % 4) + 8 * w + lane / 4;
     uint32_t st = 0, ph = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-      const Tile t = tile_at(table, i, a.E, a.ncol);
+    for (uint32_t i = first; ok && i < tiles; i += step) {
+      const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t rows = t.bt;
       for (uint32_t s = 0; s < slices; ++s) {
-        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
-        uint8_t* at = smem + st * stage_bytes;
+        const uint32_t now = st, phase = ph;
+        if (++st == stages) st = 0, ph ^= 1;
+        // A stage belongs to one group of four warps, which waits for every phase of its
+        // barrier: of one that it skipped, it could take the phase before for the next.
+        if ((now & 1) != turn) continue;
+        if (!(ok = symm::mbar_wait_warp(&bar.full[now], phase, a.budget_ns, a.ctl))) break;
+        uint8_t* at = smem + now * stage_bytes;
         const uint4* from = reinterpret_cast<const uint4*>(at + raw);
         uint32_t* to = reinterpret_cast<uint32_t*>(at + tiled);
         const uint32_t word = 4 * (8 * w + lane / 4) + lane % 4;
@@ -550,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         symm::fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) symm::mbar_arrive(&bar.placed[st]);
-        if (++st == stages) st = 0, ph ^= 1;
+        if (lane == 0) arrive_first(&bar.placed[now]);
       }
     }
     if (!ok && lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -7);
@@ -559,9 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   symm::tc_fence_before();
   __syncthreads();
+  pair_sync();  // the other CTA's MMAs, arrivals and reads of TMEM are over too
   if (warp == 1) {
     symm::tc_fence_after();
-    symm::tmem_dealloc(tmem, kTmemCols);
+    pair_tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -609,32 +628,37 @@ int make_map(const char* what, CUtensorMap* map, const void* base, uint64_t inne
 }
 
 struct Maps {
-  CUtensorMap w, ws, x64, x16, xs, xs48;
+  CUtensorMap w, ws, x64, x16, xs, xs32;
 };
 
 template <typename T, int FMT>
 int launch_product(const Maps& m, const Fp4Args& a, cudaStream_t s) {
   static std::mutex mu;
-  static bool done[64] = {};
+  static unsigned known[64] = {};  // CTA pairs that are resident at once
   int dev = 0;
   int rc = cuda_check(cudaGetDevice(&dev), "moe_fp4_expert_matmul: device");
   if (rc) return rc;
+  unsigned pairs = 0;
   {
     std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-      rc = cuda_check(cudaFuncSetAttribute((const void*)fp4_kernel<T, FMT>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep) pairs = known[dev];
+    if (!pairs) {
+      const void* kernel = (const void*)fp4_kernel<T, FMT>;
+      rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)kSmemBytes),
                       "moe_fp4_expert_matmul: kernel set-up");
       if (rc) return rc;
-      if (dev >= 0 && dev < 64) done[dev] = true;
+      pairs = resident_pairs(kernel, kThreads, kSmemBytes);
+      if (keep) known[dev] = pairs;
     }
   }
   // at most one partly filled block of rows for each expert that has rows
-  const uint64_t most = (uint64_t)a.ncol * std::min<uint64_t>(a.n, a.n / Scales<FMT>::kMaxRows + a.E);
-  const unsigned grid = (unsigned)std::min<uint64_t>((uint64_t)std::max(sm_count(), 1), most);
-  return moe::launch("moe_fp4_expert_matmul", fp4_kernel<T, FMT>, grid, kThreads, kSmemBytes, s,
-                     m.w, m.ws, m.x64, m.x16, m.xs, m.xs48, a);
+  const uint64_t most =
+      (uint64_t)a.npair * std::min<uint64_t>(a.n, a.n / Scales<FMT>::kMaxRows + a.E);
+  return launch_pairs("moe_fp4_expert_matmul", fp4_kernel<T, FMT>,
+                      (unsigned)std::min<uint64_t>(pairs, most), kThreads, kSmemBytes, s, m.w,
+                      m.ws, m.x64, m.x16, m.xs, m.xs32, a);
 }
 
 template <typename T, int FMT>
@@ -768,14 +792,14 @@ extern "C" int moe_fp4_expert_matmul(symm_heap_t* heap, const void* xc, size_t l
       rc = make_map(what, &mp.xs, xs, sb, n, 0, ldxs, 16,
                     fmt == SYMM_FP4_MX ? Scales<SYMM_FP4_MX>::kMaxRows
                                        : Scales<SYMM_FP4_NV>::kMaxRows);
-    if (!rc) rc = make_map(what, &mp.xs48, xs, sb, n, 0, ldxs, 16, 48);
+    if (!rc) rc = make_map(what, &mp.xs32, xs, sb, n, 0, ldxs, 16, 32);
     if (rc) return rc;
     cudaStream_t s = as_stream(stream);
     rc = ensure_ctrl(heap, s);
     if (rc) return rc;
     Fp4Args a{};
     a.counts = counts, a.gx = gx, a.gw = gw, a.n = (uint32_t)n, a.E = (uint32_t)E;
-    a.m = (uint32_t)m, a.k = (uint32_t)k, a.ncol = ((uint32_t)m + kBM - 1) / kBM;
+    a.m = (uint32_t)m, a.k = (uint32_t)k, a.npair = ((uint32_t)m + 2 * kBM - 1) / (2 * kBM);
     a.y = y, a.ldy = ldy, a.vec = ldy % 8 == 0 && moe::aligned(y, 16);
     a.budget_ns = heap->spin_budget;
     a.ctl = reinterpret_cast<Control*>(heap->base);
