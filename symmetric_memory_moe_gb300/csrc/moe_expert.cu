@@ -43,7 +43,7 @@ using namespace symm_host;
 namespace {
 
 constexpr uint32_t kThreads = 320, kEpilogue = 256;
-constexpr uint32_t kMaxRows = 256, kStep = 32;           // rows of a tile: the N side of a pair
+constexpr uint32_t kMaxRows = 256;                       // rows of a tile: the N side of a pair
 constexpr uint32_t kBK = 64;
 constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
 constexpr uint32_t kRingBytes = 192 * 1024;              // six stages of 128 features, 128 rows
@@ -196,12 +196,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<kMaxRows, kStep> table;
+  __shared__ Table table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
   moe::let_next_start();
   moe::wait_for_earlier();
-  const bool good = lay_out(table, a.counts, a.E, a.n);
+  const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0;
   const Ring ring = ring_of(uniform(good ? table.most / 2 : 16));
@@ -441,12 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<kMaxRows, kStep> table;
+  __shared__ Table table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
   moe::let_next_start();
   moe::wait_for_earlier();
-  const bool good = lay_out(table, a.counts, a.E, a.n);
+  const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, 1, 1);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   const uint32_t per = a.mb * a.nb, tiles = good ? a.E * per : 0;
   const uint32_t tmem = uniform(bar.tmem);
@@ -674,8 +674,8 @@ int rows_product(const char* what, const void* x, size_t ldx, const void* w, uin
   if (!rc) rc = make_map(what, &m16, x, FMT, a.k, a.n, 0, ldx, 16);
   if (rc) return rc;
   a.npair = (a.m + (KIND == kGated ? 127 : 255)) / (KIND == kGated ? 128 : 256);
-  // at most one partly filled block of rows for each expert that has rows
-  const uint64_t most = (uint64_t)a.npair * std::min<uint64_t>(a.n, a.n / kMaxRows + a.E);
+  // at most one partly filled block of rows, 64 at the least, for each expert that has rows
+  const uint64_t most = (uint64_t)a.npair * std::min<uint64_t>(a.n, a.n / 64 + a.E);
   return launch_pairs(what, rows_kernel<FMT, KIND>, (unsigned)std::min<uint64_t>(pairs, most),
                       kThreads, kSmemBytes, s, mw, m64, m16, a);
 }

@@ -17,35 +17,41 @@ enum { kErrRange = -5 };
 
 // Expert e's rows are off[e] .. off[e + 1] - 1, its blocks of rows are numbered
 // blocks[e] .. blocks[e + 1] - 1 among all experts' (times the column blocks:
-// its tiles).  A block has at most MAX rows, in whole steps of STEP.
-template <uint32_t MAX, uint32_t STEP>
+// its tiles).  A block has at most `cap` rows.
 struct Table {
   uint32_t off[kMaxExperts + 1], blocks[kMaxExperts + 1];
-  uint32_t warp_rows[kMaxWarps], warp_blocks[kMaxWarps], warp_most[kMaxWarps];
+  uint32_t warp_rows[kMaxWarps], warp_blocks[3][kMaxWarps], warp_most[kMaxWarps];
+  uint32_t cap;
   uint32_t most;  // rows of the largest block, in whole steps
 };
+constexpr uint32_t kStep = 32;  // of a tile's rows: what a pair's MMAs take
 
-template <uint32_t MAX>
-__device__ __forceinline__ uint32_t blocks_of(uint32_t rows) {
-  return (rows + MAX - 1) / MAX;
+__device__ __forceinline__ uint32_t in_steps(uint32_t rows) {
+  return (rows + kStep - 1) / kStep * kStep;
+}
+__device__ __forceinline__ uint32_t blocks_of(uint32_t rows, uint32_t cap) {
+  return (rows + cap - 1) / cap;
 }
 // Rows of each of an expert's blocks (the last one may have fewer, never none), as
 // even as whole steps allow.
-template <uint32_t MAX, uint32_t STEP>
-__device__ __forceinline__ uint32_t block_rows(uint32_t rows) {
-  const uint32_t nb = blocks_of<MAX>(rows);
-  return nb ? ((rows + nb - 1) / nb + STEP - 1) / STEP * STEP : 0;
+__device__ __forceinline__ uint32_t block_rows(uint32_t rows, uint32_t cap) {
+  const uint32_t nb = blocks_of(rows, cap);
+  return nb ? in_steps((rows + nb - 1) / nb) : 0;
+}
+// The caps to choose from.
+__device__ __forceinline__ uint32_t cap_of(uint32_t i, uint32_t max_rows) {
+  return i == 0 ? max_rows : i == 1 ? 128 : 64;
 }
 
 // Fills the table from the counts (NULL: one expert with all n rows), by all
-// threads of the block.  False where a count is negative or they exceed n.
-template <uint32_t MAX, uint32_t STEP>
-__device__ __forceinline__ bool lay_out(Table<MAX, STEP>& t, const int32_t* counts, uint32_t E,
-                                        uint32_t n) {
+// threads of the block; ncol column blocks and as many `pairs` at work decide on the
+// cap.  False where a count is negative or they exceed n.
+__device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_t E, uint32_t n,
+                                        uint32_t max_rows, uint32_t ncol, uint32_t pairs) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t per = (E + blockDim.x - 1) / blockDim.x, first = threadIdx.x * per;
   uint64_t sum = 0;  // of at most 1024 counts of at most n <= 2^24 each
-  uint32_t blocks = 0, most = 0;
+  uint32_t blocks[3] = {}, most = 0;
   bool bad = false;
   for (uint32_t e = first; e < min(E, first + per); ++e) {
     const int32_t c = counts ? counts[e] : (int32_t)n;
@@ -54,43 +60,72 @@ __device__ __forceinline__ bool lay_out(Table<MAX, STEP>& t, const int32_t* coun
       continue;
     }
     sum += (uint32_t)c;
-    blocks += blocks_of<MAX>((uint32_t)c);
-    most = max(most, block_rows<MAX, STEP>((uint32_t)c));
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i) blocks[i] += blocks_of((uint32_t)c, cap_of(i, max_rows));
+    most = max(most, (uint32_t)c);
   }
   bad |= sum > n;
   uint32_t rows = (uint32_t)min(sum, (uint64_t)n + 1);  // the whole sum stays below 2^33
-  const uint32_t own_rows = rows, own_blocks = blocks;
+  const uint32_t own_rows = rows, own_blocks[3] = {blocks[0], blocks[1], blocks[2]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t r = __shfl_up_sync(0xffffffffu, rows, o);
-    const uint32_t b = __shfl_up_sync(0xffffffffu, blocks, o);
-    if (lane >= (uint32_t)o) rows = min(rows + r, n + 1), blocks += b;
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    uint32_t b[3];
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i) b[i] = __shfl_up_sync(0xffffffffu, blocks[i], o);
+    if (lane >= (uint32_t)o) {
+      rows = min(rows + r, n + 1);
+#pragma unroll
+      for (uint32_t i = 0; i < 3; ++i) blocks[i] += b[i];
+    }
   }
-  if (lane == 31) t.warp_rows[warp] = rows, t.warp_blocks[warp] = blocks, t.warp_most[warp] = most;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    t.warp_rows[warp] = rows, t.warp_most[warp] = most;
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i) t.warp_blocks[i][warp] = blocks[i];
+  }
   __syncthreads();
-  uint32_t at = rows - own_rows, bt = blocks - own_blocks, all = 0, largest = 0;
+  uint32_t at = rows - own_rows, all = 0, all_blocks[3] = {}, before[3] = {}, largest = 0;
   for (uint32_t w = 0; w < blockDim.x / 32; ++w) {
-    if (w < warp) at += t.warp_rows[w], bt += t.warp_blocks[w];
+    if (w < warp) at += t.warp_rows[w];
     all = min(all + t.warp_rows[w], n + 1);
     largest = max(largest, t.warp_most[w]);
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i) {
+      if (w < warp) before[i] += t.warp_blocks[i][w];
+      all_blocks[i] += t.warp_blocks[i][w];
+    }
   }
   bad |= all > n;
   if (__syncthreads_or(bad)) return false;
+  // The cap with the least rounds of tiles, each as long as its rows and 64 more (the
+  // weights, that every block of rows reads again).
+  uint32_t which = 0, best = 0xffffffffu;
+#pragma unroll
+  for (uint32_t i = 0; i < 3; ++i) {
+    const uint32_t rounds = (all_blocks[i] * ncol + pairs - 1) / pairs;
+    const uint32_t cost = rounds * (min(cap_of(i, max_rows), in_steps(largest)) + 64);
+    if (cost < best) best = cost, which = i;
+  }
+  const uint32_t cap = cap_of(which, max_rows);
+  uint32_t bt = which == 0   ? before[0] + blocks[0] - own_blocks[0]
+                : which == 1 ? before[1] + blocks[1] - own_blocks[1]
+                             : before[2] + blocks[2] - own_blocks[2];
   for (uint32_t e = first; e < min(E, first + per); ++e) {
     t.off[e] = at, t.blocks[e] = bt;
     const uint32_t c = counts ? (uint32_t)counts[e] : n;
-    at += c, bt += blocks_of<MAX>(c);
-    if (e == E - 1) t.off[E] = at, t.blocks[E] = bt, t.most = largest;
+    at += c, bt += blocks_of(c, cap);
+    if (e == E - 1) t.off[E] = at, t.blocks[E] = bt;
   }
+  if (threadIdx.x == 0) t.cap = cap, t.most = min(cap, in_steps(largest));
   __syncthreads();
   return true;
 }
 
 // The expert whose blocks hold number b (below blocks[E]): the last one with
 // blocks[e] <= b.
-template <uint32_t MAX, uint32_t STEP>
-__device__ __forceinline__ uint32_t expert_of(const Table<MAX, STEP>& t, uint32_t b, uint32_t E) {
+__device__ __forceinline__ uint32_t expert_of(const Table& t, uint32_t b, uint32_t E) {
   uint32_t lo = 0, hi = E;  // blocks[lo] <= b < blocks[hi]
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) / 2;
@@ -106,19 +141,18 @@ struct Tile {
 // Tile i of ncol column blocks.  Up to eight blocks of rows share a column
 // block's weights one after another, then the next column block shares theirs:
 // what the SMs work on at a time is about as many rows as columns, which L2 holds.
-template <uint32_t MAX, uint32_t STEP>
-__device__ __forceinline__ Tile tile_at(const Table<MAX, STEP>& t, uint32_t i, uint32_t E,
-                                        uint32_t ncol) {
+__device__ __forceinline__ Tile tile_at(const Table& t, uint32_t i, uint32_t E, uint32_t ncol) {
   Tile o;
   o.e = expert_of(t, i / ncol, E);
-  const uint32_t c = t.off[o.e + 1] - t.off[o.e], nb = blocks_of<MAX>(c);
-  o.bt = block_rows<MAX, STEP>(c);
+  const uint32_t c = t.off[o.e + 1] - t.off[o.e], nb = blocks_of(c, t.cap);
+  const uint32_t full = block_rows(c, t.cap);
   const uint32_t local = i - t.blocks[o.e] * ncol, group = local / (8 * ncol);
   const uint32_t in = min(8u, nb - 8 * group), r = local - 8 * group * ncol;
   const uint32_t b = 8 * group + r % in;
   o.col = r / in;
-  o.row = t.off[o.e] + b * o.bt;
-  o.rows = min(o.bt, c - b * o.bt);
+  o.row = t.off[o.e] + b * full;
+  o.rows = min(full, c - b * full);
+  o.bt = in_steps(o.rows);
   return o;
 }
 

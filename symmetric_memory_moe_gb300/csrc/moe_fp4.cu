@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
-  __shared__ Table<S::kMaxRows, 32> table;
+  __shared__ Table table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   symm::tc_fence_after();
   moe::let_next_start();
   moe::wait_for_earlier();
-  const bool good = lay_out(table, a.counts, a.E, a.n);
+  const bool good = lay_out(table, a.counts, a.E, a.n, S::kMaxRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0, tmem = uniform(bar.tmem);
   const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -653,9 +653,8 @@ int launch_product(const Maps& m, const Fp4Args& a, cudaStream_t s) {
       if (keep) known[dev] = pairs;
     }
   }
-  // at most one partly filled block of rows for each expert that has rows
-  const uint64_t most =
-      (uint64_t)a.npair * std::min<uint64_t>(a.n, a.n / Scales<FMT>::kMaxRows + a.E);
+  // at most one partly filled block of rows, 64 at the least, for each expert that has rows
+  const uint64_t most = (uint64_t)a.npair * std::min<uint64_t>(a.n, a.n / 64 + a.E);
   return launch_pairs("moe_fp4_expert_matmul", fp4_kernel<T, FMT>,
                       (unsigned)std::min<uint64_t>(pairs, most), kThreads, kSmemBytes, s, m.w,
                       m.ws, m.x64, m.x16, m.xs, m.xs32, a);
