@@ -31,7 +31,8 @@
 // grad_kernel: a gradient of weights, dW_e = a_e^T b_e: 128 x 256 tiles, K the
 // expert's rows, both operands as stored (M- and N-major).  Rows of the next
 // expert that share the last 16-row step are zeroed in shared memory, in both
-// operands, before its MMAs: what they hold may be an infinity.
+// operands, before its MMAs: what they hold may be an infinity.  Both gradients are one
+// launch.
 #include <algorithm>
 #include <string>
 
@@ -124,7 +125,7 @@ __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
   if (warp == 1) pair_tmem_alloc(&b.tmem, 2 * kAccCols);
   symm::tc_fence_before();
   __syncthreads();
-  pair_sync();
+  pair_arrive();  // whoever touches the other CTA's barriers waits first
   symm::tc_fence_after();
 }
 __device__ __forceinline__ void leave_cta(Barriers& b, int warp) {
@@ -198,11 +199,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Barriers bar;
   __shared__ Table table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 32) prefetch_map(&map_w), prefetch_map(&map_x64), prefetch_map(&map_x16);
   set_up_cta(bar, warp);
   moe::let_next_start();
   moe::wait_for_earlier();
   const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
+  pair_wait();
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0;
   const Ring ring = ring_of(uniform(good ? table.most / 2 : 16));
   const uint32_t slices = (a.k + ring.deep * kBK - 1) / (ring.deep * kBK);
@@ -423,21 +426,47 @@ __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// One launch computes up to two gradients (of the same rows): tiles of the first, then
+// of the second.
+struct GradPart {
+  uint32_t m, nf;   // out [E][m][nf]
+  uint32_t nb, per; // blocks of 256 columns, blocks of an expert's gradient
+};
 struct GradArgs {
   const int32_t* counts;
-  uint32_t n, E, m, nf;  // out [E][m][nf]
-  uint32_t mb, nb;       // blocks of 256
+  uint32_t n, E;
+  GradPart part[2];
   uint64_t budget_ns;
   Control* ctl;
 };
+struct GradTile {
+  uint32_t which, e, m0, n0, m, nf;
+};
+// An expert's blocks of 256 columns one after another, then the next 256 rows.
+__device__ __forceinline__ GradTile grad_tile(const GradArgs& a, uint32_t i) {
+  GradTile t;
+  const uint32_t tiles0 = a.E * a.part[0].per;
+  t.which = i >= tiles0;
+  if (t.which) i -= tiles0;
+  const uint32_t per = t.which ? a.part[1].per : a.part[0].per;
+  const uint32_t nb = t.which ? a.part[1].nb : a.part[0].nb;
+  t.e = i / per;
+  const uint32_t r = i - t.e * per, mb = r / nb;
+  t.m0 = mb * 256, t.n0 = (r - mb * nb) * 256;
+  t.m = t.which ? a.part[1].m : a.part[0].m, t.nf = t.which ? a.part[1].nf : a.part[0].nf;
+  return t;
+}
 constexpr uint32_t kGradStage = 4 * 64 * 128;  // two boxes of A, two of B: 64 rows x 64 features
 constexpr uint32_t kGradStages = kRingBytes / kGradStage;
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
-    grad_kernel(const __grid_constant__ CUtensorMap map_a,
-                const __grid_constant__ CUtensorMap map_b,
-                const __grid_constant__ CUtensorMap map_out, const GradArgs a) {
+    grad_kernel(const __grid_constant__ CUtensorMap map_a0,
+                const __grid_constant__ CUtensorMap map_b0,
+                const __grid_constant__ CUtensorMap map_out0,
+                const __grid_constant__ CUtensorMap map_a1,
+                const __grid_constant__ CUtensorMap map_b1,
+                const __grid_constant__ CUtensorMap map_out1, const GradArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (symm::smem_addr(smem_raw) & 1023u)) & 1023u);
   __shared__ Barriers bar;
@@ -448,19 +477,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   moe::wait_for_earlier();
   const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, 1, 1);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
-  const uint32_t per = a.mb * a.nb, tiles = good ? a.E * per : 0;
+  pair_wait();
+  const uint32_t tiles = good ? a.E * (a.part[0].per + a.part[1].per) : 0;
   const uint32_t tmem = uniform(bar.tmem);
   const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
-  // Tile i: an expert's blocks of 256 columns one after another, then the next 256 rows.
 
   if (warp == 0) {  // ----------------------------------------- TMA producer
     const bool elected = symm::elect_one();
     uint32_t st = 0, ph = 1, it = 0;
     bool ok = true;
     for (uint32_t i = first; ok && i < tiles; i += step) {
-      const uint32_t e = i / per, m0 = i % per / a.nb * 256 + rank * kBM;
-      const uint32_t n0 = i % a.nb * 256 + rank * 128;
-      const uint32_t r0 = table.off[e], r1 = table.off[e + 1];
+      const GradTile t = grad_tile(a, i);
+      const CUtensorMap* map_a = t.which ? &map_a1 : &map_a0;
+      const CUtensorMap* map_b = t.which ? &map_b1 : &map_b0;
+      const uint32_t m0 = t.m0 + rank * kBM, n0 = t.n0 + rank * kBM;
+      const uint32_t r0 = table.off[t.e], r1 = table.off[t.e + 1];
       for (uint32_t r = r0; r < r1; r += 64) {
         if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * kGradStage;
@@ -468,10 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           symm::mbar_arrive_expect_tx(&bar.full[st], kGradStage);
 #pragma unroll
           for (uint32_t b = 0; b < 2; ++b)
-            symm::tma_load_2d(buf + b * 8192, &map_a, (int)(m0 + 64 * b), (int)r, &bar.full[st]);
+            symm::tma_load_2d(buf + b * 8192, map_a, (int)(m0 + 64 * b), (int)r, &bar.full[st]);
 #pragma unroll
           for (uint32_t b = 0; b < 2; ++b)
-            symm::tma_load_2d(buf + (2 + b) * 8192, &map_b, (int)(n0 + 64 * b), (int)r,
+            symm::tma_load_2d(buf + (2 + b) * 8192, map_b, (int)(n0 + 64 * b), (int)r,
                               &bar.full[st]);
         }
         ++it;
@@ -486,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t st = 0, ph = 0, seg = 0;
     bool ok = true;
     for (uint32_t i = first; ok && i < tiles; i += step) {
-      const uint32_t e = i / per, r0 = table.off[e], r1 = table.off[e + 1];
+      const uint32_t e = grad_tile(a, i).e, r0 = table.off[e], r1 = table.off[e + 1];
       if (r0 == r1) continue;  // the epilogue writes zeros
       const uint32_t buf = seg & 1;
       const uint32_t phase = ((seg >> 1) & 1) ^ 1u;
@@ -497,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* at = smem + st * kGradStage;
         const uint32_t left = min(64u, r1 - r), steps = (left + 15) / 16;
-        if (left % 16) {  // the next expert's rows in the last step: a line of all four boxes a turn
+        if (left % 16) {  // the next expert's rows in the last step: a line of the four boxes a turn
           uint8_t* line = at + (lane / 8) * 8192 + (lane % 8) * 16;
           for (uint32_t z = left; z < steps * 16; ++z)
             *reinterpret_cast<uint4*>(line + z * 128) = make_uint4(0, 0, 0, 0);
@@ -539,8 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool elected = symm::elect_one();
     uint32_t seg = 0;
     for (uint32_t i = first; i < tiles; i += step) {
-      const uint32_t e = i / per, n0 = i % a.nb * 256, buf = seg & 1;
-      const uint32_t m0 = i % per / a.nb * 256 + rank * kBM + 32 * q + 16 * turn;
+      const GradTile t = grad_tile(a, i);
+      const uint32_t e = t.e, n0 = t.n0, m0 = t.m0 + rank * kBM + 32 * q + 16 * turn;
+      const uint32_t m = t.m, nf = t.nf, buf = seg & 1;
       const bool any = table.off[e] != table.off[e + 1];
       if (any) {
         const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
@@ -552,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++seg;
       }
       const uint32_t taddr = tmem + ((32 * q + 16 * turn) << 16) + buf * kAccCols;
-      for (uint32_t c = 0; c < 256 && n0 + c < a.nf; c += 64) {
+      for (uint32_t c = 0; c < 256 && n0 + c < nf; c += 64) {
         uint32_t v[4][8];
         if (any) {
 #pragma unroll
@@ -563,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[0][j] = v[1][j] = v[2][j] = v[3][j] = 0;
         }
-        if (m0 >= a.m) continue;
+        if (m0 >= m) continue;
         uint32_t pk[2][8];
 #pragma unroll
         for (uint32_t o = 0; o < 2; ++o)
@@ -585,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         symm::fence_proxy_async_shared();
         __syncwarp();
         if (elected) {
-          symm::tma_store_3d(&map_out, mine, (int)(n0 + c), (int)m0, (int)e);
+          symm::tma_store_3d(t.which ? &map_out1 : &map_out0, mine, (int)(n0 + c), (int)m0, (int)e);
           bulk_commit();
         }
       }
@@ -680,22 +712,37 @@ int rows_product(const char* what, const void* x, size_t ldx, const void* w, uin
                       kThreads, kSmemBytes, s, mw, m64, m16, a);
 }
 
-// dW [E][m][nf] = a_e^T b_e of the rows a [n][m] and b [n][nf].
+// A gradient dW [E][m][nf] = a_e^T b_e of the rows a [n][m] and b [n][nf]; out NULL: none.
+struct WeightGrad {
+  const void *a, *b;
+  size_t lda, ldb;
+  void* out;
+  uint32_t m, nf;
+};
 template <int FMT>
-int weight_grad(const char* what, const void* a, size_t lda, const void* b, size_t ldb, void* out,
-                uint32_t m, uint32_t nf, const ExpertArgs& x, unsigned pairs, cudaStream_t s) {
-  CUtensorMap ma, mb, mo;
-  int rc = make_map(what, &ma, a, FMT, m, x.n, 0, lda, 64);
-  if (!rc) rc = make_map(what, &mo, out, FMT, nf, m, x.E, nf, 16);
-  if (!rc) rc = make_map(what, &mb, b, FMT, nf, x.n, 0, ldb, 64);
-  if (rc) return rc;
+int weight_grads(const char* what, const WeightGrad (&w)[2], const ExpertArgs& x, unsigned pairs,
+                 cudaStream_t s) {
+  CUtensorMap maps[2][3] = {};
   GradArgs g{};
-  g.counts = x.counts, g.n = x.n, g.E = x.E, g.m = m, g.nf = nf;
-  g.mb = (m + 255) / 256, g.nb = (nf + 255) / 256;
-  g.budget_ns = x.budget_ns, g.ctl = x.ctl;
-  const uint64_t tiles = (uint64_t)x.E * g.mb * g.nb;
+  uint64_t tiles = 0;
+  int rc = SYMM_OK, parts = 0;
+  for (const WeightGrad& p : w) {
+    if (!p.out || rc) continue;
+    CUtensorMap* m = maps[parts];
+    rc = make_map(what, &m[0], p.a, FMT, p.m, x.n, 0, p.lda, 64);
+    if (!rc) rc = make_map(what, &m[1], p.b, FMT, p.nf, x.n, 0, p.ldb, 64);
+    if (!rc) rc = make_map(what, &m[2], p.out, FMT, p.nf, p.m, x.E, p.nf, 16);
+    GradPart& to = g.part[parts++];
+    to.m = p.m, to.nf = p.nf, to.nb = (p.nf + 255) / 256;
+    to.per = (p.m + 255) / 256 * to.nb;
+    tiles += (uint64_t)x.E * to.per;
+  }
+  if (rc || !parts) return rc;
+  if (parts == 1) std::copy(maps[0], maps[0] + 3, maps[1]);  // no tile uses them
+  g.counts = x.counts, g.n = x.n, g.E = x.E, g.budget_ns = x.budget_ns, g.ctl = x.ctl;
   return launch_pairs(what, grad_kernel<FMT>, (unsigned)std::min<uint64_t>(pairs, tiles), kThreads,
-                      kSmemBytes, s, ma, mb, mo, g);
+                      kSmemBytes, s, maps[0][0], maps[0][1], maps[0][2], maps[1][0], maps[1][1],
+                      maps[1][2], g);
 }
 
 // What both entry points check of their sizes, weights and type.
@@ -749,9 +796,11 @@ int backward(const char* what, const void* dy, size_t lddy, const void* x, size_
       rc = rows_product<FMT, kDx>(what, dgu, 2 * (size_t)F, w_gu, D, 2 * F, a, pairs, s);
     }
   }
-  if (!rc && dw_d) rc = weight_grad<FMT>(what, h, F, dy, lddy, dw_d, F, D, a, pairs, s);
-  if (!rc && dw_gu)
-    rc = weight_grad<FMT>(what, x, ldx, dgu, 2 * (size_t)F, dw_gu, D, 2 * F, a, pairs, s);
+  if (!rc)
+    rc = weight_grads<FMT>(what,
+                           {{h, dy, (size_t)F, lddy, dw_d, (uint32_t)F, (uint32_t)D},
+                            {x, dgu, ldx, 2 * (size_t)F, dw_gu, (uint32_t)D, 2 * (uint32_t)F}},
+                           a, pairs, s);
   return rc;
 }
 

@@ -371,6 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Barriers bar;
   __shared__ Table table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 64) {
+    prefetch_map(&map_w), prefetch_map(&map_ws), prefetch_map(&map_x64), prefetch_map(&map_x16);
+    prefetch_map(&map_xs), prefetch_map(&map_xs32);
+  }
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
       symm::mbar_init(&bar.full[s], 1);
@@ -388,12 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) pair_tmem_alloc(&bar.tmem, kTmemCols);
   symm::tc_fence_before();
   __syncthreads();
-  pair_sync();
+  pair_arrive();  // whoever touches the other CTA's barriers waits first
   symm::tc_fence_after();
   moe::let_next_start();
   moe::wait_for_earlier();
   const bool good = lay_out(table, a.counts, a.E, a.n, S::kMaxRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
+  pair_wait();
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0, tmem = uniform(bar.tmem);
   const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
   const uint32_t slices = (a.k + kSlice - 1) / kSlice;
