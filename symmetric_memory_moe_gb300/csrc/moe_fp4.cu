@@ -31,6 +31,11 @@
 // What bounds it is the way of a stage around its ring (copies, placing, MMAs and back,
 // some 3000 cycles for 4 or 5 stages), then the issue of a slice (12 or 6 tcgen05.cp
 // and 4 MMAs from one thread, 450 cycles); the MMAs of a slice are 330.
+//
+// Measured.  32768 x 7168 in bf16, MX: 105 us to codes (85 % of the copy rate), 99 back.
+// Product, NV, 32 experts, 1024 rows each: 7168 x 4096 490 us (3.9 PFLOP/s), 2048 x 7168
+// 317 us (3.0 PFLOP/s; 584 with 2-byte stores from single CTAs); 64 rows, 7168 x 4096: 75 us,
+// the weights at 90 % of the copy rate.
 #include <algorithm>
 #include <string>
 
@@ -184,8 +189,8 @@ __device__ __forceinline__ uint32_t encode(float (&f)[8], uint32_t top, float g,
   return finite ? to_codes(f) : 0;
 }
 
-// Four vectors (two with an activation, whose rows are two) in flight a thread: one
-// left a third of the bandwidth unused (188 us for 32768 x 7168 in bf16; now see the head).
+// Four vectors (two with an activation, whose rows are two) in flight a thread: 105 us for
+// 32768 x 7168 in bf16, where one took 188.
 template <typename T, int FMT, bool GATED>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
   constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;  // of a block
