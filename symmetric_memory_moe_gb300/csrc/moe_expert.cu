@@ -54,6 +54,7 @@ namespace {
 
 constexpr uint32_t kThreads = 320, kEpilogue = 256;
 constexpr uint32_t kMaxRows = 256;                       // rows of a tile: the N side of a pair
+constexpr uint32_t kExtraRows = 64;                      // 1225 rows: 19.4 us so, 26.3 with one cap
 constexpr uint32_t kBK = 64;
 constexpr uint32_t kATile = kBM * kBK * 2;               // 16 KB
 constexpr uint32_t kRingBytes = 192 * 1024;              // six stages of 128 features, 128 rows
@@ -212,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   set_up_cta(bar, warp);
   moe::let_next_start();
   moe::wait_for_earlier();
-  const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, a.npair, gridDim.x / 2);
+  const bool good =
+      lay_out(table, a.counts, a.E, a.n, kMaxRows, kExtraRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   pair_wait();
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0;
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   set_up_cta(bar, warp);
   moe::let_next_start();
   moe::wait_for_earlier();
-  const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, 1, 1);
+  const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, 0, 1, 1);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   pair_wait();
   const uint32_t tiles = good ? a.E * (a.part[0].per + a.part[1].per) : 0;

@@ -11,7 +11,7 @@ namespace experts {
 using symm::Control;
 
 constexpr uint32_t kBM = 128;          // features of a tile: the M side
-constexpr uint32_t kMaxWarps = 18;     // of a block
+constexpr uint32_t kMaxWarps = 14;     // of a block
 constexpr uint32_t kMaxExperts = SYMM_MOE_MAX_EXPERTS;
 enum { kErrRange = -5 };
 
@@ -47,7 +47,8 @@ __device__ __forceinline__ uint32_t cap_of(uint32_t i, uint32_t max_rows) {
 // threads of the block; ncol column blocks and as many `pairs` at work decide on the
 // cap.  False where a count is negative or they exceed n.
 __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_t E, uint32_t n,
-                                        uint32_t max_rows, uint32_t ncol, uint32_t pairs) {
+                                        uint32_t max_rows, uint32_t extra, uint32_t ncol,
+                                        uint32_t pairs) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t per = (E + blockDim.x - 1) / blockDim.x, first = threadIdx.x * per;
   uint64_t sum = 0;  // of at most 1024 counts of at most n <= 2^24 each
@@ -99,13 +100,13 @@ __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_
   }
   bad |= all > n;
   if (__syncthreads_or(bad)) return false;
-  // The cap with the least rounds of tiles, each as long as its rows and 64 more (the
-  // weights, that every block of rows reads again).
+  // The cap with the least rounds of tiles, each as long as its rows and `extra` more
+  // (the weights, that every block of rows reads again, and what a slice costs besides).
   uint32_t which = 0, best = 0xffffffffu;
 #pragma unroll
   for (uint32_t i = 0; i < 3; ++i) {
     const uint32_t rounds = (all_blocks[i] * ncol + pairs - 1) / pairs;
-    const uint32_t cost = rounds * (min(cap_of(i, max_rows), in_steps(largest)) + 64);
+    const uint32_t cost = rounds * (min(cap_of(i, max_rows), in_steps(largest)) + extra);
     if (cost < best) best = cost, which = i;
   }
   const uint32_t cap = cap_of(which, max_rows);
@@ -172,14 +173,14 @@ __device__ __forceinline__ uint64_t drain_ns(uint64_t budget_ns) {
   return max(budget_ns, (uint64_t)1000000000);
 }
 
-// Whether p holds in any thread of the epilogue (a barrier of its `threads`).
-__device__ __forceinline__ bool any_of(bool p, uint32_t threads) {
+// Whether p holds in any of a group's `threads` (barrier `id` of theirs; 1: the epilogue's).
+__device__ __forceinline__ bool any_of(bool p, uint32_t threads, uint32_t id = 1) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, %3, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(threads)
+      : "r"((uint32_t)p), "r"(threads), "r"(id)
       : "memory");
   return r != 0;
 }

@@ -24,17 +24,17 @@
 //   warp 1     MMA issuer (first CTA): copies a slice's scales from shared memory
 //              into TMEM (tcgen05.cp) and issues its four tcgen05.mma, K 64
 //   warps 2-9  epilogue, as in moe_expert.cu
-//   warps 10-17  scales as they lie beside the codes (a row's one after another) into
+//   warps 10-13  scales as they lie beside the codes (a row's one after another) into
 //              the order that TMEM takes: 4 scales of each of 128 rows, row r at
-//              word r / 32 of 16-byte line r % 32.  Four warps to a stage, in turns.
+//              word r / 32 of 16-byte line r % 32, in the place where they landed
 // 192 rows (NV: 160), not 256: two accumulators and four slots of scales fill TMEM.
 // What bounds it is the way of a stage around its ring (copies, placing, MMAs and back,
-// some 3000 cycles for 4 or 5 stages), then the issue of a slice (12 or 6 tcgen05.cp
+// some 3000 cycles for 6 stages), then the issue of a slice (12 or 6 tcgen05.cp
 // and 4 MMAs from one thread, 450 cycles); the MMAs of a slice are 330.
 //
 // Measured.  32768 x 7168 in bf16, MX: 105 us to codes (85 % of the copy rate), 99 back.
-// Product, NV, 32 experts, 1024 rows each: 7168 x 4096 490 us (3.9 PFLOP/s), 2048 x 7168
-// 317 us (3.0 PFLOP/s; 584 with 2-byte stores from single CTAs); 64 rows, 7168 x 4096: 75 us,
+// Product, NV, 32 experts, 1024 rows each: 7168 x 4096 452 us (4.25 PFLOP/s), 2048 x 7168
+// 306 us (3.15 PFLOP/s; 584 with 2-byte stores from single CTAs); 64 rows, 7168 x 4096: 75 us,
 // the weights at 90 % of the copy rate.
 #include <algorithm>
 #include <string>
@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const Dequant
 }
 
 // ------------------------------------------------------------ fp4_kernel --
-constexpr uint32_t kThreads = 576, kEpilogue = 256;
+constexpr uint32_t kThreads = 448, kEpilogue = 256;
+constexpr uint32_t kExtraRows = 256;                 // 64 chose 128 rows, 474 us for MX's 418
 constexpr uint32_t kSlice = 256;                     // values of K: a row of 128 bytes
 constexpr uint32_t kATile = kBM * 128;               // 16 KB
 constexpr uint32_t kARaw = kBM * 16;                 // its scales, 16 bytes a row
@@ -401,17 +402,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   symm::tc_fence_after();
   moe::let_next_start();
   moe::wait_for_earlier();
-  const bool good = lay_out(table, a.counts, a.E, a.n, S::kMaxRows, a.npair, gridDim.x / 2);
+  const bool good =
+      lay_out(table, a.counts, a.E, a.n, S::kMaxRows, kExtraRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
   pair_wait();
   const uint32_t tiles = good ? table.blocks[a.E] * a.npair : 0, tmem = uniform(bar.tmem);
   const uint32_t rank = pair_rank(), first = blockIdx.x / 2, step = gridDim.x / 2;
   const uint32_t slices = (a.k + kSlice - 1) / kSlice;
-  // A stage: codes of A and B, their scales as loaded (A, B), and as TMEM takes them.
+  // A stage: codes of A and B, and their scales: as loaded (A, B), then as TMEM takes them.
   const uint32_t most = uniform(good ? table.most / 2 : 16);
-  const uint32_t raw = kATile + most * 128;
-  const uint32_t tiled = raw + kARaw + (most <= 16 ? 32 : S::kMaxRows) * 16;
-  const uint32_t stage_bytes = (tiled + S::kTiles * 512 * 3 + 1023) / 1024 * 1024;
+  const uint32_t raw = kATile + most * 128;  // where its scales are
+  const uint32_t stage_bytes =
+      raw + max(kARaw + (most <= 16 ? 32 : S::kMaxRows) * 16, S::kTiles * 512 * 3);
   // In TMEM two accumulators, then slots of a slice's scales: one for each stage, which
   // is free when the stage is, or as many as fit, each with a barrier of its own.
   const uint32_t acc_cols = 2 * most, row_blocks = acc_cols > 128 ? 2 : 1;
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t xd = symm::sw128_kmajor_desc(at + kATile);
         if (elected) {
           // A's tiles in K order; B's row blocks, one or two, side by side in K order
-          const uint64_t sd = scales_desc(at + tiled);
+          const uint64_t sd = scales_desc(at + raw);
 #pragma unroll
           for (uint32_t c = 0; c < S::kTiles; ++c) copy_scales(sa + 4 * c, sd + 32 * c);
           if (row_blocks == 1) {
@@ -548,38 +550,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 10) {  // ------------------------------ scales' order
     // Lane l of warp w takes row 32 (l % 4) + 8 w + l / 4 of a block of 128: its
     // words are neighbours of the other lanes' in the tile.
-    const uint32_t turn = (uint32_t)(warp - 10) / 4, w = (uint32_t)(warp - 10) % 4;
-    const uint32_t r = 32 * (lane % 4) + 8 * w + lane / 4;
+    const uint32_t w = (uint32_t)warp - 10, r = 32 * (lane % 4) + 8 * w + lane / 4;
     uint32_t st = 0, ph = 0;
     bool ok = true;
     for (uint32_t i = first; ok && i < tiles; i += step) {
       const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t rows = t.bt;
       for (uint32_t s = 0; s < slices; ++s) {
-        const uint32_t now = st, phase = ph;
-        if (++st == stages) st = 0, ph ^= 1;
-        // A stage belongs to one group of four warps, which waits for every phase of its
-        // barrier: of one that it skipped, it could take the phase before for the next.
-        if ((now & 1) != turn) continue;
-        if (!(ok = symm::mbar_wait_warp(&bar.full[now], phase, a.budget_ns, a.ctl))) break;
-        uint8_t* at = smem + now * stage_bytes;
+        ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl);
+        uint8_t* at = smem + st * stage_bytes;
         const uint4* from = reinterpret_cast<const uint4*>(at + raw);
-        uint32_t* to = reinterpret_cast<uint32_t*>(at + tiled);
+        uint32_t* to = reinterpret_cast<uint32_t*>(at + raw);
         const uint32_t word = 4 * (8 * w + lane / 4) + lane % 4;
         const bool odd = FMT == SYMM_FP4_MX && (s & 1);  // the second 8 bytes
+        uint4 v[3];  // of A's row, of B's first 128, of B's others
+        v[0] = from[r];
 #pragma unroll
-        for (uint32_t b = 0; b < 3; ++b) {  // A's rows, B's first 128, B's others
-          const uint32_t row = b == 2 ? 128 + r : r;
-          if (b && row >= rows) continue;
-          const uint4 v = from[b ? 128 + row : row];
-          const uint32_t x[4] = {odd ? v.z : v.x, odd ? v.w : v.y, v.z, v.w};
+        for (uint32_t b = 1; b < 3; ++b)
+          if (128 * b - 128 + r < rows) v[b] = from[128 * b + r];
+        // all four warps have read: the same bytes take the tiles.  One that gave up takes
+        // the others with it.
+        if (any_of(!ok, 128, 2)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (uint32_t b = 0; b < 3; ++b) {
+          if (b && 128 * b - 128 + r >= rows) continue;
+          const uint32_t x[4] = {odd ? v[b].z : v[b].x, odd ? v[b].w : v[b].y, v[b].z, v[b].w};
 #pragma unroll
           for (uint32_t c = 0; c < S::kTiles; ++c)
             to[128 * (b ? S::kTiles + 2 * c + b - 1 : c) + word] = x[c];
         }
         symm::fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) arrive_first(&bar.placed[now]);
+        if (lane == 0) arrive_first(&bar.placed[st]);
+        if (++st == stages) st = 0, ph ^= 1;
       }
     }
     if (!ok && lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -7);
