@@ -102,11 +102,13 @@ __device__ __forceinline__ bool lay_out(Table& t, const int32_t* counts, uint32_
   if (__syncthreads_or(bad)) return false;
   // The cap with the least rounds of tiles, each as long as its rows and `extra` more
   // (the weights, that every block of rows reads again, and what a slice costs besides).
-  uint32_t which = 0, best = 0xffffffffu;
+  uint32_t which = 0;
+  uint64_t best = ~0ull;
 #pragma unroll
   for (uint32_t i = 0; i < 3; ++i) {
     const uint32_t rounds = (all_blocks[i] * ncol + pairs - 1) / pairs;
-    const uint32_t cost = rounds * (min(cap_of(i, max_rows), in_steps(largest)) + extra);
+    const uint64_t cost =
+        (uint64_t)rounds * (min(cap_of(i, max_rows), in_steps(largest)) + extra);
     if (cost < best) best = cost, which = i;
   }
   const uint32_t cap = cap_of(which, max_rows);

@@ -56,7 +56,6 @@ struct QuantArgs {
   size_t ldc, lds;  // bytes
   const float* g;
   uint32_t n, k, kv;  // rows, values and vectors of 8 values of a row
-  int act;
 };
 
 // Vectors of rows [n][kv] in turn: this thread's next one is `step` vectors on.
@@ -191,9 +190,10 @@ __device__ __forceinline__ uint32_t encode(float (&f)[8], uint32_t top, float g,
 
 // Four vectors (two with an activation, whose rows are two) in flight a thread: 105 us for
 // 32768 x 7168 in bf16, where one took 188.
-template <typename T, int FMT, bool GATED>
+template <typename T, int FMT, int ACT>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
   constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;  // of a block
+  constexpr bool GATED = ACT != SYMM_ACT_NONE;
   constexpr int kFlight = GATED || sizeof(T) == 4 ? 2 : 4;
   moe::let_next_start();
   moe::wait_for_earlier();
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
         floats(r2[i], u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          f[j] = activate(a.act, f[j]) * u[j];
+          f[j] = activate(ACT, f[j]) * u[j];
           top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
         }
       } else {
@@ -677,16 +677,16 @@ int launch_product(const Maps& m, const Fp4Args& a, cudaStream_t s) {
 }
 
 template <typename T, int FMT>
-int launch_quantize(const QuantArgs& a, cudaStream_t s) {
-  return moe::launch("moe_fp4_quantize",
-                     a.act == SYMM_ACT_NONE ? quantize_kernel<T, FMT, false>
-                                            : quantize_kernel<T, FMT, true>,
-                     quant_grid(a.n, a.kv), kQuantThreads, 0, s, a);
+int launch_quantize(const QuantArgs& a, int act, cudaStream_t s) {
+  auto* kernel = act == SYMM_ACT_NONE   ? quantize_kernel<T, FMT, SYMM_ACT_NONE>
+                 : act == SYMM_ACT_SILU ? quantize_kernel<T, FMT, SYMM_ACT_SILU>
+                                        : quantize_kernel<T, FMT, SYMM_ACT_GELU>;
+  return moe::launch("moe_fp4_quantize", kernel, quant_grid(a.n, a.kv), kQuantThreads, 0, s, a);
 }
 template <typename T>
-int launch_quantize(int fmt, const QuantArgs& a, cudaStream_t s) {
-  return fmt == SYMM_FP4_MX ? launch_quantize<T, SYMM_FP4_MX>(a, s)
-                            : launch_quantize<T, SYMM_FP4_NV>(a, s);
+int launch_quantize(int fmt, int act, const QuantArgs& a, cudaStream_t s) {
+  return fmt == SYMM_FP4_MX ? launch_quantize<T, SYMM_FP4_MX>(a, act, s)
+                            : launch_quantize<T, SYMM_FP4_NV>(a, act, s);
 }
 template <typename T>
 int launch_dequantize(int fmt, const DequantArgs& a, cudaStream_t s) {
@@ -726,12 +726,12 @@ extern "C" int moe_fp4_quantize(const void* x, size_t ldx, int act, int dtype, i
     QuantArgs a{};
     a.x = x, a.ldx = ldx, a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales), a.ldc = ldc, a.lds = lds, a.g = gscale;
-    a.n = (uint32_t)n, a.k = (uint32_t)k, a.kv = (uint32_t)k / 8, a.act = act;
+    a.n = (uint32_t)n, a.k = (uint32_t)k, a.kv = (uint32_t)k / 8;
     if (fmt == SYMM_FP4_MX) a.g = nullptr;
     cudaStream_t s = as_stream(stream);
-    return dtype == SYMM_DTYPE_F32    ? launch_quantize<float>(fmt, a, s)
-           : dtype == SYMM_DTYPE_BF16 ? launch_quantize<__nv_bfloat16>(fmt, a, s)
-                                      : launch_quantize<__half>(fmt, a, s);
+    return dtype == SYMM_DTYPE_F32    ? launch_quantize<float>(fmt, act, a, s)
+           : dtype == SYMM_DTYPE_BF16 ? launch_quantize<__nv_bfloat16>(fmt, act, a, s)
+                                      : launch_quantize<__half>(fmt, act, a, s);
   });
 }
 
