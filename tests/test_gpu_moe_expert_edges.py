@@ -261,3 +261,58 @@ def test_gradients_are_differences(heap):
         # independent roundings of gu, h, dg, du and the gradient: 2^-8 of a term each at most,
         # 8 standard deviations of their sum; differences err by step^2
         assert (terms.sum() - want).abs() <= 8 * 5 * 2.0 ** -8 * terms.norm() + 1e-3
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("name,dt", [(None, "f16"), ("silu", "bf16"), (None, "f32")])
+def test_rows_of_a_wider_matrix(fmt, name, dt):
+    """x with rows further apart than they are long, what lies between never read."""
+    from test_gpu_moe_fp4 import CODES, FMTS, pack
+    k = 96
+    width = k if name is None else 2 * k
+    g = torch.Generator(device="cuda").manual_seed(k)
+    wide = torch.full((70, width + 40), float("nan"), device="cuda")
+    wide[:, :width] = torch.randn(70, width, generator=g, device="cuda")
+    wide = wide.to({"f16": torch.float16, "bf16": BF16, "f32": torch.float32}[dt])
+    alone, scales = pack(wide[:, :width].contiguous(), fmt, None, name)
+    c, s = torch.zeros_like(alone), torch.zeros_like(scales)
+    abi.moe_fp4_quantize(ptr(wide), width + 40, -1 if name is None else 0, CODES[dt], FMTS[fmt],
+                         None, 70, k, ptr(c), c.shape[1], ptr(s), s.shape[1])
+    torch.cuda.synchronize()
+    b = k // ref.BLOCK[fmt]
+    assert torch.equal(c[:, :k // 2], alone[:, :k // 2]) and torch.equal(s[:, :b], scales[:, :b])
+
+
+def test_host_threads_at_once():
+    """Four host threads with a stream, a heap and a workspace each."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    def job(j):
+        n, E, D, F = 200 + 90 * j, 1 + j, 128 + 64 * j, 72
+        h = TorchSymmHeap(1, 0)
+        i = make(n, E, D, F, "bf16", "even", seed=j)
+        y, gu = forward(h, i, "bf16", "silu", stream=torch.cuda.Stream())
+        o = [backward(h, i, gu, "bf16", "silu") for _ in range(3)]
+        h.close()
+        return i, y, o
+
+    with ThreadPoolExecutor(4) as ex:
+        done = list(ex.map(job, range(4)))
+    for i, y, o in done:
+        r = ref.ffn(i["x"], i["counts"], i["w_gu"], i["w_d"], "silu", U_OUT["bf16"], TINY["bf16"])
+        near(y, r["y"], r["ey"], "y")
+        assert all(torch.equal(o[0][k], x[k]) for x in o[1:] for k in x)
+
+
+def test_most_experts(heap):
+    """As many experts as there may be, one row each and none."""
+    i = make(512, 1024, 64, 32, "bf16", "even")
+    i["counts"] = (torch.arange(1024) % 2 == 1).to(torch.int32).cuda()
+    y, gu = forward(heap, i, "bf16", "silu")
+    r = ref.ffn(i["x"], i["counts"], i["w_gu"], i["w_d"], "silu", U_OUT["bf16"], TINY["bf16"])
+    near(y, r["y"], r["ey"], "y")
+    o = backward(heap, i, gu, "bf16", "silu")
+    g = ref.ffn_grad(i["dy"], i["x"], gu, i["counts"], i["w_gu"], i["w_d"], "silu", U_OUT["bf16"],
+                     TINY["bf16"])
+    for k in ("dx", "dw_gu", "dw_d"):
+        near(o[k], g[k], g["e" + k], k)
