@@ -171,10 +171,14 @@ __device__ __forceinline__ uint32_t encode(float (&f)[8], uint32_t top, float g,
                   : 0x7fu;
     const float unit = __fmul_rn(from_e4m3(byte), g);
     if (!(unit > 0.f)) return 0;
-    if (unit > 0x1p-100f && unit < 0x1p100f) {
-      // Markstein's theorem (1990): with y = RN(1 / b), q a neighbour of a / b and r = a -
-      // q b (exact by fma), RN(q + r y) is the correctly rounded a / b.  (Of a tiny a, r
-      // may underflow: its code is 0 either way.  -0 would become 0.)
+    // (largest quotients above 2^20 go by the division: near 2^128 q would be infinite and
+    // its remainder NaN, whose code is +6)
+    if (unit > 0x1p-100f && unit < 0x1p100f && __uint_as_float(top) < 0x1p20f * unit) {
+      // Markstein (1990): y = RN(1 / b), q = RN(a y), r = a - q b by fma; RN(q + r y) is the
+      // correctly rounded a / b.  q is within 1.5 ulp of a / b, and q + r y within 2^-24 of
+      // that before its rounding, which matters only next to a midpoint of two floats; there
+      // a float as near as q is half an ulp off and r is exact, the theorem's case.  (Of a
+      // tiny a, r may underflow: its code is 0 either way.  -0 would become 0.)
       const float y = __frcp_rn(unit);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
