@@ -354,14 +354,18 @@ def _run_own(s, c):
                            _ptr(s["scratch"]))
         return {k: s[k] for k in ("gu", "y")}
     k, fmt, kc, ks = c["k"], FORMATS[c["fmt"]], s["xc"].shape[1], s["xs"].shape[1]
+
+    def to_pack(g):  # blocks of 32 are packed without a tensor's own scale
+        return _ptr(g) if c["fmt"] == "nv" else None
+
     if c["op"] == "quant":
-        abi.moe_fp4_quantize(_ptr(s["x"]), k, ACTS["none"], dt, fmt, _ptr(s["gscale"]), n, k,
-                             _ptr(s["xc"]), kc, _ptr(s["xs"]), ks)
+        abi.moe_fp4_quantize(_ptr(s["x"]), k, ACTS["none"], dt, fmt, to_pack(s["gscale"]), n,
+                             k, _ptr(s["xc"]), kc, _ptr(s["xs"]), ks)
         abi.moe_fp4_dequantize(_ptr(s["xc"]), kc, _ptr(s["xs"]), ks, fmt, _ptr(s["gscale"]), n, k,
                                dt, _ptr(s["values"]), k)
         return dict(values=s["values"])
-    abi.moe_fp4_quantize(_ptr(s["x"]), s["x"].shape[1], ACTS[c["act"]], dt, fmt, _ptr(s["gx"]), n,
-                         k, _ptr(s["xc"]), kc, _ptr(s["xs"]), ks)
+    abi.moe_fp4_quantize(_ptr(s["x"]), s["x"].shape[1], ACTS[c["act"]], dt, fmt, to_pack(s["gx"]),
+                         n, k, _ptr(s["xc"]), kc, _ptr(s["xs"]), ks)
     abi.moe_fp4_expert_matmul(s["heap"].handle, _ptr(s["xc"]), kc, _ptr(s["xs"]), ks,
                               _ptr(s["wc"]), kc, _ptr(s["ws"]), ks, _ptr(s["counts"]),
                               _ptr(s["gx"]), _ptr(s["gw"]), fmt, dt, n, c["E"], k, c["m"],
