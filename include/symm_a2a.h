@@ -643,7 +643,9 @@ int moe_expert_ffn_backward(symm_heap_t *heap, const void *dy, size_t lddy, cons
  *         (SYMM_DTYPE_F16, _BF16 or _F32).  act SYMM_ACT_NONE: rows of k.
  *         Else rows of 2k, and what is packed is act(first k) * (last k) in 32
  *         bits: gu of the feed-forward becomes its second product's operand.
- * gscale  device float [1], positive (NULL allowed = 1; not read with MX).
+ * gscale  device float [1], positive (NULL allowed = 1).  NULL with MX, which has no
+ *         scale of the tensor's: the same number given to the way back would
+ *         multiply x by it.
  * codes, scales  device, 16-byte aligned as x; of a scale row, the k / 32 or
  *         k / 16 bytes are written.
  * 0 <= n <= 2^24, k a multiple of 32 in [32, 2^17].  n = 0 is a no-op.
@@ -653,8 +655,8 @@ int moe_fp4_quantize(const void *x, size_t ldx, int act, int dtype, int fmt, con
                      void *stream);
 
 /* And back: y [n] rows of k, ldy elements apart (a multiple of 8, 16-byte
- * aligned), of `dtype`: code * (s * gscale[0]) (gscale NULL allowed = 1, with
- * either format), rounded once.  Errors: SYMM_EINVAL, SYMM_ECUDA. */
+ * aligned), of `dtype`: code * (s * gscale[0]) (gscale NULL allowed = 1; with MX a
+ * factor on the way back alone), rounded once.  Errors: SYMM_EINVAL, SYMM_ECUDA. */
 int moe_fp4_dequantize(const void *codes, size_t ldc, const void *scales, size_t lds, int fmt,
                        const float *gscale, int n, int k, int dtype, void *y, size_t ldy,
                        void *stream);
@@ -668,7 +670,7 @@ int moe_fp4_dequantize(const void *codes, size_t ldc, const void *scales, size_t
  *         ldwc and ldws bytes apart.
  * counts  device int32 [E], as moe_expert_ffn (NULL with E = 1: all n).
  * gx      device float [1], gw device float [E] (each NULL allowed = 1): the
- *         tensors' own scales.
+ *         tensors' own scales; with MX factors of y alone.
  * y       device [n] rows of m, ldy elements apart, of `dtype` (SYMM_DTYPE_F16 or
  *         _BF16); rows behind the last expert's are left as they were.
  * Sums are in 32 bits, gx gw_e and y rounded once each.  n, k as for moe_fp4_quantize,

@@ -726,13 +726,14 @@ extern "C" int moe_fp4_quantize(const void* x, size_t ldx, int act, int dtype, i
         !moe::aligned(gscale, 4))
       return fail(SYMM_EINVAL, "moe_fp4_quantize: x, codes and scales must be 16-byte aligned, "
                                "gscale 4-byte");
+    if (fmt == SYMM_FP4_MX && gscale)
+      return fail(SYMM_EINVAL, "moe_fp4_quantize: gscale must be NULL with SYMM_FP4_MX");
     if (codes == x || scales == x || codes == scales)
       return fail(SYMM_EINVAL, "moe_fp4_quantize: outputs must not be inputs or each other");
     QuantArgs a{};
     a.x = x, a.ldx = ldx, a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint8_t*>(scales), a.ldc = ldc, a.lds = lds, a.g = gscale;
     a.n = (uint32_t)n, a.k = (uint32_t)k, a.kv = (uint32_t)k / 8;
-    if (fmt == SYMM_FP4_MX) a.g = nullptr;
     cudaStream_t s = as_stream(stream);
     return dtype == SYMM_DTYPE_F32    ? launch_quantize<float>(fmt, act, a, s)
            : dtype == SYMM_DTYPE_BF16 ? launch_quantize<__nv_bfloat16>(fmt, act, a, s)

@@ -100,11 +100,13 @@ class MoeBlock:
     def _pack_weights(self, w):
         """(codes, scales, each expert's own scale) of w [E][k][m], as rows [E * m][k]."""
         E, k, m = w.shape
-        g = torch.exp2(torch.ceil(torch.log2(w.float().abs().amax((1, 2)) / 2688)))
-        packed = [self._pack(w[e].t().contiguous(), k, abi.SYMM_ACT_NONE, g[e:e + 1])
-                  for e in range(E)]
+        g = None
+        if self.fp4 == "nv":
+            g = torch.exp2(torch.ceil(torch.log2(w.float().abs().amax((1, 2)) / 2688)))
+        packed = [self._pack(w[e].t().contiguous(), k, abi.SYMM_ACT_NONE,
+                             None if g is None else g[e:e + 1]) for e in range(E)]
         codes, scales = (torch.stack(p) for p in zip(*packed))
-        return codes, scales, g if self.fp4 == "nv" else torch.ones_like(g)
+        return codes, scales, torch.ones(E, device=w.device) if g is None else g
 
     def _project(self, packed, weights, first, counts, m):
         """Packed rows, grouped by expert, times the packed weights of experts first .. ."""
