@@ -70,9 +70,11 @@ class MoeBlock:
         n = T * k                                     # rows a PE sends, at most
         self.back_rows = n + T                        # what returns, then the shared rows
         row, cap = 2 * D, W * n                       # a PE may receive every row there is
-        self.heap = TorchSymmHeap(W, (n + 2 * cap + self.back_rows) * row + (4 << 20))
+        grads = n if F is not None and not fp4 else 0  # the experts' gradients on their way back
+        self.heap = TorchSymmHeap(W, (n + 2 * cap + self.back_rows + grads) * row + (4 << 20))
         self.send, self.recv, self.sent, self.back, self.signals = (
             self.heap.malloc(x) for x in (n * row, cap * row, cap * row, self.back_rows * row, 64))
+        self.grads = self.heap.malloc(grads * row) if grads else None
         self.cap = cap
         f32, i32 = dict(device="cuda"), dict(device="cuda", dtype=torch.int32)
         self.o = dict(experts=torch.empty(W, T, k, **i32), weights=torch.empty(W, T, k, **f32),
@@ -228,10 +230,11 @@ class MoeBlock:
                 D, _p(dw_gu[d * per]), _p(dw_d[d * per]), _p(self.ws))
             sent[d, :n][order] = dx
         returned = pairs.t().contiguous()
-        abi.shmem_alltoall(self.heap.handle, self.sent, self.back, _p(returned), W, 2 * D, self.cap,
-                           self.back_rows, _p(self.ws), self.signals)
+        # beside the rows that came back, which a second backward pass reads again
+        abi.shmem_alltoall(self.heap.handle, self.sent, self.grads, _p(returned), W, 2 * D,
+                           self.cap, T * k, _p(self.ws), self.signals)
         # row `rows` of what came back is that choice's; an absent choice's row was not sent
-        at, back = self.rows[..., :k].long(), self._rows(self.back, self.back_rows).float()
+        at, back = self.rows[..., :k].long(), self._rows(self.grads, T * k).float()
         picked = torch.gather(back, 1, at.clamp(min=0).view(W, T * k, 1).expand(-1, -1, D))
         picked = torch.where((at >= 0).view(W, T * k, 1), picked, 0.0)
         return picked.view(W, T, k, D).sum(2), dw_gu, dw_d
@@ -240,7 +243,7 @@ class MoeBlock:
         """Gradients of what ``forward`` left: dx (through the residual stream), drows (of the
         rows that came back and the shared rows), dlogits, and the vectors' gradients.  With
         feed-forward experts also theirs: dh_experts (of the norm's output, [W, T, D] in 32
-        bits), dw_gu, dw_d."""
+        bits), dw_gu, dw_d.  What ``forward`` left stays: further calls may follow."""
         if self.fp4:
             raise ValueError("experts in 4 bits have no gradients")
         W, T, D, E, k, o = self.W, self.T, self.D, self.E, self.k, self.o
