@@ -138,17 +138,6 @@ __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
   pair_arrive();  // whoever touches the other CTA's barriers waits first
   symm::tc_fence_after();
 }
-__device__ __forceinline__ void leave_cta(Barriers& b, int warp) {
-  __syncwarp();
-  symm::tc_fence_before();
-  __syncthreads();
-  pair_sync();  // the other CTA's MMAs, arrivals and reads of TMEM are over too
-  if (warp == 1) {
-    symm::tc_fence_after();
-    pair_tmem_dealloc(b.tmem, 2 * kAccCols);
-  }
-}
-
 // ------------------------------------------------------------- epilogues --
 // Fragments of 16 rows (columns of TMEM) and this warp's 32 features, as
 // tmem_frags leaves them, packed in pairs of neighbouring rows.
@@ -232,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t half = t.bt / 2, xbytes = half * 128;
       const uint32_t col = 2 * t.col + rank, row = t.row + rank * half;
       for (uint32_t s = 0; s < slices; ++s) {
-        if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
+        if (!(ok = wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * ring.stage_bytes;
         uint64_t* full = &bar.full[st];
         if (elected) {
@@ -262,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (uint32_t i = first; ok && i < tiles; i += step)
       for (uint32_t s = 0; s < slices; ++s) {
-        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        if (!(ok = wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         if (elected) arrive_first(&bar.full[st]);
         if (++st == ring.stages) st = 0, ph ^= 1;
       }
@@ -275,12 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t bt = uniform(t.bt), xbytes = bt / 2 * 128, buf = seg & 1;
       const uint32_t idesc = mma_idesc(FMT, bt, kMMajor, false);
-      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+      if (!(ok = wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
       for (uint32_t s = 0; s < slices; ++s) {
-        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        if (!(ok = wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * ring.stage_bytes;
         if (elected) {
@@ -301,8 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && elected) pair_commit(&bar.tfull[buf]);
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-    if (elected) pair_commit_own(&bar.drain);  // every MMA is complete before TMEM is freed
-    symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+    if (elected) pair_commit(&bar.drain);
   } else {  // -------------------------------------------------- epilogue
     // Two warps to each 32 TMEM lanes, which take turns at the chunks of rows.
     const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
@@ -320,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fetch_rows(g, a.gu_in, 2 * a.F, t.row + r, f, t.rows - r, width);
         fetch_rows(u, a.gu_in, 2 * a.F, t.row + r, a.F + f, t.rows - r, width);
       }
-      const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+      const bool ok = wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
       if (any_of(!ok, kEpilogue)) {  // all threads leave, or none
         if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
@@ -423,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_first(&bar.tempty[buf]);  // the accumulator is free again
     }
   }
-  leave_cta(bar, warp);
+  leave_pair(&bar.drain, bar.tmem, 2 * kAccCols, a.budget_ns);
 }
 
 // ------------------------------------------------------------ grad_kernel --
@@ -504,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t m0 = t.m0 + rank * kBM, n0 = t.n0 + rank * kBM;
       const uint32_t r0 = table.off[t.e], r1 = table.off[t.e + 1];
       for (uint32_t r = r0; r < r1; r += 64) {
-        if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
+        if (!(ok = wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * kGradStage;
         if (elected) {
           symm::mbar_arrive_expect_tx(&bar.full[st], kGradStage);
@@ -532,11 +520,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (r0 == r1) continue;  // the epilogue writes zeros
       const uint32_t buf = seg & 1;
       const uint32_t phase = ((seg >> 1) & 1) ^ 1u;
-      if (!rank && !(ok = symm::mbar_wait_warp(&bar.tempty[buf], phase, a.budget_ns, a.ctl))) break;
+      if (!rank && !(ok = wait_warp(&bar.tempty[buf], phase, a.budget_ns, a.ctl))) break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
       for (uint32_t r = r0; r < r1; r += 64) {
-        if (!(ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
+        if (!(ok = wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* at = smem + st * kGradStage;
         const uint32_t left = min(64u, r1 - r), steps = (left + 15) / 16;
         if (left % 16) {  // the next expert's rows in the last step, a line of all boxes a turn
@@ -566,10 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++seg;
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-    if (!rank) {
-      if (elected) pair_commit_own(&bar.drain);
-      symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
-    }
+    if (!rank && elected) pair_commit(&bar.drain);
   } else {  // -------------------------------------------------- epilogue
     const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
     // 16 rows of the gradient and 64 columns go out by one copy: whole lines of 128
@@ -586,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t m = t.m, nf = t.nf, buf = seg & 1;
       const bool any = table.off[e] != table.off[e + 1];
       if (any) {
-        const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+        const bool ok = wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
         if (any_of(!ok, kEpilogue)) {  // all threads leave, or none
           if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
           break;
@@ -640,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (elected) bulk_wait();
   }
-  leave_cta(bar, warp);
+  leave_pair(&bar.drain, bar.tmem, 2 * kAccCols, a.budget_ns);
 }
 
 // ------------------------------------------------------------------- host --

@@ -169,6 +169,12 @@ __device__ __forceinline__ void load_lines(uint8_t* to, const CUtensorMap* map64
   for (; r < rows; r += 16) symm::tma_load_2d(to + r * 128, map16, x, (int)(row + r), bar);
 }
 
+// The bounded wait of the experts' kernels: 16 tries at a time, so that a budget or
+// another's give-up is noticed within a tile (256 tries outlast the longest one's 0.4 ms).
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
+                                          const Control* ctl) {
+  return symm::mbar_wait_warp<16>(bar, parity, budget_ns, ctl);
+}
 // How long a CTA that gives up waits for its own copies and MMAs, which nothing
 // but the hardware holds up: a second, however short the heap's budget is.
 __device__ __forceinline__ uint64_t drain_ns(uint64_t budget_ns) {
@@ -359,14 +365,39 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar) {
 }
 // Before a CTA of a pair may leave: its copies have landed (`full`; whether or not
 // anything used them), and what uses them has released them (`empty`: arrivals
-// from the other CTA, which must find this one's shared memory).  Bounded.
+// from the other CTA, which must find this one's shared memory).  Bounded: after a
+// wait that gave up, a `full` of the first CTA may lack the second one's word for
+// good, so all of them together have the time of one.
 __device__ __forceinline__ void drain_ring(uint64_t* full, uint64_t* empty, uint32_t stages,
                                            uint32_t loads, bool ok, uint64_t budget_ns) {
   const uint32_t first = loads > stages ? loads - stages : 0;
-  for (uint32_t i = first; i < loads; ++i)
-    symm::mbar_wait(&full[i % stages], (i / stages) & 1, drain_ns(budget_ns));
+  const uint64_t t0 = symm::globaltimer_ns(), most = drain_ns(budget_ns);
+  for (uint32_t i = first; i < loads; ++i) {
+    const uint64_t gone = symm::globaltimer_ns() - t0;
+    symm::mbar_wait(&full[i % stages], (i / stages) & 1, gone < most ? most - gone : 0);
+  }
   for (uint32_t i = first; ok && i < loads; ++i)
     ok = symm::mbar_wait(&empty[i % stages], (i / stages) & 1, drain_ns(budget_ns));
+}
+// The end of a kernel of CTA pairs, by all threads: all roles of this CTA are over, and
+// the first CTA's issuer has ended with pair_commit(drain), an arrival on `drain` of both.
+// Where a wait gave up, the other roles may have left with commits on their way to this
+// CTA's barriers (`empty`, `tfull`), the second CTA's too; the last of them is `drain`'s,
+// and the MMAs are over with it.  Only then may shared memory and TMEM go.  Bounded: a
+// wait that gives up raises the heap's abort flag, which ends the issuer's own waits.
+__device__ __forceinline__ void leave_pair(uint64_t* drain, uint32_t tmem, uint32_t ncols,
+                                           uint64_t budget_ns) {
+  const uint32_t warp = uniform(threadIdx.x >> 5);
+  __syncwarp();
+  symm::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) symm::mbar_wait(drain, 0, drain_ns(budget_ns));
+  __syncwarp();
+  pair_sync();  // the other CTA's MMAs, arrivals and reads of TMEM are over too
+  if (warp == 1) {
+    symm::tc_fence_after();
+    pair_tmem_dealloc(tmem, ncols);
+  }
 }
 // Launches clusters of two CTAs, as moe::launch.
 template <typename... P, typename... A>

@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t col = 2 * t.col + rank, row = t.row + rank * half;
       const bool few = t.bt == 32;
       for (uint32_t s = 0; s < slices; ++s) {
-        if (!(ok = symm::mbar_wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
+        if (!(ok = wait_warp(&bar.empty[st], ph, a.budget_ns, a.ctl))) break;
         uint8_t* buf = smem + st * stage_bytes;
         uint64_t* full = &bar.full[st];
         if (elected) {
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = first; ok && i < tiles; i += step, ++seg) {
       const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t buf = seg & 1;
-      if (!(ok = symm::mbar_wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
+      if (!(ok = wait_warp(&bar.tempty[buf], ((seg >> 1) & 1) ^ 1u, a.budget_ns, a.ctl)))
         break;
       symm::tc_fence_after();
       const uint32_t acc = tmem + buf * acc_cols;
@@ -474,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sa = tmem + 2 * acc_cols + slot * scale_cols;
         const uint32_t sb = sa + S::kTiles * 4;
         // whoever placed the scales, here and in the other CTA, has seen the copies land
-        ok = symm::mbar_wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl) &&
+        ok = wait_warp(&bar.placed[st], ph, a.budget_ns, a.ctl) &&
              (slots == stages ||
-              symm::mbar_wait_warp(&bar.sfree[slot], sph, a.budget_ns, a.ctl));
+              wait_warp(&bar.sfree[slot], sph, a.budget_ns, a.ctl));
         if (!ok) break;
         symm::tc_fence_after();
         const uint8_t* at = smem + st * stage_bytes;
@@ -512,8 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && elected) pair_commit(&bar.tfull[buf]);
     }
     if (!ok && elected) symm::record_error(a.ctl, symm::kErrTimedOut, -5);
-    if (elected) pair_commit_own(&bar.drain);
-    symm::mbar_wait(&bar.drain, 0, drain_ns(a.budget_ns));
+    if (elected) pair_commit(&bar.drain);
   } else if (warp >= 2 && warp < 10) {  // ---------------------- epilogue
     // Two warps to each 32 TMEM lanes, which take turns at the chunks of rows.
     const uint32_t q = (uint32_t)(warp & 3), turn = (uint32_t)(warp - 2) / 4;
@@ -525,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t buf = seg & 1, f = (2 * t.col + rank) * kBM + 32 * q;
       const uint32_t width = f < a.m ? a.m - f : 0;  // features from f on that are there
       const float scale = a.gw ? gx * a.gw[t.e] : gx;
-      const bool ok = symm::mbar_wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
+      const bool ok = wait_warp(&bar.tfull[buf], (seg >> 1) & 1, a.budget_ns, a.ctl);
       if (any_of(!ok, kEpilogue)) {  // all threads leave, or none
         if (threadIdx.x == 64) symm::record_error(a.ctl, symm::kErrTimedOut, -6);
         break;
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at(table, i, a.E, a.npair);
       const uint32_t rows = t.bt;
       for (uint32_t s = 0; s < slices; ++s) {
-        ok = symm::mbar_wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl);
+        ok = wait_warp(&bar.full[st], ph, a.budget_ns, a.ctl);
         uint8_t* at = smem + st * stage_bytes;
         const uint4* from = reinterpret_cast<const uint4*>(at + raw);
         uint32_t* to = reinterpret_cast<uint32_t*>(at + raw);
@@ -595,14 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) symm::record_error(a.ctl, symm::kErrTimedOut, -7);
   }
-  __syncwarp();
-  symm::tc_fence_before();
-  __syncthreads();
-  pair_sync();  // the other CTA's MMAs, arrivals and reads of TMEM are over too
-  if (warp == 1) {
-    symm::tc_fence_after();
-    pair_tmem_dealloc(tmem, kTmemCols);
-  }
+  leave_pair(&bar.drain, tmem, kTmemCols, a.budget_ns);
 }
 
 // ------------------------------------------------------------------- host --

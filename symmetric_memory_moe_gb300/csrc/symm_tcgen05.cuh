@@ -17,28 +17,32 @@ namespace symm {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-// Bounded wait that also gives up once any waiter of the heap has given up.
+// Bounded wait that also gives up once any waiter of the heap has given up.  It looks
+// at the clock and at the others every EVERY (a power of two) tries, of some 2 us each.
+template <uint32_t EVERY = 256>
 __device__ __forceinline__ bool mbar_wait_ab(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
                                              const Control* ctl) {
   const uint64_t t0 = globaltimer_ns();
   const uint64_t max_iters = budget_ns / 32 + (1u << 20);
   for (uint64_t it = 0;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255) == 255 &&
+    if ((it & (EVERY - 1)) == EVERY - 1 &&
         (ld_relaxed_u32(&ctl->abort) || globaltimer_ns() - t0 > budget_ns || it > max_iters))
       return false;
   }
 }
 // The same by a converged warp, with one answer for all its lanes; the loop
 // with the clock stays out of line, off the path of a barrier that is ready.
+template <uint32_t EVERY>
 static __device__ __noinline__ bool mbar_wait_ab_slow(uint64_t* bar, uint32_t parity,
                                                       uint64_t budget_ns, const Control* ctl) {
-  return mbar_wait_ab(bar, parity, budget_ns, ctl);
+  return mbar_wait_ab<EVERY>(bar, parity, budget_ns, ctl);
 }
+template <uint32_t EVERY = 256>
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t budget_ns,
                                                const Control* ctl) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
-         __all_sync(0xffffffffu, mbar_wait_ab_slow(bar, parity, budget_ns, ctl));
+         __all_sync(0xffffffffu, mbar_wait_ab_slow<EVERY>(bar, parity, budget_ns, ctl));
 }
 // True in one lane of a converged warp, the same one every time.  A role that
 // one thread would do runs in the whole warp instead, with only the issuing
