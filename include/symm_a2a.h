@@ -642,7 +642,9 @@ int moe_expert_ffn_backward(symm_heap_t *heap, const void *dy, size_t lddy, cons
  * x       device [n] rows, ldx elements apart (a multiple of 8), of `dtype`
  *         (SYMM_DTYPE_F16, _BF16 or _F32).  act SYMM_ACT_NONE: rows of k.
  *         Else rows of 2k, and what is packed is act(first k) * (last k) in 32
- *         bits: gu of the feed-forward becomes its second product's operand.
+ *         bits: gu of the feed-forward becomes its second product's operand.  (SiLU's
+ *         exponential is CUDA's approximate one, within 2 + 1.2 |g| ulp; of g
+ *         below -87.3 it may be 0.)
  * gscale  device float [1], positive (NULL allowed = 1).  NULL with MX, which has no
  *         scale of the tensor's: the same number given to the way back would
  *         multiply x by it.

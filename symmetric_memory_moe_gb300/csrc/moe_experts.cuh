@@ -441,7 +441,9 @@ inline unsigned resident_pairs(const void* kernel, unsigned block, size_t smem) 
 
 // act(g) and its derivative: g sigma(g), or g Phi(g) with the normal
 // distribution's Phi.  The exponential and the quotient are the approximate
-// instructions, 2 to 3 ulp of 24 bits, before a rounding to 16 bits or fewer.
+// instructions, before a rounding to 16 bits or fewer: exp(x) errs by up to 2 + 1.2 |x|
+// ulp of 24 bits, the quotient by 2, so that sigma is within some 2^-17 of itself at
+// g = -50; where 1 + exp(-g) exceeds 2^126 (g below -87.3) the quotient is 0.
 __device__ __forceinline__ float activate(int act, float g) {
   if (act == SYMM_ACT_SILU) return __fdividef(g, 1.f + __expf(-g));
   return g * normcdff(g);
