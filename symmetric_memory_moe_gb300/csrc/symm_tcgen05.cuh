@@ -180,19 +180,32 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 namespace symm_host {
 
-// The driver's tensor-map encoder, or NULL.
+// A driver function, or NULL.
+template <typename F>
+F driver_fn(const char* name, int version) {
+  cudaDriverEntryPointQueryResult q;
+  void* p = nullptr;
+  if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<F>(p);
+}
+// The driver's tensor-map encoder, or NULL.  It wants a current context, which a host
+// thread has once a runtime call has needed one: before its first launch it may have none.
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static std::mutex mu;
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::lock_guard<std::mutex> lock(mu);
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void* p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  static PFN_cuCtxGetCurrent_v4000 current = nullptr;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!current) current = driver_fn<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
+    if (!fn) fn = driver_fn<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
   }
+  CUcontext context = nullptr;
+  int dev = 0;
+  if (current && current(&context) == CUDA_SUCCESS && !context &&
+      cudaGetDevice(&dev) == cudaSuccess)
+    cudaSetDevice(dev);  // the device that this thread's launches go to
   return fn;
 }
 
