@@ -137,12 +137,14 @@ int symm_set_spin_budget(symm_heap_t *heap, uint64_t budget_ns);
 
 /* Synchronises `stream`, then returns the first device-side error recorded in
  * the heap header since the last check (SYMM_OK; SYMM_ETIMEDOUT; SYMM_ERANGE
- * from shmem_alltoall) and clears it.  Until it is cleared, every later
- * device wait on this heap gives up at once (the abort flag stays raised),
- * so check after any launch that may have timed out.  *info (optional)
+ * from shmem_alltoall and from the experts' operators) and clears it.  Until
+ * it is cleared, every later device wait on this heap gives up at once (the
+ * abort flag stays raised), so check after any launch that may have timed out.  *info (optional)
  * receives, for a wait that gave up, the byte offset from base of its
  * signal, or SYMM_INFO_NOALLOC_SIGNAL + an offset for a signal of
- * all2all_combine_pc_noalloc (see there).  Errors: SYMM_ECUDA. */
+ * all2all_combine_pc_noalloc (see there), or a number below 0 for a barrier inside a
+ * kernel.  What the call that gave up wrote, workspace and outputs, is then undefined.
+ * Errors: SYMM_ECUDA. */
 int symm_check_error(symm_heap_t *heap, void *stream, int64_t *info);
 
 /* Message of the last failed call on this thread ("" if none). */
@@ -585,8 +587,8 @@ int moe_expert_workspace(int n, int E, int D, int F, int backward, size_t *bytes
  * x       device [n] rows of D, ldx elements apart: expert 0's rows, then
  *         expert 1's, and so on.
  * counts  device int32 [E], read by the kernels: rows of each expert (NULL
- *         with E = 1: all n).  Their sum may be below n: rows behind the last
- *         expert's are not read, and those of y and gu left as they were.  A
+ *         with E = 1: all n).  Their sum may be below n: what rows behind the last
+ *         expert's hold is not used, and those of y and gu left as they were.  A
  *         negative count, or a sum above n, is found on the device: nothing is
  *         written and symm_check_error() reports SYMM_ERANGE.
  * w_gu    device [E][D][2F], dense: Wg beside Wu; w_d device [E][F][D], dense.
@@ -625,7 +627,8 @@ int moe_expert_ffn_backward(symm_heap_t *heap, const void *dy, size_t lddy, cons
  * of mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the even element in the
  * low half, and a scale for each block of a row:
  *   SYMM_FP4_MX  blocks of 32, scales e8m0 (byte b: 2^(b - 127), 255: NaN)
- *   SYMM_FP4_NV  blocks of 16, scales e4m3, times a 32-bit number of the tensor's
+ *   SYMM_FP4_NV  blocks of 16, scales e4m3 (sign bit 0), times a 32-bit number of the
+ *                tensor's
  * A packed row is k / 2 bytes of codes and, in a buffer of its own, a row of
  * scales, one byte each in the blocks' order; the row strides ldc and lds are in
  * bytes, multiples of 16. */

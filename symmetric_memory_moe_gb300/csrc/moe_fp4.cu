@@ -27,16 +27,17 @@
 //   warps 10-13  scales as they lie beside the codes (a row's one after another) into
 //              the order that TMEM takes: 4 scales of each of 128 rows, row r at
 //              word r / 32 of 16-byte line r % 32, in the place where they landed
-// 192 rows (NV: 160), not 256: two accumulators and four slots of scales fill TMEM.
+// 192 rows (NV: 160), not 256: two accumulators and five (NV: four) slots of scales fill TMEM.
 // What bounds it is the way of a stage around its ring (copies, placing, MMAs and back,
 // some 3000 cycles for 6 stages), then the issue of a slice (12 or 6 tcgen05.cp
 // and 4 MMAs from one thread, 450 cycles); the MMAs of a slice are 330.
 //
-// Measured.  32768 x 7168 in bf16, MX: 105 us to codes (85 % of the copy rate), 99 back;
-// NV 149 to codes.  32768 x 2048 of act(g) u: 68 us with SiLU, 167 with GELU.
-// Product, NV, 32 experts, 1024 rows each: 7168 x 4096 452 us (4.25 PFLOP/s), 2048 x 7168
-// 306 us (3.15 PFLOP/s; 584 with 2-byte stores from single CTAs); 64 rows, 7168 x 4096: 75 us,
-// the weights at 90 % of the copy rate.
+// Measured.  32768 x 7168 in bf16, MX: 105 to 114 us to codes (78 to 84 % of the copy rate),
+// 99 to 103 back; NV 149 to 151 to codes, 105 back.  In 32 bits: MX 179, back 249; NV 197,
+// back 253.  32768 x 2048 of act(g) u: NV 69 us with SiLU, 167 with GELU; MX 57, 162.
+// Product, 32 experts, 1024 rows each: 7168 x 4096 NV 455 us (4.2 PFLOP/s), MX 409; 2048 x
+// 7168 NV 306 (3.15 PFLOP/s; 584 with 2-byte stores from single CTAs), MX 284; 64 rows, 7168
+// x 4096, NV: 75 us, the weights at 90 % of the copy rate.
 #include <algorithm>
 #include <string>
 
@@ -291,7 +292,7 @@ constexpr uint32_t kExtraRows = 256;                 // 64 chose 128 rows, 474 u
 constexpr uint32_t kSlice = 256;                     // values of K: a row of 128 bytes
 constexpr uint32_t kATile = kBM * 128;               // 16 KB
 constexpr uint32_t kARaw = kBM * 16;                 // its scales, 16 bytes a row
-constexpr uint32_t kRingBytes = 204 * 1024;          // four stages of 128 x 192 tiles
+constexpr uint32_t kRingBytes = 204 * 1024;          // six stages of 128 x 192 tiles
 constexpr uint32_t kMaxStages = 9;
 constexpr uint32_t kStageWarp = 16 * kLine;          // where a warp of the epilogue stages rows
 constexpr uint32_t kSmemBytes = 1024 + kRingBytes + 8 * kStageWarp;
@@ -302,7 +303,7 @@ struct Scales {
   // 512-byte tiles of a slice: 4 scales of 128 rows, the K of one MMA (NV) or two (MX)
   static constexpr uint32_t kTiles = FMT == SYMM_FP4_MX ? 2 : 4;
   static constexpr uint32_t kPerSlice = kTiles * 4;      // scales of a row
-  // most rows of a tile: TMEM holds two accumulators and the scales of four stages
+  // most rows of a tile: TMEM holds two accumulators and the scales of four slices
   static constexpr uint32_t kMaxRows = FMT == SYMM_FP4_MX ? 192 : 160;
   static_assert(2 * kMaxRows + 4 * kTiles * 4 * 3 <= kTmemCols, "TMEM");
 };
