@@ -77,6 +77,7 @@ struct ExpertArgs {
   const void* gu_in;   // kDh
   void *gu, *h, *out;  // kGated: gu (NULL allowed), h; kDh: gu is [dg | du], h; else out
   size_t ldo;
+  bool more;           // another launch of this call follows
   uint64_t budget_ns;
   Control* ctl;
 };
@@ -201,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 32) prefetch_map(&map_w), prefetch_map(&map_x64), prefetch_map(&map_x16);
   set_up_cta(bar, warp);
-  moe::let_next_start();
   moe::wait_for_earlier();
+  if (a.more) moe::let_next_start();
   const bool good =
       lay_out(table, a.counts, a.E, a.n, kMaxRows, kExtraRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
@@ -473,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Table table;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   set_up_cta(bar, warp);
-  moe::let_next_start();
   moe::wait_for_earlier();
   const bool good = lay_out(table, a.counts, a.E, a.n, kMaxRows, 0, 1, 1);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
@@ -771,10 +771,10 @@ int forward(const char* what, const void* x, size_t ldx, const void* w_gu, const
   unsigned pairs = 0;
   int rc = set_up<FMT>(&pairs);
   if (rc) return rc;
-  a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu = gu, a.h = h;
+  a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu = gu, a.h = h, a.more = true;
   rc = rows_product<FMT, kGated>(what, x, ldx, w_gu, D, 2 * F, a, pairs, s);
   if (rc) return rc;
-  a.m = (uint32_t)D, a.k = (uint32_t)F, a.out = y, a.ldo = ldy;
+  a.m = (uint32_t)D, a.k = (uint32_t)F, a.out = y, a.ldo = ldy, a.more = false;
   return rows_product<FMT, kDown>(what, h, F, w_d, F, D, a, pairs, s);
 }
 
@@ -785,11 +785,13 @@ int backward(const char* what, const void* dy, size_t lddy, const void* x, size_
              cudaStream_t s) {
   unsigned pairs = 0;
   int rc = set_up<FMT>(&pairs);
+  const bool grads = dw_gu || dw_d;
   if (!rc && a.n) {
     a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu_in = gu, a.gu = dgu, a.h = h;
+    a.more = dx || grads;
     rc = rows_product<FMT, kDh>(what, dy, lddy, w_d, F, D, a, pairs, s);
     if (!rc && dx) {
-      a.m = (uint32_t)D, a.k = 2 * (uint32_t)F, a.out = dx, a.ldo = lddx;
+      a.m = (uint32_t)D, a.k = 2 * (uint32_t)F, a.out = dx, a.ldo = lddx, a.more = grads;
       rc = rows_product<FMT, kDx>(what, dgu, 2 * (size_t)F, w_gu, D, 2 * F, a, pairs, s);
     }
   }

@@ -201,7 +201,6 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
   constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;  // of a block
   constexpr bool GATED = ACT != SYMM_ACT_NONE;
   constexpr int kFlight = GATED || sizeof(T) == 4 ? 2 : 4;
-  moe::let_next_start();
   moe::wait_for_earlier();
   const float g = a.g ? *a.g : 1.f;
   Walk w(a.kv);
@@ -262,7 +261,6 @@ struct DequantArgs {
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kQuantThreads) dequantize_kernel(const DequantArgs a) {
   constexpr uint32_t kLanes = FMT == SYMM_FP4_MX ? 4 : 2;
-  moe::let_next_start();
   moe::wait_for_earlier();
   const float g = a.g ? *a.g : 1.f;
   for (Walk w(a.kv); w.row < a.n; w.next()) {
@@ -406,7 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   pair_arrive();  // whoever touches the other CTA's barriers waits first
   symm::tc_fence_after();
-  moe::let_next_start();
   moe::wait_for_earlier();
   const bool good =
       lay_out(table, a.counts, a.E, a.n, S::kMaxRows, kExtraRows, a.npair, gridDim.x / 2);
