@@ -59,12 +59,14 @@ __device__ __forceinline__ float block_sum_once(float v, float* red) {
 // the one before it on the stream ends; wait_for_earlier() holds it (before its
 // first access to memory) until that one's writes are visible.
 // let_next_start() is for a kernel whose own second launch follows, and comes after
-// wait_for_earlier(); the last kernel of a call never calls it.  A call then starts when the
-// one before it has ended, however many are queued, and at most one grid waits.  Where
-// every kernel let the next one start, and before it had waited itself, waiting grids
-// of several calls piled up, and a queue of packings and short products of CTA pairs,
-// each of which wants two whole SMs, stopped for good: small CTAs of a later call that
-// wait hold room which a pair of an earlier grid wants.
+// wait_for_earlier(); the last kernel of a call never calls it, nor do kernels of CTA pairs
+// at all.  A call then starts when the one before it has ended, however many are queued,
+// and at most one grid waits.  Where every kernel let the next one start, and before it
+// had waited itself, waiting grids of several calls piled up, and a queue of packings
+// and short products of CTA pairs, each of which wants two whole SMs, stopped for good:
+// small CTAs of a later call that wait hold room which a pair of an earlier grid wants.
+// (Between a feed-forward's own launches it gained nothing: 23.4 us with it, 23.4 without,
+// for 32 rows on 32 experts of 1024 x 512.)
 __device__ __forceinline__ void wait_for_earlier() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

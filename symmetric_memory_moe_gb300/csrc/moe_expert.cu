@@ -77,7 +77,6 @@ struct ExpertArgs {
   const void* gu_in;   // kDh
   void *gu, *h, *out;  // kGated: gu (NULL allowed), h; kDh: gu is [dg | du], h; else out
   size_t ldo;
-  bool more;           // another launch of this call follows
   uint64_t budget_ns;
   Control* ctl;
 };
@@ -118,7 +117,7 @@ struct Barriers {
   uint64_t tfull[2], tempty[2], drain;
   uint32_t tmem;
 };
-// Barriers and TMEM, before the launch before this one has ended.
+// Barriers and TMEM.
 __device__ __forceinline__ void set_up_cta(Barriers& b, int warp) {
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < kMaxStages; ++s) {
@@ -203,7 +202,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32) prefetch_map(&map_w), prefetch_map(&map_x64), prefetch_map(&map_x16);
   set_up_cta(bar, warp);
   moe::wait_for_earlier();
-  if (a.more) moe::let_next_start();
   const bool good =
       lay_out(table, a.counts, a.E, a.n, kMaxRows, kExtraRows, a.npair, gridDim.x / 2);
   if (!good && blockIdx.x == 0 && threadIdx.x == 0) symm::record_error(a.ctl, kErrRange, -1);
@@ -771,10 +769,10 @@ int forward(const char* what, const void* x, size_t ldx, const void* w_gu, const
   unsigned pairs = 0;
   int rc = set_up<FMT>(&pairs);
   if (rc) return rc;
-  a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu = gu, a.h = h, a.more = true;
+  a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu = gu, a.h = h;
   rc = rows_product<FMT, kGated>(what, x, ldx, w_gu, D, 2 * F, a, pairs, s);
   if (rc) return rc;
-  a.m = (uint32_t)D, a.k = (uint32_t)F, a.out = y, a.ldo = ldy, a.more = false;
+  a.m = (uint32_t)D, a.k = (uint32_t)F, a.out = y, a.ldo = ldy;
   return rows_product<FMT, kDown>(what, h, F, w_d, F, D, a, pairs, s);
 }
 
@@ -785,13 +783,11 @@ int backward(const char* what, const void* dy, size_t lddy, const void* x, size_
              cudaStream_t s) {
   unsigned pairs = 0;
   int rc = set_up<FMT>(&pairs);
-  const bool grads = dw_gu || dw_d;
   if (!rc && a.n) {
     a.m = (uint32_t)F, a.k = (uint32_t)D, a.gu_in = gu, a.gu = dgu, a.h = h;
-    a.more = dx || grads;
     rc = rows_product<FMT, kDh>(what, dy, lddy, w_d, F, D, a, pairs, s);
     if (!rc && dx) {
-      a.m = (uint32_t)D, a.k = 2 * (uint32_t)F, a.out = dx, a.ldo = lddx, a.more = grads;
+      a.m = (uint32_t)D, a.k = 2 * (uint32_t)F, a.out = dx, a.ldo = lddx;
       rc = rows_product<FMT, kDx>(what, dgu, 2 * (size_t)F, w_gu, D, 2 * F, a, pairs, s);
     }
   }
